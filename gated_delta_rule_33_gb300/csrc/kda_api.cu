@@ -7,6 +7,7 @@
 
 #include "../../include/kda.h"
 #include "kda_internal.cuh"
+#include "kda_paged.cuh"
 
 namespace {
 
@@ -86,6 +87,61 @@ kda_status check_prefill_args(const void *q, const void *k, const void *v, const
         !aligned16(o) || !aligned16(initial_state) || !aligned16(final_state) ||
         !aligned16(cu_seqlens))
         return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+
+// Checks a cache description and turns it into what the kernels take.
+kda_status paged_view(const kda_paged_cache *c, kda::PagedView *view) {
+    if (c == nullptr || c->num_pages < 1 || c->page_size < 1 || c->heads < 1)
+        return KDA_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (c->dtype != KDA_BF16 && c->dtype != KDA_FP8_E4M3) return KDA_ERR_UNSUPPORTED_DTYPE;
+    if (static_cast<int64_t>(c->num_pages) * c->page_size > INT32_MAX ||
+        static_cast<int64_t>(c->heads) * c->head_dim > INT32_MAX / 4)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (c->k == nullptr || c->v == nullptr) return KDA_ERR_INVALID_ARG;
+    if ((c->k_scale == nullptr) != (c->v_scale == nullptr)) return KDA_ERR_INVALID_ARG;
+    const bool fp8 = c->dtype == KDA_FP8_E4M3;
+    if (!fp8 && c->k_scale != nullptr) return KDA_ERR_INVALID_ARG;
+    const int64_t size = fp8 ? 1 : 2;
+    // The rows of head_dim values must not overlap: in order of their strides,
+    // each dimension of more than one entry steps past all that lies inside it.
+    struct Dim {
+        int64_t stride, count;
+    } d[3] = {{c->head_stride, c->heads},
+              {c->token_stride, c->page_size},
+              {c->page_stride, c->num_pages}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (d[j].stride > d[j + 1].stride) {
+                const Dim x = d[j];
+                d[j] = d[j + 1];
+                d[j + 1] = x;
+            }
+    int64_t inside = c->head_dim;
+    for (const Dim &x : d) {
+        if (x.count == 1) continue;
+        if (x.stride < inside) return KDA_ERR_INVALID_ARG;
+        if (x.stride > INT64_MAX / 8 / x.count) return KDA_ERR_INVALID_ARG;
+        if (x.stride * size % 16 != 0) return KDA_ERR_MISALIGNED;
+        inside += x.stride * (x.count - 1);
+    }
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+        return KDA_ERR_MISALIGNED;
+    view->k = static_cast<uint8_t *>(c->k);
+    view->v = static_cast<uint8_t *>(c->v);
+    view->k_scale = c->k_scale;
+    view->v_scale = c->v_scale;
+    // the stride of a single entry is never taken
+    view->page_stride = c->num_pages == 1 ? 0 : c->page_stride * size;
+    view->token_stride = c->page_size == 1 ? 0 : c->token_stride * size;
+    view->head_stride = c->heads == 1 ? 0 : c->head_stride * size;
+    view->page = kda::FastDiv(static_cast<uint32_t>(c->page_size));
+    view->num_pages = c->num_pages;
+    view->heads = c->heads;
+    view->head_dim = c->head_dim;
+    view->fp8 = fp8;
     return KDA_OK;
 }
 
@@ -598,6 +654,116 @@ kda_status kda_chunk_backward_checkpointed(const void *q, const void *k, const v
         static_cast<const __nv_bfloat16 *>(v), g, beta, cu_seqlens, B, N, H, scale, checkpoints,
         dO, dO_dtype == KDA_BF16, dS_final, dq, dk, dv, dg, dbeta, dS0, workspace, ctas,
         dev->error_word, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_page_plan(const int32_t *cached_lens, const int32_t *new_lens,
+                         const int32_t *free_pages, int num_free, int32_t *block_table,
+                         int max_pages, int B, int page_size, int num_pages, int32_t *seq_lens,
+                         int32_t *cu_seqlens, int32_t *slot_map, int64_t N, int32_t *pages_used,
+                         void *stream) {
+    if (B < 0 || N < 0 || N > INT32_MAX || num_free < 0 || max_pages < 0 || page_size < 1 ||
+        num_pages < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (cu_seqlens == nullptr || pages_used == nullptr || (N > 0 && slot_map == nullptr) ||
+        (num_free > 0 && free_pages == nullptr))
+        return KDA_ERR_INVALID_ARG;
+    if (B > 0 && (cached_lens == nullptr || new_lens == nullptr || seq_lens == nullptr ||
+                  (max_pages > 0 && block_table == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(cached_lens) || !aligned16(new_lens) ||
+        (reinterpret_cast<uintptr_t>(free_pages) & 3u) != 0 || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(cu_seqlens) ||
+        !aligned16(slot_map) || !aligned16(pages_used))
+        return KDA_ERR_MISALIGNED;
+    // every CTA reads the lists while others write the results
+    const size_t rows = static_cast<size_t>(B) * 4;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } bufs[] = {{seq_lens, rows},
+                {cu_seqlens, rows + 4},
+                {slot_map, static_cast<size_t>(N) * 4},
+                {pages_used, 4},
+                {block_table, rows * static_cast<size_t>(max_pages)},
+                {cached_lens, rows},
+                {new_lens, rows},
+                {free_pages, static_cast<size_t>(num_free) * 4}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if (overlaps(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+                return KDA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    kda_status st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_page_plan(cached_lens, new_lens, free_pages, num_free, block_table,
+                                           max_pages, B, page_size, num_pages, seq_lens, cu_seqlens,
+                                           slot_map, N, pages_used, dev->error_word,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_paged_append(const void *k, const void *v, int64_t k_row_stride,
+                            int64_t v_row_stride, const int32_t *slot_map, int64_t N,
+                            const kda_paged_cache *cache, void *stream) {
+    kda::PagedView view;
+    kda_status st = paged_view(cache, &view);
+    if (st != KDA_OK) return st;
+    if (N < 0 || N > INT32_MAX || view.k == view.v) return KDA_ERR_INVALID_ARG;
+    if (N > 0 && (k == nullptr || v == nullptr || slot_map == nullptr)) return KDA_ERR_INVALID_ARG;
+    const int64_t width = static_cast<int64_t>(view.heads) * view.head_dim;
+    if (N > 1 && (k_row_stride < width || v_row_stride < width)) return KDA_ERR_INVALID_ARG;
+    if (k_row_stride > INT64_MAX / 4 / (N + 1) || v_row_stride > INT64_MAX / 4 / (N + 1))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slot_map) ||
+        (N > 1 && (k_row_stride % 8 != 0 || v_row_stride % 8 != 0)))
+        return KDA_ERR_MISALIGNED;
+    if (N == 0) return KDA_OK;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_paged_append(
+        static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v), k_row_stride,
+        v_row_stride, slot_map, N, view, dev->error_word, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int head_dim) {
+    if (B < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return kda::paged_decode_workspace_bytes(B, q_heads, kv_heads, head_dim);
+}
+
+kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged_cache *cache,
+                            const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                            int B, int q_heads, float scale, void *o, kda_dtype o_dtype,
+                            float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    kda::PagedView view;
+    kda_status st = paged_view(cache, &view);
+    if (st != KDA_OK) return st;
+    if (B < 0 || max_pages < 0 || q_heads < 1) return KDA_ERR_INVALID_ARG;
+    if (q_heads % view.heads != 0) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = static_cast<int64_t>(q_heads) * view.head_dim;
+    if (width > INT32_MAX || static_cast<int64_t>(B) * q_heads > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!valid_dtype(o_dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
+    if (B > 0 && (q == nullptr || seq_lens == nullptr || o == nullptr ||
+                  (max_pages > 0 && block_table == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (B > 1 && (q_row_stride < width || q_row_stride > INT64_MAX / 4 / B))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(o) ||
+        !aligned16(lse) || !aligned16(workspace) || (B > 1 && q_row_stride % 8 != 0))
+        return KDA_ERR_MISALIGNED;
+    const size_t need = kda::paged_decode_workspace_bytes(B, q_heads, view.heads, view.head_dim);
+    if (workspace_bytes < need || (need > 0 && workspace == nullptr))
+        return KDA_ERR_WORKSPACE_TOO_SMALL;
+    if (B == 0) return KDA_OK;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_paged_decode(
+        static_cast<const __nv_bfloat16 *>(q), q_row_stride, view, block_table, max_pages, seq_lens,
+        B, q_heads, scale, o, o_dtype == KDA_BF16, lse, workspace, dev->error_word, dev->num_sms,
+        static_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_debug_check_gate_division(uint64_t *mismatches, void *stream) {

@@ -20,6 +20,7 @@ from . import _build
 
 KDA_BF16 = 0
 KDA_FP32 = 1
+KDA_FP8_E4M3 = 2
 KDA_ALOG_PER_HEAD = 0
 KDA_ALOG_PER_CHANNEL = 1
 KDA_ALOG_PER_HEAD_CHANNEL = 2
@@ -118,6 +119,15 @@ def load():
         lib.kda_gate_backward.argtypes = [P, I, P, I, P, I, P, P, P, P, P, P, P, I64, I, I, P,
                                           ctypes.c_size_t, P]
         lib.kda_gate_backward.restype = I
+        lib.kda_page_plan.argtypes = [P, P, P, I, P, I, I, I, I, P, P, P, I64, P, P]
+        lib.kda_page_plan.restype = I
+        lib.kda_paged_append.argtypes = [P, P, I64, I64, P, I64, P, P]
+        lib.kda_paged_append.restype = I
+        lib.kda_paged_decode_workspace_size.argtypes = [I, I, I, I]
+        lib.kda_paged_decode_workspace_size.restype = ctypes.c_size_t
+        lib.kda_paged_decode.argtypes = [P, I64, P, P, I, P, I, I, F, P, I, P, P, ctypes.c_size_t,
+                                         P]
+        lib.kda_paged_decode.restype = I
         lib.kda_debug_check_gate_division.argtypes = [P, P]
         lib.kda_debug_check_gate_division.restype = I
         lib.kda_debug_set_wait_limit.argtypes = [I64, I64]
@@ -361,6 +371,126 @@ def kda_gate_backward(f, b, A_log, alog_mode, dt_bias, dg, dbeta, df, db, dA_log
     _check(st, "kda_gate_backward")
 
 
+class _CacheStruct(ctypes.Structure):
+    """kda_paged_cache of include/kda.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class PagedCache:
+    """One layer's paged key-value cache: the tensors, described once for the calls.
+
+    k_cache, v_cache: [num_pages, page_size, heads, head_dim], bf16 or
+    float8_e4m3fn, of equal strides, head_dim contiguous (pages stored head by
+    head are the permuted view of [num_pages, heads, page_size, head_dim]).
+    k_scale, v_scale: fp32 [heads] for an 8-bit cache, or None (1)."""
+
+    def __init__(self, k_cache, v_cache, k_scale=None, v_scale=None):
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+            raise ValueError("k_cache and v_cache are [num_pages, page_size, heads, head_dim] alike")
+        if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+            raise ValueError("k_cache and v_cache need equal strides and a contiguous head_dim")
+        if k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
+            raise ValueError("k_cache and v_cache need one dtype and device")
+        if k_cache.dtype == torch.bfloat16:
+            dtype = KDA_BF16
+        elif k_cache.dtype == torch.float8_e4m3fn:
+            dtype = KDA_FP8_E4M3
+        else:
+            raise TypeError(f"unsupported cache dtype {k_cache.dtype}")
+        num_pages, page_size, heads, head_dim = k_cache.shape
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float32 or s.shape != (heads,)
+                                  or s.device != k_cache.device):
+                raise ValueError("a scale is fp32 [heads] on the cache's device")
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device = k_cache.device
+        self.num_pages, self.page_size, self.heads, self.head_dim = k_cache.shape
+        self._struct = _CacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale),
+                                    _p(v_scale), *k_cache.stride()[:3], dtype, num_pages,
+                                    page_size, heads, head_dim)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _i32(t: Optional[torch.Tensor]):
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError(f"int32 tensor expected, got {t.dtype}")
+    return _p(t)
+
+
+def _rows(t: torch.Tensor, width: int):
+    """Pointer and row stride of [N, heads, head_dim] (or [N, width]) bf16 rows that may lie
+    further apart than their width."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"bf16 tensor expected, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if t.dim() == 3:
+        ok = (shape[1] * shape[2] == width and strides[2] == 1
+              and (shape[1] == 1 or strides[1] == shape[2]))
+    else:
+        ok = t.dim() == 2 and shape[1] == width and strides[1] == 1
+    if not ok:
+        raise ValueError(f"rows of {width} contiguous values expected")
+    return t.data_ptr(), strides[0]
+
+
+def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, seq_lens,
+                  cu_seqlens, slot_map, pages_used, stream=None):
+    """Extends block_table [B, max_pages] by pages of free_pages and maps every new token to
+    its slot; writes seq_lens [B], cu_seqlens [B+1], slot_map [N] and pages_used [1]."""
+    B, max_pages = block_table.shape
+    if (cached_lens.numel() != B or new_lens.numel() != B or seq_lens.numel() != B
+            or cu_seqlens.numel() != B + 1 or pages_used.numel() != 1):
+        raise ValueError("cached_lens, new_lens, seq_lens [B], cu_seqlens [B+1], pages_used [1]")
+    st = load().kda_page_plan(_i32(cached_lens), _i32(new_lens), _i32(free_pages),
+                              free_pages.numel(), _i32(block_table), max_pages, B, int(page_size),
+                              int(num_pages), _i32(seq_lens), _i32(cu_seqlens), _i32(slot_map),
+                              slot_map.numel(), _i32(pages_used),
+                              _stream(stream, block_table.device))
+    _check(st, "kda_page_plan")
+
+
+def kda_paged_append(k, v, slot_map, cache, stream=None):
+    """k, v bf16 [N, heads, head_dim] (rows may be slices of a wider tensor); slot_map [N]."""
+    width = cache.heads * cache.head_dim
+    N = slot_map.numel()
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError("k and v need one row per entry of slot_map")
+    kp, ks = _rows(k, width)
+    vp, vs = _rows(v, width)
+    st = load().kda_paged_append(kp, vp, ks, vs, _i32(slot_map), N, cache._ref,
+                                 _stream(stream, k.device))
+    _check(st, "kda_paged_append")
+
+
+def kda_paged_decode_workspace_size(B, q_heads, kv_heads, head_dim) -> int:
+    return int(load().kda_paged_decode_workspace_size(B, q_heads, kv_heads, head_dim))
+
+
+def kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, workspace, stream=None):
+    """q bf16 [B, q_heads, head_dim] (rows may lie apart); o alike, bf16 or fp32; lse fp32
+    [B, q_heads] or None."""
+    B, q_heads, head_dim = q.shape
+    if head_dim != cache.head_dim or o.shape != q.shape:
+        raise ValueError("q and o are [B, q_heads, head_dim] with the cache's head_dim")
+    if block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table [B, max_pages] and seq_lens [B]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * q_heads):
+        raise ValueError("lse is fp32 [B, q_heads]")
+    qp, qs = _rows(q, q_heads * head_dim)
+    st = load().kda_paged_decode(qp, qs, cache._ref, _i32(block_table), block_table.shape[1],
+                                 _i32(seq_lens), B, q_heads, float(scale), _p(o), _dtype_code(o),
+                                 _p(lse), _p(workspace),
+                                 workspace.numel() * workspace.element_size(),
+                                 _stream(stream, q.device))
+    _check(st, "kda_paged_decode")
+
+
 def kda_debug_check_gate_division(stream=None) -> int:
     """Differing results of the gate's fast division against IEEE division
     over every operand pair of its common path (0: bit-exact)."""
@@ -553,3 +683,27 @@ def decode(q, k, v, g, beta, state, scale=1.0, o_dtype=torch.bfloat16, stream=No
     o = torch.empty(B, H, v.shape[-1], dtype=o_dtype, device=q.device)
     kda_recurrent_decode(q, k, v, g, beta, state, scale, o, stream)
     return o
+
+
+def page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, num_tokens,
+              stream=None):
+    """Places a step's num_tokens new tokens (block_table is extended in place); returns
+    (seq_lens, cu_seqlens, slot_map, pages_used)."""
+    B, dev = block_table.shape[0], block_table.device
+    seq_lens, cu, slots, used = (torch.empty(n, dtype=torch.int32, device=dev)
+                                 for n in (B, B + 1, num_tokens, 1))
+    kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, seq_lens,
+                  cu, slots, used, stream)
+    return seq_lens, cu, slots, used
+
+
+def paged_decode(q, cache, block_table, seq_lens, scale=1.0, o_dtype=torch.bfloat16,
+                 want_lse=False, stream=None):
+    """Attention of one new token per sequence over the paged cache; returns (o, lse or None)."""
+    B, q_heads, head_dim = q.shape
+    o = torch.empty(B, q_heads, head_dim, dtype=o_dtype, device=q.device)
+    lse = torch.empty(B, q_heads, device=q.device) if want_lse else None
+    ws = torch.empty(max(kda_paged_decode_workspace_size(B, q_heads, cache.heads, head_dim), 16),
+                     dtype=torch.uint8, device=q.device)
+    kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, ws, stream)
+    return o, lse

@@ -63,7 +63,8 @@ typedef enum kda_status {
 
 typedef enum kda_dtype {
     KDA_BF16 = 0,
-    KDA_FP32 = 1
+    KDA_FP32 = 1,
+    KDA_FP8_E4M3 = 2                /* storage of a paged cache only (kda_paged_cache) */
 } kda_dtype;
 
 /*
@@ -522,6 +523,146 @@ kda_status kda_short_conv_qkv_step(const void *x_q, const void *x_k, const void 
                                    void *conv_state_pool, const int32_t *state_indices,
                                    int num_slots, int B, int C,
                                    void *q, void *k, void *v, void *stream);
+
+/*
+ * The paged key-value cache of the softmax-attention layers between KDA layers
+ * (K3_ARTIFACT_AUDIT.md section 3.1: 69 KDA and 24 attention layers), in
+ * preallocated pages that are written by index: the Kimi-K3 code audit's
+ * "repeated-mla-cache-concatenation" recommendation, as for the state pool of
+ * kda_recurrent_decode_indexed.  Three entry points serve one step of a batch:
+ *
+ *   kda_page_plan     block table, slot map and offsets of the step's tokens,
+ *                     from the requests' lengths, on the device (once a step)
+ *   kda_paged_append  the step's keys and values into the cache (each layer)
+ *   kda_paged_decode  attention of one new token per sequence (each layer)
+ *
+ * A slot is page * page_size + offset: the place of one token.  A sequence's
+ * position p lies in page block_table[b, p / page_size] at offset p % page_size.
+ *
+ * kda_paged_cache describes one layer's cache.  It is a host struct that the
+ * calls read before they return; the memory it points to is the caller's.
+ *
+ *   k, v            device: the cache's keys and values (equal layouts)
+ *   k_scale/v_scale fp32 [heads] device, or both NULL (1): an 8-bit cache holds
+ *                   key / k_scale[h]; must be NULL for a bf16 cache
+ *   page_stride, token_stride, head_stride
+ *                   distances in elements from a page, a token of a page and a
+ *                   head to the next; head_dim is contiguous.  Any order
+ *                   of the three (pages stored token by token or head by head,
+ *                   keys and values interleaved by page) whose rows do not
+ *                   overlap; multiples of 16 bytes.
+ *   dtype           KDA_BF16 or KDA_FP8_E4M3
+ *   num_pages, page_size, heads
+ *                   any positive numbers with num_pages * page_size < 2^31
+ *   head_dim        64, 128 or 256
+ */
+typedef struct kda_paged_cache {
+    void *k;
+    void *v;
+    const float *k_scale;
+    const float *v_scale;
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t dtype;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+} kda_paged_cache;
+
+/*
+ * kda_page_plan -- places a step's new tokens: extends the block table by
+ * pages from a free list and maps every new token to its slot.  With
+ * c = cached_lens[b], n = new_lens[b] and ceil() the number of pages of a length,
+ *
+ *   need[b] = ceil(c + n) - ceil(c),   off[b] = sum of need[a] over a < b
+ *   block_table[b, ceil(c) + i] = free_pages[off[b] + i],   i < need[b]
+ *   seq_lens[b] = c + n,   cu_seqlens[b + 1] = cu_seqlens[b] + n
+ *   slot_map[cu_seqlens[b] + j] = slot of position c + j of request b,  j < n
+ *
+ *   cached_lens  int32 [B] device: tokens already in the cache
+ *   new_lens     int32 [B] device: tokens of this step (0: none)
+ *   free_pages   int32 [num_free] device: pages to take, from the front (a list
+ *                whose front was dropped: 4-byte aligned is enough)
+ *   block_table  int32 [B, max_pages] device: the first ceil(c) entries of a
+ *                row are read, the next need[b] written, the rest left alone
+ *   seq_lens     int32 [B] written: what kda_paged_decode reads
+ *   cu_seqlens   int32 [B+1] written: what kda_chunk_prefill reads
+ *   slot_map     int32 [N] written: what kda_paged_append reads; entries past
+ *                the step's tokens are -1 (N may exceed their number)
+ *   pages_used   int32 [1] written: how many of free_pages were taken
+ *
+ * The lists are not advanced (the caller drops pages_used pages from the front),
+ * so the call may be repeated.  A request is refused, with INVALID_ARG in the
+ * device error word, if a length is negative, c + n exceeds
+ * max_pages * page_size or 2^31 - 1, or its pages or tokens end past num_free or
+ * N: its slots are -1, its row of the table is unchanged and seq_lens[b] = c (0
+ * where c itself is out of range).  Its n > 0 tokens keep their rows (offsets
+ * past N read N); its pages count for the requests after it, except where its
+ * lengths are bad.  A page outside 0 .. num_pages-1 gives its tokens slot
+ * -1 and sets INVALID_ARG too.  No output may overlap an input or another
+ * output.  B == 0 and N == 0 are allowed.
+ */
+kda_status kda_page_plan(const int32_t *cached_lens, const int32_t *new_lens,
+                         const int32_t *free_pages, int num_free, int32_t *block_table,
+                         int max_pages, int B, int page_size, int num_pages, int32_t *seq_lens,
+                         int32_t *cu_seqlens, int32_t *slot_map, int64_t N, int32_t *pages_used,
+                         void *stream);
+
+/*
+ * kda_paged_append -- writes the keys and values of N tokens to their slots:
+ *
+ *   cache.k[slot_map[n], h, :] = k[n, h, :]                       (bf16 cache)
+ *   cache.k[slot_map[n], h, :] = e4m3(k[n, h, :] / k_scale[h])    (8-bit cache)
+ *
+ * and v alike; e4m3 rounds the fp32 quotient to nearest, ties to even, and
+ * limits its magnitude to 448 (NaN stays NaN).
+ *
+ *   k, v      bf16, token n's [heads, head_dim] values from k + n * k_row_stride
+ *             (v_row_stride for v; in elements, multiples of 8, at least
+ *             heads * head_dim: both may be slices of a fused projection)
+ *   slot_map  int32 [N] device.  A negative slot leaves its token out; one past
+ *             the cache is left out too and sets INVALID_ARG in the device error
+ *             word.  Two tokens must not share a slot.
+ * The sources must not overlap the cache.  N == 0 is a no-op.
+ */
+kda_status kda_paged_append(const void *k, const void *v, int64_t k_row_stride,
+                            int64_t v_row_stride, const int32_t *slot_map, int64_t N,
+                            const kda_paged_cache *cache, void *stream);
+
+/* Bytes of device workspace kda_paged_decode needs (0 for sizes that it rejects). */
+size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * kda_paged_decode -- softmax attention of one new token per sequence over its
+ * cached keys (its own among them, once appended).  With L = seq_lens[b] and
+ * the key head of query head h being h / (q_heads / heads),
+ *
+ *   s[j] = scale * <q[b, h], key j>,  j < L
+ *   o[b, h] = sum_j exp(s[j] - lse) value j,   lse[b, h] = log sum_j exp(s[j])
+ *
+ *   q           bf16, sequence b's [q_heads, head_dim] values from
+ *               q + b * q_row_stride (elements, a multiple of 8)
+ *   block_table int32 [B, max_pages] device;  seq_lens int32 [B] device
+ *   q_heads     a positive multiple of cache->heads
+ *   o           [B, q_heads, head_dim] of o_dtype (bf16 or fp32), written.  fp32
+ *               outputs keep 16 bits of every softmax weight, bf16 ones 8.
+ *   lse         fp32 [B, q_heads] written, or NULL: with fp32 outputs, what joins
+ *               the results over two sets of keys
+ *   workspace   device scratch, >= kda_paged_decode_workspace_size() bytes,
+ *               16-byte aligned; not shared with a concurrent call
+ *
+ * An empty sequence gives o = 0 and lse = -inf.  A length below 0 or above
+ * max_pages * page_size counts as empty, and keys on a page outside
+ * 0 .. num_pages-1 are left out; both set INVALID_ARG in the device error word.
+ * Memory past a sequence's last key is not read.  Two calls on the same inputs
+ * write the same bits.  B == 0 is a no-op.
+ */
+kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged_cache *cache,
+                            const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                            int B, int q_heads, float scale, void *o, kda_dtype o_dtype,
+                            float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * kda_debug_check_gate_division -- test hook: the gate kernel's common path
