@@ -3,9 +3,9 @@ against the oracle's plain fp64 definitions.
 
 Tolerances (derived, per element).  The plan is exact; a bf16 append is a copy;
 an 8-bit append rounds the fp32 quotient to nearest: exact.  Attention: with
-w = sum_j p_j |v_j|, weights kept to 8 bits (bf16 outputs) are off by at most
-2^-9 of themselves, to 16 bits (fp32 outputs) 2^-17, which the sum carries to
-w; a bf16 output adds its own 2^-9 of |o| <= w.  Scores are fp32 sums of exact
+w = sum_j p_j |v_j|, a bf16 output is rounded by up to 2^-8 of |o| <= w, which
+leaves next to nothing for the weights; for fp32 outputs they may be off by
+2^-17 of themselves (two words of 8 bits), which the sum carries to w.  Scores are fp32 sums of exact
 products in steps of at least 8 terms: off by (D / 8 + 8) 2^-23 of
 S = max_j scale sum_d |q_d k_jd|, and ex2 and the sums by some 2^-21; a score's
 error reaches a weight and the normalisation, so twice.  lse carries the score
