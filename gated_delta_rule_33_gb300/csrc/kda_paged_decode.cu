@@ -11,33 +11,38 @@
 // Bound: every key and value is read once, 4 G flops for the 2 (or 4) bytes of
 // a value at G query heads to a key head: HBM up to G = 100.  So what matters is
 // that every SM has copies in flight from the first microsecond to the last,
-// whatever the lengths.
+// whatever the lengths, and that a warp's instructions for a tile take less time
+// than its copy.
 //
-// Split.  A unit is (sequence, key head, group of 16 query heads); its keys are
-// cut in tiles of 8 KB of keys and values (16 KB at 256 channels in bf16).  The
-// tiles of all units form one list, and each warp of the grid takes an equal,
-// contiguous piece of it: long sequences are cut, short ones share a warp, and
-// no warp has more than one tile more than another.  A piece ends in at most two
-// cut units; their parts are joined within the CTA through shared memory, and
-// what is cut between CTAs by a second, small kernel that is launched with the
-// first and waits for it (programmatic dependent launch).
+// Split.  A unit is (sequence, key head, group of up to 16 query heads); its keys
+// are cut in tiles of 4 KB of keys and 4 KB of values (8 KB each at 256 channels
+// in bf16).  The tiles of all units form one list; each CTA takes an equal,
+// contiguous piece of it and each warp an equal part of that: long sequences are
+// cut, short ones share a warp.  A warp's part ends in at most two cut units;
+// their parts are joined within the CTA through shared memory, and what is cut
+// between CTAs by a second, small kernel that is launched with the first and
+// waits for it (programmatic dependent launch).  Where the block table has no
+// room for long sequences, the pieces are moved to the units' ends instead, and
+// the second kernel is not launched.
 //
-// A warp copies its own tiles, by 16-byte cp.async into its own ring of tiles
-// (no barrier between warps), two ahead of the one it computes; the page numbers
-// of a tile are read one tile earlier still.  Rows are swizzled (16-byte pieces
-// xor row) so that ldmatrix meets no bank twice.  The products run on the warp's
-// matrix instructions with the query heads as the 16 rows: S = Q K^T, then P V
-// with S's accumulator layout as the left operand, so the weights never leave
-// the registers.  (tcgen05.mma wants 64 or 128 rows: it would idle on 16, and the
-// tensor pipe is not what binds here.)
+// A warp copies its own tiles, by 16-byte cp.async into its own ring of tile
+// halves (no barrier between warps); the page numbers of a tile are read one tile
+// earlier.  Rows are swizzled (16-byte pieces xor row) so that ldmatrix meets no
+// bank twice.  The products run on the warp's matrix instructions with the keys
+// (then the channels) as the 16 rows and 8 query heads as the columns:
+// S^T = K Q^T, O^T += V^T P^T, so that no row of the operand that is loaded is
+// padding; the weights turn from accumulator to right operand by transposing
+// 8 x 8 blocks in registers (movmatrix).  (tcgen05.mma takes 64 or 128 rows from
+// shared memory and would need the weights there; the tensor pipe does not bind
+// here: 21 % busy at 5.3 TB/s with twice the products of this form.)
 //
 // Precision: scores, maxima, sums and outputs in fp32.  For the product with the
 // values a weight is two bf16 numbers, 16 bits together: one would leave up to
 // 2^-8 of every weight, as much as the rounding of a bf16 output and far more
-// than an fp32 one may lose, and the second product is free here (see Bound).  An 8-bit
-// cache is widened to fp16, which holds every e4m3 value; the queries are scaled
-// by a power of two for each row, so that fp16 holds their bf16 values too, and
-// the weights are two fp16 numbers, times 2^15 to keep small ones normal.
+// than an fp32 one may lose, and the second product is free here (see Bound).  An
+// 8-bit cache is widened to fp16, which holds every e4m3 value; the queries are
+// scaled by a power of two for each row, so that fp16 holds their bf16 values
+// too, and the weights are two fp16 numbers, times 2^15 to keep small ones normal.
 #include <cuda_fp16.h>
 
 #include "kda_internal.cuh"
@@ -47,21 +52,28 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 16;       // query heads of a unit
 constexpr int kMaxCtas = 160;
+constexpr int kMaxWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int kD, bool kFp8>
+// kN: groups of 8 query heads in a unit.  Warps: as many as the accumulators
+// (kD / 4 * kN registers a lane) leave registers for, so that one warp's
+// instructions overlap another's waits.
+template <int kD_, bool kFp8_, int kN_>
 struct Shape {
+    static constexpr int kD = kD_, kN = kN_;
+    static constexpr bool kFp8 = kFp8_;
     static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
     static constexpr int kKeys = kRowBytes >= 256 ? 16 : 4096 / kRowBytes;  // keys of a tile
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-    static constexpr int kWarps = kHalf > 4096 ? 4 : 8;
-    static constexpr int kStages = 3;
-    static constexpr int kRing = kStages * 2 * kHalf;                      // a warp's ring
-    static constexpr int kPad = kD + 8;                                    // floats of a part's row
-    static_assert(kRows * kPad * 4 <= kRing, "a part must fit a warp's ring");
+    static constexpr int kWarps = kD * kN > 128 ? 8 : 12;
+    static constexpr int kSlots = 196608 / kWarps / kHalf;                 // halves of a warp's ring
+    static constexpr int kRing = kSlots * kHalf;
+    static constexpr int kHeads = 8 * kN;
+    static constexpr int kPitch = kD + 4;                                  // floats of a part's row
+    static_assert(kSlots >= 3 && kSlots <= 7, "");
+    static_assert(kHeads * kPitch * 4 <= kRing, "a part must fit a warp's ring");
 };
 
 // What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
@@ -72,34 +84,31 @@ struct CutMeta {
     int pad;
 };
 
-struct Layout {  // of the workspace
+struct Layout {      // of the workspace
     CutMeta *meta;   // [ctas][2]
-    float *ml;       // [ctas][2][kRows][2]
-    float *cut;      // [ctas][2][kRows][D]
-    float *head;     // [ctas][warps][kRows][D]: a warp's first part, until its CTA joins it
+    float *ml;       // [ctas][2][heads][2]
+    float *cut;      // [ctas][2][heads][D]
+    float *head;     // [ctas][warps][heads][D]: a warp's first part, until its CTA joins it
 };
 
-__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
+inline size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 
-inline size_t layout_bytes(int head_dim, uint8_t *base, Layout *l) {
-    size_t at = 0;
-    const size_t part = static_cast<size_t>(kRows) * head_dim * 4;
-    const size_t meta = at;
-    at = align256(at + kMaxCtas * 2 * sizeof(CutMeta));
-    const size_t ml = at;
-    at = align256(at + kMaxCtas * 2 * kRows * 2 * 4);
-    const size_t cut = at;
-    at = align256(at + kMaxCtas * 2 * part);
-    const size_t head = at;
-    at = align256(at + kMaxCtas * 8 * part);
+inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
+    const size_t part = static_cast<size_t>(heads) * head_dim * 4;
+    const size_t ml = align256(kMaxCtas * 2 * sizeof(CutMeta));
+    const size_t cut = align256(ml + static_cast<size_t>(kMaxCtas) * 2 * heads * 2 * 4);
+    const size_t head = align256(cut + kMaxCtas * 2 * part);
     if (l != nullptr) {
-        l->meta = reinterpret_cast<CutMeta *>(base + meta);
+        l->meta = reinterpret_cast<CutMeta *>(base);
         l->ml = reinterpret_cast<float *>(base + ml);
         l->cut = reinterpret_cast<float *>(base + cut);
         l->head = reinterpret_cast<float *>(base + head);
     }
-    return at;
+    return head + kMaxCtas * kMaxWarps * part;
 }
+
+// Query heads of a unit: 8, or 16 where the group is larger.
+inline int unit_heads(int group) { return group <= 8 ? 8 : 16; }
 
 struct Args {
     const __nv_bfloat16 *q;
@@ -115,6 +124,8 @@ struct Args {
     float *lse;
     Layout ws;
     unsigned int *err;
+    int one_page;  // a tile never spans two pages
+    int whole;     // CTAs take whole units
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -123,17 +134,23 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Volatile: they stay between the wait for a tile and the copy that replaces it.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // c (16 x 8, fp32) += a (16 x 16) b (16 x 8), bf16 or fp16 operands.
@@ -141,23 +158,21 @@ template <bool kF16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
     if constexpr (kF16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values (the low or high half of x) as two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
+// Two e4m3 values as two fp16 values: exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
     uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
     return y;
 }
 
@@ -222,6 +237,19 @@ struct Part {
     int pad;
 };
 
+// Where a unit's queries and outputs are.
+struct UnitRows {
+    int h, rows;      // key head; query heads
+    int64_t out_row;  // the first of them in [B, q_heads]
+
+    __device__ __forceinline__ UnitRows(const Args &a, int b, int u, int heads) {
+        h = u / a.head_tiles;
+        const int row0 = (u - h * a.head_tiles) * heads;
+        rows = min(heads, a.group - row0);
+        out_row = static_cast<int64_t>(b) * a.q_heads + h * a.group + row0;
+    }
+};
+
 __device__ __forceinline__ void write_out(const Args &a, int64_t at, float4 x) {
     if (a.o_bf16) {
         uint2 w;
@@ -233,23 +261,135 @@ __device__ __forceinline__ void write_out(const Args &a, int64_t at, float4 x) {
     }
 }
 
-template <int kD, bool kFp8>
-__global__ void __launch_bounds__(Shape<kD, kFp8>::kWarps * 32, 1)
-    paged_decode_kernel(const Args a) {
-    using S = Shape<kD, kFp8>;
+__device__ __forceinline__ void write_lse(const Args &a, int64_t row, float m, float l) {
+    if (a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// The tiles that a warp copies: its part of the list, one half at a time.
+template <class S>
+struct Copier {
+    static constexpr int kKeys = S::kKeys, kPieces = S::kRowBytes / 16;
+    static constexpr int kLaneRows = kKeys > 32 ? 2 : 1;
+    static constexpr int kCopies = S::kHalf / 512;           // 16-byte copies of a lane
+    Cursor<kKeys> at;
+    int64_t left;                                            // tiles to begin
+    int page[kLaneRows];                                     // of this lane's rows of tile `at`
+    bool held[kLaneRows];                                    // the row is a key of the sequence
+    uint32_t in_page[kLaneRows];
+    // the tile whose values are next: where its rows are
+    int64_t off[kLaneRows];                                  // one_page: [0], of row 0
+    int rows;                                                // rows to copy, the rest 0; -1: no tile
+    bool values;                                             // the next half
+
+    __device__ __forceinline__ void read_pages(const Args &a, int lane) {
+#pragma unroll
+        for (int i = 0; i < kLaneRows; ++i) {
+            const uint32_t r = a.one_page ? 0 : lane + 32 * i;
+            const uint32_t j = static_cast<uint32_t>(at.t) * kKeys + r;
+            uint32_t idx;
+            a.cache.page.divmod(j, idx, in_page[i]);
+            held[i] = r < kKeys && j < static_cast<uint32_t>(at.len);
+            page[i] = -1;
+            if (held[i])
+                page[i] = __ldg(a.block_table + static_cast<int64_t>(at.b) * a.max_pages + idx);
+        }
+    }
+
+    __device__ __forceinline__ void begin(const Args &a, const Cursor<kKeys> &c, int64_t tiles,
+                                          int lane) {
+        at = c;
+        left = tiles;
+        values = false;
+        read_pages(a, lane);
+    }
+
+    // Copies the next half to the slot; masks: which of the tile's rows are keys.
+    __device__ __forceinline__ void half(const Args &a, int units, int lane, uint32_t to,
+                                         uint64_t *mask) {
+        const uint8_t *src = values ? a.cache.v : a.cache.k;
+        if (!values) {
+            if (left > 0) {
+                uint64_t valid = 0;
+                const int64_t h = at.u / a.head_tiles * a.cache.head_stride;
+                if (a.one_page) {
+                    const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
+                    if (!ok) record_device_error(a.err, kDevInvalidArg);
+                    rows = ok ? min(kKeys, at.len - at.t * kKeys) : 0;
+                    off[0] = ok ? page[0] * a.cache.page_stride + in_page[0] * a.cache.token_stride + h : 0;
+                    valid = rows == 64 ? ~uint64_t{0} : (uint64_t{1} << rows) - 1;
+                } else {
+                    rows = kKeys;
+#pragma unroll
+                    for (int i = 0; i < kLaneRows; ++i) {
+                        const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
+                        if (!ok && held[i]) record_device_error(a.err, kDevInvalidArg);
+                        off[i] = ok ? page[i] * a.cache.page_stride +
+                                          in_page[i] * a.cache.token_stride + h
+                                    : -1;
+                        valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * i);
+                    }
+                }
+                if (lane == 0) *mask = valid;
+            } else {
+                rows = -1;
+            }
+        }
+        if (rows >= 0) {
+            const uint32_t r0 = lane / kPieces, c = lane % kPieces;
+            if (a.one_page) {
+                constexpr uint32_t kStep = 32 / kPieces;     // rows of one copy of the warp
+                const uint8_t *p = src + off[0] + r0 * a.cache.token_stride + c * 16;
+                const int64_t step = kStep * a.cache.token_stride;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int r = i * kStep + r0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     to + piece<S::kRowBytes>(r, c)),
+                                 "l"(r < rows ? p : src), "r"(r < rows ? 16 : 0)
+                                 : "memory");
+                    p += step;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const uint32_t r = i * 32 / kPieces + r0;
+                    const int64_t o = __shfl_sync(
+                        0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     to + piece<S::kRowBytes>(r, c)),
+                                 "l"(src + (o < 0 ? 0 : o) + c * 16), "r"(o < 0 ? 0 : 16)
+                                 : "memory");
+                }
+            }
+            if (!values) {
+                at.next(a, units);
+                if (--left > 0) read_pages(a, lane);
+            }
+        }
+        values = !values;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const Args a) {
+    constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
+    constexpr bool kFp8 = S::kFp8, kF16 = S::kFp8;
     constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kKeys = S::kKeys;
-    constexpr int kNT = kKeys / 8;        // score tiles of 8 keys
-    constexpr int kOT = kD / 8;           // output tiles of 8 channels
-    constexpr int kPieces = S::kRowBytes / 16;
+    constexpr int kBlocks = kKeys / 16;   // score blocks of 16 keys
+    constexpr int kOT = kD / 16;          // output blocks of 16 channels
     constexpr int kParts = 2 * kWarps;
-    constexpr bool kF16 = kFp8;
+    static_assert(kParts <= 32, "a warp finds the runs");
 
     extern __shared__ __align__(1024) uint8_t s_ring[];
     __shared__ int64_t s_scan[kWarps];
+    __shared__ int s_count[kWarps];
+    __shared__ int64_t s_bound[2];
     __shared__ Cursor<kKeys> s_start[kWarps];
-    __shared__ uint64_t s_valid[kWarps][S::kStages];
+    __shared__ uint64_t s_valid[kWarps][4];
     __shared__ Part s_part[kParts];
-    __shared__ float s_m[kParts][kRows], s_l[kParts][kRows];
+    __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads];
+    __shared__ int s_run[kParts], s_run_last[kParts], s_runs;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
@@ -260,11 +400,13 @@ __global__ void __launch_bounds__(Shape<kD, kFp8>::kWarps * 32, 1)
     const int chunk = (a.B + kThreads - 1) / kThreads;
     const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
     int64_t mine = 0;
+    int filled = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const int n = __ldg(a.seq_lens + b);
         const int v = valid_len(a, b);
         if (n != v && blockIdx.x == 0) record_device_error(a.err, kDevInvalidArg);
         mine += (static_cast<uint32_t>(v) + kKeys - 1) / kKeys;
+        filled += v > 0;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -272,304 +414,303 @@ __global__ void __launch_bounds__(Shape<kD, kFp8>::kWarps * 32, 1)
         const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += x;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    if (lane == 0) s_start[warp].b = -1;
+    const int filled_warp = __reduce_add_sync(0xffffffffu, filled);
+    if (lane == 31) {
+        s_scan[warp] = incl;
+        s_count[warp] = filled_warp;
+    }
     if (tid < kParts) s_part[tid].unit = -1;
     __syncthreads();
-    int64_t before = (incl - mine), total = 0;
+    int64_t before = incl - mine, total = 0, sequences = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
+        sequences += s_count[w];
     }
     before *= units;
     total *= units;
-    // as many CTAs as leave a tile to each warp, all of the grid for longer lists
-    const int64_t want = (total + kWarps - 1) / kWarps;
+    // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
+    // grid for longer lists
+    const int64_t want = a.whole ? sequences * units : (total + kWarps - 1) / kWarps;
     const int64_t ctas = want < gridDim.x ? want : gridDim.x;
-    const int64_t pieces_of = ctas * kWarps;
-    if (blockIdx.x < ctas && mine > 0) {
+    // the place of a position of the list that lies in this thread's sequences
+    auto find = [&](int64_t pos) {
+        int64_t left = pos - before;
+        Cursor<kKeys> c;
+        for (c.b = b_lo;; ++c.b) {
+            c.set_len(valid_len(a, c.b));
+            const int64_t here = static_cast<int64_t>(c.tiles) * units;
+            if (left < here) break;
+            left -= here;
+        }
+        c.u = static_cast<int>(left / c.tiles);
+        c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
+        return c;
+    };
+    auto owned = [&](int64_t pos) { return pos >= before && pos < before + mine * units; };
+    int64_t lo = 0, hi = 0;  // this CTA's piece
+    if (blockIdx.x < ctas) {
+        lo = blockIdx.x * total / ctas;
+        hi = (blockIdx.x + int64_t{1}) * total / ctas;
+        if (a.whole) {
+            if (owned(lo)) s_bound[0] = lo - find(lo).t;
+            if (owned(hi)) s_bound[1] = hi - find(hi).t;
+            if (hi == total && tid == 0) s_bound[1] = total;
+            __syncthreads();
+            lo = s_bound[0];
+            hi = s_bound[1];
+        }
         for (int w = 0; w < kWarps; ++w) {
-            const int64_t start = (static_cast<int64_t>(blockIdx.x) * kWarps + w) * total / pieces_of;
-            if (start < before || start >= before + mine * units) continue;
-            int64_t left = start - before;
-            int b = b_lo;
-            Cursor<kKeys> c;
-            for (;; ++b) {
-                c.set_len(valid_len(a, b));
-                const int64_t here = static_cast<int64_t>(c.tiles) * units;
-                if (left < here) break;
-                left -= here;
-            }
-            c.b = b;
-            c.u = static_cast<int>(left / c.tiles);
-            c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
-            s_start[w] = c;
+            const int64_t start = lo + (hi - lo) * w / kWarps;
+            if (owned(start)) s_start[w] = find(start);
         }
     }
     __syncthreads();
 
-    // ---- a warp's piece --------------------------------------------------------------------
-    const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
-    int64_t remaining = 0;
-    if (blockIdx.x < ctas) {
-        const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-        remaining = (w + 1) * total / pieces_of - w * total / pieces_of;
-    }
+    // ---- a warp's part of the piece --------------------------------------------------------
+    int64_t remaining = lo + (hi - lo) * (warp + 1) / kWarps - (lo + (hi - lo) * warp / kWarps);
     if (remaining > 0) {
-        Cursor<kKeys> cur = s_start[warp], pre = cur;
-        int64_t to_copy = remaining;
-
-        // the page of this lane's row (two rows where a tile has 64 keys) of tile `pre`
-        constexpr int kLaneRows = kKeys > 32 ? 2 : 1;
-        int page[kLaneRows];
-        bool held[kLaneRows];  // the row is a key of the sequence
-        uint32_t in_page[kLaneRows];
-        auto read_pages = [&]() {
-#pragma unroll
-            for (int i = 0; i < kLaneRows; ++i) {
-                const uint32_t r = lane + 32 * i;
-                const uint32_t j = static_cast<uint32_t>(pre.t) * kKeys + r;
-                uint32_t idx;
-                a.cache.page.divmod(j, idx, in_page[i]);
-                held[i] = r < kKeys && j < static_cast<uint32_t>(pre.len);
-                page[i] = -1;
-                if (held[i])
-                    page[i] = __ldg(a.block_table + static_cast<int64_t>(pre.b) * a.max_pages + idx);
-            }
+        const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
+        Cursor<kKeys> cur = s_start[warp];
+        Copier<S> copier;
+        copier.begin(a, cur, remaining, lane);
+        int put = 0, copied = 0;  // the slot, and the tile, of the next half to copy
+        auto copy_half = [&]() {
+            copier.half(a, units, lane, ring + put * S::kHalf, &s_valid[warp][copied & 3]);
+            if (!copier.values) ++copied;
+            put = put == S::kSlots - 1 ? 0 : put + 1;
         };
-        auto copy_tile = [&](int stage) {
-            if (to_copy > 0) {
-                --to_copy;
-                const int h = pre.u / a.head_tiles;
-                int64_t off[kLaneRows];
-                uint64_t valid = 0;
 #pragma unroll
-                for (int i = 0; i < kLaneRows; ++i) {
-                    const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
-                    if (!ok && held[i]) record_device_error(a.err, kDevInvalidArg);
-                    off[i] = ok ? page[i] * a.cache.page_stride + in_page[i] * a.cache.token_stride +
-                                      h * a.cache.head_stride
-                                : -1;
-                    valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * i);
-                }
-                if (lane == 0) s_valid[warp][stage] = valid;
-                const uint32_t to = ring + stage * 2 * S::kHalf;
-#pragma unroll
-                for (int i = 0; i < kKeys * kPieces / 32; ++i) {
-                    const uint32_t flat = i * 32 + lane;
-                    const uint32_t r = flat / kPieces, c = flat % kPieces;
-                    const int64_t o = __shfl_sync(
-                        0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
-                    const uint32_t dst = to + piece<S::kRowBytes>(r, c);
-                    const int64_t src = (o < 0 ? 0 : o) + c * 16;
-                    const int bytes = o < 0 ? 0 : 16;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                                 "l"(a.cache.k + src), "r"(bytes)
-                                 : "memory");
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + S::kHalf),
-                                 "l"(a.cache.v + src), "r"(bytes)
-                                 : "memory");
-                }
-                pre.next(a, units);
-                if (to_copy > 0) read_pages();
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        read_pages();
-#pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) copy_tile(s);
+        for (int s = 0; s < S::kSlots - 1; ++s) copy_half();
 
-        uint32_t qf[kD / 16][4];
-        float acc[kOT][4], m[2], l[2], sc[2];
+        uint32_t qf[kOT][kN][2];
+        float acc[kOT][kN][4], m[kN][2], l[kN][2], sc[kN][2];
         int begun = cur.t;  // the part's first tile
-        int stage = 0;
+        int slot = 0, tile = 0;
         bool fresh = true;
-        while (remaining > 0) {
-            const int h = cur.u / a.head_tiles, row0 = (cur.u - h * a.head_tiles) * kRows;
-            const int rows = min(kRows, a.group - row0);
+        while (true) {
+            const UnitRows rows(a, cur.b, cur.u, kHeads);
             if (fresh) {
+                // the unit's queries as the right operand (head 8 n + g); heads past the
+                // group are zero
                 fresh = false;
-                // the unit's queries as the left operand; rows past the group are zero
                 const __nv_bfloat16 *q = a.q + cur.b * a.q_row_stride +
-                                         (static_cast<int64_t>(h) * a.group + row0) * kD;
-                const bool r0 = g < rows, r1 = g + 8 < rows;
+                                         (rows.out_row - static_cast<int64_t>(cur.b) * a.q_heads) * kD;
                 const float base = a.scale * kLog2e *
-                                   (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + h));
-                sc[0] = sc[1] = base;
-                if constexpr (kFp8) {
-                    // channels 16 c + 4 tq .. + 3, as the widened keys have them
-                    uint2 x[2][kD / 16];
-                    float top[2] = {0.f, 0.f};
+                                   (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + rows.h));
 #pragma unroll
-                    for (int c = 0; c < kD / 16; ++c) {
-                        const uint2 z = make_uint2(0, 0);
-                        const int at = 16 * c + 4 * tq;
-                        x[0][c] = r0 ? __ldg(reinterpret_cast<const uint2 *>(q + g * kD + at)) : z;
-                        x[1][c] = r1 ? __ldg(reinterpret_cast<const uint2 *>(q + (g + 8) * kD + at)) : z;
+                for (int n = 0; n < kN; ++n) {
+                    const bool real = 8 * n + g < rows.rows;
+                    const __nv_bfloat16 *x = q + (8 * n + g) * kD;
+                    if constexpr (kFp8) {
+                        // channels 16 c + 4 tq .. + 3, as the widened keys have them
+                        float top = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 lo = unpack2<false>(x[i][c].x), hi = unpack2<false>(x[i][c].y);
-                            top[i] = fmaxf(fmaxf(top[i], fmaxf(fabsf(lo.x), fabsf(lo.y))),
-                                           fmaxf(fabsf(hi.x), fabsf(hi.y)));
+                        for (int c = 0; c < kOT; ++c) {
+                            uint2 z = make_uint2(0, 0);
+                            if (real) z = __ldg(reinterpret_cast<const uint2 *>(x + 16 * c + 4 * tq));
+                            qf[c][n][0] = z.x;
+                            qf[c][n][1] = z.y;
+                            const float2 u0 = unpack2<false>(z.x), u1 = unpack2<false>(z.y);
+                            top = fmaxf(fmaxf(top, fmaxf(fabsf(u0.x), fabsf(u0.y))),
+                                        fmaxf(fabsf(u1.x), fabsf(u1.y)));
                         }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-                        // 2^e with the row's largest value in [2^13, 2^14) after it; an
-                        // infinite or zero row is left as it is
-                        int e = 13 - (static_cast<int>((__float_as_uint(top[i]) >> 23) & 0xff) - 127);
-                        if (!(top[i] > 0.f) || isinf(top[i])) e = 0;
-                        // in two steps: 2^e itself may not be a float
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        // 2^e puts the head's largest value in [2^13, 2^14); an infinite or
+                        // zero head is left as it is.  In two steps: 2^e itself may not be a
+                        // float.
+                        int e = 13 - (static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 127);
+                        if (!(top > 0.f) || isinf(top)) e = 0;
                         const float f1 = exp2f(static_cast<float>(e / 2));
                         const float f2 = exp2f(static_cast<float>(e - e / 2));
-                        sc[i] = base / f1 / f2;
 #pragma unroll
-                        for (int c = 0; c < kD / 16; ++c) {
-                            float2 lo = unpack2<false>(x[i][c].x), hi = unpack2<false>(x[i][c].y);
-                            qf[c][i] = pack2<true>(lo.x * f1 * f2, lo.y * f1 * f2);
-                            qf[c][i + 2] = pack2<true>(hi.x * f1 * f2, hi.y * f1 * f2);
-                        }
-                    }
-                } else {
+                        for (int c = 0; c < kOT; ++c)
 #pragma unroll
-                    for (int c = 0; c < kD / 16; ++c) {
-                        const __nv_bfloat16 *x = q + 16 * c + 2 * tq;
-                        qf[c][0] = r0 ? __ldg(reinterpret_cast<const uint32_t *>(x + g * kD)) : 0;
-                        qf[c][1] = r1 ? __ldg(reinterpret_cast<const uint32_t *>(x + (g + 8) * kD)) : 0;
-                        qf[c][2] = r0 ? __ldg(reinterpret_cast<const uint32_t *>(x + g * kD + 8)) : 0;
-                        qf[c][3] = r1 ? __ldg(reinterpret_cast<const uint32_t *>(x + (g + 8) * kD + 8)) : 0;
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 u = unpack2<false>(qf[c][n][i]);
+                                qf[c][n][i] = pack2<true>(u.x * f1 * f2, u.y * f1 * f2);
+                            }
+                        // the scores' columns are heads 2 tq, 2 tq + 1
+                        const float mine_sc = base / f1 / f2;
+                        sc[n][0] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq);
+                        sc[n][1] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq + 4);
+                    } else {
+                        sc[n][0] = sc[n][1] = base;
+#pragma unroll
+                        for (int c = 0; c < kOT; ++c)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                qf[c][n][i] = real ? __ldg(reinterpret_cast<const uint32_t *>(
+                                                         x + 16 * c + 8 * i + 2 * tq))
+                                                   : 0;
                     }
+                    m[n][0] = m[n][1] = -INFINITY;
+                    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+                    for (int d = 0; d < kOT; ++d)
+                        acc[d][n][0] = acc[d][n][1] = acc[d][n][2] = acc[d][n][3] = 0.f;
                 }
                 begun = cur.t;
-                m[0] = m[1] = -INFINITY;
-                l[0] = l[1] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kOT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             }
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-            __syncwarp();  // the tile is in, and the one before it is read by every lane
-            copy_tile(stage == 0 ? S::kStages - 1 : stage - 1);
-            const uint32_t kt = ring + stage * 2 * S::kHalf, vt = kt + S::kHalf;
 
-            // scores: rows g, g + 8; keys 8 n + 2 tq, + 1
-            float s[kNT][4];
+            // ---- scores: keys 16 k + g, + 8; heads 8 n + 2 tq, + 1
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
+            __syncwarp();  // the keys are in, and the half before them is read by every lane
+            copy_half();
+            const uint32_t kt = ring + slot * S::kHalf;
+            slot = slot == S::kSlots - 1 ? 0 : slot + 1;
+            float s[kBlocks][kN][4];
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int c = 0; c < kPieces; c += 4) {
+                for (int n = 0; n < kN; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kOT; c += kFp8 ? 2 : 1) {
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) {
                     uint32_t r[4];
-                    ldsm4(r, kt + piece<S::kRowBytes>(8 * n + (lane & 7), c + (lane >> 3)));
+                    // rows 0-7 and 8-15 of a piece of 16 bytes, then of the next
+                    ldsm4(r, kt + piece<S::kRowBytes>(16 * k + (lane & 15),
+                                                      (kFp8 ? c : 2 * c) + (lane >> 4)));
                     if constexpr (kFp8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<kF16>(s[n], qf[c + i], e4m3x2_to_f16x2(r[i] & 0xffff),
-                                      e4m3x2_to_f16x2(r[i] >> 16));
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t f[4] = {e4m3x2_to_f16x2(r[2 * i]), e4m3x2_to_f16x2(r[2 * i + 1]),
+                                                   e4m3x2_to_f16x2(r[2 * i] >> 16),
+                                                   e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
+#pragma unroll
+                            for (int n = 0; n < kN; ++n)
+                                mma<kF16>(s[k][n], f, qf[c + i][n][0], qf[c + i][n][1]);
+                        }
                     } else {
-                        mma<kF16>(s[n], qf[c / 2], r[0], r[1]);
-                        mma<kF16>(s[n], qf[c / 2 + 1], r[2], r[3]);
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) mma<kF16>(s[k][n], r, qf[c][n][0], qf[c][n][1]);
                     }
                 }
             }
-            const uint64_t valid = s_valid[warp][stage];
+            const uint64_t valid = s_valid[warp][tile & 3];
+            ++tile;
             constexpr uint64_t kAll = kKeys == 64 ? ~uint64_t{0} : (uint64_t{1} << (kKeys & 63)) - 1;
-            float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
+            for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] *= sc[i >> 1];
-            }
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[k][n][i] *= sc[n][i & 1];
             if (valid != kAll) {
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
+                for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!(valid >> (8 * n + 2 * tq + (i & 1)) & 1)) s[n][i] = -INFINITY;
-            }
+                    for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                mt[0] = fmaxf(mt[0], fmaxf(s[n][0], s[n][1]));
-                mt[1] = fmaxf(mt[1], fmaxf(s[n][2], s[n][3]));
+                        for (int i = 0; i < 4; ++i)
+                            if (!(valid >> (16 * k + g + 8 * (i >> 1)) & 1)) s[k][n][i] = -INFINITY;
             }
-            float ref[2];
+            float ref[kN][2];
             bool grew = false;
-            float shrink[2];
+            float shrink[kN][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
-                mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2));
-                const float mn = fmaxf(m[i], mt[i]);
-                ref[i] = mn == -INFINITY ? 0.f : mn;
-                shrink[i] = ex2(m[i] - ref[i]);
-                grew |= mn > m[i];
-                m[i] = mn;
-            }
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float mt = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) mt = fmaxf(mt, fmaxf(s[k][n][i], s[k][n][i + 2]));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                    const float mn = fmaxf(m[n][i], mt);
+                    ref[n][i] = mn == -INFINITY ? 0.f : mn;
+                    shrink[n][i] = ex2(m[n][i] - ref[n][i]);
+                    grew |= mn > m[n][i];
+                    m[n][i] = mn;
+                }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) l[i] *= shrink[i];
+                for (int n = 0; n < kN; ++n) {
 #pragma unroll
-                for (int n = 0; n < kOT; ++n)
+                    for (int i = 0; i < 2; ++i) l[n][i] *= shrink[n][i];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] *= shrink[i >> 1];
-            }
-            // weights, and their product with the values 16 keys at a time
-            constexpr float kUp = kF16 ? 32768.f : 1.f;
+                    for (int d = 0; d < kOT; ++d)
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk) {
-                uint32_t p[4], p2[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // j: rows g (even) or g + 8 (odd), keys of the first or second 8
-                    const int n = 2 * kk + (j >> 1), i = j & 1;
-                    float x = ex2(s[n][2 * i] - ref[i]), y = ex2(s[n][2 * i + 1] - ref[i]);
-                    l[i] += x + y;
-                    x *= kUp;
-                    y *= kUp;
-                    p[j] = pack2<kF16>(x, y);
-                    const float2 hi = unpack2<kF16>(p[j]);
-                    p2[j] = pack2<kF16>(x - hi.x, y - hi.y);
+                        for (int i = 0; i < 4; ++i) acc[d][n][i] *= shrink[n][i & 1];
                 }
-                const uint32_t vr = 16 * kk + (lane & 15);
+            }
+            // ---- weights, in two words, as the right operand
+            constexpr float kUp = kF16 ? 32768.f : 1.f;
+            uint32_t p[kBlocks][kN][2], p2[kBlocks][kN][2];
 #pragma unroll
-                for (int c = 0; c < kPieces; c += 2) {
+            for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x = ex2(s[k][n][2 * j] - ref[n][0]);
+                        float y = ex2(s[k][n][2 * j + 1] - ref[n][1]);
+                        l[n][0] += x;
+                        l[n][1] += y;
+                        x *= kUp;
+                        y *= kUp;
+                        const uint32_t w = pack2<kF16>(x, y);
+                        const float2 first = unpack2<kF16>(w);
+                        p[k][n][j] = transpose8(w);
+                        p2[k][n][j] = transpose8(pack2<kF16>(x - first.x, y - first.y));
+                    }
+
+            // ---- outputs: channels g, g + 8 of 16 d (8-bit: 2 g, 2 g + 1)
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
+            __syncwarp();  // the values are in, and the keys are read by every lane
+            copy_half();
+            const uint32_t vt = ring + slot * S::kHalf;
+            slot = slot == S::kSlots - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+#pragma unroll
+                for (int d = 0; d < kOT; d += kFp8 ? 2 : 1) {
                     uint32_t r[4];
-                    // pieces c (r[0], r[1]) and c + 1, keys 0-7 and 8-15 of the 16
-                    ldsm4_trans(r, vt + piece<S::kRowBytes>(vr, c + (lane >> 4)));
+                    if constexpr (kFp8) {
+                        ldsm4_trans(r, vt + piece<S::kRowBytes>(16 * k + (lane & 15), d + (lane >> 4)));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (kFp8) {
-                            // bytes: channel 2 g and 2 g + 1 of key 2 tq, then of key 2 tq + 1
+                        for (int i = 0; i < 2; ++i) {
+                            // bytes: channels 2 g, 2 g + 1 of key 2 tq, then of key 2 tq + 1
                             const uint32_t x = __byte_perm(r[2 * i], 0, 0x3120);
                             const uint32_t y = __byte_perm(r[2 * i + 1], 0, 0x3120);
-                            const uint32_t e0 = e4m3x2_to_f16x2(x & 0xffff), o0 = e4m3x2_to_f16x2(x >> 16);
-                            const uint32_t e1 = e4m3x2_to_f16x2(y & 0xffff), o1 = e4m3x2_to_f16x2(y >> 16);
-                            mma<kF16>(acc[2 * (c + i)], p, e0, e1);
-                            mma<kF16>(acc[2 * (c + i) + 1], p, o0, o1);
-                            mma<kF16>(acc[2 * (c + i)], p2, e0, e1);
-                            mma<kF16>(acc[2 * (c + i) + 1], p2, o0, o1);
-                        } else {
-                            mma<kF16>(acc[c + i], p, r[2 * i], r[2 * i + 1]);
-                            mma<kF16>(acc[c + i], p2, r[2 * i], r[2 * i + 1]);
+                            const uint32_t f[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16),
+                                                   e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
+#pragma unroll
+                            for (int n = 0; n < kN; ++n) {
+                                mma<kF16>(acc[d + i][n], f, p[k][n][0], p[k][n][1]);
+                                mma<kF16>(acc[d + i][n], f, p2[k][n][0], p2[k][n][1]);
+                            }
+                        }
+                    } else {
+                        // pieces 2 d and 2 d + 1 of keys 0-7, then of keys 8-15
+                        ldsm4_trans(r, vt + piece<S::kRowBytes>(16 * k + (lane & 7) + ((lane >> 4) << 3),
+                                                                2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) {
+                            mma<kF16>(acc[d][n], r, p[k][n][0], p[k][n][1]);
+                            mma<kF16>(acc[d][n], r, p2[k][n][0], p2[k][n][1]);
                         }
                     }
                 }
             }
 
-            // ---- the end of a unit, or of the piece
+            // ---- the end of a unit, or of the warp's part
             --remaining;
             const bool ends = cur.t == cur.tiles - 1;
             if (ends || remaining == 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                }
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
+                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
+                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
+                    }
                 const bool whole = ends && begun == 0;
-                const int64_t unit = static_cast<int64_t>(cur.b) * units + cur.u;
-                const int64_t out_row = static_cast<int64_t>(cur.b) * a.q_heads + h * a.group + row0;
                 float *part = nullptr;
                 int pitch = kD;
                 if (!whole) {
@@ -578,127 +719,128 @@ __global__ void __launch_bounds__(Shape<kD, kFp8>::kWarps * 32, 1)
                         asm volatile("cp.async.wait_all;" ::: "memory");
                         __syncwarp();  // the ring is free: the part goes there
                         part = reinterpret_cast<float *>(s_ring + warp * S::kRing);
-                        pitch = S::kPad;
+                        pitch = S::kPitch;
                     } else {
-                        part = a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows * kD;
+                        part = a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kHeads * kD;
                     }
-                    if (tq == 0) {
-                        s_m[at][g] = m[0];
-                        s_m[at][g + 8] = m[1];
-                        s_l[at][g] = l[0];
-                        s_l[at][g + 8] = l[1];
+                    if (g == 0) {
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                s_m[at][8 * n + 2 * tq + i] = m[n][i];
+                                s_l[at][8 * n + 2 * tq + i] = l[n][i];
+                            }
                     }
                     if (lane == 0) {
-                        s_part[at].unit = unit;
+                        s_part[at].unit = static_cast<int64_t>(cur.b) * units + cur.u;
                         s_part[at].starts = begun == 0;
                         s_part[at].ends = ends;
                         s_part[at].in_global = remaining != 0;
                     }
                 }
-                const float vs = (a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + h)) / kUp;
+                const float vs = (a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + rows.h)) / kUp;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = g + 8 * i;
-                    if (row >= rows) continue;
-                    const float f = whole ? (l[i] == 0.f ? 0.f : vs / l[i]) : vs;
-                    if (whole && tq == 0 && a.lse != nullptr)
-                        a.lse[out_row + row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
-                    if constexpr (kFp8) {
+                for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int c = 0; c < kD / 16; ++c) {
-                            const float4 x = make_float4(acc[2 * c][2 * i] * f, acc[2 * c + 1][2 * i] * f,
-                                                         acc[2 * c][2 * i + 1] * f,
-                                                         acc[2 * c + 1][2 * i + 1] * f);
-                            const int d = 16 * c + 4 * tq;
-                            if (whole) write_out(a, (out_row + row) * kD + d, x);
-                            else *reinterpret_cast<float4 *>(part + row * pitch + d) = x;
-                        }
-                    } else {
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = 8 * n + 2 * tq + i;
+                        if (row >= rows.rows) continue;
+                        const float f = whole ? (l[n][i] == 0.f ? 0.f : vs / l[n][i]) : vs;
+                        if (whole && g == 0) write_lse(a, rows.out_row + row, m[n][i], l[n][i]);
 #pragma unroll
-                        for (int n = 0; n < kOT; ++n) {
-                            const float x = acc[n][2 * i] * f, y = acc[n][2 * i + 1] * f;
-                            const int d = 8 * n + 2 * tq;
+                        for (int d = 0; d < kOT; ++d) {
+                            const float x = acc[d][n][i] * f, y = acc[d][n][i + 2] * f;
+                            const int dx = 16 * d + (kFp8 ? 2 * g : g), dy = kFp8 ? dx + 1 : dx + 8;
                             if (!whole) {
-                                *reinterpret_cast<float2 *>(part + row * pitch + d) = make_float2(x, y);
+                                part[row * pitch + dx] = x;
+                                part[row * pitch + dy] = y;
                             } else if (a.o_bf16) {
-                                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) +
-                                                              (out_row + row) * kD + d) = pack2<false>(x, y);
+                                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (rows.out_row + row) * kD;
+                                o[dx] = __float2bfloat16_rn(x);
+                                o[dy] = __float2bfloat16_rn(y);
                             } else {
-                                *reinterpret_cast<float2 *>(static_cast<float *>(a.o) +
-                                                            (out_row + row) * kD + d) = make_float2(x, y);
+                                float *o = static_cast<float *>(a.o) + (rows.out_row + row) * kD;
+                                o[dx] = x;
+                                o[dy] = y;
                             }
                         }
                     }
-                }
                 fresh = true;
+                if (remaining == 0) break;
             }
             cur.next(a, units);
-            stage = stage == S::kStages - 1 ? 0 : stage + 1;
         }
     }
     __syncthreads();
 
     // ---- joining the CTA's parts: runs of one unit, in the list's order ------------------
-    if (tid < 2) a.ws.meta[blockIdx.x * 2 + tid].unit = -1;
+    if (warp == 0) {
+        const int64_t unit = lane < kParts ? s_part[lane].unit : -1;
+        const uint32_t valid = __ballot_sync(0xffffffffu, unit >= 0);
+        const uint32_t below = valid & ((1u << lane) - 1);
+        const int64_t prev = __shfl_sync(0xffffffffu, unit, below == 0 ? 0 : 31 - __clz(below));
+        const bool first = unit >= 0 && (below == 0 || prev != unit);
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].unit = -1;
+        __syncwarp();
+        if (first) {
+            const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
+            const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);
+            const int r = __popc(firsts & ((1u << lane) - 1)), last = 31 - __clz(run);
+            s_run[r] = lane;
+            s_run_last[r] = last;
+            const bool starts = s_part[lane].starts, ends = s_part[last].ends;
+            if (!(starts && ends)) {
+                CutMeta &meta = a.ws.meta[blockIdx.x * 2 + (starts ? 1 : 0)];
+                meta.unit = unit;
+                meta.ends = ends;
+            }
+        }
+        if (lane == 0) s_runs = __popc(firsts);
+    }
     __syncthreads();
-    for (int e0 = 0; e0 < kParts;) {
+    constexpr int kPer = kHeads * (kD / 4);
+    for (int i = tid; i < s_runs * kPer; i += kThreads) {
+        const int r = i / kPer, row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
+        const int e0 = s_run[r], e1 = s_run_last[r];
         const int64_t unit = s_part[e0].unit;
-        if (unit < 0) {
-            ++e0;
-            continue;
+        const int b = static_cast<int>(unit / units);
+        const UnitRows rows(a, b, static_cast<int>(unit - static_cast<int64_t>(b) * units), kHeads);
+        if (row >= rows.rows) continue;
+        float mm = -INFINITY, ll = 0.f;
+        for (int e = e0; e <= e1; ++e)
+            if (s_part[e].unit >= 0) mm = fmaxf(mm, s_m[e][row]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = e0; e <= e1; ++e) {
+            if (s_part[e].unit < 0) continue;
+            const float w = ex2(s_m[e][row] - ref);
+            const float *part =
+                s_part[e].in_global
+                    ? a.ws.head + ((static_cast<int64_t>(blockIdx.x) * kWarps + (e >> 1)) * kHeads + row) * kD
+                    : reinterpret_cast<const float *>(s_ring + (e >> 1) * S::kRing) + row * S::kPitch;
+            const float4 y = *reinterpret_cast<const float4 *>(part + d);
+            ll += w * s_l[e][row];
+            x.x += w * y.x;
+            x.y += w * y.y;
+            x.z += w * y.z;
+            x.w += w * y.w;
         }
-        int e1 = e0 + 1, last = e0;  // the run is e0 .. e1 - 1 (places without a part among them)
-        while (e1 < kParts && (s_part[e1].unit < 0 || s_part[e1].unit == unit)) {
-            if (s_part[e1].unit == unit) last = e1;
-            ++e1;
-        }
-        const bool starts = s_part[e0].starts, ends = s_part[last].ends;
-        const int b = static_cast<int>(unit / units), u = static_cast<int>(unit - static_cast<int64_t>(b) * units);
-        const int h = u / a.head_tiles, row0 = (u - h * a.head_tiles) * kRows;
-        const int rows = min(kRows, a.group - row0);
-        const int64_t out_row = static_cast<int64_t>(b) * a.q_heads + h * a.group + row0;
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0);
-        for (int i = tid; i < rows * (kD / 4); i += kThreads) {
-            const int row = i / (kD / 4), d = i % (kD / 4) * 4;
-            float mm = -INFINITY;
-            for (int e = e0; e <= last; ++e)
-                if (s_part[e].unit == unit) mm = fmaxf(mm, s_m[e][row]);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int e = e0; e <= last; ++e) {
-                if (s_part[e].unit != unit) continue;
-                const float w = ex2(s_m[e][row] - ref);
-                const float *part =
-                    s_part[e].in_global
-                        ? a.ws.head + ((static_cast<int64_t>(blockIdx.x) * kWarps + (e >> 1)) * kRows + row) * kD
-                        : reinterpret_cast<const float *>(s_ring + (e >> 1) * S::kRing) + row * S::kPad;
-                const float4 y = *reinterpret_cast<const float4 *>(part + d);
-                ll += w * s_l[e][row];
-                x.x += w * y.x;
-                x.y += w * y.y;
-                x.z += w * y.z;
-                x.w += w * y.w;
-            }
-            if (starts && ends) {
-                const float f = ll == 0.f ? 0.f : 1.f / ll;
-                write_out(a, (out_row + row) * kD + d,
-                          make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-                if (d == 0 && a.lse != nullptr)
-                    a.lse[out_row + row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-            } else {
-                *reinterpret_cast<float4 *>(a.ws.cut + (slot * kRows + row) * kD + d) = x;
-                if (d == 0) {
-                    a.ws.ml[(slot * kRows + row) * 2] = mm;
-                    a.ws.ml[(slot * kRows + row) * 2 + 1] = ll;
-                }
+        const bool starts = s_part[e0].starts;
+        if (starts && s_part[e1].ends) {
+            const float f = ll == 0.f ? 0.f : 1.f / ll;
+            write_out(a, (rows.out_row + row) * kD + d,
+                      make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+            if (d == 0) write_lse(a, rows.out_row + row, mm, ll);
+        } else {
+            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * kHeads + row;
+            *reinterpret_cast<float4 *>(a.ws.cut + at * kD + d) = x;
+            if (d == 0) {
+                a.ws.ml[at * 2] = mm;
+                a.ws.ml[at * 2 + 1] = ll;
             }
         }
-        if (tid == 0 && !(starts && ends)) {
-            a.ws.meta[slot].unit = unit;
-            a.ws.meta[slot].ends = ends;
-        }
-        e0 = last + 1;
     }
 
     // ---- sequences without keys ----------------------------------------------------------
@@ -714,7 +856,7 @@ __global__ void __launch_bounds__(Shape<kD, kFp8>::kWarps * 32, 1)
 
 // Joins the parts of the unit that CTA blockIdx.x of the first kernel began and
 // did not finish: its slot 1 and slot 0 of the CTAs after it, up to the last.
-template <int kD>
+template <int kD, int kHeads>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c0 = blockIdx.x;
@@ -722,20 +864,17 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
     if (first.unit < 0) return;
     const int units = a.cache.heads * a.head_tiles;
     const int b = static_cast<int>(first.unit / units);
-    const int u = static_cast<int>(first.unit - static_cast<int64_t>(b) * units);
-    const int h = u / a.head_tiles, row0 = (u - h * a.head_tiles) * kRows;
-    const int rows = min(kRows, a.group - row0);
-    const int64_t out_row = static_cast<int64_t>(b) * a.q_heads + h * a.group + row0;
+    const UnitRows rows(a, b, static_cast<int>(first.unit - static_cast<int64_t>(b) * units), kHeads);
     int c1 = c0 + 1;  // the last part's CTA
-    while (c1 < gridDim.x - 1 && a.ws.meta[c1 * 2].ends == 0) ++c1;
-    for (int i = threadIdx.x; i < rows * (kD / 4); i += blockDim.x) {
+    while (c1 < static_cast<int>(gridDim.x) - 1 && a.ws.meta[c1 * 2].ends == 0) ++c1;
+    for (int i = threadIdx.x; i < rows.rows * (kD / 4); i += blockDim.x) {
         const int row = i / (kD / 4), d = i % (kD / 4) * 4;
         float mm = -INFINITY, ll = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = c0; c <= c1; ++c) {
-            const int64_t slot = static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0);
-            const float mc = a.ws.ml[(slot * kRows + row) * 2], lc = a.ws.ml[(slot * kRows + row) * 2 + 1];
-            const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + (slot * kRows + row) * kD + d);
+            const int64_t at = (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kHeads + row;
+            const float mc = a.ws.ml[at * 2], lc = a.ws.ml[at * 2 + 1];
+            const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + at * kD + d);
             const float mn = fmaxf(mm, mc), ref = mn == -INFINITY ? 0.f : mn;
             const float f = ex2(mm - ref), w = ex2(mc - ref);
             ll = ll * f + lc * w;
@@ -746,22 +885,25 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
             mm = mn;
         }
         const float f = ll == 0.f ? 0.f : 1.f / ll;
-        write_out(a, (out_row + row) * kD + d, make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-        if (d == 0 && a.lse != nullptr)
-            a.lse[out_row + row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        write_out(a, (rows.out_row + row) * kD + d, make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+        if (d == 0) write_lse(a, rows.out_row + row, mm, ll);
     }
 }
 
-template <int kD, bool kFp8>
-cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
-    using S = Shape<kD, kFp8>;
+template <class S>
+cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
     constexpr int kSmem = S::kWarps * S::kRing;
-    const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(&paged_decode_kernel<kD, kFp8>), kSmem);
+    const cudaError_t e =
+        ensure_dynamic_smem(reinterpret_cast<const void *>(&paged_decode_kernel<S>), kSmem);
     if (e != cudaSuccess) return e;
-    paged_decode_kernel<kD, kFp8><<<ctas, S::kWarps * 32, kSmem, s>>>(a);
+    const int page_size = static_cast<int>(a.cache.page.d);
+    a.one_page = page_size % S::kKeys == 0;
+    // Whole units to a CTA where a unit is at most two tiles to a warp: then a CTA's
+    // load is uneven by less than what the second kernel would cost.
+    a.whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
+    paged_decode_kernel<S><<<ctas, S::kWarps * 32, kSmem, s>>>(a);
     const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return e1;
+    if (e1 != cudaSuccess || a.whole) return e1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -771,18 +913,22 @@ cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<kD>, a);
+    return cudaLaunchKernelEx(&cfg, join_kernel<S::kD, S::kHeads>, a);
 }
 
 template <int kD>
-cudaError_t launch_dim(const Args &a, int ctas, cudaStream_t s) {
-    return a.cache.fp8 ? launch_shape<kD, true>(a, ctas, s) : launch_shape<kD, false>(a, ctas, s);
+cudaError_t launch_dim(const Args &a, int heads, int ctas, cudaStream_t s) {
+    if (heads == 8)
+        return a.cache.fp8 ? launch_shape<Shape<kD, true, 1>>(a, ctas, s)
+                           : launch_shape<Shape<kD, false, 1>>(a, ctas, s);
+    return a.cache.fp8 ? launch_shape<Shape<kD, true, 2>>(a, ctas, s)
+                       : launch_shape<Shape<kD, false, 2>>(a, ctas, s);
 }
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int, int, int, int head_dim) {
-    return layout_bytes(head_dim, nullptr, nullptr);
+size_t paged_decode_workspace_bytes(int, int q_heads, int kv_heads, int head_dim) {
+    return layout_bytes(unit_heads(q_heads / kv_heads), head_dim, nullptr, nullptr);
 }
 
 cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
@@ -800,17 +946,18 @@ cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
     a.B = B;
     a.q_heads = q_heads;
     a.group = q_heads / cache.heads;
-    a.head_tiles = (a.group + kRows - 1) / kRows;
+    const int heads = unit_heads(a.group);
+    a.head_tiles = (a.group + heads - 1) / heads;
     a.scale = scale;
     a.o = o;
     a.o_bf16 = o_bf16;
     a.lse = lse;
     a.err = err;
-    layout_bytes(cache.head_dim, static_cast<uint8_t *>(workspace), &a.ws);
+    layout_bytes(heads, cache.head_dim, static_cast<uint8_t *>(workspace), &a.ws);
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-    return cache.head_dim == 64    ? launch_dim<64>(a, ctas, s)
-           : cache.head_dim == 128 ? launch_dim<128>(a, ctas, s)
-                                   : launch_dim<256>(a, ctas, s);
+    return cache.head_dim == 64    ? launch_dim<64>(a, heads, ctas, s)
+           : cache.head_dim == 128 ? launch_dim<128>(a, heads, ctas, s)
+                                   : launch_dim<256>(a, heads, ctas, s);
 }
 
 }  // namespace kda
