@@ -52,7 +52,7 @@
 namespace kda {
 namespace {
 
-constexpr int kMaxCtas = 160;
+constexpr int kMaxCtas = 160;  // at most the join kernel's threads
 constexpr int kMaxWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -79,8 +79,8 @@ struct Shape {
 // What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
 // in slot 0, its last unit's (begun here, not finished) in slot 1.
 struct CutMeta {
-    int64_t unit;  // -1: none
-    int ends;      // the unit's last key is in this part
+    int b, u;  // b = -1: none
+    int ends;  // the unit's last key is in this part
     int pad;
 };
 
@@ -124,7 +124,6 @@ struct Args {
     float *lse;
     Layout ws;
     unsigned int *err;
-    int one_page;  // a tile never spans two pages
     int whole;     // CTAs take whole units
 };
 
@@ -199,6 +198,12 @@ __device__ __forceinline__ uint32_t piece(uint32_t r, uint32_t c) {
     else return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r >> 1) & 7)) << 4);
 }
 
+// n / d, n >= 0, d > 0: by 32 bits where they hold n (a 64-bit division is a call).
+__device__ __forceinline__ int64_t div64(int64_t n, uint32_t d) {
+    if (n >> 32 == 0) return static_cast<uint32_t>(n) / d;
+    return static_cast<uint64_t>(n) / d;
+}
+
 __device__ __forceinline__ int valid_len(const Args &a, int b) {
     const int n = __ldg(a.seq_lens + b);
     return n < 0 || n > static_cast<int64_t>(a.max_pages) * a.cache.page.d ? 0 : n;
@@ -231,10 +236,9 @@ struct Cursor {
 
 // A part of a unit as a warp leaves it for its CTA.
 struct Part {
-    int64_t unit;    // b * units + u; -1: none
+    int b, u;        // b = -1: none
     int starts, ends;
     int in_global;   // its sums are in the workspace (else in the warp's ring)
-    int pad;
 };
 
 // Where a unit's queries and outputs are.
@@ -266,10 +270,11 @@ __device__ __forceinline__ void write_lse(const Args &a, int64_t row, float m, f
 }
 
 // The tiles that a warp copies: its part of the list, one half at a time.
-template <class S>
+// kOnePage: a tile never spans two pages.
+template <class S, bool kOnePage>
 struct Copier {
     static constexpr int kKeys = S::kKeys, kPieces = S::kRowBytes / 16;
-    static constexpr int kLaneRows = kKeys > 32 ? 2 : 1;
+    static constexpr int kLaneRows = !kOnePage && kKeys > 32 ? 2 : 1;
     static constexpr int kCopies = S::kHalf / 512;           // 16-byte copies of a lane
     Cursor<kKeys> at;
     int64_t left;                                            // tiles to begin
@@ -277,14 +282,14 @@ struct Copier {
     bool held[kLaneRows];                                    // the row is a key of the sequence
     uint32_t in_page[kLaneRows];
     // the tile whose values are next: where its rows are
-    int64_t off[kLaneRows];                                  // one_page: [0], of row 0
+    int64_t off[kLaneRows];                                  // kOnePage: of row 0
     int rows;                                                // rows to copy, the rest 0; -1: no tile
     bool values;                                             // the next half
 
     __device__ __forceinline__ void read_pages(const Args &a, int lane) {
 #pragma unroll
         for (int i = 0; i < kLaneRows; ++i) {
-            const uint32_t r = a.one_page ? 0 : lane + 32 * i;
+            const uint32_t r = kOnePage ? 0 : lane + 32 * i;
             const uint32_t j = static_cast<uint32_t>(at.t) * kKeys + r;
             uint32_t idx;
             a.cache.page.divmod(j, idx, in_page[i]);
@@ -311,7 +316,7 @@ struct Copier {
             if (left > 0) {
                 uint64_t valid = 0;
                 const int64_t h = at.u / a.head_tiles * a.cache.head_stride;
-                if (a.one_page) {
+                if constexpr (kOnePage) {
                     const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
                     if (!ok) record_device_error(a.err, kDevInvalidArg);
                     rows = ok ? min(kKeys, at.len - at.t * kKeys) : 0;
@@ -336,7 +341,7 @@ struct Copier {
         }
         if (rows >= 0) {
             const uint32_t r0 = lane / kPieces, c = lane % kPieces;
-            if (a.one_page) {
+            if constexpr (kOnePage) {
                 constexpr uint32_t kStep = 32 / kPieces;     // rows of one copy of the warp
                 const uint8_t *p = src + off[0] + r0 * a.cache.token_stride + c * 16;
                 const int64_t step = kStep * a.cache.token_stride;
@@ -371,7 +376,7 @@ struct Copier {
     }
 };
 
-template <class S>
+template <class S, bool kOnePage>
 __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const Args a) {
     constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
     constexpr bool kFp8 = S::kFp8, kF16 = S::kFp8;
@@ -382,10 +387,6 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     static_assert(kParts <= 32, "a warp finds the runs");
 
     extern __shared__ __align__(1024) uint8_t s_ring[];
-    __shared__ int64_t s_scan[kWarps];
-    __shared__ int s_count[kWarps];
-    __shared__ int64_t s_bound[2];
-    __shared__ Cursor<kKeys> s_start[kWarps];
     __shared__ uint64_t s_valid[kWarps][4];
     __shared__ Part s_part[kParts];
     __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads];
@@ -395,85 +396,79 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     const int g = lane >> 2, tq = lane & 3;
     const int units = a.cache.heads * a.head_tiles;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (lane < 2) s_part[2 * warp + lane].b = -1;
+    __syncwarp();
 
-    // ---- the list: tiles before each sequence, and where this CTA's warps begin ----------
-    const int chunk = (a.B + kThreads - 1) / kThreads;
-    const int b_lo = min(a.B, tid * chunk), b_hi = min(a.B, b_lo + chunk);
+    // ---- the list: tiles before each sequence.  Every warp sums for itself (the
+    // lengths come out of L1 after the first): no barrier before the first copy.
+    const int chunk = (a.B + 31) / 32;
+    const int b_lo = min(a.B, lane * chunk), b_hi = min(a.B, b_lo + chunk);
+    int64_t before = 0;  // tiles of a unit each, of the sequences before this lane's
     int64_t mine = 0;
     int filled = 0;
+#pragma unroll 4
     for (int b = b_lo; b < b_hi; ++b) {
-        const int n = __ldg(a.seq_lens + b);
         const int v = valid_len(a, b);
-        if (n != v && blockIdx.x == 0) record_device_error(a.err, kDevInvalidArg);
         mine += (static_cast<uint32_t>(v) + kKeys - 1) / kKeys;
         filled += v > 0;
     }
-    int64_t incl = mine;
+    before = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += x;
+        const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += x;
     }
-    const int filled_warp = __reduce_add_sync(0xffffffffu, filled);
-    if (lane == 31) {
-        s_scan[warp] = incl;
-        s_count[warp] = filled_warp;
-    }
-    if (tid < kParts) s_part[tid].unit = -1;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0, sequences = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-        sequences += s_count[w];
-    }
-    before *= units;
-    total *= units;
+    const int64_t total = __shfl_sync(0xffffffffu, before, 31) * units;
+    before = (before - mine) * units;
+    const int64_t after = before + mine * units;
     // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
     // grid for longer lists
-    const int64_t want = a.whole ? sequences * units : (total + kWarps - 1) / kWarps;
-    const int64_t ctas = want < gridDim.x ? want : gridDim.x;
-    // the place of a position of the list that lies in this thread's sequences
+    int64_t want;
+    if (a.whole) want = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, filled)) * units;
+    else want = static_cast<uint64_t>(total + kWarps - 1) / kWarps;
+    const uint32_t ctas = static_cast<uint32_t>(want < gridDim.x ? want : gridDim.x);
+    // the place of a position < total of the list
     auto find = [&](int64_t pos) {
-        int64_t left = pos - before;
         Cursor<kKeys> c;
-        for (c.b = b_lo;; ++c.b) {
-            c.set_len(valid_len(a, c.b));
-            const int64_t here = static_cast<int64_t>(c.tiles) * units;
-            if (left < here) break;
-            left -= here;
+        const bool owner = pos >= before && pos < after;
+        if (owner) {
+            int64_t left = pos - before;
+            for (c.b = b_lo;; ++c.b) {
+                c.set_len(valid_len(a, c.b));
+                const int64_t here = static_cast<int64_t>(c.tiles) * units;
+                if (left < here) break;
+                left -= here;
+            }
+            c.u = static_cast<int>(div64(left, c.tiles));
+            c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
         }
-        c.u = static_cast<int>(left / c.tiles);
-        c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
+        const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
+        c.b = __shfl_sync(0xffffffffu, c.b, src);
+        c.u = __shfl_sync(0xffffffffu, c.u, src);
+        c.t = __shfl_sync(0xffffffffu, c.t, src);
+        c.set_len(__shfl_sync(0xffffffffu, c.len, src));
         return c;
     };
-    auto owned = [&](int64_t pos) { return pos >= before && pos < before + mine * units; };
-    int64_t lo = 0, hi = 0;  // this CTA's piece
+    int64_t remaining = 0, begin = 0;  // this warp's tiles
     if (blockIdx.x < ctas) {
-        lo = blockIdx.x * total / ctas;
-        hi = (blockIdx.x + int64_t{1}) * total / ctas;
+        const int64_t q = div64(total, ctas);
+        const int64_t r = total - q * ctas;  // the first r CTAs take one more
+        int64_t lo = blockIdx.x * q + min(static_cast<int64_t>(blockIdx.x), r);
+        int64_t hi = lo + q + (blockIdx.x < r);
         if (a.whole) {
-            if (owned(lo)) s_bound[0] = lo - find(lo).t;
-            if (owned(hi)) s_bound[1] = hi - find(hi).t;
-            if (hi == total && tid == 0) s_bound[1] = total;
-            __syncthreads();
-            lo = s_bound[0];
-            hi = s_bound[1];
+            if (hi < total) hi -= find(hi).t;
+            lo -= find(lo).t;
         }
-        for (int w = 0; w < kWarps; ++w) {
-            const int64_t start = lo + (hi - lo) * w / kWarps;
-            if (owned(start)) s_start[w] = find(start);
-        }
+        const int64_t per = static_cast<uint64_t>(hi - lo) / kWarps, more = hi - lo - per * kWarps;
+        begin = lo + warp * per + min(static_cast<int64_t>(warp), more);
+        remaining = per + (warp < more);
     }
-    __syncthreads();
 
     // ---- a warp's part of the piece --------------------------------------------------------
-    int64_t remaining = lo + (hi - lo) * (warp + 1) / kWarps - (lo + (hi - lo) * warp / kWarps);
     if (remaining > 0) {
         const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
-        Cursor<kKeys> cur = s_start[warp];
-        Copier<S> copier;
+        Cursor<kKeys> cur = find(begin);
+        Copier<S, kOnePage> copier;
         copier.begin(a, cur, remaining, lane);
         int put = 0, copied = 0;  // the slot, and the tile, of the next half to copy
         auto copy_half = [&]() {
@@ -481,7 +476,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
             if (!copier.values) ++copied;
             put = put == S::kSlots - 1 ? 0 : put + 1;
         };
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < S::kSlots - 1; ++s) copy_half();
 
         uint32_t qf[kOT][kN][2];
@@ -733,7 +728,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                             }
                     }
                     if (lane == 0) {
-                        s_part[at].unit = static_cast<int64_t>(cur.b) * units + cur.u;
+                        s_part[at].b = cur.b;
+                        s_part[at].u = cur.u;
                         s_part[at].starts = begun == 0;
                         s_part[at].ends = ends;
                         s_part[at].in_global = remaining != 0;
@@ -776,13 +772,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
 
     // ---- joining the CTA's parts: runs of one unit, in the list's order ------------------
     if (warp == 0) {
-        const int64_t unit = lane < kParts ? s_part[lane].unit : -1;
-        const uint32_t valid = __ballot_sync(0xffffffffu, unit >= 0);
+        const int b = lane < kParts ? s_part[lane].b : -1, u = lane < kParts ? s_part[lane].u : 0;
+        const uint32_t valid = __ballot_sync(0xffffffffu, b >= 0);
         const uint32_t below = valid & ((1u << lane) - 1);
-        const int64_t prev = __shfl_sync(0xffffffffu, unit, below == 0 ? 0 : 31 - __clz(below));
-        const bool first = unit >= 0 && (below == 0 || prev != unit);
+        const int src = below == 0 ? 0 : 31 - __clz(below);
+        const int prev_b = __shfl_sync(0xffffffffu, b, src), prev_u = __shfl_sync(0xffffffffu, u, src);
+        const bool first = b >= 0 && (below == 0 || prev_b != b || prev_u != u);
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-        if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].unit = -1;
+        if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].b = -1;
         __syncwarp();
         if (first) {
             const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
@@ -793,7 +790,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
             const bool starts = s_part[lane].starts, ends = s_part[last].ends;
             if (!(starts && ends)) {
                 CutMeta &meta = a.ws.meta[blockIdx.x * 2 + (starts ? 1 : 0)];
-                meta.unit = unit;
+                meta.b = b;
+                meta.u = u;
                 meta.ends = ends;
             }
         }
@@ -804,17 +802,15 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     for (int i = tid; i < s_runs * kPer; i += kThreads) {
         const int r = i / kPer, row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
         const int e0 = s_run[r], e1 = s_run_last[r];
-        const int64_t unit = s_part[e0].unit;
-        const int b = static_cast<int>(unit / units);
-        const UnitRows rows(a, b, static_cast<int>(unit - static_cast<int64_t>(b) * units), kHeads);
+        const UnitRows rows(a, s_part[e0].b, s_part[e0].u, kHeads);
         if (row >= rows.rows) continue;
         float mm = -INFINITY, ll = 0.f;
         for (int e = e0; e <= e1; ++e)
-            if (s_part[e].unit >= 0) mm = fmaxf(mm, s_m[e][row]);
+            if (s_part[e].b >= 0) mm = fmaxf(mm, s_m[e][row]);
         const float ref = mm == -INFINITY ? 0.f : mm;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int e = e0; e <= e1; ++e) {
-            if (s_part[e].unit < 0) continue;
+            if (s_part[e].b < 0) continue;
             const float w = ex2(s_m[e][row] - ref);
             const float *part =
                 s_part[e].in_global
@@ -846,6 +842,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     // ---- sequences without keys ----------------------------------------------------------
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (valid_len(a, b) > 0) continue;
+        if (tid == 0 && __ldg(a.seq_lens + b) != 0) record_device_error(a.err, kDevInvalidArg);
         for (int i = tid; i < a.q_heads * (kD / 4); i += kThreads)
             write_out(a, static_cast<int64_t>(b) * a.q_heads * kD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
         if (a.lse != nullptr)
@@ -861,16 +858,23 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c0 = blockIdx.x;
     const CutMeta first = a.ws.meta[c0 * 2 + 1];
-    if (first.unit < 0) return;
-    const int units = a.cache.heads * a.head_tiles;
-    const int b = static_cast<int>(first.unit / units);
-    const UnitRows rows(a, b, static_cast<int>(first.unit - static_cast<int64_t>(b) * units), kHeads);
-    int c1 = c0 + 1;  // the last part's CTA
-    while (c1 < static_cast<int>(gridDim.x) - 1 && a.ws.meta[c1 * 2].ends == 0) ++c1;
+    // the last part's CTA: the next one whose slot 0 ends its unit
+    __shared__ int s_last;
+    if (threadIdx.x == 0) s_last = gridDim.x - 1;
+    __syncthreads();
+    const int c = c0 + 1 + threadIdx.x;
+    if (first.b >= 0 && c < static_cast<int>(gridDim.x) && a.ws.meta[c * 2].b >= 0 &&
+        a.ws.meta[c * 2].ends)
+        atomicMin(&s_last, c);
+    __syncthreads();
+    if (first.b < 0) return;
+    const int c1 = s_last;
+    const UnitRows rows(a, first.b, first.u, kHeads);
     for (int i = threadIdx.x; i < rows.rows * (kD / 4); i += blockDim.x) {
         const int row = i / (kD / 4), d = i % (kD / 4) * 4;
         float mm = -INFINITY, ll = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
             const int64_t at = (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kHeads + row;
             const float mc = a.ws.ml[at * 2], lc = a.ws.ml[at * 2 + 1];
@@ -893,15 +897,14 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
 template <class S>
 cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
     constexpr int kSmem = S::kWarps * S::kRing;
-    const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(&paged_decode_kernel<S>), kSmem);
-    if (e != cudaSuccess) return e;
     const int page_size = static_cast<int>(a.cache.page.d);
-    a.one_page = page_size % S::kKeys == 0;
+    auto kern = page_size % S::kKeys == 0 ? paged_decode_kernel<S, true> : paged_decode_kernel<S, false>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSmem);
+    if (e != cudaSuccess) return e;
     // Whole units to a CTA where a unit is at most two tiles to a warp: then a CTA's
     // load is uneven by less than what the second kernel would cost.
     a.whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
-    paged_decode_kernel<S><<<ctas, S::kWarps * 32, kSmem, s>>>(a);
+    kern<<<ctas, S::kWarps * 32, kSmem, s>>>(a);
     const cudaError_t e1 = cudaGetLastError();
     if (e1 != cudaSuccess || a.whole) return e1;
     cudaLaunchAttribute attr;
