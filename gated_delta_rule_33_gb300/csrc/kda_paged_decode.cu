@@ -43,6 +43,8 @@
 // 8-bit cache is widened to fp16, which holds every e4m3 value; the queries are
 // scaled by a power of two for each row, so that fp16 holds their bf16 values
 // too, and the weights are two fp16 numbers, times 2^15 to keep small ones normal.
+#include <cfloat>
+
 #include <cuda_fp16.h>
 
 #include "kda_internal.cuh"
@@ -57,6 +59,8 @@ constexpr int kMaxWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
+
 // kN: groups of 8 query heads in a unit.  Warps: as many as the accumulators
 // (kD / 4 * kN registers a lane) leave registers for, so that one warp's
 // instructions overlap another's waits.
@@ -67,13 +71,13 @@ struct Shape {
     static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
     static constexpr int kKeys = kRowBytes >= 256 ? 16 : 4096 / kRowBytes;  // keys of a tile
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-    static constexpr int kWarps = kD * kN > 128 ? 8 : 12;
-    static constexpr int kSlots = 196608 / kWarps / kHalf;                 // halves of a warp's ring
-    static constexpr int kRing = kSlots * kHalf;
+        static constexpr int kWarps = kD * kN > 128 ? 8 : 12;
+    static constexpr int kSlots = kWarps == 12 || kHalf > 4096 ? 3 : 4;    // halves of a warp's ring
     static constexpr int kHeads = 8 * kN;
     static constexpr int kPitch = kD + 4;                                  // floats of a part's row
-    static_assert(kSlots >= 3 && kSlots <= 7, "");
-    static_assert(kHeads * kPitch * 4 <= kRing, "a part must fit a warp's ring");
+    // the ring takes the warp's last part in the end
+    static constexpr int kRing = max_of(kSlots * kHalf, (kHeads * kPitch * 4 + 1023) / 1024 * 1024);
+    static_assert(kSlots >= 3 && kSlots <= 7, "the masks' ring holds the tiles in flight");
 };
 
 // What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
@@ -269,6 +273,15 @@ __device__ __forceinline__ void write_lse(const Args &a, int64_t row, float m, f
     if (a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// 16 bytes to shared memory, or zeros (nothing is read then).  Evicted from L2
+// first: a key is read once, and what else is there (weights, code) is not.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool real) {
+    asm volatile("{\n\t.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+                 "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;\n\t}" ::"r"(dst),
+                 "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+
 // The tiles that a warp copies: its part of the list, one half at a time.
 // kOnePage: a tile never spans two pages.
 template <class S, bool kOnePage>
@@ -348,10 +361,7 @@ struct Copier {
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i) {
                     const int r = i * kStep + r0;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                     to + piece<S::kRowBytes>(r, c)),
-                                 "l"(r < rows ? p : src), "r"(r < rows ? 16 : 0)
-                                 : "memory");
+                    copy16(to + piece<S::kRowBytes>(r, c), r < rows ? p : src, r < rows);
                     p += step;
                 }
             } else {
@@ -360,10 +370,7 @@ struct Copier {
                     const uint32_t r = i * 32 / kPieces + r0;
                     const int64_t o = __shfl_sync(
                         0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                     to + piece<S::kRowBytes>(r, c)),
-                                 "l"(src + (o < 0 ? 0 : o) + c * 16), "r"(o < 0 ? 0 : 16)
-                                 : "memory");
+                    copy16(to + piece<S::kRowBytes>(r, c), src + (o < 0 ? 0 : o) + c * 16, o >= 0);
                 }
             }
             if (!values) {
@@ -384,13 +391,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     constexpr int kBlocks = kKeys / 16;   // score blocks of 16 keys
     constexpr int kOT = kD / 16;          // output blocks of 16 channels
     constexpr int kParts = 2 * kWarps;
+    constexpr float kUp = kF16 ? 15.f : 0.f;  // log2 of what the weights are multiplied by
     static_assert(kParts <= 32, "a warp finds the runs");
 
     extern __shared__ __align__(1024) uint8_t s_ring[];
     __shared__ uint64_t s_valid[kWarps][4];
     __shared__ Part s_part[kParts];
-    __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads];
-    __shared__ int s_run[kParts], s_run_last[kParts], s_runs;
+    __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads], s_w[kParts][kHeads];
+    __shared__ int s_run[kParts], s_run_last[kParts], s_run_of[kParts], s_runs;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
@@ -450,6 +458,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         return c;
     };
     int64_t remaining = 0, begin = 0;  // this warp's tiles
+    int64_t paced = 0;                 // fours of tiles that every warp of the CTA has
     if (blockIdx.x < ctas) {
         const int64_t q = div64(total, ctas);
         const int64_t r = total - q * ctas;  // the first r CTAs take one more
@@ -462,6 +471,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         const int64_t per = static_cast<uint64_t>(hi - lo) / kWarps, more = hi - lo - per * kWarps;
         begin = lo + warp * per + min(static_cast<int64_t>(warp), more);
         remaining = per + (warp < more);
+        paced = per / 4;
     }
 
     // ---- a warp's part of the piece --------------------------------------------------------
@@ -492,8 +502,12 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                 fresh = false;
                 const __nv_bfloat16 *q = a.q + cur.b * a.q_row_stride +
                                          (rows.out_row - static_cast<int64_t>(cur.b) * a.q_heads) * kD;
-                const float base = a.scale * kLog2e *
-                                   (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + rows.h));
+                const float factor = a.scale * kLog2e *
+                                     (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + rows.h));
+                // a negative factor's sign goes to the queries; zero times a left-out key's
+                // -inf would be NaN
+                const float base = fmaxf(fabsf(factor), FLT_MIN);
+                const uint32_t sign = factor < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
                     const bool real = 8 * n + g < rows.rows;
@@ -525,10 +539,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const float2 u = unpack2<false>(qf[c][n][i]);
-                                qf[c][n][i] = pack2<true>(u.x * f1 * f2, u.y * f1 * f2);
+                                qf[c][n][i] = pack2<true>(u.x * f1 * f2, u.y * f1 * f2) ^ sign;
                             }
                         // the scores' columns are heads 2 tq, 2 tq + 1
-                        const float mine_sc = base / f1 / f2;
+                        const float mine_sc = fmaxf(base / f1 / f2, FLT_MIN);
                         sc[n][0] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq);
                         sc[n][1] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq + 4);
                     } else {
@@ -538,7 +552,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 qf[c][n][i] = real ? __ldg(reinterpret_cast<const uint32_t *>(
-                                                         x + 16 * c + 8 * i + 2 * tq))
+                                                         x + 16 * c + 8 * i + 2 * tq)) ^ sign
                                                    : 0;
                     }
                     m[n][0] = m[n][1] = -INFINITY;
@@ -549,6 +563,11 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                 }
                 begun = cur.t;
             }
+
+            // the warps of a CTA keep pace, four tiles at a time, as far as all have tiles:
+            // otherwise the last ends some 8 % after the first
+            if ((tile & 3) == 3 && --paced >= 0)
+                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 
             // ---- scores: keys 16 k + g, + 8; heads 8 n + 2 tq, + 1
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
@@ -588,12 +607,6 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
             const uint64_t valid = s_valid[warp][tile & 3];
             ++tile;
             constexpr uint64_t kAll = kKeys == 64 ? ~uint64_t{0} : (uint64_t{1} << (kKeys & 63)) - 1;
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[k][n][i] *= sc[n][i & 1];
             if (valid != kAll) {
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k)
@@ -603,6 +616,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                         for (int i = 0; i < 4; ++i)
                             if (!(valid >> (16 * k + g + 8 * (i >> 1)) & 1)) s[k][n][i] = -INFINITY;
             }
+            // m: the largest product so far, unscaled (the scale is not negative); a weight is
+            // 2^(s sc - ref), times 2^15 where it is to be fp16
             float ref[kN][2];
             bool grew = false;
             float shrink[kN][2];
@@ -617,10 +632,11 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
                     const float mn = fmaxf(m[n][i], mt);
-                    ref[n][i] = mn == -INFINITY ? 0.f : mn;
-                    shrink[n][i] = ex2(m[n][i] - ref[n][i]);
+                    ref[n][i] = mn == -INFINITY ? 0.f : mn * sc[n][i];
+                    shrink[n][i] = ex2(m[n][i] * sc[n][i] - ref[n][i]);
                     grew |= mn > m[n][i];
                     m[n][i] = mn;
+                    ref[n][i] -= kUp;
                 }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -634,7 +650,6 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                 }
             }
             // ---- weights, in two words, as the right operand
-            constexpr float kUp = kF16 ? 32768.f : 1.f;
             uint32_t p[kBlocks][kN][2], p2[kBlocks][kN][2];
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
@@ -642,12 +657,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float x = ex2(s[k][n][2 * j] - ref[n][0]);
-                        float y = ex2(s[k][n][2 * j + 1] - ref[n][1]);
+                        const float x = ex2(fmaf(s[k][n][2 * j], sc[n][0], -ref[n][0]));
+                        const float y = ex2(fmaf(s[k][n][2 * j + 1], sc[n][1], -ref[n][1]));
                         l[n][0] += x;
                         l[n][1] += y;
-                        x *= kUp;
-                        y *= kUp;
                         const uint32_t w = pack2<kF16>(x, y);
                         const float2 first = unpack2<kF16>(w);
                         p[k][n][j] = transpose8(w);
@@ -704,6 +717,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
                         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
                         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
+                        m[n][i] = m[n][i] == -INFINITY ? m[n][i] : m[n][i] * sc[n][i] - kUp;
                     }
                 const bool whole = ends && begun == 0;
                 float *part = nullptr;
@@ -735,7 +749,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
                         s_part[at].in_global = remaining != 0;
                     }
                 }
-                const float vs = (a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + rows.h)) / kUp;
+                const float vs = a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + rows.h);
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -781,6 +795,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].b = -1;
         __syncwarp();
+        if (b >= 0) s_run_of[lane] = __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
         if (first) {
             const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
             const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);
@@ -798,26 +813,48 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         if (lane == 0) s_runs = __popc(firsts);
     }
     __syncthreads();
+    // the parts' weights, for each head of a run; a whole unit's hold 1 / l too
+    for (int i = tid; i < kParts * kHeads; i += kThreads) {
+        const int e = i / kHeads, row = i % kHeads;
+        if (s_part[e].b < 0) continue;
+        const int r = s_run_of[e], e0 = s_run[r], e1 = s_run_last[r];
+        float mm = -INFINITY, ll = 0.f;
+        for (int j = e0; j <= e1; ++j)
+            if (s_part[j].b >= 0) mm = fmaxf(mm, s_m[j][row]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        for (int j = e0; j <= e1; ++j)
+            if (s_part[j].b >= 0) ll += ex2(s_m[j][row] - ref) * s_l[j][row];
+        const bool whole = s_part[e0].starts && s_part[e1].ends;
+        float w = ex2(s_m[e][row] - ref);
+        if (whole) w = ll == 0.f ? 0.f : w / ll;
+        s_w[e][row] = w;
+        if (e != e0) continue;
+        const UnitRows rows(a, s_part[e].b, s_part[e].u, kHeads);
+        if (row >= rows.rows) continue;
+        if (whole) {
+            write_lse(a, rows.out_row + row, mm, ll);
+        } else {
+            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s_part[e0].starts ? 1 : 0)) * kHeads + row;
+            *reinterpret_cast<float2 *>(a.ws.ml + at * 2) = make_float2(mm, ll);
+        }
+    }
+    __syncthreads();
     constexpr int kPer = kHeads * (kD / 4);
     for (int i = tid; i < s_runs * kPer; i += kThreads) {
         const int r = i / kPer, row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
         const int e0 = s_run[r], e1 = s_run_last[r];
         const UnitRows rows(a, s_part[e0].b, s_part[e0].u, kHeads);
         if (row >= rows.rows) continue;
-        float mm = -INFINITY, ll = 0.f;
-        for (int e = e0; e <= e1; ++e)
-            if (s_part[e].b >= 0) mm = fmaxf(mm, s_m[e][row]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int e = e0; e <= e1; ++e) {
             if (s_part[e].b < 0) continue;
-            const float w = ex2(s_m[e][row] - ref);
+            const float w = s_w[e][row];
             const float *part =
                 s_part[e].in_global
                     ? a.ws.head + ((static_cast<int64_t>(blockIdx.x) * kWarps + (e >> 1)) * kHeads + row) * kD
                     : reinterpret_cast<const float *>(s_ring + (e >> 1) * S::kRing) + row * S::kPitch;
             const float4 y = *reinterpret_cast<const float4 *>(part + d);
-            ll += w * s_l[e][row];
             x.x += w * y.x;
             x.y += w * y.y;
             x.z += w * y.z;
@@ -825,17 +862,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         }
         const bool starts = s_part[e0].starts;
         if (starts && s_part[e1].ends) {
-            const float f = ll == 0.f ? 0.f : 1.f / ll;
-            write_out(a, (rows.out_row + row) * kD + d,
-                      make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-            if (d == 0) write_lse(a, rows.out_row + row, mm, ll);
+            write_out(a, (rows.out_row + row) * kD + d, x);
         } else {
             const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * kHeads + row;
             *reinterpret_cast<float4 *>(a.ws.cut + at * kD + d) = x;
-            if (d == 0) {
-                a.ws.ml[at * 2] = mm;
-                a.ws.ml[at * 2 + 1] = ll;
-            }
         }
     }
 
@@ -853,45 +883,83 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
 
 // Joins the parts of the unit that CTA blockIdx.x of the first kernel began and
 // did not finish: its slot 1 and slot 0 of the CTAs after it, up to the last.
+// blockIdx.y: 64 channels.  The weights of all parts first (a warp to a head),
+// then the sums, whose loads do not wait for one another.
+constexpr int kJoinThreads = 256;
+
 template <int kD, int kHeads>
-__global__ void __launch_bounds__(256) join_kernel(const Args a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+    constexpr int kQuads = 16;                                       // float4s of 64 channels
+    constexpr int kGroups = kJoinThreads / (kHeads * kQuads);        // share the parts
+    __shared__ float s_w[kMaxCtas][kHeads];
+    __shared__ float4 s_sum[kGroups > 1 ? kGroups : 1][kHeads * kQuads];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c0 = blockIdx.x, ctas = gridDim.x;
+    if (tid == 0) s_last = ctas - 1;
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c0 = blockIdx.x;
     const CutMeta first = a.ws.meta[c0 * 2 + 1];
     // the last part's CTA: the next one whose slot 0 ends its unit
-    __shared__ int s_last;
-    if (threadIdx.x == 0) s_last = gridDim.x - 1;
-    __syncthreads();
-    const int c = c0 + 1 + threadIdx.x;
-    if (first.b >= 0 && c < static_cast<int>(gridDim.x) && a.ws.meta[c * 2].b >= 0 &&
-        a.ws.meta[c * 2].ends)
-        atomicMin(&s_last, c);
+    const int c = c0 + 1 + tid;
+    if (c < ctas) {
+        const CutMeta next = a.ws.meta[c * 2];
+        if (next.b >= 0 && next.ends) atomicMin(&s_last, c);
+    }
     __syncthreads();
     if (first.b < 0) return;
-    const int c1 = s_last;
+    const int parts = s_last - c0 + 1;
     const UnitRows rows(a, first.b, first.u, kHeads);
-    for (int i = threadIdx.x; i < rows.rows * (kD / 4); i += blockDim.x) {
-        const int row = i / (kD / 4), d = i % (kD / 4) * 4;
+    // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
+    auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+    for (int row = warp; row < rows.rows; row += kJoinThreads / 32) {
         float mm = -INFINITY, ll = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t at = (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kHeads + row;
-            const float mc = a.ws.ml[at * 2], lc = a.ws.ml[at * 2 + 1];
-            const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + at * kD + d);
-            const float mn = fmaxf(mm, mc), ref = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(mm - ref), w = ex2(mc - ref);
-            ll = ll * f + lc * w;
-            x.x = x.x * f + y.x * w;
-            x.y = x.y * f + y.y * w;
-            x.z = x.z * f + y.z * w;
-            x.w = x.w * f + y.w * w;
-            mm = mn;
+        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, a.ws.ml[(slot(i) * kHeads + row) * 2]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 x = *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
+            const float w = ex2(x.x - ref);
+            s_w[i][row] = w;
+            ll += w * x.y;
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+        __syncwarp();
         const float f = ll == 0.f ? 0.f : 1.f / ll;
-        write_out(a, (rows.out_row + row) * kD + d, make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-        if (d == 0) write_lse(a, rows.out_row + row, mm, ll);
+        for (int i = lane; i < parts; i += 32) s_w[i][row] *= f;
+        if (lane == 0 && blockIdx.y == 0) write_lse(a, rows.out_row + row, mm, ll);
     }
+    __syncthreads();
+    const int item = tid % (kHeads * kQuads), group = tid / (kHeads * kQuads);
+    const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < rows.rows) {
+#pragma unroll 8
+        for (int i = group; i < parts; i += kGroups) {
+            const float w = s_w[i][row];
+            const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + (slot(i) * kHeads + row) * kD + d);
+            x.x += w * y.x;
+            x.y += w * y.y;
+            x.z += w * y.z;
+            x.w += w * y.w;
+        }
+    }
+    if constexpr (kGroups > 1) {
+        s_sum[group][item] = x;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+            const float4 y = s_sum[i][item];
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+        }
+    }
+    if (row < rows.rows) write_out(a, (rows.out_row + row) * kD + d, x);
 }
 
 template <class S>
@@ -911,8 +979,8 @@ cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(ctas, S::kD / 64);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

@@ -417,26 +417,39 @@ class PagedCache:
         self._ref = ctypes.addressof(self._struct)
 
 
-def _i32(t: Optional[torch.Tensor]):
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError(f"int32 tensor expected, got {t.dtype}")
-    return _p(t)
+# The paged calls run once a layer and token, where the host's time counts: pointers go as
+# plain integers, and the current stream's handle is asked for without a Stream object.
+
+def _ptr(t: torch.Tensor, dtype: torch.dtype) -> int:
+    if t.dtype is not dtype:
+        raise TypeError(f"{dtype} tensor expected, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("libkda needs contiguous tensors")
+    return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, width: int):
-    """Pointer and row stride of [N, heads, head_dim] (or [N, width]) bf16 rows that may lie
-    further apart than their width."""
-    if t.dtype != torch.bfloat16:
+def _rows(t: torch.Tensor, heads: int, head_dim: int):
+    """Pointer and row stride of bf16 [N, heads, head_dim] (or [N, heads * head_dim]) rows that
+    may lie further apart than their width."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"bf16 tensor expected, got {t.dtype}")
     shape, strides = t.shape, t.stride()
-    if t.dim() == 3:
-        ok = (shape[1] * shape[2] == width and strides[2] == 1
-              and (shape[1] == 1 or strides[1] == shape[2]))
+    if len(shape) == 3:
+        ok = (shape[1] == heads and shape[2] == head_dim and strides[2] == 1
+              and (heads == 1 or strides[1] == head_dim))
     else:
-        ok = t.dim() == 2 and shape[1] == width and strides[1] == 1
+        ok = len(shape) == 2 and shape[1] == heads * head_dim and strides[1] == 1
     if not ok:
-        raise ValueError(f"rows of {width} contiguous values expected")
+        raise ValueError(f"rows of {heads} x {head_dim} contiguous values expected")
     return t.data_ptr(), strides[0]
+
+
+def _handle(stream, t: torch.Tensor) -> int:
+    if stream is None:
+        if not t.is_cuda:
+            raise ValueError("libkda needs CUDA tensors")
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, seq_lens,
@@ -447,25 +460,27 @@ def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num
     if (cached_lens.numel() != B or new_lens.numel() != B or seq_lens.numel() != B
             or cu_seqlens.numel() != B + 1 or pages_used.numel() != 1):
         raise ValueError("cached_lens, new_lens, seq_lens [B], cu_seqlens [B+1], pages_used [1]")
-    st = load().kda_page_plan(_i32(cached_lens), _i32(new_lens), _i32(free_pages),
-                              free_pages.numel(), _i32(block_table), max_pages, B, int(page_size),
-                              int(num_pages), _i32(seq_lens), _i32(cu_seqlens), _i32(slot_map),
-                              slot_map.numel(), _i32(pages_used),
-                              _stream(stream, block_table.device))
-    _check(st, "kda_page_plan")
+    i32 = torch.int32
+    st = (_lib or load()).kda_page_plan(
+        _ptr(cached_lens, i32), _ptr(new_lens, i32), _ptr(free_pages, i32), free_pages.numel(),
+        _ptr(block_table, i32), max_pages, B, page_size, num_pages, _ptr(seq_lens, i32),
+        _ptr(cu_seqlens, i32), _ptr(slot_map, i32), slot_map.numel(), _ptr(pages_used, i32),
+        _handle(stream, block_table))
+    if st:
+        raise KDAError(st, "kda_page_plan")
 
 
 def kda_paged_append(k, v, slot_map, cache, stream=None):
     """k, v bf16 [N, heads, head_dim] (rows may be slices of a wider tensor); slot_map [N]."""
-    width = cache.heads * cache.head_dim
     N = slot_map.numel()
-    if k.shape[0] != N or v.shape[0] != N:
+    if len(k) != N or len(v) != N:
         raise ValueError("k and v need one row per entry of slot_map")
-    kp, ks = _rows(k, width)
-    vp, vs = _rows(v, width)
-    st = load().kda_paged_append(kp, vp, ks, vs, _i32(slot_map), N, cache._ref,
-                                 _stream(stream, k.device))
-    _check(st, "kda_paged_append")
+    kp, ks = _rows(k, cache.heads, cache.head_dim)
+    vp, vs = _rows(v, cache.heads, cache.head_dim)
+    st = (_lib or load()).kda_paged_append(kp, vp, ks, vs, _ptr(slot_map, torch.int32), N,
+                                           cache._ref, _handle(stream, k))
+    if st:
+        raise KDAError(st, "kda_paged_append")
 
 
 def kda_paged_decode_workspace_size(B, q_heads, kv_heads, head_dim) -> int:
@@ -475,20 +490,25 @@ def kda_paged_decode_workspace_size(B, q_heads, kv_heads, head_dim) -> int:
 def kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, workspace, stream=None):
     """q bf16 [B, q_heads, head_dim] (rows may lie apart); o alike, bf16 or fp32; lse fp32
     [B, q_heads] or None."""
-    B, q_heads, head_dim = q.shape
-    if head_dim != cache.head_dim or o.shape != q.shape:
+    shape = q.shape
+    B, q_heads, head_dim = shape
+    table_rows, max_pages = block_table.shape
+    if head_dim != cache.head_dim or o.shape != shape:
         raise ValueError("q and o are [B, q_heads, head_dim] with the cache's head_dim")
-    if block_table.shape[0] != B or seq_lens.numel() != B:
+    if table_rows != B or seq_lens.numel() != B:
         raise ValueError("block_table [B, max_pages] and seq_lens [B]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * q_heads):
+    if lse is not None and lse.numel() != B * q_heads:
         raise ValueError("lse is fp32 [B, q_heads]")
-    qp, qs = _rows(q, q_heads * head_dim)
-    st = load().kda_paged_decode(qp, qs, cache._ref, _i32(block_table), block_table.shape[1],
-                                 _i32(seq_lens), B, q_heads, float(scale), _p(o), _dtype_code(o),
-                                 _p(lse), _p(workspace),
-                                 workspace.numel() * workspace.element_size(),
-                                 _stream(stream, q.device))
-    _check(st, "kda_paged_decode")
+    qp, qs = _rows(q, q_heads, head_dim)
+    o_dtype = o.dtype
+    st = (_lib or load()).kda_paged_decode(
+        qp, qs, cache._ref, _ptr(block_table, torch.int32), max_pages,
+        _ptr(seq_lens, torch.int32), B, q_heads, scale, _ptr(o, o_dtype),
+        KDA_BF16 if o_dtype is torch.bfloat16 else _dtype_code(o),
+        None if lse is None else _ptr(lse, torch.float32), _ptr(workspace, workspace.dtype),
+        workspace.nbytes, _handle(stream, q))
+    if st:
+        raise KDAError(st, "kda_paged_decode")
 
 
 def kda_debug_check_gate_division(stream=None) -> int:
