@@ -69,10 +69,13 @@ struct Shape {
     static constexpr int kD = kD_, kN = kN_;
     static constexpr bool kFp8 = kFp8_;
     static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
-    static constexpr int kKeys = kRowBytes >= 256 ? 16 : 4096 / kRowBytes;  // keys of a tile
+    // keys of a tile: 4 KB of them, 2 KB where 32 heads' scores would fill the registers
+    static constexpr int kKeys = max_of(16, (kN == 4 ? 2048 : 4096) / kRowBytes);
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-        static constexpr int kWarps = kD * kN > 128 ? 8 : 12;
-    static constexpr int kSlots = kWarps == 12 || kHalf > 4096 ? 3 : 4;    // halves of a warp's ring
+        static constexpr int kWarps = kN == 4 || kD == 256 ? 8 : 12;
+    // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
+    // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
+    static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
     static constexpr int kHeads = 8 * kN;
     static constexpr int kPitch = kD + 4;                                  // floats of a part's row
     // the ring takes the warp's last part in the end
@@ -111,8 +114,11 @@ inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
     return head + kMaxCtas * kMaxWarps * part;
 }
 
-// Query heads of a unit: 8, or 16 where the group is larger.
-inline int unit_heads(int group) { return group <= 8 ? 8 : 16; }
+// Query heads of a unit: all of a group of up to 32 (16 at 256 channels), in 8, 16
+// or 32, so that its keys are read once.
+inline int unit_heads(int group, int head_dim) {
+    return group <= 8 ? 8 : group <= 16 || head_dim == 256 ? 16 : 32;
+}
 
 struct Args {
     const __nv_bfloat16 *q;
@@ -245,6 +251,17 @@ struct Part {
     int in_global;   // its sums are in the workspace (else in the warp's ring)
 };
 
+// A part's sums, and the parts of one unit, when a CTA joins them.
+struct PartAt {
+    const float *sums;  // [heads][pitch], shared or global
+    int pitch, part, run;
+};
+struct Run {
+    int begin, end;     // parts
+    int rows, whole;    // query heads; the unit's first and last keys are among them
+    int64_t out_row, slot;
+};
+
 // Where a unit's queries and outputs are.
 struct UnitRows {
     int h, rows;      // key head; query heads
@@ -297,7 +314,6 @@ struct Copier {
     // the tile whose values are next: where its rows are
     int64_t off[kLaneRows];                                  // kOnePage: of row 0
     int rows;                                                // rows to copy, the rest 0; -1: no tile
-    bool values;                                             // the next half
 
     __device__ __forceinline__ void read_pages(const Args &a, int lane) {
 #pragma unroll
@@ -317,74 +333,101 @@ struct Copier {
                                           int lane) {
         at = c;
         left = tiles;
-        values = false;
         read_pages(a, lane);
     }
 
-    // Copies the next half to the slot; masks: which of the tile's rows are keys.
-    __device__ __forceinline__ void half(const Args &a, int units, int lane, uint32_t to,
+    // Copies the keys of the next tile to the slot; mask: which of its rows are keys.
+    __device__ __forceinline__ void keys(const Args &a, int units, int lane, uint32_t to,
                                          uint64_t *mask) {
-        const uint8_t *src = values ? a.cache.v : a.cache.k;
-        if (!values) {
-            if (left > 0) {
-                uint64_t valid = 0;
-                const int64_t h = at.u / a.head_tiles * a.cache.head_stride;
-                if constexpr (kOnePage) {
-                    const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
-                    if (!ok) record_device_error(a.err, kDevInvalidArg);
-                    rows = ok ? min(kKeys, at.len - at.t * kKeys) : 0;
-                    off[0] = ok ? page[0] * a.cache.page_stride + in_page[0] * a.cache.token_stride + h : 0;
-                    valid = rows == 64 ? ~uint64_t{0} : (uint64_t{1} << rows) - 1;
-                } else {
-                    rows = kKeys;
-#pragma unroll
-                    for (int i = 0; i < kLaneRows; ++i) {
-                        const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
-                        if (!ok && held[i]) record_device_error(a.err, kDevInvalidArg);
-                        off[i] = ok ? page[i] * a.cache.page_stride +
-                                          in_page[i] * a.cache.token_stride + h
-                                    : -1;
-                        valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * i);
-                    }
-                }
-                if (lane == 0) *mask = valid;
-            } else {
-                rows = -1;
-            }
-        }
-        if (rows >= 0) {
-            const uint32_t r0 = lane / kPieces, c = lane % kPieces;
+        rows = -1;
+        if (left > 0) {
+            uint64_t valid = 0;
+            const int64_t h = (a.head_tiles == 1 ? at.u : at.u / a.head_tiles) * a.cache.head_stride;
             if constexpr (kOnePage) {
-                constexpr uint32_t kStep = 32 / kPieces;     // rows of one copy of the warp
-                const uint8_t *p = src + off[0] + r0 * a.cache.token_stride + c * 16;
-                const int64_t step = kStep * a.cache.token_stride;
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int r = i * kStep + r0;
-                    copy16(to + piece<S::kRowBytes>(r, c), r < rows ? p : src, r < rows);
-                    p += step;
-                }
+                const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
+                if (!ok) record_device_error(a.err, kDevInvalidArg);
+                rows = ok ? min(kKeys, at.len - at.t * kKeys) : 0;
+                off[0] = ok ? page[0] * a.cache.page_stride + in_page[0] * a.cache.token_stride + h : 0;
+                valid = rows == 64 ? ~uint64_t{0} : (uint64_t{1} << rows) - 1;
             } else {
+                rows = kKeys;
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const uint32_t r = i * 32 / kPieces + r0;
-                    const int64_t o = __shfl_sync(
-                        0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
-                    copy16(to + piece<S::kRowBytes>(r, c), src + (o < 0 ? 0 : o) + c * 16, o >= 0);
+                for (int i = 0; i < kLaneRows; ++i) {
+                    const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
+                    if (!ok && held[i]) record_device_error(a.err, kDevInvalidArg);
+                    off[i] = ok ? page[i] * a.cache.page_stride + in_page[i] * a.cache.token_stride + h
+                                : -1;
+                    valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * i);
                 }
             }
-            if (!values) {
-                at.next(a, units);
-                if (--left > 0) read_pages(a, lane);
+            if (lane == 0) *mask = valid;
+            copy(a, a.cache.k, lane, to);
+            at.next(a, units);
+            if (--left > 0) read_pages(a, lane);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    // Copies the values of the tile whose keys were last.
+    __device__ __forceinline__ void values(const Args &a, int lane, uint32_t to) {
+        if (rows >= 0) copy(a, a.cache.v, lane, to);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    __device__ __forceinline__ void copy(const Args &a, const uint8_t *src, int lane, uint32_t to) {
+        const uint32_t r0 = lane / kPieces, c = lane % kPieces;
+        if constexpr (kOnePage) {
+            constexpr uint32_t kStep = 32 / kPieces;     // rows of one copy of the warp
+            const uint8_t *p = src + off[0] + r0 * a.cache.token_stride + c * 16;
+            const int64_t step = kStep * a.cache.token_stride;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r = i * kStep + r0;
+                copy16(to + piece<S::kRowBytes>(r, c), r < rows ? p : src, r < rows);
+                p += step;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const uint32_t r = i * 32 / kPieces + r0;
+                const int64_t o = __shfl_sync(
+                    0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
+                copy16(to + piece<S::kRowBytes>(r, c), src + (o < 0 ? 0 : o) + c * 16, o >= 0);
             }
         }
-        values = !values;
-        asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
 
+// The place of position `pos` < the total of the list; called by a whole warp, whose
+// lanes hold the sequences from b_lo on at positions before .. after - 1.  Not inlined:
+// it is wanted three times, and short calls wait for instructions more than for anything.
+template <int kKeys>
+__device__ __noinline__ Cursor<kKeys> find_tile(const Args &a, int units, int64_t pos, int b_lo,
+                                                int64_t before, int64_t after) {
+    Cursor<kKeys> c;
+    c.b = c.u = c.t = c.len = 0;
+    const bool owner = pos >= before && pos < after;
+    if (owner) {
+        int64_t left = pos - before;
+        for (c.b = b_lo;; ++c.b) {
+            c.set_len(valid_len(a, c.b));
+            const int64_t here = static_cast<int64_t>(c.tiles) * units;
+            if (left < here) break;
+            left -= here;
+        }
+        c.u = static_cast<int>(div64(left, c.tiles));
+        c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
+    }
+    const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
+    c.b = __shfl_sync(0xffffffffu, c.b, src);
+    c.u = __shfl_sync(0xffffffffu, c.u, src);
+    c.t = __shfl_sync(0xffffffffu, c.t, src);
+    c.set_len(__shfl_sync(0xffffffffu, c.len, src));
+    return c;
+}
+
 template <class S, bool kOnePage>
-__global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const Args a) {
+__global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const __grid_constant__ Args a) {
     constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
     constexpr bool kFp8 = S::kFp8, kF16 = S::kFp8;
     constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kKeys = S::kKeys;
@@ -398,7 +441,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     __shared__ uint64_t s_valid[kWarps][4];
     __shared__ Part s_part[kParts];
     __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads], s_w[kParts][kHeads];
-    __shared__ int s_run[kParts], s_run_last[kParts], s_run_of[kParts], s_runs;
+    __shared__ Run s_run[kParts];
+    __shared__ PartAt s_at[kParts];
+    __shared__ int s_runs, s_parts;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
@@ -435,28 +480,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     if (a.whole) want = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, filled)) * units;
     else want = static_cast<uint64_t>(total + kWarps - 1) / kWarps;
     const uint32_t ctas = static_cast<uint32_t>(want < gridDim.x ? want : gridDim.x);
-    // the place of a position < total of the list
-    auto find = [&](int64_t pos) {
-        Cursor<kKeys> c;
-        const bool owner = pos >= before && pos < after;
-        if (owner) {
-            int64_t left = pos - before;
-            for (c.b = b_lo;; ++c.b) {
-                c.set_len(valid_len(a, c.b));
-                const int64_t here = static_cast<int64_t>(c.tiles) * units;
-                if (left < here) break;
-                left -= here;
-            }
-            c.u = static_cast<int>(div64(left, c.tiles));
-            c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
-        }
-        const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
-        c.b = __shfl_sync(0xffffffffu, c.b, src);
-        c.u = __shfl_sync(0xffffffffu, c.u, src);
-        c.t = __shfl_sync(0xffffffffu, c.t, src);
-        c.set_len(__shfl_sync(0xffffffffu, c.len, src));
-        return c;
-    };
+    auto find = [&](int64_t pos) { return find_tile<kKeys>(a, units, pos, b_lo, before, after); };
     int64_t remaining = 0, begin = 0;  // this warp's tiles
     int64_t paced = 0;                 // fours of tiles that every warp of the CTA has
     if (blockIdx.x < ctas) {
@@ -480,14 +504,25 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
         Cursor<kKeys> cur = find(begin);
         Copier<S, kOnePage> copier;
         copier.begin(a, cur, remaining, lane);
-        int put = 0, copied = 0;  // the slot, and the tile, of the next half to copy
-        auto copy_half = [&]() {
-            copier.half(a, units, lane, ring + put * S::kHalf, &s_valid[warp][copied & 3]);
-            if (!copier.values) ++copied;
-            put = put == S::kSlots - 1 ? 0 : put + 1;
+        int put = 0, copied = 0;  // the slot of the next half to copy; tiles begun
+        auto next_slot = [&](int s) { return s == S::kSlots - 1 ? 0 : s + 1; };
+        auto copy_keys = [&]() {
+            copier.keys(a, units, lane, ring + put * S::kHalf, &s_valid[warp][copied++ & 3]);
+            put = next_slot(put);
         };
+        auto copy_values = [&]() {
+            copier.values(a, lane, ring + put * S::kHalf);
+            put = next_slot(put);
+        };
+        // kSlots - 1 halves ahead: with an odd number of slots the keys of a tile are
+        // replaced by keys, with an even number by values
+        constexpr bool kOdd = S::kSlots % 2 == 1;
 #pragma unroll 1
-        for (int s = 0; s < S::kSlots - 1; ++s) copy_half();
+        for (int i = 0; i < (S::kSlots - 1) / 2; ++i) {
+            copy_keys();
+            copy_values();
+        }
+        if (!kOdd) copy_keys();
 
         uint32_t qf[kOT][kN][2];
         float acc[kOT][kN][4], m[kN][2], l[kN][2], sc[kN][2];
@@ -572,9 +607,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
             // ---- scores: keys 16 k + g, + 8; heads 8 n + 2 tq, + 1
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
             __syncwarp();  // the keys are in, and the half before them is read by every lane
-            copy_half();
+            if (kOdd) copy_keys();
+            else copy_values();
             const uint32_t kt = ring + slot * S::kHalf;
-            slot = slot == S::kSlots - 1 ? 0 : slot + 1;
+            slot = next_slot(slot);
             float s[kBlocks][kN][4];
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
@@ -670,9 +706,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
             // ---- outputs: channels g, g + 8 of 16 d (8-bit: 2 g, 2 g + 1)
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
             __syncwarp();  // the values are in, and the keys are read by every lane
-            copy_half();
+            if (kOdd) copy_values();
+            else copy_keys();
             const uint32_t vt = ring + slot * S::kHalf;
-            slot = slot == S::kSlots - 1 ? 0 : slot + 1;
+            slot = next_slot(slot);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
 #pragma unroll
@@ -784,89 +821,93 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const A
     }
     __syncthreads();
 
-    // ---- joining the CTA's parts: runs of one unit, in the list's order ------------------
+    // ---- joining the CTA's parts: the parts there are, and the runs of one unit among
+    // them, in the list's order
     if (warp == 0) {
-        const int b = lane < kParts ? s_part[lane].b : -1, u = lane < kParts ? s_part[lane].u : 0;
-        const uint32_t valid = __ballot_sync(0xffffffffu, b >= 0);
+        Part part;
+        part.b = -1;
+        if (lane < kParts) part = s_part[lane];
+        const uint32_t valid = __ballot_sync(0xffffffffu, part.b >= 0);
         const uint32_t below = valid & ((1u << lane) - 1);
         const int src = below == 0 ? 0 : 31 - __clz(below);
-        const int prev_b = __shfl_sync(0xffffffffu, b, src), prev_u = __shfl_sync(0xffffffffu, u, src);
-        const bool first = b >= 0 && (below == 0 || prev_b != b || prev_u != u);
+        const int prev_b = __shfl_sync(0xffffffffu, part.b, src);
+        const int prev_u = __shfl_sync(0xffffffffu, part.u, src);
+        const bool first = part.b >= 0 && (below == 0 || prev_b != part.b || prev_u != part.u);
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
+        const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);  // up to its end
+        const int ends = __shfl_sync(0xffffffffu, part.ends, run == 0 ? 0 : 31 - __clz(run));
         if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].b = -1;
         __syncwarp();
-        if (b >= 0) s_run_of[lane] = __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
+        const int at = __popc(below), r = __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
+        if (part.b >= 0) {
+            PartAt &x = s_at[at];
+            x.part = lane;
+            x.run = r;
+            x.pitch = part.in_global ? kD : S::kPitch;
+            x.sums = part.in_global
+                         ? a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + (lane >> 1)) * kHeads * kD
+                         : reinterpret_cast<const float *>(s_ring + (lane >> 1) * S::kRing);
+        }
         if (first) {
-            const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
-            const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);
-            const int r = __popc(firsts & ((1u << lane) - 1)), last = 31 - __clz(run);
-            s_run[r] = lane;
-            s_run_last[r] = last;
-            const bool starts = s_part[lane].starts, ends = s_part[last].ends;
-            if (!(starts && ends)) {
-                CutMeta &meta = a.ws.meta[blockIdx.x * 2 + (starts ? 1 : 0)];
-                meta.b = b;
-                meta.u = u;
+            const UnitRows rows(a, part.b, part.u, kHeads);
+            Run &x = s_run[r];
+            x.begin = at;
+            x.end = __popc(run);
+            x.rows = rows.rows;
+            x.whole = part.starts && ends;
+            x.out_row = rows.out_row;
+            x.slot = static_cast<int64_t>(blockIdx.x) * 2 + (part.starts ? 1 : 0);
+            if (!x.whole) {
+                CutMeta &meta = a.ws.meta[x.slot];
+                meta.b = part.b;
+                meta.u = part.u;
                 meta.ends = ends;
             }
         }
-        if (lane == 0) s_runs = __popc(firsts);
+        if (lane == 0) {
+            s_runs = __popc(firsts);
+            s_parts = __popc(valid);
+        }
     }
     __syncthreads();
-    // the parts' weights, for each head of a run; a whole unit's hold 1 / l too
-    for (int i = tid; i < kParts * kHeads; i += kThreads) {
+    // the parts' weights, for each head; a whole unit's hold 1 / l too
+    for (int i = tid; i < s_parts * kHeads; i += kThreads) {
         const int e = i / kHeads, row = i % kHeads;
-        if (s_part[e].b < 0) continue;
-        const int r = s_run_of[e], e0 = s_run[r], e1 = s_run_last[r];
+        const Run run = s_run[s_at[e].run];
+        if (row >= run.rows) continue;
         float mm = -INFINITY, ll = 0.f;
-        for (int j = e0; j <= e1; ++j)
-            if (s_part[j].b >= 0) mm = fmaxf(mm, s_m[j][row]);
+#pragma unroll 4
+        for (int j = run.begin; j < run.end; ++j) mm = fmaxf(mm, s_m[s_at[j].part][row]);
         const float ref = mm == -INFINITY ? 0.f : mm;
-        for (int j = e0; j <= e1; ++j)
-            if (s_part[j].b >= 0) ll += ex2(s_m[j][row] - ref) * s_l[j][row];
-        const bool whole = s_part[e0].starts && s_part[e1].ends;
-        float w = ex2(s_m[e][row] - ref);
-        if (whole) w = ll == 0.f ? 0.f : w / ll;
+#pragma unroll 4
+        for (int j = run.begin; j < run.end; ++j)
+            ll += ex2(s_m[s_at[j].part][row] - ref) * s_l[s_at[j].part][row];
+        float w = ex2(s_m[s_at[e].part][row] - ref);
+        if (run.whole) w = ll == 0.f ? 0.f : w / ll;
         s_w[e][row] = w;
-        if (e != e0) continue;
-        const UnitRows rows(a, s_part[e].b, s_part[e].u, kHeads);
-        if (row >= rows.rows) continue;
-        if (whole) {
-            write_lse(a, rows.out_row + row, mm, ll);
-        } else {
-            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s_part[e0].starts ? 1 : 0)) * kHeads + row;
-            *reinterpret_cast<float2 *>(a.ws.ml + at * 2) = make_float2(mm, ll);
-        }
+        if (e != run.begin) continue;
+        if (run.whole) write_lse(a, run.out_row + row, mm, ll);
+        else *reinterpret_cast<float2 *>(a.ws.ml + (run.slot * kHeads + row) * 2) = make_float2(mm, ll);
     }
     __syncthreads();
     constexpr int kPer = kHeads * (kD / 4);
     for (int i = tid; i < s_runs * kPer; i += kThreads) {
-        const int r = i / kPer, row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
-        const int e0 = s_run[r], e1 = s_run_last[r];
-        const UnitRows rows(a, s_part[e0].b, s_part[e0].u, kHeads);
-        if (row >= rows.rows) continue;
+        const Run run = s_run[i / kPer];
+        const int row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
+        if (row >= run.rows) continue;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int e = e0; e <= e1; ++e) {
-            if (s_part[e].b < 0) continue;
+        for (int e = run.begin; e < run.end; ++e) {
             const float w = s_w[e][row];
-            const float *part =
-                s_part[e].in_global
-                    ? a.ws.head + ((static_cast<int64_t>(blockIdx.x) * kWarps + (e >> 1)) * kHeads + row) * kD
-                    : reinterpret_cast<const float *>(s_ring + (e >> 1) * S::kRing) + row * S::kPitch;
-            const float4 y = *reinterpret_cast<const float4 *>(part + d);
+            const float4 y = *reinterpret_cast<const float4 *>(s_at[e].sums + row * s_at[e].pitch + d);
             x.x += w * y.x;
             x.y += w * y.y;
             x.z += w * y.z;
             x.w += w * y.w;
         }
-        const bool starts = s_part[e0].starts;
-        if (starts && s_part[e1].ends) {
-            write_out(a, (rows.out_row + row) * kD + d, x);
-        } else {
-            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * kHeads + row;
-            *reinterpret_cast<float4 *>(a.ws.cut + at * kD + d) = x;
-        }
+        if (run.whole) write_out(a, (run.out_row + row) * kD + d, x);
+        else *reinterpret_cast<float4 *>(a.ws.cut + (run.slot * kHeads + row) * kD + d) = x;
     }
 
     // ---- sequences without keys ----------------------------------------------------------
@@ -890,16 +931,26 @@ constexpr int kJoinThreads = 256;
 template <int kD, int kHeads>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
     constexpr int kQuads = 16;                                       // float4s of 64 channels
-    constexpr int kGroups = kJoinThreads / (kHeads * kQuads);        // share the parts
+    constexpr int kItems = kHeads * kQuads;
+    constexpr int kGroups = max_of(1, kJoinThreads / kItems);        // share the parts
     __shared__ float s_w[kMaxCtas][kHeads];
-    __shared__ float4 s_sum[kGroups > 1 ? kGroups : 1][kHeads * kQuads];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x, ctas = gridDim.x;
     if (tid == 0) s_last = ctas - 1;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
+    auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
     const CutMeta first = a.ws.meta[c0 * 2 + 1];
+    // the first 32 parts' maxima and sums, before it is known how many there are
+    constexpr int kRowsOfWarp = kHeads / (kJoinThreads / 32);
+    float2 ml[kRowsOfWarp];
+#pragma unroll
+    for (int k = 0; k < kRowsOfWarp; ++k)
+        if (c0 + lane < ctas)
+            ml[k] = *reinterpret_cast<const float2 *>(
+                a.ws.ml + (slot(lane) * kHeads + warp + k * (kJoinThreads / 32)) * 2);
     // the last part's CTA: the next one whose slot 0 ends its unit
     const int c = c0 + 1 + tid;
     if (c < ctas) {
@@ -910,43 +961,57 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
     if (first.b < 0) return;
     const int parts = s_last - c0 + 1;
     const UnitRows rows(a, first.b, first.u, kHeads);
-    // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
-    auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
-    for (int row = warp; row < rows.rows; row += kJoinThreads / 32) {
+#pragma unroll
+    for (int k = 0; k < kRowsOfWarp; ++k) {
+        const int row = warp + k * (kJoinThreads / 32);
+        if (row >= rows.rows) break;
+        auto at = [&](int i) {
+            return i == lane ? ml[k]
+                             : *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
+        };
         float mm = -INFINITY, ll = 0.f;
-        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, a.ws.ml[(slot(i) * kHeads + row) * 2]);
+        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, at(i).x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
         const float ref = mm == -INFINITY ? 0.f : mm;
         for (int i = lane; i < parts; i += 32) {
-            const float2 x = *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
+            const float2 x = at(i);
             const float w = ex2(x.x - ref);
             s_w[i][row] = w;
             ll += w * x.y;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-        __syncwarp();
         const float f = ll == 0.f ? 0.f : 1.f / ll;
         for (int i = lane; i < parts; i += 32) s_w[i][row] *= f;
         if (lane == 0 && blockIdx.y == 0) write_lse(a, rows.out_row + row, mm, ll);
     }
     __syncthreads();
-    const int item = tid % (kHeads * kQuads), group = tid / (kHeads * kQuads);
-    const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < rows.rows) {
+    auto sum = [&](int item, int group) {
+        const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows.rows) {
 #pragma unroll 8
-        for (int i = group; i < parts; i += kGroups) {
-            const float w = s_w[i][row];
-            const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + (slot(i) * kHeads + row) * kD + d);
-            x.x += w * y.x;
-            x.y += w * y.y;
-            x.z += w * y.z;
-            x.w += w * y.w;
+            for (int i = group; i < parts; i += kGroups) {
+                const float w = s_w[i][row];
+                const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + (slot(i) * kHeads + row) * kD + d);
+                x.x += w * y.x;
+                x.y += w * y.y;
+                x.z += w * y.z;
+                x.w += w * y.w;
+            }
         }
-    }
+        return x;
+    };
+    auto out = [&](int item, float4 x) {
+        const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
+        if (row < rows.rows) write_out(a, (rows.out_row + row) * kD + d, x);
+    };
     if constexpr (kGroups > 1) {
+        static_assert(kGroups * kItems == kJoinThreads, "a thread to an item and group");
+        __shared__ float4 s_sum[kGroups][kItems];
+        const int item = tid % kItems, group = tid / kItems;
+        float4 x = sum(item, group);
         s_sum[group][item] = x;
         __syncthreads();
         if (group > 0) return;
@@ -958,8 +1023,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
             x.z += y.z;
             x.w += y.w;
         }
+        out(item, x);
+    } else {
+        for (int item = tid; item < kItems; item += kJoinThreads) out(item, sum(item, 0));
     }
-    if (row < rows.rows) write_out(a, (rows.out_row + row) * kD + d, x);
 }
 
 template <class S>
@@ -992,6 +1059,11 @@ cudaError_t launch_dim(const Args &a, int heads, int ctas, cudaStream_t s) {
     if (heads == 8)
         return a.cache.fp8 ? launch_shape<Shape<kD, true, 1>>(a, ctas, s)
                            : launch_shape<Shape<kD, false, 1>>(a, ctas, s);
+    if constexpr (kD <= 128) {
+        if (heads == 32)
+            return a.cache.fp8 ? launch_shape<Shape<kD, true, 4>>(a, ctas, s)
+                               : launch_shape<Shape<kD, false, 4>>(a, ctas, s);
+    }
     return a.cache.fp8 ? launch_shape<Shape<kD, true, 2>>(a, ctas, s)
                        : launch_shape<Shape<kD, false, 2>>(a, ctas, s);
 }
@@ -999,7 +1071,7 @@ cudaError_t launch_dim(const Args &a, int heads, int ctas, cudaStream_t s) {
 }  // namespace
 
 size_t paged_decode_workspace_bytes(int, int q_heads, int kv_heads, int head_dim) {
-    return layout_bytes(unit_heads(q_heads / kv_heads), head_dim, nullptr, nullptr);
+    return layout_bytes(unit_heads(q_heads / kv_heads, head_dim), head_dim, nullptr, nullptr);
 }
 
 cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
@@ -1017,7 +1089,7 @@ cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
     a.B = B;
     a.q_heads = q_heads;
     a.group = q_heads / cache.heads;
-    const int heads = unit_heads(a.group);
+    const int heads = unit_heads(a.group, cache.head_dim);
     a.head_tiles = (a.group + heads - 1) / heads;
     a.scale = scale;
     a.o = o;
