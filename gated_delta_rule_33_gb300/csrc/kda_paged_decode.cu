@@ -85,14 +85,7 @@ struct Shape {
 
 // What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
 // in slot 0, its last unit's (begun here, not finished) in slot 1.
-struct CutMeta {
-    int b, u;  // b = -1: none
-    int ends;  // the unit's last key is in this part
-    int pad;
-};
-
 struct Layout {      // of the workspace
-    CutMeta *meta;   // [ctas][2]
     float *ml;       // [ctas][2][heads][2]
     float *cut;      // [ctas][2][heads][D]
     float *head;     // [ctas][warps][heads][D]: a warp's first part, until its CTA joins it
@@ -102,12 +95,10 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 
 inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
     const size_t part = static_cast<size_t>(heads) * head_dim * 4;
-    const size_t ml = align256(kMaxCtas * 2 * sizeof(CutMeta));
-    const size_t cut = align256(ml + static_cast<size_t>(kMaxCtas) * 2 * heads * 2 * 4);
+    const size_t cut = align256(static_cast<size_t>(kMaxCtas) * 2 * heads * 2 * 4);
     const size_t head = align256(cut + kMaxCtas * 2 * part);
     if (l != nullptr) {
-        l->meta = reinterpret_cast<CutMeta *>(base);
-        l->ml = reinterpret_cast<float *>(base + ml);
+        l->ml = reinterpret_cast<float *>(base);
         l->cut = reinterpret_cast<float *>(base + cut);
         l->head = reinterpret_cast<float *>(base + head);
     }
@@ -134,7 +125,6 @@ struct Args {
     float *lse;
     Layout ws;
     unsigned int *err;
-    int whole;     // CTAs take whole units
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -398,9 +388,9 @@ struct Copier {
     }
 };
 
-// The place of position `pos` < the total of the list; called by a whole warp, whose
-// lanes hold the sequences from b_lo on at positions before .. after - 1.  Not inlined:
-// it is wanted three times, and short calls wait for instructions more than for anything.
+// The place of position pos < the total of the list; called by a whole warp, whose lanes
+// hold the sequences from b_lo on, at positions before .. after - 1.  Not inlined: it is
+// wanted three times, and short calls wait for instructions more than for anything.
 template <int kKeys>
 __device__ __noinline__ Cursor<kKeys> find_tile(const Args &a, int units, int64_t pos, int b_lo,
                                                 int64_t before, int64_t after) {
@@ -426,6 +416,113 @@ __device__ __noinline__ Cursor<kKeys> find_tile(const Args &a, int units, int64_
     return c;
 }
 
+// The list of tiles and its pieces, as a warp sees it: every warp sums the lengths for
+// itself (they come out of L1 after the first), lane i over sequences
+// i ceil(B / 32) .. , so that no barrier precedes the first copy.
+template <int kKeys, int kWarps>
+struct List {
+    int64_t before, after;   // positions of the list in this lane's sequences
+    int64_t total, q, r;     // CTA i's piece: q positions, one more in the first r
+    int b_lo, units;
+    int filled, filled_before;  // sequences with keys: this lane's, and before them
+    uint32_t ctas;           // that have a piece
+    bool one_each, whole;    // pieces are units, or end where units end
+
+    static __device__ __forceinline__ uint32_t tiles_of(const Args &a, int b) {
+        return (static_cast<uint32_t>(valid_len(a, b)) + kKeys - 1) / kKeys;
+    }
+
+    __device__ __forceinline__ List(const Args &a, int lane, int grid) {
+        units = a.cache.heads * a.head_tiles;
+        const int chunk = (a.B + 31) / 32;
+        b_lo = min(a.B, lane * chunk);
+        const int b_hi = min(a.B, b_lo + chunk);
+        int64_t mine = 0;
+        uint32_t longest = 0;
+        filled = 0;
+#pragma unroll 4
+        for (int b = b_lo; b < b_hi; ++b) {
+            const uint32_t n = tiles_of(a, b);
+            mine += n;
+            filled += n > 0;
+            longest = max(longest, n);
+        }
+        before = mine;
+        filled_before = filled;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
+            const int y = __shfl_up_sync(0xffffffffu, filled_before, d);
+            if (lane >= d) {
+                before += x;
+                filled_before += y;
+            }
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        total = __shfl_sync(0xffffffffu, before, 31) * units;
+        const int sequences = __shfl_sync(0xffffffffu, filled_before, 31);
+        filled_before -= filled;
+        before = (before - mine) * units;
+        after = before + mine * units;
+        // Whole units to a CTA where that makes no CTA's load larger by more than two tiles a
+        // warp (0.2 us a tile; joining between CTAs costs some 5 us, with its launch): one
+        // unit each where there are few, pieces moved back to a unit's start where units
+        // are short.
+        const int64_t all_units = static_cast<int64_t>(sequences) * units;
+        one_each = all_units <= grid && longest <= div64(total, grid) + 2 * kWarps;
+        whole = one_each || longest <= 2 * kWarps;
+        // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
+        // grid for longer lists
+        const int64_t want = whole ? all_units : static_cast<uint64_t>(total + kWarps - 1) / kWarps;
+        ctas = static_cast<uint32_t>(want < grid ? want : grid);
+        q = ctas == 0 ? 0 : div64(total, ctas);
+        r = total - q * ctas;
+    }
+
+    // The place of position pos < total; called by a whole warp.
+    __device__ __forceinline__ Cursor<kKeys> find(const Args &a, int64_t pos) const {
+        return find_tile<kKeys>(a, units, pos, b_lo, before, after);
+    }
+
+    // Where an even piece begins, and which holds a position (not `whole`).
+    __device__ __forceinline__ int64_t even_begin(int64_t cta) const { return cta * q + min(cta, r); }
+    __device__ __forceinline__ int even_piece_of(int64_t pos) const {
+        const int64_t longer = r * (q + 1);
+        return static_cast<int>(pos < longer ? div64(pos, static_cast<uint32_t>(q + 1))
+                                             : r + div64(pos - longer, static_cast<uint32_t>(q)));
+    }
+
+    // CTA `cta`'s piece, cta < ctas; called by a whole warp.
+    __device__ __forceinline__ void piece(const Args &a, uint32_t cta, int64_t &lo, int64_t &hi) const {
+        if (one_each) {
+            // unit `cta`: of the sequence before which there are `skip` with keys
+            const int skip = cta / units, u = cta - skip * units;
+            const bool owner = skip >= filled_before && skip < filled_before + filled;
+            if (owner) {
+                int left = skip - filled_before;
+                lo = before;
+                for (int b = b_lo;; ++b) {
+                    hi = tiles_of(a, b);
+                    if (hi > 0 && --left < 0) break;
+                    lo += hi * units;
+                }
+                lo += u * hi;
+                hi += lo;
+            }
+            const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
+            lo = __shfl_sync(0xffffffffu, lo, src);
+            hi = __shfl_sync(0xffffffffu, hi, src);
+            return;
+        }
+        lo = even_begin(cta);
+        hi = even_begin(cta + int64_t{1});
+        if (whole) {
+            if (hi < total) hi -= find(a, hi).t;
+            lo -= find(a, lo).t;
+        }
+    }
+};
+
 template <class S, bool kOnePage>
 __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const __grid_constant__ Args a) {
     constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
@@ -447,51 +544,17 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
-    const int units = a.cache.heads * a.head_tiles;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane < 2) s_part[2 * warp + lane].b = -1;
     __syncwarp();
 
-    // ---- the list: tiles before each sequence.  Every warp sums for itself (the
-    // lengths come out of L1 after the first): no barrier before the first copy.
-    const int chunk = (a.B + 31) / 32;
-    const int b_lo = min(a.B, lane * chunk), b_hi = min(a.B, b_lo + chunk);
-    int64_t before = 0;  // tiles of a unit each, of the sequences before this lane's
-    int64_t mine = 0;
-    int filled = 0;
-#pragma unroll 4
-    for (int b = b_lo; b < b_hi; ++b) {
-        const int v = valid_len(a, b);
-        mine += (static_cast<uint32_t>(v) + kKeys - 1) / kKeys;
-        filled += v > 0;
-    }
-    before = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += x;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, before, 31) * units;
-    before = (before - mine) * units;
-    const int64_t after = before + mine * units;
-    // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
-    // grid for longer lists
-    int64_t want;
-    if (a.whole) want = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, filled)) * units;
-    else want = static_cast<uint64_t>(total + kWarps - 1) / kWarps;
-    const uint32_t ctas = static_cast<uint32_t>(want < gridDim.x ? want : gridDim.x);
-    auto find = [&](int64_t pos) { return find_tile<kKeys>(a, units, pos, b_lo, before, after); };
+    const List<kKeys, kWarps> list(a, lane, gridDim.x);
+    const int units = list.units;
     int64_t remaining = 0, begin = 0;  // this warp's tiles
     int64_t paced = 0;                 // fours of tiles that every warp of the CTA has
-    if (blockIdx.x < ctas) {
-        const int64_t q = div64(total, ctas);
-        const int64_t r = total - q * ctas;  // the first r CTAs take one more
-        int64_t lo = blockIdx.x * q + min(static_cast<int64_t>(blockIdx.x), r);
-        int64_t hi = lo + q + (blockIdx.x < r);
-        if (a.whole) {
-            if (hi < total) hi -= find(hi).t;
-            lo -= find(lo).t;
-        }
+    if (blockIdx.x < list.ctas) {
+        int64_t lo, hi;
+        list.piece(a, blockIdx.x, lo, hi);
         const int64_t per = static_cast<uint64_t>(hi - lo) / kWarps, more = hi - lo - per * kWarps;
         begin = lo + warp * per + min(static_cast<int64_t>(warp), more);
         remaining = per + (warp < more);
@@ -501,7 +564,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
     // ---- a warp's part of the piece --------------------------------------------------------
     if (remaining > 0) {
         const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
-        Cursor<kKeys> cur = find(begin);
+        Cursor<kKeys> cur = list.find(a, begin);
         Copier<S, kOnePage> copier;
         copier.begin(a, cur, remaining, lane);
         int put = 0, copied = 0;  // the slot of the next half to copy; tiles begun
@@ -837,8 +900,6 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
         const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
         const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);  // up to its end
         const int ends = __shfl_sync(0xffffffffu, part.ends, run == 0 ? 0 : 31 - __clz(run));
-        if (lane < 2) a.ws.meta[blockIdx.x * 2 + lane].b = -1;
-        __syncwarp();
         const int at = __popc(below), r = __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
         if (part.b >= 0) {
             PartAt &x = s_at[at];
@@ -858,12 +919,6 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
             x.whole = part.starts && ends;
             x.out_row = rows.out_row;
             x.slot = static_cast<int64_t>(blockIdx.x) * 2 + (part.starts ? 1 : 0);
-            if (!x.whole) {
-                CutMeta &meta = a.ws.meta[x.slot];
-                meta.b = part.b;
-                meta.u = part.u;
-                meta.ends = ends;
-            }
         }
         if (lane == 0) {
             s_runs = __popc(firsts);
@@ -924,58 +979,73 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 
 // Joins the parts of the unit that CTA blockIdx.x of the first kernel began and
 // did not finish: its slot 1 and slot 0 of the CTAs after it, up to the last.
-// blockIdx.y: 64 channels.  The weights of all parts first (a warp to a head),
-// then the sums, whose loads do not wait for one another.
+// blockIdx.y: 64 channels.  Which parts those are follows from the lengths, so it
+// is known before the wait; after it there is one trip to memory, for the parts'
+// maxima and sums together with the first of their products.
 constexpr int kJoinThreads = 256;
 
-template <int kD, int kHeads>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+template <class S>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+    constexpr int kD = S::kD, kHeads = S::kHeads;
     constexpr int kQuads = 16;                                       // float4s of 64 channels
     constexpr int kItems = kHeads * kQuads;
     constexpr int kGroups = max_of(1, kJoinThreads / kItems);        // share the parts
+    constexpr int kTurns = max_of(1, kItems / kJoinThreads);         // items of a thread
+    constexpr int kAhead = 8 / kTurns;                               // parts read ahead, each
+    constexpr int kRowsOfWarp = kHeads / (kJoinThreads / 32);
     __shared__ float s_w[kMaxCtas][kHeads];
-    __shared__ int s_last;
+    __shared__ float4 s_sum[kGroups][kItems];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c0 = blockIdx.x, ctas = gridDim.x;
-    if (tid == 0) s_last = ctas - 1;
-    __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x;
+
+    const List<S::kKeys, S::kWarps> list(a, lane, gridDim.x);
+    const int64_t hi = list.even_begin(c0 + int64_t{1});
+    bool mine = !list.whole && c0 < static_cast<int>(list.ctas) && hi < list.total;
+    Cursor<S::kKeys> cut = {};
+    if (mine) cut = list.find(a, hi);
+    if (cut.t == 0 || hi - cut.t < list.even_begin(c0)) mine = false;  // not cut, or begun before
+    if (!mine) {
+        // the kernels after this one count on the first having ended when this one has
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int parts = list.even_piece_of(hi - cut.t + cut.tiles - 1) - c0 + 1;
+    const UnitRows rows(a, cut.b, cut.u, kHeads);
     // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
     auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
-    const CutMeta first = a.ws.meta[c0 * 2 + 1];
-    // the first 32 parts' maxima and sums, before it is known how many there are
-    constexpr int kRowsOfWarp = kHeads / (kJoinThreads / 32);
+    auto ml_at = [&](int i, int row) {
+        return *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
+    };
+    const int group = tid / kItems;                                  // 0 where a thread has turns
+    auto sums_at = [&](int i, int turn) {
+        const int item = (tid + turn * kJoinThreads) % kItems;
+        return *reinterpret_cast<const float4 *>(
+            a.ws.cut + (slot(i) * kHeads + item / kQuads) * kD + blockIdx.y * 64 + item % kQuads * 4);
+    };
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float2 ml[kRowsOfWarp];
 #pragma unroll
     for (int k = 0; k < kRowsOfWarp; ++k)
-        if (c0 + lane < ctas)
-            ml[k] = *reinterpret_cast<const float2 *>(
-                a.ws.ml + (slot(lane) * kHeads + warp + k * (kJoinThreads / 32)) * 2);
-    // the last part's CTA: the next one whose slot 0 ends its unit
-    const int c = c0 + 1 + tid;
-    if (c < ctas) {
-        const CutMeta next = a.ws.meta[c * 2];
-        if (next.b >= 0 && next.ends) atomicMin(&s_last, c);
-    }
-    __syncthreads();
-    if (first.b < 0) return;
-    const int parts = s_last - c0 + 1;
-    const UnitRows rows(a, first.b, first.u, kHeads);
+        if (lane < parts) ml[k] = ml_at(lane, warp + k * (kJoinThreads / 32));
+    // (rows past the group's heads are read like the others and not written)
+    float4 y[kTurns][kAhead];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k)
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (group + j * kGroups < parts) y[k][j] = sums_at(group + j * kGroups, k);
 #pragma unroll
     for (int k = 0; k < kRowsOfWarp; ++k) {
         const int row = warp + k * (kJoinThreads / 32);
         if (row >= rows.rows) break;
-        auto at = [&](int i) {
-            return i == lane ? ml[k]
-                             : *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
-        };
-        float mm = -INFINITY, ll = 0.f;
-        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, at(i).x);
+        float mm = lane < parts ? ml[k].x : -INFINITY, ll = 0.f;
+        for (int i = lane + 32; i < parts; i += 32) mm = fmaxf(mm, ml_at(i, row).x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
         const float ref = mm == -INFINITY ? 0.f : mm;
         for (int i = lane; i < parts; i += 32) {
-            const float2 x = at(i);
+            const float2 x = i == lane ? ml[k] : ml_at(i, row);
             const float w = ex2(x.x - ref);
             s_w[i][row] = w;
             ll += w * x.y;
@@ -987,61 +1057,54 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
         if (lane == 0 && blockIdx.y == 0) write_lse(a, rows.out_row + row, mm, ll);
     }
     __syncthreads();
-    auto sum = [&](int item, int group) {
-        const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int item = (tid + k * kJoinThreads) % kItems, row = item / kQuads;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](int i, float4 v) {
+            const float w = s_w[i][row];
+            x.x += w * v.x;
+            x.y += w * v.y;
+            x.z += w * v.z;
+            x.w += w * v.w;
+        };
         if (row < rows.rows) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (group + j * kGroups < parts) add(group + j * kGroups, y[k][j]);
 #pragma unroll 8
-            for (int i = group; i < parts; i += kGroups) {
-                const float w = s_w[i][row];
-                const float4 y = *reinterpret_cast<const float4 *>(a.ws.cut + (slot(i) * kHeads + row) * kD + d);
-                x.x += w * y.x;
-                x.y += w * y.y;
-                x.z += w * y.z;
-                x.w += w * y.w;
+            for (int i = group + kAhead * kGroups; i < parts; i += kGroups) add(i, sums_at(i, k));
+        }
+        if constexpr (kGroups > 1) {
+            s_sum[group][item] = x;
+            __syncthreads();
+            if (group > 0) return;
+#pragma unroll
+            for (int i = 1; i < kGroups; ++i) {
+                const float4 v = s_sum[i][item];
+                x.x += v.x;
+                x.y += v.y;
+                x.z += v.z;
+                x.w += v.w;
             }
         }
-        return x;
-    };
-    auto out = [&](int item, float4 x) {
-        const int row = item / kQuads, d = blockIdx.y * 64 + item % kQuads * 4;
-        if (row < rows.rows) write_out(a, (rows.out_row + row) * kD + d, x);
-    };
-    if constexpr (kGroups > 1) {
-        static_assert(kGroups * kItems == kJoinThreads, "a thread to an item and group");
-        __shared__ float4 s_sum[kGroups][kItems];
-        const int item = tid % kItems, group = tid / kItems;
-        float4 x = sum(item, group);
-        s_sum[group][item] = x;
-        __syncthreads();
-        if (group > 0) return;
-#pragma unroll
-        for (int i = 1; i < kGroups; ++i) {
-            const float4 y = s_sum[i][item];
-            x.x += y.x;
-            x.y += y.y;
-            x.z += y.z;
-            x.w += y.w;
-        }
-        out(item, x);
-    } else {
-        for (int item = tid; item < kItems; item += kJoinThreads) out(item, sum(item, 0));
+        if (row < rows.rows)
+            write_out(a, (rows.out_row + row) * kD + blockIdx.y * 64 + item % kQuads * 4, x);
     }
 }
 
 template <class S>
-cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
+cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
     constexpr int kSmem = S::kWarps * S::kRing;
     const int page_size = static_cast<int>(a.cache.page.d);
     auto kern = page_size % S::kKeys == 0 ? paged_decode_kernel<S, true> : paged_decode_kernel<S, false>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSmem);
     if (e != cudaSuccess) return e;
-    // Whole units to a CTA where a unit is at most two tiles to a warp: then a CTA's
-    // load is uneven by less than what the second kernel would cost.
-    a.whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
+    // a table without room for longer units: the kernel cuts none (see List)
+    const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
     kern<<<ctas, S::kWarps * 32, kSmem, s>>>(a);
     const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess || a.whole) return e1;
+    if (e1 != cudaSuccess || whole) return e1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1051,7 +1114,7 @@ cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<S::kD, S::kHeads>, a);
+    return cudaLaunchKernelEx(&cfg, join_kernel<S>, a);
 }
 
 template <int kD>
