@@ -4,9 +4,12 @@
 //   (8-bit: e4m3(x / scale[h]), the fp32 quotient rounded to nearest)
 //
 // A copy: HBM-bound, 4 (or 3) bytes moved per value.  A thread moves 16-byte
-// pieces of the flattened [token, head, channel] rows, four of them so that the
-// loads overlap; neighbouring threads move neighbouring pieces, so that both
-// sides are whole 32-byte sectors in any layout.
+// pieces of the flattened [token, head, channel] rows; neighbouring threads move
+// neighbouring pieces, so that both sides are whole 32-byte sectors in any
+// layout.  Two pieces to a thread overlap their loads (16384 tokens of 8 heads of
+// 128, bf16: 21.5 us, 92 % of HBM; 23.3 with one, 21.6 with four); an 8-bit piece
+// is two loads already (9001 tokens of 4 heads of 256: 10.2 us with one, 11.0
+// with two).  Both sides are streamed past L2's other contents.
 #include <cuda_fp8.h>
 
 #include "kda_internal.cuh"
@@ -16,7 +19,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;
+template <bool kFp8>
+constexpr int kUnits = kFp8 ? 1 : 2;
 
 // x / y, y a positive normal scale with reciprocal r: one correction with the
 // exact remainder rounds the quotient correctly (Markstein, IBM J. Res. Dev.
@@ -53,15 +57,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
     uint8_t *dst = is_v ? cache.v : cache.k;
     const float *scales = is_v ? cache.v_scale : cache.k_scale;
 
-    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnits);
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnits<kFp8>);
     const int64_t n0 = u0 / row.d;
     const uint32_t r0 = static_cast<uint32_t>(u0 - n0 * row.d);
 
-    uint4 val[kUnits][kFp8 ? 2 : 1];
-    int slot[kUnits];
-    int head[kUnits], dim[kUnits];
+    uint4 val[kUnits<kFp8>][kFp8 ? 2 : 1];
+    int slot[kUnits<kFp8>];
+    int head[kUnits<kFp8>], dim[kUnits<kFp8>];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
+    for (int i = 0; i < kUnits<kFp8>; ++i) {
         uint32_t dn, u;
         row.divmod(r0 + threadIdx.x + i * kThreads, dn, u);
         const int64_t n = n0 + dn;
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
         }
     }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
+    for (int i = 0; i < kUnits<kFp8>; ++i) {
         if (slot[i] < 0) continue;
         uint32_t p, r;
         cache.page.divmod(static_cast<uint32_t>(slot[i]), p, r);
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
         } else {
             out = val[i][0];
         }
-        *reinterpret_cast<uint4 *>(to) = out;
+        __stcs(reinterpret_cast<uint4 *>(to), out);
     }
 }
 
@@ -109,7 +113,8 @@ cudaError_t launch_paged_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v,
                                 const int32_t *slot_map, int64_t N, const PagedView &cache,
                                 unsigned int *err, cudaStream_t s) {
     const uint32_t units = static_cast<uint32_t>(cache.heads) * cache.head_dim / (cache.fp8 ? 16 : 8);
-    const int64_t ctas = (N * units + kThreads * kUnits - 1) / (kThreads * kUnits);
+    const int per_cta = kThreads * (cache.fp8 ? kUnits<true> : kUnits<false>);
+    const int64_t ctas = (N * units + per_cta - 1) / per_cta;
     int dim_shift = 0;
     while ((1 << dim_shift) < cache.head_dim) ++dim_shift;
     const dim3 grid(static_cast<unsigned>(ctas), 2);

@@ -1,1140 +1,15 @@
-// kda_paged_decode.cu -- softmax attention of one new token per sequence over a
-// paged key-value cache.
-//
-//   s_j = scale <q, k_j>,  m = max_j s_j,  l = sum_j e^{s_j - m}
-//   o = sum_j e^{s_j - m} v_j / l,  lse = m + log l
-//
-// and over any partition of the keys, from the parts' (m_i, l_i, a_i) with
-// a_i = sum e^{s_j - m_i} v_j:  m = max m_i,  l = sum e^{m_i - m} l_i,
-// o = sum e^{m_i - m} a_i / l.  Powers of two throughout: the scores carry log2 e.
-//
-// Bound: every key and value is read once, 4 G flops for the 2 (or 4) bytes of
-// a value at G query heads to a key head: HBM up to G = 100.  So what matters is
-// that every SM has copies in flight from the first microsecond to the last,
-// whatever the lengths, and that a warp's instructions for a tile take less time
-// than its copy.
-//
-// Split.  A unit is (sequence, key head, group of up to 16 query heads); its keys
-// are cut in tiles of 4 KB of keys and 4 KB of values (8 KB each at 256 channels
-// in bf16).  The tiles of all units form one list; each CTA takes an equal,
-// contiguous piece of it and each warp an equal part of that: long sequences are
-// cut, short ones share a warp.  A warp's part ends in at most two cut units;
-// their parts are joined within the CTA through shared memory, and what is cut
-// between CTAs by a second, small kernel that is launched with the first and
-// waits for it (programmatic dependent launch).  Where the block table has no
-// room for long sequences, the pieces are moved to the units' ends instead, and
-// the second kernel is not launched.
-//
-// A warp copies its own tiles, by 16-byte cp.async into its own ring of tile
-// halves (no barrier between warps); the page numbers of a tile are read one tile
-// earlier.  Rows are swizzled (16-byte pieces xor row) so that ldmatrix meets no
-// bank twice.  The products run on the warp's matrix instructions with the keys
-// (then the channels) as the 16 rows and 8 query heads as the columns:
-// S^T = K Q^T, O^T += V^T P^T, so that no row of the operand that is loaded is
-// padding; the weights turn from accumulator to right operand by transposing
-// 8 x 8 blocks in registers (movmatrix).  (tcgen05.mma takes 64 or 128 rows from
-// shared memory and would need the weights there; the tensor pipe does not bind
-// here: 21 % busy at 5.3 TB/s with twice the products of this form.)
-//
-// Precision: scores, maxima, sums and outputs in fp32.  For the product with the
-// values a weight is two bf16 numbers, 16 bits together: one would leave up to
-// 2^-8 of every weight, as much as the rounding of a bf16 output and far more
-// than an fp32 one may lose, and the second product is free here (see Bound).  An
-// 8-bit cache is widened to fp16, which holds every e4m3 value; the queries are
-// scaled by a power of two for each row, so that fp16 holds their bf16 values
-// too, and the weights are two fp16 numbers, times 2^15 to keep small ones normal.
-#include <cfloat>
-
-#include <cuda_fp16.h>
-
-#include "kda_internal.cuh"
-#include "kda_paged.cuh"
-#include "kda_sm100.cuh"
+// kda_paged_decode.cu -- the launcher of the one-token attention over a paged
+// cache (kernels: kda_paged_decode.cuh), and its kernels for 128 channels.
+#include "kda_paged_decode.cuh"
 
 namespace kda {
-namespace {
-
-constexpr int kMaxCtas = 160;  // at most the join kernel's threads
-constexpr int kMaxWarps = 16;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-constexpr int max_of(int a, int b) { return a > b ? a : b; }
-
-// kN: groups of 8 query heads in a unit.  Warps: as many as the accumulators
-// (kD / 4 * kN registers a lane) leave registers for, so that one warp's
-// instructions overlap another's waits.
-template <int kD_, bool kFp8_, int kN_>
-struct Shape {
-    static constexpr int kD = kD_, kN = kN_;
-    static constexpr bool kFp8 = kFp8_;
-    static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
-    // keys of a tile: 4 KB of them, 2 KB where 32 heads' scores would fill the registers
-    static constexpr int kKeys = max_of(16, (kN == 4 ? 2048 : 4096) / kRowBytes);
-    static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-        static constexpr int kWarps = kN == 4 || kD == 256 ? 8 : 12;
-    // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
-    // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
-    static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
-    static constexpr int kHeads = 8 * kN;
-    static constexpr int kPitch = kD + 4;                                  // floats of a part's row
-    // the ring takes the warp's last part in the end
-    static constexpr int kRing = max_of(kSlots * kHalf, (kHeads * kPitch * 4 + 1023) / 1024 * 1024);
-    static_assert(kSlots >= 3 && kSlots <= 7, "the masks' ring holds the tiles in flight");
-};
-
-// What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
-// in slot 0, its last unit's (begun here, not finished) in slot 1.
-struct Layout {      // of the workspace
-    float *ml;       // [ctas][2][heads][2]
-    float *cut;      // [ctas][2][heads][D]
-    float *head;     // [ctas][warps][heads][D]: a warp's first part, until its CTA joins it
-};
-
-inline size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
-
-inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
-    const size_t part = static_cast<size_t>(heads) * head_dim * 4;
-    const size_t cut = align256(static_cast<size_t>(kMaxCtas) * 2 * heads * 2 * 4);
-    const size_t head = align256(cut + kMaxCtas * 2 * part);
-    if (l != nullptr) {
-        l->ml = reinterpret_cast<float *>(base);
-        l->cut = reinterpret_cast<float *>(base + cut);
-        l->head = reinterpret_cast<float *>(base + head);
-    }
-    return head + kMaxCtas * kMaxWarps * part;
-}
-
-// Query heads of a unit: all of a group of up to 32 (16 at 256 channels), in 8, 16
-// or 32, so that its keys are read once.
-inline int unit_heads(int group, int head_dim) {
-    return group <= 8 ? 8 : group <= 16 || head_dim == 256 ? 16 : 32;
-}
-
-struct Args {
-    const __nv_bfloat16 *q;
-    int64_t q_row_stride;
-    PagedView cache;
-    const int32_t *block_table;
-    int max_pages;
-    const int32_t *seq_lens;
-    int B, q_heads, group, head_tiles;
-    float scale;
-    void *o;
-    int o_bf16;
-    float *lse;
-    Layout ws;
-    unsigned int *err;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Volatile: they stay between the wait for a tile and the copy that replaces it.
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-// The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), bf16 or fp16 operands.
-template <bool kF16>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-    if constexpr (kF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two e4m3 values as two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-    uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
-    return y;
-}
-
-template <bool kF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (kF16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-template <bool kF16>
-__device__ __forceinline__ float2 unpack2(uint32_t x) {
-    if constexpr (kF16) return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-    else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x));
-}
-
-// Byte offset of 16-byte piece `c` of row `r` of a tile half.
-template <int kRowBytes>
-__device__ __forceinline__ uint32_t piece(uint32_t r, uint32_t c) {
-    if constexpr (kRowBytes >= 128) return r * kRowBytes + ((c ^ (r & 7)) << 4);
-    else return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r >> 1) & 7)) << 4);
-}
-
-// n / d, n >= 0, d > 0: by 32 bits where they hold n (a 64-bit division is a call).
-__device__ __forceinline__ int64_t div64(int64_t n, uint32_t d) {
-    if (n >> 32 == 0) return static_cast<uint32_t>(n) / d;
-    return static_cast<uint64_t>(n) / d;
-}
-
-__device__ __forceinline__ int valid_len(const Args &a, int b) {
-    const int n = __ldg(a.seq_lens + b);
-    return n < 0 || n > static_cast<int64_t>(a.max_pages) * a.cache.page.d ? 0 : n;
-}
-
-// A place in the list of tiles.
-template <int kKeys>
-struct Cursor {
-    int b, u, t;    // sequence, unit of the sequence, tile of the unit
-    int len, tiles;
-
-    __device__ __forceinline__ void set_len(int n) {
-        len = n;
-        tiles = static_cast<int>((static_cast<uint32_t>(n) + kKeys - 1) / kKeys);
-    }
-    __device__ __forceinline__ void next(const Args &a, int units) {
-        if (++t < tiles) return;
-        t = 0;
-        if (++u < units) return;
-        u = 0;
-        do {
-            if (++b >= a.B) {
-                tiles = len = 0;
-                return;
-            }
-            set_len(valid_len(a, b));
-        } while (tiles == 0);
-    }
-};
-
-// A part of a unit as a warp leaves it for its CTA.
-struct Part {
-    int b, u;        // b = -1: none
-    int starts, ends;
-    int in_global;   // its sums are in the workspace (else in the warp's ring)
-};
-
-// A part's sums, and the parts of one unit, when a CTA joins them.
-struct PartAt {
-    const float *sums;  // [heads][pitch], shared or global
-    int pitch, part, run;
-};
-struct Run {
-    int begin, end;     // parts
-    int rows, whole;    // query heads; the unit's first and last keys are among them
-    int64_t out_row, slot;
-};
-
-// Where a unit's queries and outputs are.
-struct UnitRows {
-    int h, rows;      // key head; query heads
-    int64_t out_row;  // the first of them in [B, q_heads]
-
-    __device__ __forceinline__ UnitRows(const Args &a, int b, int u, int heads) {
-        h = u / a.head_tiles;
-        const int row0 = (u - h * a.head_tiles) * heads;
-        rows = min(heads, a.group - row0);
-        out_row = static_cast<int64_t>(b) * a.q_heads + h * a.group + row0;
-    }
-};
-
-__device__ __forceinline__ void write_out(const Args &a, int64_t at, float4 x) {
-    if (a.o_bf16) {
-        uint2 w;
-        w.x = pack2<false>(x.x, x.y);
-        w.y = pack2<false>(x.z, x.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at) = w;
-    } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) = x;
-    }
-}
-
-__device__ __forceinline__ void write_lse(const Args &a, int64_t row, float m, float l) {
-    if (a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-// 16 bytes to shared memory, or zeros (nothing is read then).  Evicted from L2
-// first: a key is read once, and what else is there (weights, code) is not.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool real) {
-    asm volatile("{\n\t.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
-                 "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, pol;\n\t}" ::"r"(dst),
-                 "l"(src), "r"(real ? 16 : 0)
-                 : "memory");
-}
-
-// The tiles that a warp copies: its part of the list, one half at a time.
-// kOnePage: a tile never spans two pages.
-template <class S, bool kOnePage>
-struct Copier {
-    static constexpr int kKeys = S::kKeys, kPieces = S::kRowBytes / 16;
-    static constexpr int kLaneRows = !kOnePage && kKeys > 32 ? 2 : 1;
-    static constexpr int kCopies = S::kHalf / 512;           // 16-byte copies of a lane
-    Cursor<kKeys> at;
-    int64_t left;                                            // tiles to begin
-    int page[kLaneRows];                                     // of this lane's rows of tile `at`
-    bool held[kLaneRows];                                    // the row is a key of the sequence
-    uint32_t in_page[kLaneRows];
-    // the tile whose values are next: where its rows are
-    int64_t off[kLaneRows];                                  // kOnePage: of row 0
-    int rows;                                                // rows to copy, the rest 0; -1: no tile
-
-    __device__ __forceinline__ void read_pages(const Args &a, int lane) {
-#pragma unroll
-        for (int i = 0; i < kLaneRows; ++i) {
-            const uint32_t r = kOnePage ? 0 : lane + 32 * i;
-            const uint32_t j = static_cast<uint32_t>(at.t) * kKeys + r;
-            uint32_t idx;
-            a.cache.page.divmod(j, idx, in_page[i]);
-            held[i] = r < kKeys && j < static_cast<uint32_t>(at.len);
-            page[i] = -1;
-            if (held[i])
-                page[i] = __ldg(a.block_table + static_cast<int64_t>(at.b) * a.max_pages + idx);
-        }
-    }
-
-    __device__ __forceinline__ void begin(const Args &a, const Cursor<kKeys> &c, int64_t tiles,
-                                          int lane) {
-        at = c;
-        left = tiles;
-        read_pages(a, lane);
-    }
-
-    // Copies the keys of the next tile to the slot; mask: which of its rows are keys.
-    __device__ __forceinline__ void keys(const Args &a, int units, int lane, uint32_t to,
-                                         uint64_t *mask) {
-        rows = -1;
-        if (left > 0) {
-            uint64_t valid = 0;
-            const int64_t h = (a.head_tiles == 1 ? at.u : at.u / a.head_tiles) * a.cache.head_stride;
-            if constexpr (kOnePage) {
-                const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
-                if (!ok) record_device_error(a.err, kDevInvalidArg);
-                rows = ok ? min(kKeys, at.len - at.t * kKeys) : 0;
-                off[0] = ok ? page[0] * a.cache.page_stride + in_page[0] * a.cache.token_stride + h : 0;
-                valid = rows == 64 ? ~uint64_t{0} : (uint64_t{1} << rows) - 1;
-            } else {
-                rows = kKeys;
-#pragma unroll
-                for (int i = 0; i < kLaneRows; ++i) {
-                    const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
-                    if (!ok && held[i]) record_device_error(a.err, kDevInvalidArg);
-                    off[i] = ok ? page[i] * a.cache.page_stride + in_page[i] * a.cache.token_stride + h
-                                : -1;
-                    valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * i);
-                }
-            }
-            if (lane == 0) *mask = valid;
-            copy(a, a.cache.k, lane, to);
-            at.next(a, units);
-            if (--left > 0) read_pages(a, lane);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-
-    // Copies the values of the tile whose keys were last.
-    __device__ __forceinline__ void values(const Args &a, int lane, uint32_t to) {
-        if (rows >= 0) copy(a, a.cache.v, lane, to);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-
-    __device__ __forceinline__ void copy(const Args &a, const uint8_t *src, int lane, uint32_t to) {
-        const uint32_t r0 = lane / kPieces, c = lane % kPieces;
-        if constexpr (kOnePage) {
-            constexpr uint32_t kStep = 32 / kPieces;     // rows of one copy of the warp
-            const uint8_t *p = src + off[0] + r0 * a.cache.token_stride + c * 16;
-            const int64_t step = kStep * a.cache.token_stride;
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int r = i * kStep + r0;
-                copy16(to + piece<S::kRowBytes>(r, c), r < rows ? p : src, r < rows);
-                p += step;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const uint32_t r = i * 32 / kPieces + r0;
-                const int64_t o = __shfl_sync(
-                    0xffffffffu, off[kLaneRows > 1 ? (i * 32 / kPieces) / 32 : 0], r & 31);
-                copy16(to + piece<S::kRowBytes>(r, c), src + (o < 0 ? 0 : o) + c * 16, o >= 0);
-            }
-        }
-    }
-};
-
-// The place of position pos < the total of the list; called by a whole warp, whose lanes
-// hold the sequences from b_lo on, at positions before .. after - 1.  Not inlined: it is
-// wanted three times, and short calls wait for instructions more than for anything.
-template <int kKeys>
-__device__ __noinline__ Cursor<kKeys> find_tile(const Args &a, int units, int64_t pos, int b_lo,
-                                                int64_t before, int64_t after) {
-    Cursor<kKeys> c;
-    c.b = c.u = c.t = c.len = 0;
-    const bool owner = pos >= before && pos < after;
-    if (owner) {
-        int64_t left = pos - before;
-        for (c.b = b_lo;; ++c.b) {
-            c.set_len(valid_len(a, c.b));
-            const int64_t here = static_cast<int64_t>(c.tiles) * units;
-            if (left < here) break;
-            left -= here;
-        }
-        c.u = static_cast<int>(div64(left, c.tiles));
-        c.t = static_cast<int>(left - static_cast<int64_t>(c.u) * c.tiles);
-    }
-    const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
-    c.b = __shfl_sync(0xffffffffu, c.b, src);
-    c.u = __shfl_sync(0xffffffffu, c.u, src);
-    c.t = __shfl_sync(0xffffffffu, c.t, src);
-    c.set_len(__shfl_sync(0xffffffffu, c.len, src));
-    return c;
-}
-
-// The list of tiles and its pieces, as a warp sees it: every warp sums the lengths for
-// itself (they come out of L1 after the first), lane i over sequences
-// i ceil(B / 32) .. , so that no barrier precedes the first copy.
-template <int kKeys, int kWarps>
-struct List {
-    int64_t before, after;   // positions of the list in this lane's sequences
-    int64_t total, q, r;     // CTA i's piece: q positions, one more in the first r
-    int b_lo, units;
-    int filled, filled_before;  // sequences with keys: this lane's, and before them
-    uint32_t ctas;           // that have a piece
-    bool one_each, whole;    // pieces are units, or end where units end
-
-    static __device__ __forceinline__ uint32_t tiles_of(const Args &a, int b) {
-        return (static_cast<uint32_t>(valid_len(a, b)) + kKeys - 1) / kKeys;
-    }
-
-    __device__ __forceinline__ List(const Args &a, int lane, int grid) {
-        units = a.cache.heads * a.head_tiles;
-        const int chunk = (a.B + 31) / 32;
-        b_lo = min(a.B, lane * chunk);
-        const int b_hi = min(a.B, b_lo + chunk);
-        int64_t mine = 0;
-        uint32_t longest = 0;
-        filled = 0;
-#pragma unroll 4
-        for (int b = b_lo; b < b_hi; ++b) {
-            const uint32_t n = tiles_of(a, b);
-            mine += n;
-            filled += n > 0;
-            longest = max(longest, n);
-        }
-        before = mine;
-        filled_before = filled;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
-            const int y = __shfl_up_sync(0xffffffffu, filled_before, d);
-            if (lane >= d) {
-                before += x;
-                filled_before += y;
-            }
-        }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        total = __shfl_sync(0xffffffffu, before, 31) * units;
-        const int sequences = __shfl_sync(0xffffffffu, filled_before, 31);
-        filled_before -= filled;
-        before = (before - mine) * units;
-        after = before + mine * units;
-        // Whole units to a CTA where that makes no CTA's load larger by more than two tiles a
-        // warp (0.2 us a tile; joining between CTAs costs some 5 us, with its launch): one
-        // unit each where there are few, pieces moved back to a unit's start where units
-        // are short.
-        const int64_t all_units = static_cast<int64_t>(sequences) * units;
-        one_each = all_units <= grid && longest <= div64(total, grid) + 2 * kWarps;
-        whole = one_each || longest <= 2 * kWarps;
-        // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
-        // grid for longer lists
-        const int64_t want = whole ? all_units : static_cast<uint64_t>(total + kWarps - 1) / kWarps;
-        ctas = static_cast<uint32_t>(want < grid ? want : grid);
-        q = ctas == 0 ? 0 : div64(total, ctas);
-        r = total - q * ctas;
-    }
-
-    // The place of position pos < total; called by a whole warp.
-    __device__ __forceinline__ Cursor<kKeys> find(const Args &a, int64_t pos) const {
-        return find_tile<kKeys>(a, units, pos, b_lo, before, after);
-    }
-
-    // Where an even piece begins, and which holds a position (not `whole`).
-    __device__ __forceinline__ int64_t even_begin(int64_t cta) const { return cta * q + min(cta, r); }
-    __device__ __forceinline__ int even_piece_of(int64_t pos) const {
-        const int64_t longer = r * (q + 1);
-        return static_cast<int>(pos < longer ? div64(pos, static_cast<uint32_t>(q + 1))
-                                             : r + div64(pos - longer, static_cast<uint32_t>(q)));
-    }
-
-    // CTA `cta`'s piece, cta < ctas; called by a whole warp.
-    __device__ __forceinline__ void piece(const Args &a, uint32_t cta, int64_t &lo, int64_t &hi) const {
-        if (one_each) {
-            // unit `cta`: of the sequence before which there are `skip` with keys
-            const int skip = cta / units, u = cta - skip * units;
-            const bool owner = skip >= filled_before && skip < filled_before + filled;
-            if (owner) {
-                int left = skip - filled_before;
-                lo = before;
-                for (int b = b_lo;; ++b) {
-                    hi = tiles_of(a, b);
-                    if (hi > 0 && --left < 0) break;
-                    lo += hi * units;
-                }
-                lo += u * hi;
-                hi += lo;
-            }
-            const int src = 31 - __clz(__ballot_sync(0xffffffffu, owner));
-            lo = __shfl_sync(0xffffffffu, lo, src);
-            hi = __shfl_sync(0xffffffffu, hi, src);
-            return;
-        }
-        lo = even_begin(cta);
-        hi = even_begin(cta + int64_t{1});
-        if (whole) {
-            if (hi < total) hi -= find(a, hi).t;
-            lo -= find(a, lo).t;
-        }
-    }
-};
-
-template <class S, bool kOnePage>
-__global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const __grid_constant__ Args a) {
-    constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
-    constexpr bool kFp8 = S::kFp8, kF16 = S::kFp8;
-    constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kKeys = S::kKeys;
-    constexpr int kBlocks = kKeys / 16;   // score blocks of 16 keys
-    constexpr int kOT = kD / 16;          // output blocks of 16 channels
-    constexpr int kParts = 2 * kWarps;
-    constexpr float kUp = kF16 ? 15.f : 0.f;  // log2 of what the weights are multiplied by
-    static_assert(kParts <= 32, "a warp finds the runs");
-
-    extern __shared__ __align__(1024) uint8_t s_ring[];
-    __shared__ uint64_t s_valid[kWarps][4];
-    __shared__ Part s_part[kParts];
-    __shared__ float s_m[kParts][kHeads], s_l[kParts][kHeads], s_w[kParts][kHeads];
-    __shared__ Run s_run[kParts];
-    __shared__ PartAt s_at[kParts];
-    __shared__ int s_runs, s_parts;
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, tq = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (lane < 2) s_part[2 * warp + lane].b = -1;
-    __syncwarp();
-
-    const List<kKeys, kWarps> list(a, lane, gridDim.x);
-    const int units = list.units;
-    int64_t remaining = 0, begin = 0;  // this warp's tiles
-    int64_t paced = 0;                 // fours of tiles that every warp of the CTA has
-    if (blockIdx.x < list.ctas) {
-        int64_t lo, hi;
-        list.piece(a, blockIdx.x, lo, hi);
-        const int64_t per = static_cast<uint64_t>(hi - lo) / kWarps, more = hi - lo - per * kWarps;
-        begin = lo + warp * per + min(static_cast<int64_t>(warp), more);
-        remaining = per + (warp < more);
-        paced = per / 4;
-    }
-
-    // ---- a warp's part of the piece --------------------------------------------------------
-    if (remaining > 0) {
-        const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
-        Cursor<kKeys> cur = list.find(a, begin);
-        Copier<S, kOnePage> copier;
-        copier.begin(a, cur, remaining, lane);
-        int put = 0, copied = 0;  // the slot of the next half to copy; tiles begun
-        auto next_slot = [&](int s) { return s == S::kSlots - 1 ? 0 : s + 1; };
-        auto copy_keys = [&]() {
-            copier.keys(a, units, lane, ring + put * S::kHalf, &s_valid[warp][copied++ & 3]);
-            put = next_slot(put);
-        };
-        auto copy_values = [&]() {
-            copier.values(a, lane, ring + put * S::kHalf);
-            put = next_slot(put);
-        };
-        // kSlots - 1 halves ahead: with an odd number of slots the keys of a tile are
-        // replaced by keys, with an even number by values
-        constexpr bool kOdd = S::kSlots % 2 == 1;
-#pragma unroll 1
-        for (int i = 0; i < (S::kSlots - 1) / 2; ++i) {
-            copy_keys();
-            copy_values();
-        }
-        if (!kOdd) copy_keys();
-
-        uint32_t qf[kOT][kN][2];
-        float acc[kOT][kN][4], m[kN][2], l[kN][2], sc[kN][2];
-        int begun = cur.t;  // the part's first tile
-        int slot = 0, tile = 0;
-        bool fresh = true;
-        while (true) {
-            const UnitRows rows(a, cur.b, cur.u, kHeads);
-            if (fresh) {
-                // the unit's queries as the right operand (head 8 n + g); heads past the
-                // group are zero
-                fresh = false;
-                const __nv_bfloat16 *q = a.q + cur.b * a.q_row_stride +
-                                         (rows.out_row - static_cast<int64_t>(cur.b) * a.q_heads) * kD;
-                const float factor = a.scale * kLog2e *
-                                     (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + rows.h));
-                // a negative factor's sign goes to the queries; zero times a left-out key's
-                // -inf would be NaN
-                const float base = fmaxf(fabsf(factor), FLT_MIN);
-                const uint32_t sign = factor < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-                for (int n = 0; n < kN; ++n) {
-                    const bool real = 8 * n + g < rows.rows;
-                    const __nv_bfloat16 *x = q + (8 * n + g) * kD;
-                    if constexpr (kFp8) {
-                        // channels 16 c + 4 tq .. + 3, as the widened keys have them
-                        float top = 0.f;
-#pragma unroll
-                        for (int c = 0; c < kOT; ++c) {
-                            uint2 z = make_uint2(0, 0);
-                            if (real) z = __ldg(reinterpret_cast<const uint2 *>(x + 16 * c + 4 * tq));
-                            qf[c][n][0] = z.x;
-                            qf[c][n][1] = z.y;
-                            const float2 u0 = unpack2<false>(z.x), u1 = unpack2<false>(z.y);
-                            top = fmaxf(fmaxf(top, fmaxf(fabsf(u0.x), fabsf(u0.y))),
-                                        fmaxf(fabsf(u1.x), fabsf(u1.y)));
-                        }
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        // 2^e puts the head's largest value in [2^13, 2^14); an infinite or
-                        // zero head is left as it is.  In two steps: 2^e itself may not be a
-                        // float.
-                        int e = 13 - (static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 127);
-                        if (!(top > 0.f) || isinf(top)) e = 0;
-                        const float f1 = exp2f(static_cast<float>(e / 2));
-                        const float f2 = exp2f(static_cast<float>(e - e / 2));
-#pragma unroll
-                        for (int c = 0; c < kOT; ++c)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float2 u = unpack2<false>(qf[c][n][i]);
-                                qf[c][n][i] = pack2<true>(u.x * f1 * f2, u.y * f1 * f2) ^ sign;
-                            }
-                        // the scores' columns are heads 2 tq, 2 tq + 1
-                        const float mine_sc = fmaxf(base / f1 / f2, FLT_MIN);
-                        sc[n][0] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq);
-                        sc[n][1] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq + 4);
-                    } else {
-                        sc[n][0] = sc[n][1] = base;
-#pragma unroll
-                        for (int c = 0; c < kOT; ++c)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                qf[c][n][i] = real ? __ldg(reinterpret_cast<const uint32_t *>(
-                                                         x + 16 * c + 8 * i + 2 * tq)) ^ sign
-                                                   : 0;
-                    }
-                    m[n][0] = m[n][1] = -INFINITY;
-                    l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-                    for (int d = 0; d < kOT; ++d)
-                        acc[d][n][0] = acc[d][n][1] = acc[d][n][2] = acc[d][n][3] = 0.f;
-                }
-                begun = cur.t;
-            }
-
-            // the warps of a CTA keep pace, four tiles at a time, as far as all have tiles:
-            // otherwise the last ends some 8 % after the first
-            if ((tile & 3) == 3 && --paced >= 0)
-                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-
-            // ---- scores: keys 16 k + g, + 8; heads 8 n + 2 tq, + 1
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
-            __syncwarp();  // the keys are in, and the half before them is read by every lane
-            if (kOdd) copy_keys();
-            else copy_values();
-            const uint32_t kt = ring + slot * S::kHalf;
-            slot = next_slot(slot);
-            float s[kBlocks][kN][4];
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-                for (int n = 0; n < kN; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
-#pragma unroll
-            for (int c = 0; c < kOT; c += kFp8 ? 2 : 1) {
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
-                    uint32_t r[4];
-                    // rows 0-7 and 8-15 of a piece of 16 bytes, then of the next
-                    ldsm4(r, kt + piece<S::kRowBytes>(16 * k + (lane & 15),
-                                                      (kFp8 ? c : 2 * c) + (lane >> 4)));
-                    if constexpr (kFp8) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t f[4] = {e4m3x2_to_f16x2(r[2 * i]), e4m3x2_to_f16x2(r[2 * i + 1]),
-                                                   e4m3x2_to_f16x2(r[2 * i] >> 16),
-                                                   e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
-#pragma unroll
-                            for (int n = 0; n < kN; ++n)
-                                mma<kF16>(s[k][n], f, qf[c + i][n][0], qf[c + i][n][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < kN; ++n) mma<kF16>(s[k][n], r, qf[c][n][0], qf[c][n][1]);
-                    }
-                }
-            }
-            const uint64_t valid = s_valid[warp][tile & 3];
-            ++tile;
-            constexpr uint64_t kAll = kKeys == 64 ? ~uint64_t{0} : (uint64_t{1} << (kKeys & 63)) - 1;
-            if (valid != kAll) {
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-                    for (int n = 0; n < kN; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!(valid >> (16 * k + g + 8 * (i >> 1)) & 1)) s[k][n][i] = -INFINITY;
-            }
-            // m: the largest product so far, unscaled (the scale is not negative); a weight is
-            // 2^(s sc - ref), times 2^15 where it is to be fp16
-            float ref[kN][2];
-            bool grew = false;
-            float shrink[kN][2];
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float mt = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) mt = fmaxf(mt, fmaxf(s[k][n][i], s[k][n][i + 2]));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    const float mn = fmaxf(m[n][i], mt);
-                    ref[n][i] = mn == -INFINITY ? 0.f : mn * sc[n][i];
-                    shrink[n][i] = ex2(m[n][i] * sc[n][i] - ref[n][i]);
-                    grew |= mn > m[n][i];
-                    m[n][i] = mn;
-                    ref[n][i] -= kUp;
-                }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int n = 0; n < kN; ++n) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) l[n][i] *= shrink[n][i];
-#pragma unroll
-                    for (int d = 0; d < kOT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[d][n][i] *= shrink[n][i & 1];
-                }
-            }
-            // ---- weights, in two words, as the right operand
-            uint32_t p[kBlocks][kN][2], p2[kBlocks][kN][2];
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float x = ex2(fmaf(s[k][n][2 * j], sc[n][0], -ref[n][0]));
-                        const float y = ex2(fmaf(s[k][n][2 * j + 1], sc[n][1], -ref[n][1]));
-                        l[n][0] += x;
-                        l[n][1] += y;
-                        const uint32_t w = pack2<kF16>(x, y);
-                        const float2 first = unpack2<kF16>(w);
-                        p[k][n][j] = transpose8(w);
-                        p2[k][n][j] = transpose8(pack2<kF16>(x - first.x, y - first.y));
-                    }
-
-            // ---- outputs: channels g, g + 8 of 16 d (8-bit: 2 g, 2 g + 1)
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kSlots - 2) : "memory");
-            __syncwarp();  // the values are in, and the keys are read by every lane
-            if (kOdd) copy_values();
-            else copy_keys();
-            const uint32_t vt = ring + slot * S::kHalf;
-            slot = next_slot(slot);
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-#pragma unroll
-                for (int d = 0; d < kOT; d += kFp8 ? 2 : 1) {
-                    uint32_t r[4];
-                    if constexpr (kFp8) {
-                        ldsm4_trans(r, vt + piece<S::kRowBytes>(16 * k + (lane & 15), d + (lane >> 4)));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            // bytes: channels 2 g, 2 g + 1 of key 2 tq, then of key 2 tq + 1
-                            const uint32_t x = __byte_perm(r[2 * i], 0, 0x3120);
-                            const uint32_t y = __byte_perm(r[2 * i + 1], 0, 0x3120);
-                            const uint32_t f[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16),
-                                                   e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
-#pragma unroll
-                            for (int n = 0; n < kN; ++n) {
-                                mma<kF16>(acc[d + i][n], f, p[k][n][0], p[k][n][1]);
-                                mma<kF16>(acc[d + i][n], f, p2[k][n][0], p2[k][n][1]);
-                            }
-                        }
-                    } else {
-                        // pieces 2 d and 2 d + 1 of keys 0-7, then of keys 8-15
-                        ldsm4_trans(r, vt + piece<S::kRowBytes>(16 * k + (lane & 7) + ((lane >> 4) << 3),
-                                                                2 * d + ((lane >> 3) & 1)));
-#pragma unroll
-                        for (int n = 0; n < kN; ++n) {
-                            mma<kF16>(acc[d][n], r, p[k][n][0], p[k][n][1]);
-                            mma<kF16>(acc[d][n], r, p2[k][n][0], p2[k][n][1]);
-                        }
-                    }
-                }
-            }
-
-            // ---- the end of a unit, or of the warp's part
-            --remaining;
-            const bool ends = cur.t == cur.tiles - 1;
-            if (ends || remaining == 0) {
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
-                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
-                        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
-                        m[n][i] = m[n][i] == -INFINITY ? m[n][i] : m[n][i] * sc[n][i] - kUp;
-                    }
-                const bool whole = ends && begun == 0;
-                float *part = nullptr;
-                int pitch = kD;
-                if (!whole) {
-                    const int at = 2 * warp + (remaining == 0 ? 1 : 0);
-                    if (remaining == 0) {
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        __syncwarp();  // the ring is free: the part goes there
-                        part = reinterpret_cast<float *>(s_ring + warp * S::kRing);
-                        pitch = S::kPitch;
-                    } else {
-                        part = a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kHeads * kD;
-                    }
-                    if (g == 0) {
-#pragma unroll
-                        for (int n = 0; n < kN; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                s_m[at][8 * n + 2 * tq + i] = m[n][i];
-                                s_l[at][8 * n + 2 * tq + i] = l[n][i];
-                            }
-                    }
-                    if (lane == 0) {
-                        s_part[at].b = cur.b;
-                        s_part[at].u = cur.u;
-                        s_part[at].starts = begun == 0;
-                        s_part[at].ends = ends;
-                        s_part[at].in_global = remaining != 0;
-                    }
-                }
-                const float vs = a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + rows.h);
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = 8 * n + 2 * tq + i;
-                        if (row >= rows.rows) continue;
-                        const float f = whole ? (l[n][i] == 0.f ? 0.f : vs / l[n][i]) : vs;
-                        if (whole && g == 0) write_lse(a, rows.out_row + row, m[n][i], l[n][i]);
-#pragma unroll
-                        for (int d = 0; d < kOT; ++d) {
-                            const float x = acc[d][n][i] * f, y = acc[d][n][i + 2] * f;
-                            const int dx = 16 * d + (kFp8 ? 2 * g : g), dy = kFp8 ? dx + 1 : dx + 8;
-                            if (!whole) {
-                                part[row * pitch + dx] = x;
-                                part[row * pitch + dy] = y;
-                            } else if (a.o_bf16) {
-                                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (rows.out_row + row) * kD;
-                                o[dx] = __float2bfloat16_rn(x);
-                                o[dy] = __float2bfloat16_rn(y);
-                            } else {
-                                float *o = static_cast<float *>(a.o) + (rows.out_row + row) * kD;
-                                o[dx] = x;
-                                o[dy] = y;
-                            }
-                        }
-                    }
-                fresh = true;
-                if (remaining == 0) break;
-            }
-            cur.next(a, units);
-        }
-    }
-    __syncthreads();
-
-    // ---- joining the CTA's parts: the parts there are, and the runs of one unit among
-    // them, in the list's order
-    if (warp == 0) {
-        Part part;
-        part.b = -1;
-        if (lane < kParts) part = s_part[lane];
-        const uint32_t valid = __ballot_sync(0xffffffffu, part.b >= 0);
-        const uint32_t below = valid & ((1u << lane) - 1);
-        const int src = below == 0 ? 0 : 31 - __clz(below);
-        const int prev_b = __shfl_sync(0xffffffffu, part.b, src);
-        const int prev_u = __shfl_sync(0xffffffffu, part.u, src);
-        const bool first = part.b >= 0 && (below == 0 || prev_b != part.b || prev_u != part.u);
-        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-        const uint32_t later = lane == 31 ? 0 : firsts >> (lane + 1) << (lane + 1);
-        const uint32_t run = later == 0 ? valid : valid & ((later & -later) - 1);  // up to its end
-        const int ends = __shfl_sync(0xffffffffu, part.ends, run == 0 ? 0 : 31 - __clz(run));
-        const int at = __popc(below), r = __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
-        if (part.b >= 0) {
-            PartAt &x = s_at[at];
-            x.part = lane;
-            x.run = r;
-            x.pitch = part.in_global ? kD : S::kPitch;
-            x.sums = part.in_global
-                         ? a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + (lane >> 1)) * kHeads * kD
-                         : reinterpret_cast<const float *>(s_ring + (lane >> 1) * S::kRing);
-        }
-        if (first) {
-            const UnitRows rows(a, part.b, part.u, kHeads);
-            Run &x = s_run[r];
-            x.begin = at;
-            x.end = __popc(run);
-            x.rows = rows.rows;
-            x.whole = part.starts && ends;
-            x.out_row = rows.out_row;
-            x.slot = static_cast<int64_t>(blockIdx.x) * 2 + (part.starts ? 1 : 0);
-        }
-        if (lane == 0) {
-            s_runs = __popc(firsts);
-            s_parts = __popc(valid);
-        }
-    }
-    __syncthreads();
-    // the parts' weights, for each head; a whole unit's hold 1 / l too
-    for (int i = tid; i < s_parts * kHeads; i += kThreads) {
-        const int e = i / kHeads, row = i % kHeads;
-        const Run run = s_run[s_at[e].run];
-        if (row >= run.rows) continue;
-        float mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-        for (int j = run.begin; j < run.end; ++j) mm = fmaxf(mm, s_m[s_at[j].part][row]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-        for (int j = run.begin; j < run.end; ++j)
-            ll += ex2(s_m[s_at[j].part][row] - ref) * s_l[s_at[j].part][row];
-        float w = ex2(s_m[s_at[e].part][row] - ref);
-        if (run.whole) w = ll == 0.f ? 0.f : w / ll;
-        s_w[e][row] = w;
-        if (e != run.begin) continue;
-        if (run.whole) write_lse(a, run.out_row + row, mm, ll);
-        else *reinterpret_cast<float2 *>(a.ws.ml + (run.slot * kHeads + row) * 2) = make_float2(mm, ll);
-    }
-    __syncthreads();
-    constexpr int kPer = kHeads * (kD / 4);
-    for (int i = tid; i < s_runs * kPer; i += kThreads) {
-        const Run run = s_run[i / kPer];
-        const int row = i % kPer / (kD / 4), d = i % (kD / 4) * 4;
-        if (row >= run.rows) continue;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int e = run.begin; e < run.end; ++e) {
-            const float w = s_w[e][row];
-            const float4 y = *reinterpret_cast<const float4 *>(s_at[e].sums + row * s_at[e].pitch + d);
-            x.x += w * y.x;
-            x.y += w * y.y;
-            x.z += w * y.z;
-            x.w += w * y.w;
-        }
-        if (run.whole) write_out(a, (run.out_row + row) * kD + d, x);
-        else *reinterpret_cast<float4 *>(a.ws.cut + (run.slot * kHeads + row) * kD + d) = x;
-    }
-
-    // ---- sequences without keys ----------------------------------------------------------
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (valid_len(a, b) > 0) continue;
-        if (tid == 0 && __ldg(a.seq_lens + b) != 0) record_device_error(a.err, kDevInvalidArg);
-        for (int i = tid; i < a.q_heads * (kD / 4); i += kThreads)
-            write_out(a, static_cast<int64_t>(b) * a.q_heads * kD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-        if (a.lse != nullptr)
-            for (int i = tid; i < a.q_heads; i += kThreads)
-                a.lse[static_cast<int64_t>(b) * a.q_heads + i] = -INFINITY;
-    }
-}
-
-// Joins the parts of the unit that CTA blockIdx.x of the first kernel began and
-// did not finish: its slot 1 and slot 0 of the CTAs after it, up to the last.
-// blockIdx.y: 64 channels.  Which parts those are follows from the lengths, so it
-// is known before the wait; after it there is one trip to memory, for the parts'
-// maxima and sums together with the first of their products.
-constexpr int kJoinThreads = 256;
-
-template <class S>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
-    constexpr int kD = S::kD, kHeads = S::kHeads;
-    constexpr int kQuads = 16;                                       // float4s of 64 channels
-    constexpr int kItems = kHeads * kQuads;
-    constexpr int kGroups = max_of(1, kJoinThreads / kItems);        // share the parts
-    constexpr int kTurns = max_of(1, kItems / kJoinThreads);         // items of a thread
-    constexpr int kAhead = 8 / kTurns;                               // parts read ahead, each
-    constexpr int kRowsOfWarp = kHeads / (kJoinThreads / 32);
-    __shared__ float s_w[kMaxCtas][kHeads];
-    __shared__ float4 s_sum[kGroups][kItems];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c0 = blockIdx.x;
-
-    const List<S::kKeys, S::kWarps> list(a, lane, gridDim.x);
-    const int64_t hi = list.even_begin(c0 + int64_t{1});
-    bool mine = !list.whole && c0 < static_cast<int>(list.ctas) && hi < list.total;
-    Cursor<S::kKeys> cut = {};
-    if (mine) cut = list.find(a, hi);
-    if (cut.t == 0 || hi - cut.t < list.even_begin(c0)) mine = false;  // not cut, or begun before
-    if (!mine) {
-        // the kernels after this one count on the first having ended when this one has
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
-    const int parts = list.even_piece_of(hi - cut.t + cut.tiles - 1) - c0 + 1;
-    const UnitRows rows(a, cut.b, cut.u, kHeads);
-    // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
-    auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
-    auto ml_at = [&](int i, int row) {
-        return *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
-    };
-    const int group = tid / kItems;                                  // 0 where a thread has turns
-    auto sums_at = [&](int i, int turn) {
-        const int item = (tid + turn * kJoinThreads) % kItems;
-        return *reinterpret_cast<const float4 *>(
-            a.ws.cut + (slot(i) * kHeads + item / kQuads) * kD + blockIdx.y * 64 + item % kQuads * 4);
-    };
-
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    float2 ml[kRowsOfWarp];
-#pragma unroll
-    for (int k = 0; k < kRowsOfWarp; ++k)
-        if (lane < parts) ml[k] = ml_at(lane, warp + k * (kJoinThreads / 32));
-    // (rows past the group's heads are read like the others and not written)
-    float4 y[kTurns][kAhead];
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k)
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (group + j * kGroups < parts) y[k][j] = sums_at(group + j * kGroups, k);
-#pragma unroll
-    for (int k = 0; k < kRowsOfWarp; ++k) {
-        const int row = warp + k * (kJoinThreads / 32);
-        if (row >= rows.rows) break;
-        float mm = lane < parts ? ml[k].x : -INFINITY, ll = 0.f;
-        for (int i = lane + 32; i < parts; i += 32) mm = fmaxf(mm, ml_at(i, row).x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 x = i == lane ? ml[k] : ml_at(i, row);
-            const float w = ex2(x.x - ref);
-            s_w[i][row] = w;
-            ll += w * x.y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-        const float f = ll == 0.f ? 0.f : 1.f / ll;
-        for (int i = lane; i < parts; i += 32) s_w[i][row] *= f;
-        if (lane == 0 && blockIdx.y == 0) write_lse(a, rows.out_row + row, mm, ll);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
-        const int item = (tid + k * kJoinThreads) % kItems, row = item / kQuads;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](int i, float4 v) {
-            const float w = s_w[i][row];
-            x.x += w * v.x;
-            x.y += w * v.y;
-            x.z += w * v.z;
-            x.w += w * v.w;
-        };
-        if (row < rows.rows) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (group + j * kGroups < parts) add(group + j * kGroups, y[k][j]);
-#pragma unroll 8
-            for (int i = group + kAhead * kGroups; i < parts; i += kGroups) add(i, sums_at(i, k));
-        }
-        if constexpr (kGroups > 1) {
-            s_sum[group][item] = x;
-            __syncthreads();
-            if (group > 0) return;
-#pragma unroll
-            for (int i = 1; i < kGroups; ++i) {
-                const float4 v = s_sum[i][item];
-                x.x += v.x;
-                x.y += v.y;
-                x.z += v.z;
-                x.w += v.w;
-            }
-        }
-        if (row < rows.rows)
-            write_out(a, (rows.out_row + row) * kD + blockIdx.y * 64 + item % kQuads * 4, x);
-    }
-}
-
-template <class S>
-cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
-    constexpr int kSmem = S::kWarps * S::kRing;
-    const int page_size = static_cast<int>(a.cache.page.d);
-    auto kern = page_size % S::kKeys == 0 ? paged_decode_kernel<S, true> : paged_decode_kernel<S, false>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSmem);
-    if (e != cudaSuccess) return e;
-    // a table without room for longer units: the kernel cuts none (see List)
-    const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
-    kern<<<ctas, S::kWarps * 32, kSmem, s>>>(a);
-    const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess || whole) return e1;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, S::kD / 64);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<S>, a);
-}
-
-template <int kD>
-cudaError_t launch_dim(const Args &a, int heads, int ctas, cudaStream_t s) {
-    if (heads == 8)
-        return a.cache.fp8 ? launch_shape<Shape<kD, true, 1>>(a, ctas, s)
-                           : launch_shape<Shape<kD, false, 1>>(a, ctas, s);
-    if constexpr (kD <= 128) {
-        if (heads == 32)
-            return a.cache.fp8 ? launch_shape<Shape<kD, true, 4>>(a, ctas, s)
-                               : launch_shape<Shape<kD, false, 4>>(a, ctas, s);
-    }
-    return a.cache.fp8 ? launch_shape<Shape<kD, true, 2>>(a, ctas, s)
-                       : launch_shape<Shape<kD, false, 2>>(a, ctas, s);
-}
-
-}  // namespace
+namespace paged {
+extern template cudaError_t launch_paged_decode_dim<64>(const Args &, bool, int, int, cudaStream_t);
+extern template cudaError_t launch_paged_decode_dim<256>(const Args &, bool, int, int, cudaStream_t);
+}  // namespace paged
 
 size_t paged_decode_workspace_bytes(int, int q_heads, int kv_heads, int head_dim) {
-    return layout_bytes(unit_heads(q_heads / kv_heads, head_dim), head_dim, nullptr, nullptr);
+    return paged::layout_bytes(paged::unit_heads(q_heads / kv_heads, head_dim), head_dim, nullptr, nullptr);
 }
 
 cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
@@ -1142,7 +17,7 @@ cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
                                 const int32_t *seq_lens, int B, int q_heads, float scale, void *o,
                                 bool o_bf16, float *lse, void *workspace, unsigned int *err,
                                 int num_sms, cudaStream_t s) {
-    Args a;
+    paged::Args a;
     a.q = q;
     a.q_row_stride = q_row_stride;
     a.cache = cache;
@@ -1152,18 +27,18 @@ cudaError_t launch_paged_decode(const __nv_bfloat16 *q, int64_t q_row_stride,
     a.B = B;
     a.q_heads = q_heads;
     a.group = q_heads / cache.heads;
-    const int heads = unit_heads(a.group, cache.head_dim);
+    const int heads = paged::unit_heads(a.group, cache.head_dim);
     a.head_tiles = (a.group + heads - 1) / heads;
     a.scale = scale;
     a.o = o;
-    a.o_bf16 = o_bf16;
     a.lse = lse;
     a.err = err;
-    layout_bytes(heads, cache.head_dim, static_cast<uint8_t *>(workspace), &a.ws);
-    const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-    return cache.head_dim == 64    ? launch_dim<64>(a, heads, ctas, s)
-           : cache.head_dim == 128 ? launch_dim<128>(a, heads, ctas, s)
-                                   : launch_dim<256>(a, heads, ctas, s);
+    paged::layout_bytes(heads, cache.head_dim, static_cast<uint8_t *>(workspace), &a.ws);
+    const int ctas = num_sms < paged::kMaxCtas ? num_sms : paged::kMaxCtas;
+    const auto launch = cache.head_dim == 64    ? paged::launch_paged_decode_dim<64>
+                        : cache.head_dim == 128 ? paged::launch_paged_decode_dim<128>
+                                                : paged::launch_paged_decode_dim<256>;
+    return launch(a, o_bf16, heads, ctas, s);
 }
 
 }  // namespace kda

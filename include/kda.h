@@ -646,8 +646,9 @@ size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int hea
  *               q + b * q_row_stride (elements, a multiple of 8)
  *   block_table int32 [B, max_pages] device;  seq_lens int32 [B] device
  *   q_heads     a positive multiple of cache->heads
- *   o           [B, q_heads, head_dim] of o_dtype (bf16 or fp32), written; every
- *               softmax weight is kept to 16 bits
+ *   o           [B, q_heads, head_dim] of o_dtype (bf16 or fp32), written; a
+ *               softmax weight is kept to 16 bits for bf16 outputs, 22 or more for
+ *               fp32 ones
  *   lse         fp32 [B, q_heads] written, or NULL: with fp32 outputs, what joins
  *               the results over two sets of keys
  *   workspace   device scratch, >= kda_paged_decode_workspace_size() bytes,
