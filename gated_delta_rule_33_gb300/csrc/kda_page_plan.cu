@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile;
     const int64_t t1 = t0 + kTile < N ? t0 + kTile : N;
     const int64_t cap = static_cast<int64_t>(max_pages) * page.d;
+    wait_for_kernel_before();
     auto pages_of = [&](int n) { return n <= 0 ? 0 : static_cast<int>(page.div(n - 1)) + 1; };
 
     int4 c4 = load4(cached_lens, tid * kItems, B), n4 = load4(new_lens, tid * kItems, B);
@@ -226,11 +227,10 @@ cudaError_t launch_page_plan(const int32_t *cached_lens, const int32_t *new_lens
     auto kern = B <= 1024 ? plan_kernel<256> : plan_kernel<512>;
     const int threads = B <= 1024 ? 256 : 512, tile = threads * kItems;
     const int64_t ctas = N > 0 ? (N + tile - 1) / tile : 1;
-    kern<<<static_cast<unsigned>(ctas), threads, 0, s>>>(
-        cached_lens, new_lens, free_pages, num_free, block_table, max_pages, B,
-        FastDiv(static_cast<uint32_t>(page_size)), num_pages, seq_lens, cu_seqlens, slot_map, N,
-        pages_used, err);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(static_cast<unsigned>(ctas)), threads, 0, s, cached_lens, new_lens,
+                        free_pages, num_free, block_table, max_pages, B,
+                        FastDiv(static_cast<uint32_t>(page_size)), num_pages, seq_lens, cu_seqlens,
+                        slot_map, N, pages_used, err);
 }
 
 }  // namespace kda

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
     int64_t v_row_stride, const int32_t *__restrict__ slot_map, int64_t N, const PagedView cache,
     FastDiv row, int dim_shift, unsigned int *err) {
     constexpr int kVals = kFp8 ? 16 : 8;
+    wait_for_kernel_before();
     const bool is_v = blockIdx.y != 0;
     const __nv_bfloat16 *x = is_v ? v : k;
     const int64_t x_stride = is_v ? v_row_stride : k_row_stride;
@@ -119,13 +120,8 @@ cudaError_t launch_paged_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v,
     while ((1 << dim_shift) < cache.head_dim) ++dim_shift;
     const dim3 grid(static_cast<unsigned>(ctas), 2);
     const FastDiv row(units);
-    if (cache.fp8)
-        append_kernel<true><<<grid, kThreads, 0, s>>>(k, v, k_row_stride, v_row_stride, slot_map, N,
-                                                      cache, row, dim_shift, err);
-    else
-        append_kernel<false><<<grid, kThreads, 0, s>>>(k, v, k_row_stride, v_row_stride, slot_map,
-                                                       N, cache, row, dim_shift, err);
-    return cudaGetLastError();
+    return launch_early(cache.fp8 ? append_kernel<true> : append_kernel<false>, grid, kThreads, 0, s,
+                        k, v, k_row_stride, v_row_stride, slot_map, N, cache, row, dim_shift, err);
 }
 
 }  // namespace kda

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_kernel_before();
     if (lane < 2) s_part[2 * warp + lane].b = -1;
     __syncwarp();
 
@@ -1042,7 +1042,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     __shared__ float4 s_sum[kGroups][kItems];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x;
-
+    // (the first kernel's blocks have all waited for what was before them, so the lengths
+    // may be read here)
     const List<S::kKeys, S::kWarps> list(a, lane, gridDim.x);
     const int64_t hi = list.even_begin(c0 + int64_t{1});
     bool mine = !list.whole && c0 < static_cast<int>(list.ctas) && hi < list.total;
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (cut.t == 0 || hi - cut.t < list.even_begin(c0)) mine = false;  // not cut, or begun before
     if (!mine) {
         // the kernels after this one count on the first having ended when this one has
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_kernel_before();
         return;
     }
     const int parts = list.even_piece_of(hi - cut.t + cut.tiles - 1) - c0 + 1;
@@ -1068,7 +1069,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             a.ws.cut + (slot(i) * kHeads + item / kQuads) * kD + blockIdx.y * 64 + item % kQuads * 4);
     };
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_kernel_before();
     float2 ml[kRowsOfWarp];
 #pragma unroll
     for (int k = 0; k < kRowsOfWarp; ++k)
@@ -1147,19 +1148,9 @@ cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // a table without room for longer units: the kernel cuts none (see List)
     const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
-    kern<<<ctas, S::kWarps * 32, kSmem, s>>>(a);
-    const cudaError_t e1 = cudaGetLastError();
+    const cudaError_t e1 = launch_early(kern, dim3(ctas), S::kWarps * 32, kSmem, s, a);
     if (e1 != cudaSuccess || whole) return e1;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, S::kD / 64);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<S>, a);
+    return launch_early(join_kernel<S>, dim3(ctas, S::kD / 64), kJoinThreads, 0, s, a);
 }
 
 template <int kD, bool kFp8, bool kWide>

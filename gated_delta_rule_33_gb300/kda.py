@@ -429,8 +429,8 @@ def _ptr(t: torch.Tensor, dtype: torch.dtype) -> int:
 
 
 def _rows(t: torch.Tensor, heads: int, head_dim: int):
-    """Pointer and row stride of bf16 [N, heads, head_dim] (or [N, heads * head_dim]) rows that
-    may lie further apart than their width."""
+    """Pointer, row stride and number of bf16 [N, heads, head_dim] (or [N, heads * head_dim])
+    rows, which may lie further apart than their width."""
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"bf16 tensor expected, got {t.dtype}")
     shape, strides = t.shape, t.stride()
@@ -441,7 +441,7 @@ def _rows(t: torch.Tensor, heads: int, head_dim: int):
         ok = len(shape) == 2 and shape[1] == heads * head_dim and strides[1] == 1
     if not ok:
         raise ValueError(f"rows of {heads} x {head_dim} contiguous values expected")
-    return t.data_ptr(), strides[0]
+    return t.data_ptr(), strides[0], shape[0]
 
 
 def _handle(stream, t: torch.Tensor) -> int:
@@ -473,10 +473,10 @@ def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num
 def kda_paged_append(k, v, slot_map, cache, stream=None):
     """k, v bf16 [N, heads, head_dim] (rows may be slices of a wider tensor); slot_map [N]."""
     N = slot_map.numel()
-    if len(k) != N or len(v) != N:
+    kp, ks, kn = _rows(k, cache.heads, cache.head_dim)
+    vp, vs, vn = _rows(v, cache.heads, cache.head_dim)
+    if kn != N or vn != N:
         raise ValueError("k and v need one row per entry of slot_map")
-    kp, ks = _rows(k, cache.heads, cache.head_dim)
-    vp, vs = _rows(v, cache.heads, cache.head_dim)
     st = (_lib or load()).kda_paged_append(kp, vp, ks, vs, _ptr(slot_map, torch.int32), N,
                                            cache._ref, _handle(stream, k))
     if st:
@@ -499,7 +499,7 @@ def kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, workspace, 
         raise ValueError("block_table [B, max_pages] and seq_lens [B]")
     if lse is not None and lse.numel() != B * q_heads:
         raise ValueError("lse is fp32 [B, q_heads]")
-    qp, qs = _rows(q, q_heads, head_dim)
+    qp, qs, _ = _rows(q, q_heads, head_dim)
     o_dtype = o.dtype
     st = (_lib or load()).kda_paged_decode(
         qp, qs, cache._ref, _ptr(block_table, torch.int32), max_pages,
