@@ -760,10 +760,14 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
     DeviceInfo *dev = nullptr;
     st = current_device(&dev);
     if (st != KDA_OK) return st;
-    return from_cuda(kda::launch_paged_decode(
-        static_cast<const __nv_bfloat16 *>(q), q_row_stride, view, block_table, max_pages, seq_lens,
-        B, q_heads, scale, o, o_dtype == KDA_BF16, lse, workspace, dev->error_word, dev->num_sms,
-        static_cast<cudaStream_t>(stream)));
+    try {
+        return from_cuda(kda::launch_paged_decode(
+            static_cast<const __nv_bfloat16 *>(q), q_row_stride, view, block_table, max_pages,
+            seq_lens, B, q_heads, scale, o, o_dtype == KDA_BF16, lse, workspace, dev->error_word,
+            dev->num_sms, static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
 }
 
 kda_status kda_debug_check_gate_division(uint64_t *mismatches, void *stream) {
