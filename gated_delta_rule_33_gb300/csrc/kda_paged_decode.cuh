@@ -61,13 +61,14 @@ namespace kda {
 namespace paged {
 
 constexpr int kMaxCtas = 160;  // at most the join kernel's threads
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 12;
+constexpr int kMaxSide = 4;   // key heads side by side
 
 // What is cut at a CTA's ends: its first unit's part (begun by an earlier CTA)
 // in slot 0, its last unit's (begun here, not finished) in slot 1.
 struct Layout {      // of the workspace
-    float *ml;       // [ctas][2][heads][2]
-    float *cut;      // [ctas][2][heads][D]
+    float *ml;       // [ctas][2][side][heads][2], side: key heads side by side (see List)
+    float *cut;      // [ctas][2][side][heads][D]
     float *head;     // [ctas][warps][heads][D]: a warp's first part, until its CTA joins it
 };
 
@@ -75,8 +76,8 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 
 inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
     const size_t part = static_cast<size_t>(heads) * head_dim * 4;
-    const size_t cut = align256(static_cast<size_t>(kMaxCtas) * 2 * heads * 2 * 4);
-    const size_t head = align256(cut + kMaxCtas * 2 * part);
+    const size_t cut = align256(static_cast<size_t>(kMaxCtas) * 2 * kMaxSide * heads * 2 * 4);
+    const size_t head = align256(cut + kMaxCtas * 2 * kMaxSide * part);
     if (l != nullptr) {
         l->ml = reinterpret_cast<float *>(base);
         l->cut = reinterpret_cast<float *>(base + cut);
@@ -104,12 +105,14 @@ struct Args {
     float *lse;
     Layout ws;
     unsigned int *err;
+    int side_log;  // key heads that may go side by side (see List), as a power of two
 };
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kSideTiles = 8;  // heads go side by side in lists of so many tiles a warp
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
@@ -128,6 +131,8 @@ struct Shape {
     // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
     // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
     static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
+    // key heads may go side by side (see List): short rows, and HBM-bound
+    static constexpr bool kSide = kRowBytes < 256 && (kD == 64 || kN == 1);
     static constexpr int kHeads = 8 * kN;
     static constexpr int kPitch = kD + 4;                                  // floats of a part's row
     // the ring takes the warp's last part in the end
@@ -306,6 +311,7 @@ struct Copier {
     static constexpr int kLaneRows = !kOnePage && kKeys > 32 ? 2 : 1;
     static constexpr int kCopies = S::kHalf / 512;           // 16-byte copies of a lane
     Cursor<kKeys> at;
+    int side_log, side;                                      // the list's, and this warp's head
     int64_t left;                                            // tiles to begin
     int page[kLaneRows];                                     // of this lane's rows of tile `at`
     bool held[kLaneRows];                                    // the row is a key of the sequence
@@ -329,8 +335,10 @@ struct Copier {
     }
 
     __device__ __forceinline__ void begin(const Args &a, const Cursor<kKeys> &c, int64_t tiles,
-                                          int lane) {
+                                          int log, int head, int lane) {
         at = c;
+        side_log = log;
+        side = head;
         left = tiles;
         read_pages(a, lane);
     }
@@ -341,7 +349,8 @@ struct Copier {
         rows = -1;
         if (left > 0) {
             uint64_t valid = 0;
-            const int64_t h = (a.head_tiles == 1 ? at.u : at.u / a.head_tiles) * a.cache.head_stride;
+            const int u = S::kSide ? (at.u << side_log) + side : at.u;
+            const int64_t h = (a.head_tiles == 1 ? u : u / a.head_tiles) * a.cache.head_stride;
             if constexpr (kOnePage) {
                 const bool ok = page[0] >= 0 && page[0] < a.cache.num_pages;
                 if (!ok) record_device_error(a.err, kDevInvalidArg);
@@ -428,11 +437,19 @@ __device__ __noinline__ Cursor<kKeys> find_tile(const Args &a, int units, int64_
 // The list of tiles and its pieces, as a warp sees it: every warp sums the lengths for
 // itself (they come out of L1 after the first), lane i over sequences
 // i ceil(B / 32) .. , so that no barrier precedes the first copy.
-template <int kKeys, int kWarps>
+//
+// Where a token's rows lie head by head and are short (64 or 128 bytes), warps that read one
+// head's take a part of each DRAM burst and page.  In long lists 2 or 4 neighbouring key
+// heads then go side by side: a place of the list is a tile of each of them, and warp w of
+// a CTA walks the CTA's piece for head w mod 2 or 4, so that the CTA's warps read
+// neighbouring rows at nearly the same time.
+template <class S>
 struct List {
+    static constexpr int kKeys = S::kKeys, kWarps = S::kWarps;
     int64_t before, after;   // positions of the list in this lane's sequences
     int64_t total, q, r;     // CTA i's piece: q positions, one more in the first r
-    int b_lo, units;
+    int b_lo, units;         // units of a sequence (of the heads side by side, each)
+    int many_log;            // side by side, as a power of two
     int filled, filled_before;  // sequences with keys: this lane's, and before them
     uint32_t ctas;           // that have a piece
     bool one_each, whole;    // pieces are units, or end where units end
@@ -442,7 +459,6 @@ struct List {
     }
 
     __device__ __forceinline__ List(const Args &a, int lane, int grid) {
-        units = a.cache.heads * a.head_tiles;
         const int chunk = (a.B + 31) / 32;
         b_lo = min(a.B, lane * chunk);
         const int b_hi = min(a.B, b_lo + chunk);
@@ -468,7 +484,11 @@ struct List {
             }
         }
         longest = __reduce_max_sync(0xffffffffu, longest);
-        total = __shfl_sync(0xffffffffu, before, 31) * units;
+        const int64_t tiles = __shfl_sync(0xffffffffu, before, 31);
+        units = a.cache.heads * a.head_tiles;
+        many_log = tiles * units >= kSideTiles * kWarps * static_cast<int64_t>(grid) ? a.side_log : 0;
+        units >>= side_log();
+        total = tiles * units;
         const int sequences = __shfl_sync(0xffffffffu, filled_before, 31);
         filled_before -= filled;
         before = (before - mine) * units;
@@ -478,15 +498,19 @@ struct List {
         // unit each where there are few, pieces moved back to a unit's start where units
         // are short.
         const int64_t all_units = static_cast<int64_t>(sequences) * units;
-        one_each = all_units <= grid && longest <= div64(total, grid) + 2 * kWarps;
-        whole = one_each || longest <= 2 * kWarps;
+        one_each = all_units <= grid && longest <= div64(total, grid) + 2 * warps();
+        whole = one_each || longest <= 2 * warps();
         // as many CTAs as leave a tile to each warp (a unit to each CTA), all of the
         // grid for longer lists
-        const int64_t want = whole ? all_units : static_cast<uint64_t>(total + kWarps - 1) / kWarps;
+        const int64_t want = whole ? all_units : div64(total + warps() - 1, warps());
         ctas = static_cast<uint32_t>(want < grid ? want : grid);
         q = ctas == 0 ? 0 : div64(total, ctas);
         r = total - q * ctas;
     }
+
+    __device__ __forceinline__ int side_log() const { return S::kSide ? many_log : 0; }
+    // a CTA's warps for each of the heads side by side
+    __device__ __forceinline__ int warps() const { return kWarps >> side_log(); }
 
     // The place of position pos < total; called by a whole warp.
     __device__ __forceinline__ Cursor<kKeys> find(const Args &a, int64_t pos) const {
@@ -557,28 +581,32 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tq = lane & 3;
     wait_for_kernel_before();
-    if (lane < 2) s_part[2 * warp + lane].b = -1;
-    __syncwarp();
 
-    const List<kKeys, kWarps> list(a, lane, gridDim.x);
-    const int units = list.units;
+    const List<S> list(a, lane, gridDim.x);
+    const int units = list.units, side_log = list.side_log();
+    // this warp's head of those side by side, its place among the warps of that head, and
+    // in the order that parts are joined in
+    const int side = warp & ((1 << side_log) - 1), sub = warp >> side_log;
+    const int place = side * list.warps() + sub;
+    if (lane < 2) s_part[2 * place + lane].b = -1;
+    __syncwarp();
     int64_t remaining = 0, begin = 0;  // this warp's tiles
     int64_t paced = 0;                 // fours of tiles that every warp of the CTA has
     if (blockIdx.x < list.ctas) {
         int64_t lo, hi;
         list.piece(a, blockIdx.x, lo, hi);
-        const int64_t per = static_cast<uint64_t>(hi - lo) / kWarps, more = hi - lo - per * kWarps;
-        begin = lo + warp * per + min(static_cast<int64_t>(warp), more);
-        remaining = per + (warp < more);
+        const int64_t per = div64(hi - lo, list.warps()), more = hi - lo - per * list.warps();
+        begin = lo + sub * per + min(static_cast<int64_t>(sub), more);
+        remaining = per + (sub < more);
         paced = per / 4;
     }
 
     // ---- a warp's part of the piece --------------------------------------------------------
     if (remaining > 0) {
-        const uint32_t ring = sm100::smem_addr(s_ring) + warp * S::kRing;
+        const uint32_t ring = sm100::smem_addr(s_ring) + place * S::kRing;
         Cursor<kKeys> cur = list.find(a, begin);
         Copier<S, kOnePage> copier;
-        copier.begin(a, cur, remaining, lane);
+        copier.begin(a, cur, remaining, side_log, side, lane);
         int put = 0, copied = 0;  // the slot of the next half to copy; tiles begun
         auto next_slot = [&](int s) { return s == S::kSlots - 1 ? 0 : s + 1; };
         auto copy_keys = [&]() {
@@ -605,7 +633,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
         int slot = 0, tile = 0;
         bool fresh = true;
         while (true) {
-            const UnitRows rows(a, cur.b, cur.u, kHeads);
+            const int unit = (cur.u << side_log) + side;
+            const UnitRows rows(a, cur.b, unit, kHeads);
             if (fresh) {
                 // the unit's queries as the right operand (head 8 n + g); heads past the
                 // group are zero
@@ -868,14 +897,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                 float *part = nullptr;
                 int pitch = kD;
                 if (!whole) {
-                    const int at = 2 * warp + (remaining == 0 ? 1 : 0);
+                    const int at = 2 * place + (remaining == 0 ? 1 : 0);
                     if (remaining == 0) {
                         asm volatile("cp.async.wait_all;" ::: "memory");
                         __syncwarp();  // the ring is free: the part goes there
-                        part = reinterpret_cast<float *>(s_ring + warp * S::kRing);
+                        part = reinterpret_cast<float *>(s_ring + place * S::kRing);
                         pitch = S::kPitch;
                     } else {
-                        part = a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kHeads * kD;
+                        part = a.ws.head + (static_cast<int64_t>(blockIdx.x) * kWarps + place) * kHeads * kD;
                     }
                     if (g == 0) {
 #pragma unroll
@@ -888,7 +917,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                     }
                     if (lane == 0) {
                         s_part[at].b = cur.b;
-                        s_part[at].u = cur.u;
+                        s_part[at].u = unit;
                         s_part[at].starts = begun == 0;
                         s_part[at].ends = ends;
                         s_part[at].in_global = remaining != 0;
@@ -963,7 +992,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
             x.rows = rows.rows;
             x.whole = part.starts && ends;
             x.out_row = rows.out_row;
-            x.slot = static_cast<int64_t>(blockIdx.x) * 2 + (part.starts ? 1 : 0);
+            x.slot = ((static_cast<int64_t>(blockIdx.x) * 2 + (part.starts ? 1 : 0)) << side_log) +
+                     (part.u & ((1 << side_log) - 1));
         }
         if (lane == 0) {
             s_runs = __popc(firsts);
@@ -1024,7 +1054,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 
 // Joins the parts of the unit that CTA blockIdx.x of the first kernel began and
 // did not finish: its slot 1 and slot 0 of the CTAs after it, up to the last.
-// blockIdx.y: 64 channels.  Which parts those are follows from the lengths, so it
+// blockIdx.y: 64 channels; .z: of the heads side by side.  Which parts those are follows from the lengths, so it
 // is known before the wait; after it there is one trip to memory, for the parts'
 // maxima and sums together with the first of their products.
 constexpr int kJoinThreads = 256;
@@ -1044,10 +1074,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int c0 = blockIdx.x;
     // (the first kernel's blocks have all waited for what was before them, so the lengths
     // may be read here)
-    const List<S::kKeys, S::kWarps> list(a, lane, gridDim.x);
+    const List<S> list(a, lane, gridDim.x);
     const int64_t hi = list.even_begin(c0 + int64_t{1});
     bool mine = !list.whole && c0 < static_cast<int>(list.ctas) && hi < list.total;
     Cursor<S::kKeys> cut = {};
+    if (blockIdx.z >> list.side_log() != 0) mine = false;
     if (mine) cut = list.find(a, hi);
     if (cut.t == 0 || hi - cut.t < list.even_begin(c0)) mine = false;  // not cut, or begun before
     if (!mine) {
@@ -1056,9 +1087,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         return;
     }
     const int parts = list.even_piece_of(hi - cut.t + cut.tiles - 1) - c0 + 1;
-    const UnitRows rows(a, cut.b, cut.u, kHeads);
+    const UnitRows rows(a, cut.b, (cut.u << list.side_log()) + blockIdx.z, kHeads);
     // part i's sums: slot 1 of CTA c0, slot 0 of CTA c0 + i
-    auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+    auto slot = [&](int i) {
+        return ((static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) << list.side_log()) + blockIdx.z;
+    };
     auto ml_at = [&](int i, int row) {
         return *reinterpret_cast<const float2 *>(a.ws.ml + (slot(i) * kHeads + row) * 2);
     };
@@ -1140,17 +1173,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 template <class S>
-cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
+cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
     constexpr int kSmem = S::kWarps * S::kRing;
     const int page_size = static_cast<int>(a.cache.page.d);
     auto kern = page_size % S::kKeys == 0 ? paged_decode_kernel<S, true> : paged_decode_kernel<S, false>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSmem);
     if (e != cudaSuccess) return e;
+    // heads side by side: a token's, next to each other, where a row is less than 256 bytes
+    // (64 channels, 8 bits: 134 us without, 80 with; bf16: 159 and 145; 128 channels, bf16:
+    // 145 and 146)
+    a.side_log = 0;
+    if (S::kSide && a.head_tiles == 1 && a.cache.head_stride == S::kRowBytes)
+        while (2 << a.side_log <= kMaxSide && a.cache.heads % (2 << a.side_log) == 0) ++a.side_log;
     // a table without room for longer units: the kernel cuts none (see List)
-    const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * S::kWarps * S::kKeys;
+    const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * (S::kWarps >> a.side_log) * S::kKeys;
     const cudaError_t e1 = launch_early(kern, dim3(ctas), S::kWarps * 32, kSmem, s, a);
     if (e1 != cudaSuccess || whole) return e1;
-    return launch_early(join_kernel<S>, dim3(ctas, S::kD / 64), kJoinThreads, 0, s, a);
+    return launch_early(join_kernel<S>, dim3(ctas, S::kD / 64, 1 << a.side_log), kJoinThreads, 0, s, a);
 }
 
 template <int kD, bool kFp8, bool kWide>

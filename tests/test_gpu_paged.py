@@ -125,6 +125,19 @@ def test_decode_long(lib, lens, cache, D, G):
         check_decode(x, o, lse)
 
 
+@pytest.mark.parametrize("H,G,D,cache,lens", [(32, 2, 64, "fp8", [9001, 20000, 0, 1, 11111]),
+                                               (6, 1, 64, "bf16", [40000, 77, 41003]),
+                                               (8, 8, 128, "fp8", [30001, 33333]),
+                                               (32, 9, 64, "bf16", [100] * 190 + [3])])
+def test_decode_heads_side_by_side(lib, H, G, D, cache, lens):
+    """Lists long enough that neighbouring heads of short rows are walked together."""
+    x = attention_case(lens, H, G, D, 64, cache, "token", seed=H)
+    for dt in (torch.bfloat16, torch.float32):
+        o, lse = run_decode(lib, x, dt)
+        assert lib.kda_get_last_device_error() == 0
+        check_decode(x, o, lse)
+
+
 def test_decode_many_short(lib):
     """More sequences than blocks, most of them of a few keys."""
     gen = np.random.default_rng(5)
