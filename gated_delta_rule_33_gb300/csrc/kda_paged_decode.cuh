@@ -86,10 +86,11 @@ inline size_t layout_bytes(int heads, int head_dim, uint8_t *base, Layout *l) {
     return head + kMaxCtas * kMaxWarps * part;
 }
 
-// Query heads of a unit: all of a group of up to 32 (16 at 256 channels), in 8, 16
-// or 32, so that its keys are read once.
+// Query heads of a unit: all of a group of up to 32 (16 at 256 channels), in eights, so
+// that its keys are read once; of a larger group as many as share its units evenly.
 inline int unit_heads(int group, int head_dim) {
-    return group <= 8 ? 8 : group <= 16 || head_dim == 256 ? 16 : 32;
+    const int most = head_dim == 256 ? 16 : 32, units = (group + most - 1) / most;
+    return (group + units * 8 - 1) / (units * 8) * 8;
 }
 
 struct Args {
@@ -124,10 +125,10 @@ struct Shape {
     static constexpr int kD = kD_, kN = kN_;
     static constexpr bool kFp8 = kFp8_, kWide = kWide_;
     static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
-    // keys of a tile: 4 KB of them, 2 KB where 32 heads' scores would fill the registers
-    static constexpr int kKeys = max_of(16, (kN == 4 ? 2048 : 4096) / kRowBytes);
+    // keys of a tile: 4 KB of them, 2 KB where 24 or 32 heads' scores would fill the registers
+    static constexpr int kKeys = max_of(16, (kN >= 3 ? 2048 : 4096) / kRowBytes);
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-        static constexpr int kWarps = kN == 4 || kD == 256 ? 8 : 12;
+        static constexpr int kWarps = kN >= 3 || kD == 256 ? 8 : 12;
     // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
     // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
     static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
@@ -1065,7 +1066,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     constexpr int kQuads = 16;                                       // float4s of 64 channels
     constexpr int kItems = kHeads * kQuads;
     constexpr int kGroups = max_of(1, kJoinThreads / kItems);        // share the parts
-    constexpr int kTurns = max_of(1, kItems / kJoinThreads);         // items of a thread
+    constexpr int kTurns = (kItems + kJoinThreads - 1) / kJoinThreads;  // items of a thread; the
+    // last turn may do items again
     constexpr int kAhead = 8 / kTurns;                               // parts read ahead, each
     constexpr int kRowsOfWarp = kHeads / (kJoinThreads / 32);
     __shared__ float s_w[kMaxCtas][kHeads];
@@ -1196,6 +1198,7 @@ template <int kD, bool kFp8, bool kWide>
 cudaError_t launch_heads(const Args &a, int heads, int ctas, cudaStream_t s) {
     if (heads == 8) return launch_shape<Shape<kD, kFp8, 1, kWide>>(a, ctas, s);
     if constexpr (kD <= 128) {
+        if (heads == 24) return launch_shape<Shape<kD, kFp8, 3, kWide>>(a, ctas, s);
         if (heads == 32) return launch_shape<Shape<kD, kFp8, 4, kWide>>(a, ctas, s);
     }
     return launch_shape<Shape<kD, kFp8, 2, kWide>>(a, ctas, s);

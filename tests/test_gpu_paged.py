@@ -115,7 +115,8 @@ def test_decode(lib, H, G, D, page, cache, order, o_dtype):
 @pytest.mark.parametrize("lens", [[20011], [5000, 1, 0, 9999], [4096] * 5 + [3], [0, 0], [1]])
 @pytest.mark.parametrize("cache,D,G", [("bf16", 128, 8), ("fp8", 128, 4), ("bf16", 64, 1),
                                        ("bf16", 256, 6), ("bf16", 128, 24), ("fp8", 64, 32),
-                                       ("fp8", 128, 30), ("bf16", 256, 20), ("bf16", 64, 13)])
+                                       ("fp8", 128, 30), ("bf16", 256, 20), ("bf16", 64, 13),
+                                       ("bf16", 128, 48), ("fp8", 64, 70), ("bf16", 256, 40)])
 def test_decode_long(lib, lens, cache, D, G):
     """Lengths that are split over many blocks and joined."""
     x = attention_case(lens, 2, G, D, 64, cache, "token", seed=len(lens), peak=3.0)
