@@ -128,7 +128,8 @@ struct Shape {
     // keys of a tile: 4 KB of them, 2 KB where 24 or 32 heads' scores would fill the registers
     static constexpr int kKeys = max_of(16, (kN >= 3 ? 2048 : 4096) / kRowBytes);
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-        static constexpr int kWarps = kN >= 3 || kD == 256 ? 8 : 12;
+        static constexpr int kWarps = kD == 256 || kN == 4 || (kN == 3 && kD == 128) ? 8 : 12;
+    static_assert(kWarps % kMaxSide == 0, "heads side by side share the warps evenly");
     // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
     // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
     static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
@@ -138,6 +139,12 @@ struct Shape {
     static constexpr int kPitch = kD + 4;                                  // floats of a part's row
     // the ring takes the warp's last part in the end
     static constexpr int kRing = max_of(kSlots * kHalf, (kHeads * kPitch * 4 + 1023) / 1024 * 1024);
+    // The queries lie beside the ring, as operands, where they would fill the registers (32
+    // heads of 128: 251 us with spills, 208 so; 16 over 8 bits: 200 and 185).
+    static constexpr int kQBytes = kD / 16 * kN * 256;
+    static constexpr bool kQShared = kD * kN >= 256 && kWarps * (kRing + kQBytes) <= 220 * 1024;
+    static constexpr int kQ = kQShared ? kQBytes : 0;
+    static constexpr int kSmem = kWarps * (kRing + kQ);
     static_assert(kSlots >= 3 && kSlots <= 7, "the masks' ring holds the tiles in flight");
 };
 
@@ -629,6 +636,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
         if (!kOdd) copy_keys();
 
         uint32_t qf[kOT][kN][2];
+        uint2 *q_here = reinterpret_cast<uint2 *>(s_ring + kWarps * S::kRing + place * S::kQ) + lane;
         float acc[kOT][kN][4], m[kN][2], minus[kN][2], l[kN][2], sc[kN][2];
         int begun = cur.t;  // the part's first tile
         int slot = 0, tile = 0;
@@ -695,6 +703,11 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                                                          x + 16 * c + 8 * i + 2 * tq)) ^ sign
                                                    : 0;
                     }
+                    if constexpr (S::kQShared) {
+#pragma unroll
+                        for (int c = 0; c < kOT; ++c)
+                            q_here[(c * kN + n) * 32] = make_uint2(qf[c][n][0], qf[c][n][1]);
+                    }
                     m[n][0] = m[n][1] = -INFINITY;
                     minus[n][0] = minus[n][1] = 0.f;
                     l[n][0] = l[n][1] = 0.f;
@@ -717,6 +730,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
             else copy_values();
             const uint32_t kt = ring + slot * S::kHalf;
             slot = next_slot(slot);
+            auto query = [&](int c, int n) {
+                return S::kQShared ? q_here[(c * kN + n) * 32] : make_uint2(qf[c][n][0], qf[c][n][1]);
+            };
             float s[kBlocks][kN][4];
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
@@ -737,12 +753,17 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                                                    e4m3x2_to_f16x2(r[2 * i] >> 16),
                                                    e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
 #pragma unroll
-                            for (int n = 0; n < kN; ++n)
-                                mma<kF16>(s[k][n], f, qf[c + i][n][0], qf[c + i][n][1]);
+                            for (int n = 0; n < kN; ++n) {
+                                const uint2 q = query(c + i, n);
+                                mma<kF16>(s[k][n], f, q.x, q.y);
+                            }
                         }
                     } else {
 #pragma unroll
-                        for (int n = 0; n < kN; ++n) mma<kF16>(s[k][n], r, qf[c][n][0], qf[c][n][1]);
+                        for (int n = 0; n < kN; ++n) {
+                            const uint2 q = query(c, n);
+                            mma<kF16>(s[k][n], r, q.x, q.y);
+                        }
                     }
                 }
             }
@@ -1176,10 +1197,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 template <class S>
 cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
-    constexpr int kSmem = S::kWarps * S::kRing;
     const int page_size = static_cast<int>(a.cache.page.d);
     auto kern = page_size % S::kKeys == 0 ? paged_decode_kernel<S, true> : paged_decode_kernel<S, false>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSmem);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), S::kSmem);
     if (e != cudaSuccess) return e;
     // heads side by side: a token's, next to each other, where a row is less than 256 bytes
     // (64 channels, 8 bits: 134 us without, 80 with; bf16: 159 and 145; 128 channels, bf16:
@@ -1189,7 +1209,7 @@ cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
         while (2 << a.side_log <= kMaxSide && a.cache.heads % (2 << a.side_log) == 0) ++a.side_log;
     // a table without room for longer units: the kernel cuts none (see List)
     const bool whole = static_cast<int64_t>(a.max_pages) * page_size <= 2 * (S::kWarps >> a.side_log) * S::kKeys;
-    const cudaError_t e1 = launch_early(kern, dim3(ctas), S::kWarps * 32, kSmem, s, a);
+    const cudaError_t e1 = launch_early(kern, dim3(ctas), S::kWarps * 32, S::kSmem, s, a);
     if (e1 != cudaSuccess || whole) return e1;
     return launch_early(join_kernel<S>, dim3(ctas, S::kD / 64, 1 << a.side_log), kJoinThreads, 0, s, a);
 }
