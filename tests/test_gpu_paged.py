@@ -129,9 +129,14 @@ def test_decode_long(lib, lens, cache, D, G):
 @pytest.mark.parametrize("H,G,D,cache,lens", [(32, 2, 64, "fp8", [9001, 20000, 0, 1, 11111]),
                                                (6, 1, 64, "bf16", [40000, 77, 41003]),
                                                (8, 8, 128, "fp8", [30001, 33333]),
-                                               (32, 9, 64, "bf16", [100] * 190 + [3])])
+                                               (32, 9, 64, "bf16", [100] * 190 + [3]),
+                                               (2, 40, 128, "bf16", [40000, 30000]),
+                                               (1, 100, 128, "bf16", [60000, 5, 500]),
+                                               (2, 70, 256, "fp8", [25000, 1]),
+                                               (1, 200, 64, "bf16", [70000, 200])])
 def test_decode_heads_side_by_side(lib, H, G, D, cache, lens):
-    """Lists long enough that neighbouring heads of short rows are walked together."""
+    """Lists long enough that neighbouring heads of short rows are walked together, and
+    groups of several units."""
     x = attention_case(lens, H, G, D, 64, cache, "token", seed=H)
     for dt in (torch.bfloat16, torch.float32):
         o, lse = run_decode(lib, x, dt)
