@@ -9,19 +9,23 @@
 // o = sum e^{m_i - m} a_i / l.  Powers of two throughout: the scores carry log2 e.
 //
 // Bound: every key and value is read once, 4 G flops for the 2 (or 4) bytes of
-// a value at G query heads to a key head: HBM up to G = 100.  So what matters is
-// that every SM has copies in flight from the first microsecond to the last,
-// whatever the lengths, and that a warp's instructions for a tile take less time
-// than its copy.
+// a value at G query heads to a key head: HBM up to G = 100, had the tensor cores' full
+// rate.  So what matters is that every SM has copies in flight from the first microsecond
+// to the last, whatever the lengths, and that a warp's instructions for a tile take less
+// time than its copy.  Measured, 8 query heads to a key head of 128: 64 sequences of 16 to
+// 16384 keys 127 us (94 % of HBM), one of 262149 keys 163 us (97 %), 256 of 3500 to 8192 in
+// 8 bits 451 us (100 %).  16 heads over 8 bits (74 %) and 24 or more (32: 66 %) are bound by
+// the warps' instructions.
 //
-// Split.  A unit is (sequence, key head, group of up to 16 query heads); its keys
+// Split.  A unit is (sequence, key head, group of 8, 16, 24 or 32 query heads); its keys
 // are cut in tiles of 4 KB of keys and 4 KB of values (8 KB each at 256 channels
-// in bf16).  The tiles of all units form one list; each CTA takes an equal,
+// in bf16, 2 KB for 24 or 32 heads).  The tiles of all units form one list; each CTA takes an equal,
 // contiguous piece of it and each warp an equal part of that: long sequences are
 // cut, short ones share a warp.  A warp's part ends in at most two cut units;
 // their parts are joined within the CTA through shared memory, and what is cut
 // between CTAs by a second, small kernel that is launched with the first and
-// waits for it (programmatic dependent launch).  Where the block table has no
+// waits for it (programmatic dependent launch; a join by the CTA that is last to write
+// its part ends 2 us later: fences and a count cost more than the kernel).  Where the block table has no
 // room for long sequences, the pieces are moved to the units' ends instead, and
 // the second kernel is not launched.
 //
@@ -33,8 +37,8 @@
 // S^T = K Q^T, O^T += V^T P^T, so that no row of the operand that is loaded is
 // padding; the weights turn from accumulator to right operand by transposing
 // 8 x 8 blocks in registers (movmatrix).  (tcgen05.mma takes 64 or 128 rows from
-// shared memory and would need the weights there; the tensor pipe does not bind
-// here: 21 % busy at 5.3 TB/s with twice the products of this form.)
+// shared memory and would need the weights there; at 8 heads the tensor pipe is 12 %
+// busy, 27 % over 8 bits; at 16 over 8 bits 41 %.)
 //
 // Precision: scores, maxima, sums and outputs in fp32.  For the product with the
 // values a weight is a sum of bf16 numbers: two, 16 bits together, for a bf16
@@ -117,9 +121,9 @@ constexpr int kSideTiles = 8;  // heads go side by side in lists of so many tile
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
-// kN: groups of 8 query heads in a unit.  kWide: fp32 outputs.  Warps: as many as the accumulators
-// (kD / 4 * kN registers a lane) leave registers for, so that one warp's
-// instructions overlap another's waits.
+// kN: groups of 8 query heads in a unit.  kWide: fp32 outputs.  Warps: as many as the
+// accumulators (kD / 4 * kN registers a lane) leave registers for, so that one warp's
+// instructions overlap another's waits (24 heads of 64: 118 us with 8, 110 with 12).
 template <int kD_, bool kFp8_, int kN_, bool kWide_>
 struct Shape {
     static constexpr int kD = kD_, kN = kN_;
@@ -128,7 +132,7 @@ struct Shape {
     // keys of a tile: 4 KB of them, 2 KB where 24 or 32 heads' scores would fill the registers
     static constexpr int kKeys = max_of(16, (kN >= 3 ? 2048 : 4096) / kRowBytes);
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
-        static constexpr int kWarps = kD == 256 || kN == 4 || (kN == 3 && kD == 128) ? 8 : 12;
+    static constexpr int kWarps = kD == 256 || kN == 4 || (kN == 3 && kD == 128) ? 8 : 12;
     static_assert(kWarps % kMaxSide == 0, "heads side by side share the warps evenly");
     // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
     // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
