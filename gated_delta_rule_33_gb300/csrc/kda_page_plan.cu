@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(
     // a request at its first token in the CTA's range: its first row (which may lie before
     // the range) and tokens, its cached tokens, its place in the free list; its number, -1
     // where it is refused, -2 where no request starts
-    __shared__ int s_cu[kTile], s_count[kTile], s_cached[kTile], s_off[kTile], s_b[kTile];
+    __shared__ int s_cu[kTile], s_count[kTile], s_cached[kTile], s_off[kTile];
+    __shared__ __align__(16) int s_b[kTile];  // read four at a time
     __shared__ uint32_t s_tok[kWarps], s_pg[kWarps];
     __shared__ int s_max[kWarps];
     __shared__ int s_used;
