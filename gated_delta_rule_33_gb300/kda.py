@@ -409,7 +409,7 @@ class PagedCache:
                 raise ValueError("a scale is fp32 [heads] on the cache's device")
         self.k_cache, self.v_cache = k_cache, v_cache
         self.k_scale, self.v_scale = k_scale, v_scale
-        self.device = k_cache.device
+        self.device, self._index = k_cache.device, k_cache.get_device()
         self.num_pages, self.page_size, self.heads, self.head_dim = k_cache.shape
         self._struct = _CacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale),
                                     _p(v_scale), *k_cache.stride()[:3], dtype, num_pages,
@@ -444,11 +444,15 @@ def _rows(t: torch.Tensor, heads: int, head_dim: int):
     return t.data_ptr(), strides[0], shape[0]
 
 
-def _handle(stream, t: torch.Tensor) -> int:
+def _handle(stream, index: int, *tensors: torch.Tensor) -> int:
+    """The stream's handle, once every tensor of the call is known to be on GPU `index`."""
+    if index < 0:
+        raise ValueError("libkda needs CUDA tensors")
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError(f"tensors of one call on one GPU expected: cuda:{index} and {t.device}")
     if stream is None:
-        if not t.is_cuda:
-            raise ValueError("libkda needs CUDA tensors")
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -465,7 +469,8 @@ def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num
         _ptr(cached_lens, i32), _ptr(new_lens, i32), _ptr(free_pages, i32), free_pages.numel(),
         _ptr(block_table, i32), max_pages, B, page_size, num_pages, _ptr(seq_lens, i32),
         _ptr(cu_seqlens, i32), _ptr(slot_map, i32), slot_map.numel(), _ptr(pages_used, i32),
-        _handle(stream, block_table))
+        _handle(stream, block_table.get_device(), cached_lens, new_lens, free_pages, seq_lens,
+                cu_seqlens, slot_map, pages_used))
     if st:
         raise KDAError(st, "kda_page_plan")
 
@@ -478,7 +483,7 @@ def kda_paged_append(k, v, slot_map, cache, stream=None):
     if kn != N or vn != N:
         raise ValueError("k and v need one row per entry of slot_map")
     st = (_lib or load()).kda_paged_append(kp, vp, ks, vs, _ptr(slot_map, torch.int32), N,
-                                           cache._ref, _handle(stream, k))
+                                           cache._ref, _handle(stream, cache._index, k, v, slot_map))
     if st:
         raise KDAError(st, "kda_paged_append")
 
@@ -501,12 +506,13 @@ def kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, workspace, 
         raise ValueError("lse is fp32 [B, q_heads]")
     qp, qs, _ = _rows(q, q_heads, head_dim)
     o_dtype = o.dtype
+    extra = (workspace,) if lse is None else (workspace, lse)
     st = (_lib or load()).kda_paged_decode(
         qp, qs, cache._ref, _ptr(block_table, torch.int32), max_pages,
         _ptr(seq_lens, torch.int32), B, q_heads, scale, _ptr(o, o_dtype),
         KDA_BF16 if o_dtype is torch.bfloat16 else _dtype_code(o),
         None if lse is None else _ptr(lse, torch.float32), _ptr(workspace, workspace.dtype),
-        workspace.nbytes, _handle(stream, q))
+        workspace.nbytes, _handle(stream, cache._index, q, block_table, seq_lens, o, *extra))
     if st:
         raise KDAError(st, "kda_paged_decode")
 
