@@ -10,6 +10,8 @@ KDA; if libkda.so is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 from typing import Optional, Tuple
@@ -539,6 +541,28 @@ def kda_get_last_device_error(stream=None) -> int:
 
 # --- conveniences (allocate outputs with torch, then call the entry points) -----
 
+def _allocates(f):
+    """Lets a convenience allocate on the stream that its kernels run on.  A workspace is
+    dropped while they may still run, and torch gives freed memory out again in the order of
+    the stream that it was allocated on.  (So the outputs are that stream's too: whoever uses
+    them on another waits for it and records that use, as for any torch tensor.)"""
+    names = list(inspect.signature(f).parameters)
+    place = names.index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[place] if len(args) > place else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            first = args[0] if args else kw[names[0]]
+            stream = torch.cuda.ExternalStream(int(stream), first.device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+@_allocates
 def gate(f, b, A_log, dt_bias, alog_mode=KDA_ALOG_PER_CHANNEL, stream=None
          ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     N, H, K = f.shape
@@ -548,6 +572,7 @@ def gate(f, b, A_log, dt_bias, alog_mode=KDA_ALOG_PER_CHANNEL, stream=None
     return g, beta
 
 
+@_allocates
 def prefill(q, k, v, g, beta, cu_seqlens=None, scale=1.0, initial_state=None,
             o_dtype=torch.bfloat16, output_final_state=True, stream=None):
     N, H, K = q.shape
@@ -561,6 +586,7 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, scale=1.0, initial_state=None,
     return o, final
 
 
+@_allocates
 def prefill_gated(q, k, v, f, b, A_log, dt_bias, alog_mode=KDA_ALOG_PER_CHANNEL, cu_seqlens=None,
                   scale=1.0, initial_state=None, o_dtype=torch.bfloat16, output_final_state=True,
                   stream=None):
@@ -576,6 +602,7 @@ def prefill_gated(q, k, v, f, b, A_log, dt_bias, alog_mode=KDA_ALOG_PER_CHANNEL,
     return o, final
 
 
+@_allocates
 def decode_indexed(q, k, v, g, beta, state_pool, state_indices, scale=1.0, o_dtype=torch.bfloat16,
                    stream=None):
     B, H, K = q.shape
@@ -584,6 +611,7 @@ def decode_indexed(q, k, v, g, beta, state_pool, state_indices, scale=1.0, o_dty
     return o
 
 
+@_allocates
 def short_conv(x_q, x_k, x_v, w_q, w_k, w_v, cu_seqlens=None, conv_state=None,
                output_final_state=True, stream=None):
     """The pre-step on the three streams; returns (q, k, v, final conv state or None)."""
@@ -597,6 +625,7 @@ def short_conv(x_q, x_k, x_v, w_q, w_k, w_v, cu_seqlens=None, conv_state=None,
     return q, k, v, final
 
 
+@_allocates
 def short_conv_step(x_q, x_k, x_v, w_q, w_k, w_v, conv_state_pool, state_indices=None,
                     stream=None):
     """One token per sequence; the pool is updated in place.  Returns (q, k, v)."""
@@ -606,6 +635,7 @@ def short_conv_step(x_q, x_k, x_v, w_q, w_k, w_v, conv_state_pool, state_indices
     return q, k, v
 
 
+@_allocates
 def backward(q, k, v, g, beta, dO, cu_seqlens=None, scale=1.0, initial_state=None,
              dS_final=None, want_dS0=True, stream=None):
     """Gradients of the recurrence; returns (dq, dk, dv, dg, dbeta, dS0 or None)."""
@@ -624,6 +654,7 @@ def backward(q, k, v, g, beta, dO, cu_seqlens=None, scale=1.0, initial_state=Non
     return dq, dk, dv, dg, dbeta, dS0
 
 
+@_allocates
 def backward_chunked(q, k, v, g, beta, dO, cu_seqlens=None, scale=1.0, initial_state=None,
                      dS_final=None, want_dS0=True, stream=None):
     """Gradients of the recurrence by the chunked tensor-core backward;
@@ -643,6 +674,7 @@ def backward_chunked(q, k, v, g, beta, dO, cu_seqlens=None, scale=1.0, initial_s
     return dq, dk, dv, dg, dbeta, dS0
 
 
+@_allocates
 def prefill_checkpointed(q, k, v, g, beta, cu_seqlens=None, scale=1.0, initial_state=None,
                          o_dtype=torch.bfloat16, stream=None):
     """The chunked prefill that also keeps the chunk-start states for the backward;
@@ -661,6 +693,7 @@ def prefill_checkpointed(q, k, v, g, beta, cu_seqlens=None, scale=1.0, initial_s
     return o, final, ckpt
 
 
+@_allocates
 def backward_from_checkpoints(q, k, v, g, beta, dO, checkpoints, cu_seqlens=None, scale=1.0,
                               dS_final=None, want_dS0=True, stream=None):
     """Gradients by the chunked backward from the checkpoints of prefill_checkpointed;
@@ -680,6 +713,7 @@ def backward_from_checkpoints(q, k, v, g, beta, dO, checkpoints, cu_seqlens=None
     return dq, dk, dv, dg, dbeta, dS0
 
 
+@_allocates
 def decode_gated(q, k, v, f, b, A_log, dt_bias, state_pool, alog_mode=KDA_ALOG_PER_CHANNEL,
                  state_indices=None, scale=1.0, o_dtype=torch.bfloat16, stream=None):
     B, H, K = q.shape
@@ -689,6 +723,7 @@ def decode_gated(q, k, v, f, b, A_log, dt_bias, state_pool, alog_mode=KDA_ALOG_P
     return o
 
 
+@_allocates
 def gate_backward(f, b, A_log, dt_bias, dg, dbeta, alog_mode=KDA_ALOG_PER_CHANNEL,
                   stream=None):
     """Returns (df, db or None, dA_log, ddt_bias)."""
@@ -704,6 +739,7 @@ def gate_backward(f, b, A_log, dt_bias, dg, dbeta, alog_mode=KDA_ALOG_PER_CHANNE
     return df, db, dA, ddt
 
 
+@_allocates
 def decode(q, k, v, g, beta, state, scale=1.0, o_dtype=torch.bfloat16, stream=None):
     B, H, K = q.shape
     o = torch.empty(B, H, v.shape[-1], dtype=o_dtype, device=q.device)
@@ -711,6 +747,7 @@ def decode(q, k, v, g, beta, state, scale=1.0, o_dtype=torch.bfloat16, stream=No
     return o
 
 
+@_allocates
 def page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, num_tokens,
               stream=None):
     """Places a step's num_tokens new tokens (block_table is extended in place); returns
@@ -723,6 +760,7 @@ def page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num_pag
     return seq_lens, cu, slots, used
 
 
+@_allocates
 def paged_decode(q, cache, block_table, seq_lens, scale=1.0, o_dtype=torch.bfloat16,
                  want_lse=False, stream=None):
     """Attention of one new token per sequence over the paged cache; returns (o, lse or None)."""
