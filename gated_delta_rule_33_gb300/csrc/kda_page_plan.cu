@@ -26,18 +26,15 @@ __device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x +
 
 // Four consecutive values of a list of n; zeros past its end.
 __device__ __forceinline__ int4 load4(const int32_t *p, int64_t i, int64_t n) {
-    if (i + 4 <= n) return __ldg(reinterpret_cast<const int4 *>(p + i));
-    return make_int4(i < n ? __ldg(p + i) : 0, i + 1 < n ? __ldg(p + i + 1) : 0,
-                     i + 2 < n ? __ldg(p + i + 2) : 0, 0);
+    if (i + 4 <= n) return *reinterpret_cast<const int4 *>(p + i);
+    return make_int4(i < n ? p[i] : 0, i + 1 < n ? p[i + 1] : 0, i + 2 < n ? p[i + 2] : 0, 0);
 }
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) plan_kernel(
-    const int32_t *__restrict__ cached_lens, const int32_t *__restrict__ new_lens,
-    const int32_t *__restrict__ free_pages, int num_free, int32_t *block_table, int max_pages,
-    int B, FastDiv page, int num_pages, int32_t *__restrict__ seq_lens,
-    int32_t *__restrict__ cu_seqlens, int32_t *__restrict__ slot_map, int64_t N,
-    int32_t *__restrict__ pages_used, unsigned int *err) {
+    const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages, int num_free,
+    int32_t *block_table, int max_pages, int B, FastDiv page, int num_pages, int32_t *seq_lens,
+    int32_t *cu_seqlens, int32_t *slot_map, int64_t N, int32_t *pages_used, unsigned int *err) {
     constexpr int kTile = kThreads * kItems, kWarps = kThreads / 32;
     // a request at its first token in the CTA's range: its first row (which may lie before
     // the range) and tokens, its cached tokens, its place in the free list; its number, -1
@@ -175,11 +172,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(
     int p[kItems];
     uint32_t r[kItems];
     bool placed[kItems];
+    int64_t taken[kItems];  // the table's entry for a page that the token begins, -1: none
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int at = max(from[i], before) - 1;
         placed[i] = false;
         p[i] = -1;
+        taken[i] = -1;
         if (t + i >= t1 || at < 0) continue;
         const int b = s_b[at], cached = s_cached[at];
         const int64_t j = t + i - s_cu[at];
@@ -192,10 +191,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(
         if (static_cast<int>(idx) < held) {
             p[i] = block_table[entry];
         } else {
-            p[i] = __ldg(free_pages + s_off[at] + static_cast<int>(idx) - held);
-            if (r[i] == 0) block_table[entry] = p[i];
+            p[i] = free_pages[s_off[at] + static_cast<int>(idx) - held];
+            if (r[i] == 0) taken[i] = entry;
         }
     }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (taken[i] >= 0) block_table[taken[i]] = p[i];
     int slot[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {

@@ -33,9 +33,23 @@ struct FastDiv {
 // The paged kernels are launched so that their blocks may be set up while the kernel
 // before them ends (programmatic dependent launch): they wait for that kernel, all of
 // it, before they touch memory, and only then let the next one be set up.
+//
+// What they read after the wait may have been written while they were being set up, so
+// it is read by ordinary loads: not by __ldg or through __restrict__, which promise that
+// the data stays as it is for as long as the kernel lives and which nothing keeps below
+// the wait.
 __device__ __forceinline__ void wait_for_kernel_before() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// An ordinary 16-byte load whose data is not wanted again.
+__device__ __forceinline__ uint4 load_once(const uint4 *p) {
+    uint4 x;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
 }
 
 template <class... Params, class... Args>

@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t to_e4m3x4(const uint32_t lo, const uint32_t 
 // cache): 16 bytes of the cache.
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads) append_kernel(
-    const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v, int64_t k_row_stride,
-    int64_t v_row_stride, const int32_t *__restrict__ slot_map, int64_t N, const PagedView cache,
+    const __nv_bfloat16 *k, const __nv_bfloat16 *v, int64_t k_row_stride,
+    int64_t v_row_stride, const int32_t *slot_map, int64_t N, const PagedView cache,
     FastDiv row, int dim_shift, unsigned int *err) {
     constexpr int kVals = kFp8 ? 16 : 8;
     wait_for_kernel_before();
@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
         const int64_t n = n0 + dn;
         slot[i] = -1;
         if (n < N) {
-            slot[i] = __ldg(slot_map + n);
+            slot[i] = slot_map[n];
             const int flat = static_cast<int>(u) * kVals;
             head[i] = flat >> dim_shift;
             dim[i] = flat - (head[i] << dim_shift);
             const uint4 *src = reinterpret_cast<const uint4 *>(x + n * x_stride + flat);
-            val[i][0] = __ldcs(src);
-            if constexpr (kFp8) val[i][1] = __ldcs(src + 1);
+            val[i][0] = load_once(src);
+            if constexpr (kFp8) val[i][1] = load_once(src + 1);
         }
     }
 #pragma unroll
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
                       head[i] * cache.head_stride + dim[i] * (kFp8 ? 1 : 2);
         uint4 out;
         if constexpr (kFp8) {
-            const float y = scales == nullptr ? 1.f : __ldg(scales + head[i]);
+            const float y = scales == nullptr ? 1.f : scales[head[i]];
             const float rcp = __frcp_rn(y);
             out.x = to_e4m3x4(val[i][0].x, val[i][0].y, y, rcp);
             out.y = to_e4m3x4(val[i][0].z, val[i][0].w, y, rcp);

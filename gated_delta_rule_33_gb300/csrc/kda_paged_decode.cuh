@@ -230,7 +230,7 @@ __device__ __forceinline__ int64_t div64(int64_t n, uint32_t d) {
 }
 
 __device__ __forceinline__ int valid_len(const Args &a, int b) {
-    const int n = __ldg(a.seq_lens + b);
+    const int n = a.seq_lens[b];
     return n < 0 || n > static_cast<int64_t>(a.max_pages) * a.cache.page.d ? 0 : n;
 }
 
@@ -342,7 +342,7 @@ struct Copier {
             held[i] = r < kKeys && j < static_cast<uint32_t>(at.len);
             page[i] = -1;
             if (held[i])
-                page[i] = __ldg(a.block_table + static_cast<int64_t>(at.b) * a.max_pages + idx);
+                page[i] = a.block_table[static_cast<int64_t>(at.b) * a.max_pages + idx];
         }
     }
 
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                 const __nv_bfloat16 *q = a.q + cur.b * a.q_row_stride +
                                          (rows.out_row - static_cast<int64_t>(cur.b) * a.q_heads) * kD;
                 const float factor = a.scale * kLog2e *
-                                     (a.cache.k_scale == nullptr ? 1.f : __ldg(a.cache.k_scale + rows.h));
+                                     (a.cache.k_scale == nullptr ? 1.f : a.cache.k_scale[rows.h]);
                 // a negative factor's sign goes to the queries; zero times a left-out key's
                 // -inf would be NaN
                 const float base = fmaxf(fabsf(factor), FLT_MIN);
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 #pragma unroll
                         for (int c = 0; c < kOT; ++c) {
                             uint2 z = make_uint2(0, 0);
-                            if (real) z = __ldg(reinterpret_cast<const uint2 *>(x + 16 * c + 4 * tq));
+                            if (real) z = *reinterpret_cast<const uint2 *>(x + 16 * c + 4 * tq);
                             qf[c][n][0] = z.x;
                             qf[c][n][1] = z.y;
                             const float2 u0 = unpack2<false>(z.x), u1 = unpack2<false>(z.y);
@@ -703,8 +703,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                         for (int c = 0; c < kOT; ++c)
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                qf[c][n][i] = real ? __ldg(reinterpret_cast<const uint32_t *>(
-                                                         x + 16 * c + 8 * i + 2 * tq)) ^ sign
+                                qf[c][n][i] = real ? *reinterpret_cast<const uint32_t *>(
+                                                         x + 16 * c + 8 * i + 2 * tq) ^ sign
                                                    : 0;
                     }
                     if constexpr (S::kQShared) {
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                         s_part[at].in_global = remaining != 0;
                     }
                 }
-                const float vs = a.cache.v_scale == nullptr ? 1.f : __ldg(a.cache.v_scale + rows.h);
+                const float vs = a.cache.v_scale == nullptr ? 1.f : a.cache.v_scale[rows.h];
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
     // ---- sequences without keys ----------------------------------------------------------
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (valid_len(a, b) > 0) continue;
-        if (tid == 0 && __ldg(a.seq_lens + b) != 0) record_device_error(a.err, kDevInvalidArg);
+        if (tid == 0 && a.seq_lens[b] != 0) record_device_error(a.err, kDevInvalidArg);
         for (int i = tid; i < a.q_heads * (kD / 4); i += kThreads)
             write_out<S::kWide>(a, static_cast<int64_t>(b) * a.q_heads * kD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
         if (a.lse != nullptr)
@@ -1099,8 +1099,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     __shared__ float4 s_sum[kGroups][kItems];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x;
-    // (the first kernel's blocks have all waited for what was before them, so the lengths
-    // may be read here)
+    // (this kernel is set up once the first one's blocks have all waited for what was before
+    // them, so the lengths, which the first one does not write, may be read here)
     const List<S> list(a, lane, gridDim.x);
     const int64_t hi = list.even_begin(c0 + int64_t{1});
     bool mine = !list.whole && c0 < static_cast<int>(list.ctas) && hi < list.total;
