@@ -152,6 +152,9 @@ struct Shape {
     static_assert(kSlots >= 3 && kSlots <= 7, "the masks' ring holds the tiles in flight");
 };
 
+// x, or the least normal number where x is below it; a NaN stays (fmaxf would drop it).
+__device__ __forceinline__ float at_least_normal(float x) { return x < FLT_MIN ? FLT_MIN : x; }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                                      (a.cache.k_scale == nullptr ? 1.f : a.cache.k_scale[rows.h]);
                 // a negative factor's sign goes to the queries; zero times a left-out key's
                 // -inf would be NaN
-                const float base = fmaxf(fabsf(factor), FLT_MIN);
+                const float base = at_least_normal(fabsf(factor));
                 const uint32_t sign = factor < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                                 qf[c][n][i] = pack2<true>(u.x * f1 * f2, u.y * f1 * f2) ^ sign;
                             }
                         // the scores' columns are heads 2 tq, 2 tq + 1
-                        const float mine_sc = fmaxf(base / f1 / f2, FLT_MIN);
+                        const float mine_sc = at_least_normal(base / f1 / f2);
                         sc[n][0] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq);
                         sc[n][1] = __shfl_sync(0xffffffffu, mine_sc, 8 * tq + 4);
                     } else {
