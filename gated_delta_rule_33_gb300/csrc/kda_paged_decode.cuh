@@ -580,9 +580,11 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
     constexpr int kBlocks = kKeys / 16;   // score blocks of 16 keys
     constexpr int kOT = kD / 16;          // output blocks of 16 channels
     constexpr int kParts = 2 * kWarps;
-    // log2 of what the weights are multiplied by, and of the most that one may be over 1:
-    // together below fp16's 2^16
-    constexpr float kUp = kF16 ? 8.f : 0.f, kSlack = 7.f;
+    // log2 of the most that a weight may be over 1 (see the reference below), and of what
+    // the weights are multiplied by: with it at most 1, so that no sum leaves fp32 that a
+    // sum of weights times values would not, or over 8 bits, where values are small, just
+    // below fp16's 2^16
+    constexpr float kSlack = 7.f, kUp = kF16 ? 15.f - kSlack : -kSlack;
     static_assert(kParts <= 32, "a warp finds the runs");
 
     extern __shared__ __align__(1024) uint8_t s_ring[];
