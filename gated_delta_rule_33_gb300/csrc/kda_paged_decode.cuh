@@ -161,6 +161,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The largest of three, NaN where one of them is.
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
+}
+
 // Volatile: they stay between the wait for a tile and the copy that replaces it.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -571,6 +578,82 @@ struct List {
     }
 };
 
+__device__ __forceinline__ bool any_nonfinite(uint32_t two_bf16) {
+    return (two_bf16 & 0x7f80u) == 0x7f80u || (two_bf16 & 0x7f800000u) == 0x7f800000u;
+}
+
+// An infinite value times a weight in words is a NaN, from the words that are 0 or negative.
+// So where a sum of the part of a unit that keys j0 .. j1 - 1 make is NaN, it is taken again
+// over the infinite and NaN values alone, with whole weights, as fp32 arithmetic has it; a
+// sum that meets none stays NaN.  Rare and slow: not inlined, and nothing of it is on the way
+// of finite values (inlined it costs the kernel registers: 64 ragged sequences 127 -> 130 us,
+// 12 heads of 256 160 -> 265).
+// The unit: of sequence b, query heads `out_row` .. + rows - 1 on key head h.  sums: the
+// lane's, [d][n][4]; sc, minus: [n][2], as in the kernel.
+template <class S>
+__device__ __noinline__ void nonfinite_sums(const Args &a, int b, int h, int num_rows,
+                                            int64_t out_row, int64_t j0, int64_t j1, float *sums,
+                                            const float *sc, const float *minus) {
+    constexpr int kD = S::kD, kN = S::kN, kSums = kD / 4 * kN;
+    const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+    uint32_t was[(kSums + 31) / 32] = {};  // the sums that are NaN
+#pragma unroll
+    for (int e = 0; e < kSums; ++e)
+        if (isnan(sums[e])) {
+            was[e / 32] |= 1u << (e % 32);
+            sums[e] = 0.f;
+        }
+    const __nv_bfloat16 *q = a.q + b * a.q_row_stride + (out_row - static_cast<int64_t>(b) * a.q_heads) * kD;
+#pragma unroll 1
+    for (; j0 < j1; j0 += 32) {
+        // a lane looks through a key's values
+        int64_t off = 0;
+        bool hit = false;
+        if (j0 + lane < j1) {
+            uint32_t idx, r;
+            a.cache.page.divmod(static_cast<uint32_t>(j0 + lane), idx, r);
+            const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + idx];
+            if (page >= 0 && page < a.cache.num_pages) {
+                off = page * a.cache.page_stride + r * a.cache.token_stride + h * a.cache.head_stride;
+                const uint4 *v = reinterpret_cast<const uint4 *>(a.cache.v + off);
+#pragma unroll 4
+                for (int c = 0; c < kD / 8; ++c) {
+                    const uint4 x = v[c];
+                    hit |= any_nonfinite(x.x) || any_nonfinite(x.y) || any_nonfinite(x.z) ||
+                           any_nonfinite(x.w);
+                }
+            }
+        }
+#pragma unroll 1
+        for (uint32_t hits = __ballot_sync(0xffffffffu, hit); hits != 0; hits &= hits - 1) {
+            const int64_t at = __shfl_sync(0xffffffffu, off, __ffs(hits) - 1);
+            const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(a.cache.k + at);
+            const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(a.cache.v + at);
+            float w[kN][2] = {};
+#pragma unroll 1
+            for (int row = 0; row < num_rows; ++row) {
+                float dot = 0.f;
+                for (int c = lane; c < kD; c += 32)
+                    dot = fmaf(bf16_to_f32(q[row * kD + c]), bf16_to_f32(k[c]), dot);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+                if (a.scale < 0.f) dot = -dot;
+#pragma unroll
+                for (int e = 0; e < 2 * kN; ++e)
+                    if (row == 8 * (e / 2) + 2 * tq + e % 2) w[e / 2][e % 2] = ex2(fmaf(dot, sc[e], minus[e]));
+            }
+#pragma unroll
+            for (int e = 0; e < kSums; ++e) {
+                const float x = bf16_to_f32(v[16 * (e / (kN * 4)) + g + 8 * (e % 4 / 2)]);
+                if (!isfinite(x) && (was[e / 32] >> (e % 32) & 1) != 0) sums[e] += w[e / 4 % kN][e % 2] * x;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kSums; ++e)
+        if ((was[e / 32] >> (e % 32) & 1) != 0 && sums[e] == 0.f) sums[e] = NAN;
+}
+
 template <class S, bool kOnePage>
 __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const __grid_constant__ Args a) {
     constexpr int kD = S::kD, kN = S::kN, kHeads = S::kHeads;
@@ -924,6 +1007,33 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
                         m[n][i] -= kUp;  // the sums carry 2^kUp
                     }
+                if constexpr (!kFp8) {  // (8 bits hold no infinity)
+                    bool nan = false;
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float t[2] = {l[n][i], l[n][i]};
+#pragma unroll
+                            for (int d = 0; d < kOT; ++d) t[d & 1] = max3_nan(t[d & 1], acc[d][n][i], acc[d][n][i + 2]);
+                            nan |= isnan(t[0] + t[1]) && !isnan(l[n][i]);
+                        }
+                    if (__any_sync(0xffffffffu, nan)) {
+                        float sums[kOT * kN * 4], of_heads[2][kN * 2];
+#pragma unroll
+                        for (int e = 0; e < kOT * kN * 4; ++e) sums[e] = acc[e / (kN * 4)][e / 4 % kN][e % 4];
+#pragma unroll
+                        for (int e = 0; e < kN * 2; ++e) {
+                            of_heads[0][e] = sc[e / 2][e % 2];
+                            of_heads[1][e] = minus[e / 2][e % 2];
+                        }
+                        nonfinite_sums<S>(a, cur.b, rows.h, rows.rows, rows.out_row, begun * kKeys,
+                                          min(int64_t{cur.len}, (cur.t + int64_t{1}) * kKeys), sums,
+                                          of_heads[0], of_heads[1]);
+#pragma unroll
+                        for (int e = 0; e < kOT * kN * 4; ++e) acc[e / (kN * 4)][e / 4 % kN][e % 4] = sums[e];
+                    }
+                }
                 const bool whole = ends && begun == 0;
                 float *part = nullptr;
                 int pitch = kD;

@@ -657,8 +657,10 @@ size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int hea
  * An empty sequence gives o = 0 and lse = -inf.  A length below 0 or above
  * max_pages * page_size counts as empty, and keys on a page outside
  * 0 .. num_pages-1 are left out; both set INVALID_ARG in the device error word.
- * Memory past a sequence's last key is not read.  Two calls on the same inputs
- * write the same bits.  B == 0 is a no-op.
+ * Memory past a sequence's last key is not read.  Infinities and NaN among q, the
+ * keys and the values act as in fp32 arithmetic (an infinite value of a key with
+ * weight gives an infinite output; a call that meets one takes longer).  Two calls
+ * on the same inputs write the same bits.  B == 0 is a no-op.
  */
 kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged_cache *cache,
                             const int32_t *block_table, int max_pages, const int32_t *seq_lens,
