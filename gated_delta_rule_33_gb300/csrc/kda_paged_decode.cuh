@@ -49,8 +49,12 @@
 // 5e-7): an fp32 output takes each tile's products in a sum of their own and adds
 // it in fp32.  An 8-bit cache is widened to fp16, which holds every e4m3 value; the
 // queries are scaled by a power of two for each head, so that fp16 holds their bf16
-// values too, and the weights are two fp16 numbers, 22 bits, times 2^8 to keep
-// small ones normal.
+// values too, and the weights are two fp16 numbers, 22 bits, of the weight times 2^13
+// (2^12).  fp16 ends at 2^-24, so these words keep a weight to 2^-38 of the largest,
+// which a bf16 output covers.  For an fp32 output the second word is 2^12 times larger,
+// its products have a sum of their own in each tile, and a weight is kept to 2^-49 of
+// the largest (fp32 outputs of 16 heads over 8 bits 189.6 us without that, 195.7 with
+// it; 8 heads of 256 153 and 161).  The sums of the weights are fp32 throughout.
 #pragma once
 
 #include <cfloat>
@@ -664,10 +668,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
     constexpr int kOT = kD / 16;          // output blocks of 16 channels
     constexpr int kParts = 2 * kWarps;
     // log2 of the most that a weight may be over 1 (see the reference below), and of what
-    // the weights are multiplied by: with it at most 1, so that no sum leaves fp32 that a
-    // sum of weights times values would not, or over 8 bits, where values are small, just
-    // below fp16's 2^16
-    constexpr float kSlack = 7.f, kUp = kF16 ? 15.f - kSlack : -kSlack;
+    // the weights are multiplied by.  With it at most 1 over bf16, so that no sum leaves
+    // fp32 that a sum of weights times values would not; just below fp16's 2^16 over 8 bits,
+    // where values are small: what the words drop is then a fixed part of the largest weight
+    // (see Precision), smaller the nearer the reference is (16 heads 184.0 us with 7, 184.8
+    // with 3, 185.4 with 2, 187.1 with 1).
+    constexpr float kSlack = !kF16 ? 7.f : kWide ? 3.f : 2.f, kUp = kF16 ? 15.f - kSlack : -kSlack;
+    // what an fp32 output's second fp16 word is multiplied by: below 2^15 then, like the first
+    constexpr float kLow = kF16 && kWide ? 4096.f : 1.f;
     static_assert(kParts <= 32, "a warp finds the runs");
 
     extern __shared__ __align__(1024) uint8_t s_ring[];
@@ -923,7 +931,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                         const uint32_t w = pack2<kF16>(x, y);
                         const float2 first = unpack2<kF16>(w);
                         p[k][n][j] = transpose8(w);
-                        const uint32_t w2 = pack2<kF16>(x - first.x, y - first.y);
+                        const uint32_t w2 = pack2<kF16>((x - first.x) * kLow, (y - first.y) * kLow);
                         p2[k][n][j] = transpose8(w2);
                         if constexpr (kThird) {
                             const float2 second = unpack2<kF16>(w2);
@@ -940,15 +948,16 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
             const uint32_t vt = ring + slot * S::kHalf;
             slot = next_slot(slot);
             constexpr int kStep = kFp8 ? 2 : 1;   // blocks of 16 channels to a load
-            // channels 16 d .. of the 16 keys k: to[i], block d + i, += their products
-            auto products = [&](int k, int d, float(*to)[kN][4]) {
+            // channels 16 d .. of the 16 keys k: to[i], block d + i, += their products with the
+            // weights' first words, and second[i] (may be to[i]) with the others
+            auto products = [&](int k, int d, float(*to)[kN][4], float(*second)[kN][4]) {
                 uint32_t r[4];
                 auto product = [&](int i, const uint32_t (&f)[4]) {
 #pragma unroll
                     for (int n = 0; n < kN; ++n) {
                         mma<kF16>(to[i][n], f, p[k][n][0], p[k][n][1]);
-                        mma<kF16>(to[i][n], f, p2[k][n][0], p2[k][n][1]);
-                        if constexpr (kThird) mma<kF16>(to[i][n], f, p3[k][n][0], p3[k][n][1]);
+                        mma<kF16>(second[i][n], f, p2[k][n][0], p2[k][n][1]);
+                        if constexpr (kThird) mma<kF16>(second[i][n], f, p3[k][n][0], p3[k][n][1]);
                     }
                 };
                 if constexpr (kFp8) {
@@ -972,26 +981,32 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
             if constexpr (kWide) {
 #pragma unroll
                 for (int d = 0; d < kOT; d += kStep) {
-                    float own[kStep][kN][4];      // this tile's products
-#pragma unroll
-                    for (int i = 0; i < kStep; ++i)
-#pragma unroll
-                        for (int n = 0; n < kN; ++n)
-                            own[i][n][0] = own[i][n][1] = own[i][n][2] = own[i][n][3] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) products(k, d, own);
+                    // this tile's products in a sum of their own; scaled words' in another
+                    float own[kStep][kN][4], low[kStep][kN][4];
 #pragma unroll
                     for (int i = 0; i < kStep; ++i)
 #pragma unroll
                         for (int n = 0; n < kN; ++n)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[d + i][n][j] += own[i][n][j];
+                            for (int j = 0; j < 4; ++j) own[i][n][j] = low[i][n][j] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) products(k, d, own, kF16 ? low : own);
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i)
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float &sum = acc[d + i][n][j];
+                                sum += own[i][n][j];
+                                if constexpr (kF16) sum = fmaf(low[i][n][j], 1.f / kLow, sum);
+                            }
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                    for (int d = 0; d < kOT; d += kStep) products(k, d, acc + d);
+                    for (int d = 0; d < kOT; d += kStep) products(k, d, acc + d, acc + d);
             }
 
             // ---- the end of a unit, or of the warp's part

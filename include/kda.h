@@ -648,7 +648,8 @@ size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int hea
  *   q_heads     a positive multiple of cache->heads
  *   o           [B, q_heads, head_dim] of o_dtype (bf16 or fp32), written; a
  *               softmax weight is kept to 16 bits for bf16 outputs, 22 or more for
- *               fp32 ones
+ *               fp32 ones; over an 8-bit cache, to that or to 2^-37 (fp32 outputs:
+ *               2^-48) of the largest weight, whichever is coarser
  *   lse         fp32 [B, q_heads] written, or NULL: with fp32 outputs, what joins
  *               the results over two sets of keys
  *   workspace   device scratch, >= kda_paged_decode_workspace_size() bytes,
