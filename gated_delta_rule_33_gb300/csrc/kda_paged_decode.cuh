@@ -45,9 +45,10 @@
 // output (one would leave up to 2^-8 of every weight, as much as the output's own
 // rounding), three, 24 bits, for an fp32 one; the products are free here (see
 // Bound).  The matrix instructions cut their sums off instead of rounding them,
-// which adds up over some hundred tiles (2.7e-6 of an fp32 output, fp32 arithmetic
-// 5e-7): an fp32 output takes each tile's products in a sum of their own and adds
-// it in fp32.  An 8-bit cache is widened to fp16, which holds every e4m3 value; the
+// which adds up over a warp's tiles (some 4e-5 over 300; fp32 arithmetic 5e-7): an fp32 output, and a bf16 one of up to 8 heads, takes each tile's
+// products in a sum of their own and adds it in fp32.  A bf16 output of more heads does
+// not, where that costs up to 12 % (32 heads 205 and 230 us; 8 heads 140.4 and 140.9).
+// An 8-bit cache is widened to fp16, which holds every e4m3 value; the
 // queries are scaled by a power of two for each head, so that fp16 holds their bf16
 // values too, and the weights are two fp16 numbers, 22 bits, of the weight times 2^13
 // (2^12).  fp16 ends at 2^-24, so these words keep a weight to 2^-38 of the largest,
@@ -144,6 +145,8 @@ struct Shape {
     // key heads may go side by side (see List): short rows, and HBM-bound
     static constexpr bool kSide = kRowBytes < 256 && (kD == 64 || kN == 1);
     static constexpr int kHeads = 8 * kN;
+    // each tile's products in sums of their own (see Precision)
+    static constexpr bool kApart = kWide || kN == 1;
     static constexpr int kPitch = kD + 4;                                  // floats of a part's row
     // the ring takes the warp's last part in the end
     static constexpr int kRing = max_of(kSlots * kHalf, (kHeads * kPitch * 4 + 1023) / 1024 * 1024);
@@ -978,7 +981,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                     product(0, r);
                 }
             };
-            if constexpr (kWide) {
+            if constexpr (S::kApart) {
 #pragma unroll
                 for (int d = 0; d < kOT; d += kStep) {
                     // this tile's products in a sum of their own; scaled words' in another
@@ -990,7 +993,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
 #pragma unroll
                             for (int j = 0; j < 4; ++j) own[i][n][j] = low[i][n][j] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) products(k, d, own, kF16 ? low : own);
+                    for (int k = 0; k < kBlocks; ++k) products(k, d, own, kLow != 1.f ? low : own);
 #pragma unroll
                     for (int i = 0; i < kStep; ++i)
 #pragma unroll
@@ -999,7 +1002,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) paged_decode_kernel(const _
                             for (int j = 0; j < 4; ++j) {
                                 float &sum = acc[d + i][n][j];
                                 sum += own[i][n][j];
-                                if constexpr (kF16) sum = fmaf(low[i][n][j], 1.f / kLow, sum);
+                                if constexpr (kLow != 1.f) sum = fmaf(low[i][n][j], 1.f / kLow, sum);
                             }
                 }
             } else {
