@@ -45,9 +45,10 @@
 // output (one would leave up to 2^-8 of every weight, as much as the output's own
 // rounding), three, 24 bits, for an fp32 one; the products are free here (see
 // Bound).  The matrix instructions cut their sums off instead of rounding them,
-// which adds up over a warp's tiles (some 4e-5 over 300; fp32 arithmetic 5e-7): an fp32 output, and a bf16 one of up to 8 heads, takes each tile's
-// products in a sum of their own and adds it in fp32.  A bf16 output of more heads does
-// not, where that costs up to 12 % (32 heads 205 and 230 us; 8 heads 140.4 and 140.9).
+// which adds up over a warp's tiles (4e-5 over 300; fp32 arithmetic 5e-7): an fp32
+// output, and a bf16 one of up to 8 heads, takes each tile's products in a sum of their
+// own and adds it in fp32.  A bf16 output of more heads does not, where that costs up to
+// 12 % (32 heads 205 and 230 us; 8 heads 140.4 and 140.9).
 // An 8-bit cache is widened to fp16, which holds every e4m3 value; the
 // queries are scaled by a power of two for each head, so that fp16 holds their bf16
 // values too, and the weights are two fp16 numbers, 22 bits, of the weight times 2^13
