@@ -145,6 +145,13 @@ kda_status paged_view(const kda_paged_cache *c, kda::PagedView *view) {
     return KDA_OK;
 }
 
+// Whether kda_paged_decode takes so many query heads and sequences.
+bool paged_decode_sizes(int B, int q_heads, int kv_heads, int head_dim) {
+    return q_heads % kv_heads == 0 && static_cast<int64_t>(q_heads) * head_dim <= INT32_MAX &&
+           static_cast<int64_t>(kv_heads) * head_dim <= INT32_MAX / 4 &&
+           static_cast<int64_t>(B) * q_heads <= INT32_MAX;
+}
+
 }  // namespace
 
 namespace kda {
@@ -726,8 +733,9 @@ kda_status kda_paged_append(const void *k, const void *v, int64_t k_row_stride,
 }
 
 size_t kda_paged_decode_workspace_size(int B, int q_heads, int kv_heads, int head_dim) {
-    if (B < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
-        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    if (B < 0 || kv_heads < 1 || q_heads < 1 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        !paged_decode_sizes(B, q_heads, kv_heads, head_dim))
         return 0;
     return kda::paged_decode_workspace_bytes(B, q_heads, kv_heads, head_dim);
 }
@@ -740,10 +748,8 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
     kda_status st = paged_view(cache, &view);
     if (st != KDA_OK) return st;
     if (B < 0 || max_pages < 0 || q_heads < 1) return KDA_ERR_INVALID_ARG;
-    if (q_heads % view.heads != 0) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!paged_decode_sizes(B, q_heads, view.heads, view.head_dim)) return KDA_ERR_UNSUPPORTED_SHAPE;
     const int64_t width = static_cast<int64_t>(q_heads) * view.head_dim;
-    if (width > INT32_MAX || static_cast<int64_t>(B) * q_heads > INT32_MAX)
-        return KDA_ERR_UNSUPPORTED_SHAPE;
     if (!valid_dtype(o_dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
     if (B > 0 && (q == nullptr || seq_lens == nullptr || o == nullptr ||
                   (max_pages > 0 && block_table == nullptr)))
