@@ -18,16 +18,16 @@
 // the warps' instructions.
 //
 // Split.  A unit is (sequence, key head, group of 8, 16, 24 or 32 query heads); its keys
-// are cut in tiles of 4 KB of keys and 4 KB of values (8 KB each at 256 channels
-// in bf16, 2 KB for 24 or 32 heads).  The tiles of all units form one list; each CTA takes an equal,
-// contiguous piece of it and each warp an equal part of that: long sequences are
-// cut, short ones share a warp.  A warp's part ends in at most two cut units;
+// are cut in tiles of 4 KB of keys and 4 KB of values (2 KB each for 24 or 32 heads,
+// but 16 keys at least: 8 KB at 256 channels in bf16, 4 KB at 128).  The tiles of all
+// units form one list; each CTA takes an equal, contiguous piece of it and each warp an
+// equal part of that: long sequences are cut, short ones share a warp.  A warp's part ends in at most two cut units;
 // their parts are joined within the CTA through shared memory, and what is cut
 // between CTAs by a second, small kernel that is launched with the first and
 // waits for it (programmatic dependent launch; a join by the CTA that is last to write
-// its part ends 2 us later: fences and a count cost more than the kernel).  Where the block table has no
-// room for long sequences, the pieces are moved to the units' ends instead, and
-// the second kernel is not launched.
+// its part ends 2 us later: fences and a count cost more than the kernel).  Where the
+// block table has no room for long sequences, the pieces are moved to the units' ends
+// instead, and the second kernel is not launched.
 //
 // A warp copies its own tiles, by 16-byte cp.async into its own ring of tile
 // halves (no barrier between warps); the page numbers of a tile are read one tile
@@ -70,7 +70,7 @@
 namespace kda {
 namespace paged {
 
-constexpr int kMaxCtas = 160;  // at most the join kernel's threads
+constexpr int kMaxCtas = 160;  // sizes the workspace and the join's weights; more SMs stay idle
 constexpr int kMaxWarps = 12;
 constexpr int kMaxSide = 4;   // key heads side by side
 
@@ -135,14 +135,17 @@ struct Shape {
     static constexpr int kD = kD_, kN = kN_;
     static constexpr bool kFp8 = kFp8_, kWide = kWide_;
     static constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
-    // keys of a tile: 4 KB of them, 2 KB where 24 or 32 heads' scores would fill the registers
+    // keys of a tile: 4 KB of them, 2 KB where 24 or 32 heads' scores would fill the registers,
+    // but 16, the rows of a product, in any case (8 KB of 256 channels in bf16; of 128, 4 KB)
     static constexpr int kKeys = max_of(16, (kN >= 3 ? 2048 : 4096) / kRowBytes);
     static constexpr int kHalf = kKeys * kRowBytes;                        // its keys, in bytes
     static constexpr int kWarps = kD == 256 || kN == 4 || (kN == 3 && kD == 128) ? 8 : 12;
     static_assert(kWarps % kMaxSide == 0, "heads side by side share the warps evenly");
-    // halves of a warp's ring: some 96 KB in flight an SM (more gain nothing, and keep
-    // the SMs further apart: one sequence of 262149 keys 168 us at 96, 181 at 144 KB)
-    static constexpr int kSlots = kHalf < 4096 ? 7 : kWarps == 12 || kHalf > 4096 ? 3 : 4;
+    // halves of a warp's ring: one that is read, and 96 KB in flight an SM in the others
+    // (more gain nothing, and keep the SMs further apart: one sequence of 262149 keys 168 us
+    // at 96, 181 at 144 KB; 24 heads of 64 104.0 and 104.6), but two of them in any case
+    // (128 KB at 256 channels in bf16)
+    static constexpr int kSlots = max_of(2, 96 * 1024 / (kWarps * kHalf)) + 1;
     // key heads may go side by side (see List): short rows, and HBM-bound
     static constexpr bool kSide = kRowBytes < 256 && (kD == 64 || kN == 1);
     static constexpr int kHeads = 8 * kN;
