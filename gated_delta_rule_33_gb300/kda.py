@@ -446,13 +446,14 @@ def _rows(t: torch.Tensor, heads: int, head_dim: int):
     return t.data_ptr(), strides[0], shape[0]
 
 
-def _handle(stream, index: int, *tensors: torch.Tensor) -> int:
-    """The stream's handle, once every tensor of the call is known to be on GPU `index`."""
+def _elsewhere(index: int, *tensors: torch.Tensor) -> ValueError:
+    """What to raise where the tensors of one call are not all on GPU `index`."""
     if index < 0:
-        raise ValueError("libkda needs CUDA tensors")
-    for t in tensors:
-        if t.get_device() != index:
-            raise ValueError(f"tensors of one call on one GPU expected: cuda:{index} and {t.device}")
+        return ValueError("libkda needs CUDA tensors")
+    return ValueError(f"tensors on cuda:{index} expected, got {[str(t.device) for t in tensors]}")
+
+
+def _handle(stream, index: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
@@ -466,13 +467,18 @@ def kda_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, num
     if (cached_lens.numel() != B or new_lens.numel() != B or seq_lens.numel() != B
             or cu_seqlens.numel() != B + 1 or pages_used.numel() != 1):
         raise ValueError("cached_lens, new_lens, seq_lens [B], cu_seqlens [B+1], pages_used [1]")
+    gpu = block_table.get_device()
+    if not (0 <= gpu == cached_lens.get_device() == new_lens.get_device() == free_pages.get_device()
+            == seq_lens.get_device() == cu_seqlens.get_device() == slot_map.get_device()
+            == pages_used.get_device()):
+        raise _elsewhere(gpu, cached_lens, new_lens, free_pages, seq_lens, cu_seqlens, slot_map,
+                         pages_used)
     i32 = torch.int32
     st = (_lib or load()).kda_page_plan(
         _ptr(cached_lens, i32), _ptr(new_lens, i32), _ptr(free_pages, i32), free_pages.numel(),
         _ptr(block_table, i32), max_pages, B, page_size, num_pages, _ptr(seq_lens, i32),
         _ptr(cu_seqlens, i32), _ptr(slot_map, i32), slot_map.numel(), _ptr(pages_used, i32),
-        _handle(stream, block_table.get_device(), cached_lens, new_lens, free_pages, seq_lens,
-                cu_seqlens, slot_map, pages_used))
+        _handle(stream, gpu))
     if st:
         raise KDAError(st, "kda_page_plan")
 
@@ -484,8 +490,12 @@ def kda_paged_append(k, v, slot_map, cache, stream=None):
     vp, vs, vn = _rows(v, cache.heads, cache.head_dim)
     if kn != N or vn != N:
         raise ValueError("k and v need one row per entry of slot_map")
-    st = (_lib or load()).kda_paged_append(kp, vp, ks, vs, _ptr(slot_map, torch.int32), N,
-                                           cache._ref, _handle(stream, cache._index, k, v, slot_map))
+    slots = _ptr(slot_map, torch.int32)
+    gpu = cache._index
+    if not (0 <= gpu == k.get_device() == v.get_device() == slot_map.get_device()):
+        raise _elsewhere(gpu, k, v, slot_map)
+    st = (_lib or load()).kda_paged_append(kp, vp, ks, vs, slots, N, cache._ref,
+                                           _handle(stream, gpu))
     if st:
         raise KDAError(st, "kda_paged_append")
 
@@ -508,13 +518,17 @@ def kda_paged_decode(q, cache, block_table, seq_lens, scale, o, lse, workspace, 
         raise ValueError("lse is fp32 [B, q_heads]")
     qp, qs, _ = _rows(q, q_heads, head_dim)
     o_dtype = o.dtype
-    extra = (workspace,) if lse is None else (workspace, lse)
+    gpu = cache._index
+    if not (0 <= gpu == q.get_device() == block_table.get_device() == seq_lens.get_device()
+            == o.get_device() == workspace.get_device()
+            == (gpu if lse is None else lse.get_device())):
+        raise _elsewhere(gpu, q, block_table, seq_lens, o, workspace, *([] if lse is None else [lse]))
     st = (_lib or load()).kda_paged_decode(
         qp, qs, cache._ref, _ptr(block_table, torch.int32), max_pages,
         _ptr(seq_lens, torch.int32), B, q_heads, scale, _ptr(o, o_dtype),
         KDA_BF16 if o_dtype is torch.bfloat16 else _dtype_code(o),
         None if lse is None else _ptr(lse, torch.float32), _ptr(workspace, workspace.dtype),
-        workspace.nbytes, _handle(stream, cache._index, q, block_table, seq_lens, o, *extra))
+        workspace.nbytes, _handle(stream, gpu))
     if st:
         raise KDAError(st, "kda_paged_decode")
 
