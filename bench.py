@@ -877,7 +877,7 @@ def run_ours(args):
 
 def run_profile_case(args):
     """A few launches of one kernel at a chosen size, for ncu captures
-    (`ncu -k regex:<kernel> -s <warm-up launches> -c 1 python bench.py --profile ...`).
+    (`ncu --clock-control none -k regex:<kernel> -s <warm-up launches> -c 1 python bench.py --profile ...`).
     Prints one line; its timings are not bench values."""
     import gated_delta_rule_33_gb300 as kda
     from gated_delta_rule_33_gb300 import synth
