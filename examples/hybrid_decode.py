@@ -5,8 +5,10 @@ of memory for a request: a KDA state in a slot of a pool, and keys and values in
 pages of a cache.  This example runs both through a serving loop on synthetic
 projections: prompts are placed and cached (one plan serves every layer), then
 the requests decode token by token; one ends, gives its pages and its state slot
-back, and another takes its place.  The attention outputs are checked against a
-plain softmax over the keys that were appended.
+back, and another takes its place.  A prompt runs through the KDA layer and its keys
+and values are cached; the attention layer's own outputs for it are not computed here,
+as the library has that attention for one new token per sequence only.  The attention
+outputs are checked against a plain softmax over the keys that were appended.
 
     python examples/hybrid_decode.py            # needs the built library and a GB300
 """
@@ -75,6 +77,7 @@ class Server:
         return rows[:, :self.q_heads * self.head_dim].view(-1, self.q_heads, self.head_dim)
 
     def prompts(self, new_lens):
+        """Prompts through the KDA layer, and into the attention layer's cache."""
         cu, slots = self.plan(new_lens)
         q, k, v, g, beta = self.kda_inputs(sum(new_lens))
         _, states = kda.prefill(q, k, v, g, beta, cu_seqlens=cu, initial_state=self.states)

@@ -225,8 +225,8 @@ cudaError_t launch_page_plan(const int32_t *cached_lens, const int32_t *new_lens
                              int32_t *seq_lens, int32_t *cu_seqlens, int32_t *slot_map, int64_t N,
                              int32_t *pages_used, unsigned int *err, cudaStream_t s) {
     // 512 threads scan 2048 requests at once; up to half as many are done sooner by 256,
-    // whose barriers are cheaper (2048 requests, 260 thousand tokens: 7.4 us, 9.8 with 256;
-    // 8 requests: 4.4 us, 4.9 with 512)
+    // whose barriers are cheaper (2048 requests, 260 thousand tokens: 6.8 us, 9.0 with 256;
+    // 8 requests: 3.7 us, 4.4 with 512)
     auto kern = B <= 1024 ? plan_kernel<256> : plan_kernel<512>;
     const int threads = B <= 1024 ? 256 : 512, tile = threads * kItems;
     const int64_t ctas = N > 0 ? (N + tile - 1) / tile : 1;

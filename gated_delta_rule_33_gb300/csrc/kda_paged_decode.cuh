@@ -13,8 +13,8 @@
 // rate.  So what matters is that every SM has copies in flight from the first microsecond
 // to the last, whatever the lengths, and that a warp's instructions for a tile take less
 // time than its copy.  Measured, 8 query heads to a key head of 128: 64 sequences of 16 to
-// 16384 keys 127 us (94 % of HBM), one of 262149 keys 163 us (97 %), 256 of 3500 to 8192 in
-// 8 bits 451 us (100 %).  16 heads over 8 bits (74 %) and 24 or more (32: 66 %) are bound by
+// 16384 keys 129 us (92 % of HBM), one of 262149 keys 163 us (97 %), 256 of 3500 to 8192 in
+// 8 bits 453 us (100 %).  16 heads over 8 bits (73 %) and 24 or more (32: 67 %) are bound by
 // the warps' instructions.
 //
 // Split.  A unit is (sequence, key head, group of 8, 16, 24 or 32 query heads); its keys
@@ -37,8 +37,8 @@
 // S^T = K Q^T, O^T += V^T P^T, so that no row of the operand that is loaded is
 // padding; the weights turn from accumulator to right operand by transposing
 // 8 x 8 blocks in registers (movmatrix).  (tcgen05.mma takes 64 or 128 rows from
-// shared memory and would need the weights there; at 8 heads the tensor pipe is 12 %
-// busy, 27 % over 8 bits; at 16 over 8 bits 41 %.)
+// shared memory and would need the weights there; at 8 heads the tensor pipe is 14 %
+// busy, 28 % over 8 bits; at 16 over 8 bits 41 %.)
 //
 // Precision: scores, maxima, sums and outputs in fp32.  For the product with the
 // values a weight is a sum of bf16 numbers: two, 16 bits together, for a bf16
@@ -129,7 +129,7 @@ constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
 // kN: groups of 8 query heads in a unit.  kWide: fp32 outputs.  Warps: as many as the
 // accumulators (kD / 4 * kN registers a lane) leave registers for, so that one warp's
-// instructions overlap another's waits (24 heads of 64: 118 us with 8, 110 with 12).
+// instructions overlap another's waits (24 heads of 64: 118 us with 8, 110 with 12; now 104).
 template <int kD_, bool kFp8_, int kN_, bool kWide_>
 struct Shape {
     static constexpr int kD = kD_, kN = kN_;
@@ -155,7 +155,7 @@ struct Shape {
     // the ring takes the warp's last part in the end
     static constexpr int kRing = max_of(kSlots * kHalf, (kHeads * kPitch * 4 + 1023) / 1024 * 1024);
     // The queries lie beside the ring, as operands, where they would fill the registers (32
-    // heads of 128: 251 us with spills, 208 so; 16 over 8 bits: 200 and 185).
+    // heads of 128: 251 us with spills, 208 so, now 205; 16 over 8 bits: 200 and 185).
     static constexpr int kQBytes = kD / 16 * kN * 256;
     static constexpr bool kQShared = kD * kN >= 256 && kWarps * (kRing + kQBytes) <= 220 * 1024;
     static constexpr int kQ = kQShared ? kQBytes : 0;

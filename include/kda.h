@@ -525,11 +525,15 @@ kda_status kda_short_conv_qkv_step(const void *x_q, const void *x_k, const void 
                                    void *q, void *k, void *v, void *stream);
 
 /*
- * The paged key-value cache of the softmax-attention layers between KDA layers
- * (K3_ARTIFACT_AUDIT.md section 3.1: 69 KDA and 24 attention layers), in
- * preallocated pages that are written by index: the Kimi-K3 code audit's
- * "repeated-mla-cache-concatenation" recommendation, as for the state pool of
- * kda_recurrent_decode_indexed.  Three entry points serve one step of a batch:
+ * A paged key-value cache for softmax-attention layers that stand between KDA
+ * layers and keep keys and values per head, of equal head_dim, in preallocated
+ * pages that are written by index (what the Kimi-K3 code audit's finding
+ * "repeated-mla-cache-concatenation" asks for, as for the state pool of
+ * kda_recurrent_decode_indexed).  It does not hold that model's own attention
+ * layers (K3_ARTIFACT_AUDIT.md section 3.1: 24 beside 69 KDA layers), whose cache
+ * is one latent of 512 + 64 values a token for all heads.  Attention is for one
+ * new token per sequence; a prompt's own attention over its keys is the caller's.
+ * Three entry points serve one step of a batch:
  *
  *   kda_page_plan     block table, slot map and offsets of the step's tokens,
  *                     from the requests' lengths, on the device (once a step)
