@@ -75,3 +75,12 @@ def test_dropped_memory_stays_with_its_stream(lib, case, as_handle):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert a is None or torch.equal(a, b)
+
+
+def test_handle_of_the_default_stream(lib):
+    size, call = prefill(lib)
+    want = [x.clone() for x in call(None)]
+    got = call(torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
