@@ -8,6 +8,7 @@
 #include "../../include/kda.h"
 #include "kda_internal.cuh"
 #include "kda_paged.cuh"
+#include "kda_tree.cuh"
 
 namespace {
 
@@ -150,6 +151,23 @@ bool paged_decode_sizes(int B, int q_heads, int kv_heads, int head_dim) {
     return q_heads % kv_heads == 0 && static_cast<int64_t>(q_heads) * head_dim <= INT32_MAX &&
            static_cast<int64_t>(kv_heads) * head_dim <= INT32_MAX / 4 &&
            static_cast<int64_t>(B) * q_heads <= INT32_MAX;
+}
+
+constexpr int kMaxTreeRequests = 65535;  // a dimension of the grid
+
+// What the calls over trees of drafted tokens have in common.
+kda_status tree_sizes(int B, int64_t N, int max_nodes, int num_slots, const int32_t *slots) {
+    if (B < 0 || B > kMaxTreeRequests || N < 0 || N > INT32_MAX || num_slots < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (max_nodes < 1 || max_nodes > KDA_TREE_MAX_NODES) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (slots == nullptr && num_slots < B) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// Whether kda_paged_tree_decode takes so many query heads and nodes.
+bool paged_tree_sizes(int B, int max_nodes, int q_heads, int kv_heads, int head_dim) {
+    return paged_decode_sizes(B, q_heads, kv_heads, head_dim) &&
+           static_cast<int64_t>(B) * q_heads <= INT32_MAX / max_nodes;
 }
 
 }  // namespace
@@ -771,6 +789,404 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
             static_cast<const __nv_bfloat16 *>(q), q_row_stride, view, block_table, max_pages,
             seq_lens, B, q_heads, scale, o, o_dtype == KDA_BF16, lse, workspace, dev->error_word,
             dev->num_sms, static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
+}
+
+kda_status kda_recurrent_tree_decode(const void *q, const void *k, const void *v, const float *g,
+                                     const float *beta, const void *state_pool,
+                                     kda_dtype state_dtype, const int32_t *state_indices,
+                                     int num_slots, const int32_t *cu_seqlens,
+                                     const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                     int H, int K, int V, float scale, void *o, kda_dtype o_dtype,
+                                     float *u, void *stream) {
+    kda_status st = tree_sizes(B, N, max_nodes, num_slots, state_indices);
+    if (st != KDA_OK) return st;
+    if (H < 1) return KDA_ERR_INVALID_ARG;
+    if (K != 128 || V != 128 || static_cast<int64_t>(B) * H > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!valid_dtype(o_dtype) || !valid_dtype(state_dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
+    if (B == 0) return KDA_OK;
+    if (cu_seqlens == nullptr || state_pool == nullptr ||
+        (N > 0 && (q == nullptr || k == nullptr || v == nullptr || g == nullptr ||
+                   beta == nullptr || ancestors == nullptr || o == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) ||
+        !aligned16(state_pool) || !aligned16(state_indices) || !aligned16(cu_seqlens) ||
+        !aligned16(ancestors) || !aligned16(o) || !aligned16(u))
+        return KDA_ERR_MISALIGNED;
+    const size_t values = static_cast<size_t>(N) * H * 128;
+    const size_t o_bytes = values * (o_dtype == KDA_BF16 ? 2 : 4);
+    const void *ins[5] = {q, k, v, g, state_pool};
+    const size_t pool = static_cast<size_t>(num_slots) * H * 16384 * (state_dtype == KDA_BF16 ? 2 : 4);
+    const size_t in_bytes[5] = {values * 2, values * 2, values * 2, values * 4, pool};
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(o, o_bytes, ins[i], in_bytes[i]) || overlaps(u, values * 4, ins[i], in_bytes[i]))
+            return KDA_ERR_INVALID_ARG;
+    if (overlaps(o, o_bytes, u, values * 4)) return KDA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    kda::TreeStep a = {};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.g = g;
+    a.beta = beta;
+    a.pool = const_cast<void *>(state_pool);
+    a.slots = state_indices;
+    a.num_slots = num_slots;
+    a.cu = cu_seqlens;
+    a.ancestors = ancestors;
+    a.B = B;
+    a.H = H;
+    a.max_nodes = max_nodes;
+    a.N = N;
+    a.scale = scale;
+    a.o = o;
+    a.u = u;
+    a.err = dev->error_word;
+    try {
+        return from_cuda(kda::launch_tree_decode(a, state_dtype == KDA_BF16, o_dtype == KDA_BF16,
+                                                 static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
+}
+
+kda_status kda_recurrent_tree_commit(const void *k, const float *g, const float *u,
+                                     void *state_pool, kda_dtype state_dtype,
+                                     const int32_t *state_indices, int num_slots,
+                                     const int32_t *cu_seqlens, const uint64_t *ancestors,
+                                     const int32_t *last, int B, int64_t N, int max_nodes, int H,
+                                     int K, int V, void *stream) {
+    kda_status st = tree_sizes(B, N, max_nodes, num_slots, state_indices);
+    if (st != KDA_OK) return st;
+    if (H < 1) return KDA_ERR_INVALID_ARG;
+    if (K != 128 || V != 128 || static_cast<int64_t>(B) * H > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!valid_dtype(state_dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
+    if (B == 0) return KDA_OK;
+    if (cu_seqlens == nullptr || state_pool == nullptr || last == nullptr ||
+        (N > 0 && (k == nullptr || g == nullptr || u == nullptr || ancestors == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(g) || !aligned16(u) || !aligned16(state_pool) ||
+        !aligned16(state_indices) || !aligned16(cu_seqlens) || !aligned16(ancestors) ||
+        !aligned16(last))
+        return KDA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    kda::TreeStep a = {};
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.g = g;
+    a.pool = state_pool;
+    a.slots = state_indices;
+    a.num_slots = num_slots;
+    a.cu = cu_seqlens;
+    a.ancestors = ancestors;
+    a.last = last;
+    a.B = B;
+    a.H = H;
+    a.max_nodes = max_nodes;
+    a.N = N;
+    a.u = const_cast<float *>(u);
+    a.err = dev->error_word;
+    try {
+        return from_cuda(kda::launch_tree_commit(a, state_dtype == KDA_BF16,
+                                                 static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
+}
+
+kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void *x_v,
+                                   const float *w_q, const float *w_k, const float *w_v,
+                                   const void *conv_state_pool, const int32_t *state_indices,
+                                   int num_slots, const int32_t *cu_seqlens,
+                                   const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                   int C, void *q, void *k, void *v, void *stream) {
+    kda_status st = tree_sizes(B, N, max_nodes, num_slots, state_indices);
+    if (st != KDA_OK) return st;
+    if (C < 128 || C % 128 != 0) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (B == 0) return KDA_OK;
+    if (cu_seqlens == nullptr || conv_state_pool == nullptr || (N > 0 && ancestors == nullptr))
+        return KDA_ERR_INVALID_ARG;
+    const void *xs[3] = {x_q, x_k, x_v};
+    const float *ws[3] = {w_q, w_k, w_v};
+    void *ys[3] = {q, k, v};
+    const size_t bytes = static_cast<size_t>(N) * C * 2;
+    const size_t pool = static_cast<size_t>(num_slots) * 9 * C * 2;
+    for (int i = 0; i < 3; ++i) {
+        if (N > 0 && (xs[i] == nullptr || ws[i] == nullptr || ys[i] == nullptr))
+            return KDA_ERR_INVALID_ARG;
+        if (!aligned16(xs[i]) || !aligned16(ws[i]) || !aligned16(ys[i])) return KDA_ERR_MISALIGNED;
+        for (int j = 0; j < 3; ++j)
+            if (overlaps(ys[i], bytes, xs[j], bytes) ||
+                overlaps(ys[i], bytes, ws[j], static_cast<size_t>(C) * 16) ||
+                (i < j && overlaps(ys[i], bytes, ys[j], bytes)))
+                return KDA_ERR_INVALID_ARG;
+        if (overlaps(ys[i], bytes, conv_state_pool, pool)) return KDA_ERR_INVALID_ARG;
+    }
+    if (!aligned16(conv_state_pool) || !aligned16(state_indices) || !aligned16(cu_seqlens) ||
+        !aligned16(ancestors))
+        return KDA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    kda::TreeConv a = {};
+    for (int i = 0; i < 3; ++i) {
+        a.x[i] = static_cast<const __nv_bfloat16 *>(xs[i]);
+        a.w[i] = ws[i];
+        a.y[i] = static_cast<__nv_bfloat16 *>(ys[i]);
+    }
+    a.pool = static_cast<__nv_bfloat16 *>(const_cast<void *>(conv_state_pool));
+    a.slots = state_indices;
+    a.num_slots = num_slots;
+    a.cu = cu_seqlens;
+    a.ancestors = ancestors;
+    a.B = B;
+    a.C = C;
+    a.max_nodes = max_nodes;
+    a.N = N;
+    a.err = dev->error_word;
+    return from_cuda(kda::launch_tree_conv(a, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_short_conv_tree_commit(const void *x_q, const void *x_k, const void *x_v,
+                                      void *conv_state_pool, const int32_t *state_indices,
+                                      int num_slots, const int32_t *cu_seqlens,
+                                      const uint64_t *ancestors, const int32_t *last, int B,
+                                      int64_t N, int max_nodes, int C, void *stream) {
+    kda_status st = tree_sizes(B, N, max_nodes, num_slots, state_indices);
+    if (st != KDA_OK) return st;
+    if (C < 128 || C % 128 != 0) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (B == 0) return KDA_OK;
+    if (cu_seqlens == nullptr || conv_state_pool == nullptr || last == nullptr ||
+        (N > 0 && (x_q == nullptr || x_k == nullptr || x_v == nullptr || ancestors == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x_q) || !aligned16(x_k) || !aligned16(x_v) || !aligned16(conv_state_pool) ||
+        !aligned16(state_indices) || !aligned16(cu_seqlens) || !aligned16(ancestors) ||
+        !aligned16(last))
+        return KDA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    kda::TreeConv a = {};
+    a.x[0] = static_cast<const __nv_bfloat16 *>(x_q);
+    a.x[1] = static_cast<const __nv_bfloat16 *>(x_k);
+    a.x[2] = static_cast<const __nv_bfloat16 *>(x_v);
+    a.pool = static_cast<__nv_bfloat16 *>(conv_state_pool);
+    a.slots = state_indices;
+    a.num_slots = num_slots;
+    a.cu = cu_seqlens;
+    a.ancestors = ancestors;
+    a.last = last;
+    a.B = B;
+    a.C = C;
+    a.max_nodes = max_nodes;
+    a.N = N;
+    a.err = dev->error_word;
+    return from_cuda(kda::launch_tree_conv_commit(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_paged_tree_decode_workspace_size(int B, int max_nodes, int q_heads, int kv_heads,
+                                            int head_dim) {
+    if (B < 0 || B > kMaxTreeRequests || max_nodes < 1 || max_nodes > KDA_TREE_MAX_NODES ||
+        kv_heads < 1 || q_heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        !paged_tree_sizes(B, max_nodes, q_heads, kv_heads, head_dim))
+        return 0;
+    return kda::paged_tree_workspace_bytes(B, max_nodes, q_heads, kv_heads, head_dim);
+}
+
+kda_status kda_paged_tree_decode(const void *q, int64_t q_row_stride, const kda_paged_cache *cache,
+                                 const int32_t *block_table, int max_pages,
+                                 const int32_t *seq_lens, const int32_t *cu_seqlens,
+                                 const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                 int q_heads, float scale, void *o, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    kda::PagedView view;
+    kda_status st = paged_view(cache, &view);
+    if (st != KDA_OK) return st;
+    st = tree_sizes(B, N, max_nodes, B, nullptr);
+    if (st != KDA_OK) return st;
+    if (max_pages < 0 || q_heads < 1) return KDA_ERR_INVALID_ARG;
+    if (!paged_tree_sizes(B, max_nodes, q_heads, view.heads, view.head_dim) ||
+        N > INT32_MAX / q_heads)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = static_cast<int64_t>(q_heads) * view.head_dim;
+    if (B > 0 && (seq_lens == nullptr || cu_seqlens == nullptr ||
+                  (max_pages > 0 && block_table == nullptr) ||
+                  (N > 0 && (q == nullptr || ancestors == nullptr || o == nullptr))))
+        return KDA_ERR_INVALID_ARG;
+    if (N > 1 && (q_row_stride < width || q_row_stride > INT64_MAX / 4 / N))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) ||
+        !aligned16(cu_seqlens) || !aligned16(ancestors) || !aligned16(o) || !aligned16(lse) ||
+        !aligned16(workspace) || (N > 1 && q_row_stride % 8 != 0))
+        return KDA_ERR_MISALIGNED;
+    const size_t need =
+        kda::paged_tree_workspace_bytes(B, max_nodes, q_heads, view.heads, view.head_dim);
+    if (workspace_bytes < need || (need > 0 && workspace == nullptr))
+        return KDA_ERR_WORKSPACE_TOO_SMALL;
+    if (B == 0 || N == 0) return KDA_OK;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    kda::TreeAttention a = {};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.q_row_stride = N > 1 ? q_row_stride : 0;
+    a.cache = view;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.cu = cu_seqlens;
+    a.ancestors = ancestors;
+    a.B = B;
+    a.q_heads = q_heads;
+    a.group = q_heads / view.heads;
+    a.max_nodes = max_nodes;
+    a.N = N;
+    a.scale = scale;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    a.workspace = static_cast<uint8_t *>(workspace);
+    a.err = dev->error_word;
+    try {
+        return from_cuda(kda::launch_paged_tree_decode(a, dev->num_sms,
+                                                       static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
+}
+
+kda_status kda_paged_compact(const kda_paged_cache *cache, const int32_t *block_table,
+                             int max_pages, const int32_t *seq_lens, const int32_t *cu_seqlens,
+                             const uint64_t *ancestors, const int32_t *last, int B, int64_t N,
+                             int max_nodes, int32_t *kept_lens, void *stream) {
+    kda::PagedView view;
+    kda_status st = paged_view(cache, &view);
+    if (st != KDA_OK) return st;
+    st = tree_sizes(B, N, max_nodes, B, nullptr);
+    if (st != KDA_OK) return st;
+    if (max_pages < 0 || view.k == view.v) return KDA_ERR_INVALID_ARG;
+    if (B > 0 && (seq_lens == nullptr || cu_seqlens == nullptr || last == nullptr ||
+                  (max_pages > 0 && block_table == nullptr) || (N > 0 && ancestors == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(block_table) || !aligned16(seq_lens) || !aligned16(cu_seqlens) ||
+        !aligned16(ancestors) || !aligned16(last) || !aligned16(kept_lens))
+        return KDA_ERR_MISALIGNED;
+    const size_t rows = static_cast<size_t>(B) * 4;
+    if (overlaps(kept_lens, rows, seq_lens, rows) || overlaps(kept_lens, rows, last, rows) ||
+        overlaps(kept_lens, rows, cu_seqlens, rows + 4) ||
+        overlaps(kept_lens, rows, ancestors, static_cast<size_t>(N) * 8) ||
+        overlaps(kept_lens, rows, block_table, rows * static_cast<size_t>(max_pages)))
+        return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_paged_compact(view, block_table, max_pages, seq_lens, cu_seqlens,
+                                               ancestors, last, B, N, max_nodes, kept_lens,
+                                               dev->error_word, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_page_fork(const int32_t *src, const int32_t *dst, int num_forks, int32_t *seq_lens,
+                         const int32_t *free_pages, int num_free, int32_t *block_table,
+                         int max_pages, int B, int page_size, int num_pages, int32_t *shares,
+                         int32_t *copies, int32_t *pages_used, void *stream) {
+    if (num_forks < 0 || num_free < 0 || max_pages < 0 || B < 0 || page_size < 1 || num_pages < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (pages_used == nullptr || (num_free > 0 && free_pages == nullptr) ||
+        (num_pages > 0 && shares == nullptr) || (B > 0 && seq_lens == nullptr) ||
+        (B > 0 && max_pages > 0 && block_table == nullptr) ||
+        (num_forks > 0 && (src == nullptr || dst == nullptr || copies == nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(src) || !aligned16(dst) || !aligned16(seq_lens) ||
+        (reinterpret_cast<uintptr_t>(free_pages) & 3u) != 0 || !aligned16(block_table) ||
+        !aligned16(shares) || !aligned16(copies) || !aligned16(pages_used))
+        return KDA_ERR_MISALIGNED;
+    const size_t rows = static_cast<size_t>(B) * 4, forks = static_cast<size_t>(num_forks) * 4;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } bufs[] = {{seq_lens, rows},
+                {block_table, rows * static_cast<size_t>(max_pages)},
+                {shares, static_cast<size_t>(num_pages) * 4},
+                {copies, forks * 3},
+                {pages_used, 4},
+                {src, forks},
+                {dst, forks},
+                {free_pages, static_cast<size_t>(num_free) * 4}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if (overlaps(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+                return KDA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    kda_status st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_page_fork(src, dst, num_forks, seq_lens, free_pages, num_free,
+                                           block_table, max_pages, B, page_size, num_pages, shares,
+                                           copies, pages_used, dev->error_word,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_paged_copy(const int32_t *copies, int num_copies, const kda_paged_cache *cache,
+                          void *stream) {
+    kda::PagedView view;
+    kda_status st = paged_view(cache, &view);
+    if (st != KDA_OK) return st;
+    if (num_copies < 0 || view.k == view.v || (num_copies > 0 && copies == nullptr))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(copies)) return KDA_ERR_MISALIGNED;
+    if (num_copies == 0) return KDA_OK;
+    DeviceInfo *dev = nullptr;
+    st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::launch_paged_copy(copies, num_copies, view, dev->error_word,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_page_release(const int32_t *seq_lens, const int32_t *kept_lens,
+                            const int32_t *block_table, int max_pages, int B, int page_size,
+                            int num_pages, int32_t *shares, int32_t *freed, int max_freed,
+                            int32_t *num_freed, void *stream) {
+    if (max_pages < 0 || B < 0 || page_size < 1 || num_pages < 0 || max_freed < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (num_freed == nullptr || (max_freed > 0 && freed == nullptr) ||
+        (num_pages > 0 && shares == nullptr) ||
+        (B > 0 && (seq_lens == nullptr || kept_lens == nullptr ||
+                   (max_pages > 0 && block_table == nullptr))))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(seq_lens) || !aligned16(kept_lens) || !aligned16(block_table) ||
+        !aligned16(shares) || (reinterpret_cast<uintptr_t>(freed) & 3u) != 0 ||
+        !aligned16(num_freed))
+        return KDA_ERR_MISALIGNED;
+    const size_t rows = static_cast<size_t>(B) * 4;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } bufs[] = {{shares, static_cast<size_t>(num_pages) * 4},
+                {freed, static_cast<size_t>(max_freed) * 4},
+                {num_freed, 4},
+                {seq_lens, rows},
+                {kept_lens, rows},
+                {block_table, rows * static_cast<size_t>(max_pages)}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (overlaps(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+                return KDA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    kda_status st = current_device(&dev);
+    if (st != KDA_OK) return st;
+    try {
+        return from_cuda(kda::launch_page_release(seq_lens, kept_lens, block_table, max_pages, B,
+                                                  page_size, num_pages, shares, freed, max_freed,
+                                                  num_freed, dev->error_word,
+                                                  static_cast<cudaStream_t>(stream)));
     } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
         return KDA_ERR_CUDA;
     }

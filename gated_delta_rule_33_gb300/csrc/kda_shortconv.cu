@@ -25,6 +25,8 @@
 // (f32x2 instructions, each the IEEE operation on both halves).
 #include "kda_f32x2.cuh"
 #include "kda_internal.cuh"
+#include "kda_sm100.cuh"
+#include "kda_tree.cuh"
 
 namespace kda {
 namespace {
@@ -325,7 +327,109 @@ __global__ void __launch_bounds__(kWarps * 32) short_conv_step_kernel(
     }
 }
 
+// A tree of drafted tokens per request; the pool is read, not changed.  grid = (channel
+// groups of kWarpCh, B, 3 streams).  The three inputs before a node's own are those of its
+// nearest ancestors, then the carried ones, the last of them first.  The block stages the
+// request's rows of its channels, and its carried rows, in shared memory: each is an input of
+// every node below it, and comes from memory once.
+__global__ void __launch_bounds__(kWarps * 32) tree_conv_kernel(const TreeConv a) {
+    extern __shared__ __align__(16) uint8_t s_rows[];  // [max_nodes + 3][kWarpCh] bf16
+    const int z = blockIdx.z, b = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * kWarpCh + lane * kLaneCh;
+    const bool active = c < a.C;
+    const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
+    const int sl = a.slots != nullptr ? a.slots[b] : b;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && (t.bad || sl >= a.num_slots))
+        record_device_error(a.err, kDevInvalidArg);
+    __nv_bfloat16 *y = pick(a.y, z) + t.first * a.C + c;
+    if (t.n == 0 || sl < 0 || sl >= a.num_slots) {
+        Pair zero[kLanePairs];
+        zero_row(zero);
+        for (int i = warp; i < t.rows; i += kWarps)
+            if (active) store_row(y + static_cast<int64_t>(i) * a.C, zero);
+        return;
+    }
+    const __nv_bfloat16 *x = pick(a.x, z) + t.first * a.C + c;
+    uint8_t *mine = s_rows + lane * kLaneCh * 2;
+    for (int i = warp; i < t.n + kHalo; i += kWarps) {
+        const __nv_bfloat16 *src = i < t.n ? x + static_cast<int64_t>(i) * a.C
+                                           : a.pool + state_index(sl, z, i - t.n, a.C, c);
+        sm100::cp_async_16(mine + i * kWarpCh * 2, active ? src : a.pool, active);
+    }
+    Pair w[kLanePairs][kTaps];
+    load_taps(pick(a.w, z), c, active, w);
+    sm100::cp_async_wait_all();
+    __syncthreads();
+    auto row = [&](int i, Pair (&r)[kLanePairs]) {
+        unpack_row(*reinterpret_cast<const uint4 *>(mine + i * kWarpCh * 2), r);
+    };
+    for (int i = warp; i < t.n; i += kWarps) {
+        uint64_t above = a.ancestors[t.first + i] & bits_below(i);
+        Pair win[kHalo][kLanePairs], xt[kLanePairs], out[kLanePairs];
+        row(i, xt);
+        int carried = t.n + kHalo;
+#pragma unroll
+        for (int r = kHalo - 1; r >= 0; --r) {
+            if (above != 0) {
+                const int j = top_bit(above);
+                above ^= uint64_t{1} << j;
+                row(j, win[r]);
+            } else {
+                row(--carried, win[r]);
+            }
+        }
+        conv_row(w, win, xt, z < 2, out);
+        if (active) store_row(y + static_cast<int64_t>(i) * a.C, out);
+    }
+}
+
+// The carried inputs after the path of node last[b]: the last three of what there was and the
+// path's.  A thread moves 8 channels; grid as above, with kWarps groups a block.
+__global__ void __launch_bounds__(kWarps * 32) tree_conv_commit_kernel(const TreeConv a) {
+    const int z = blockIdx.z, b = blockIdx.y;
+    const int c = (blockIdx.x * kWarps * 32 + threadIdx.x) * kLaneCh;
+    const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
+    const int sl = a.slots != nullptr ? a.slots[b] : b, end = a.last[b];
+    if (threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && (t.bad || sl >= a.num_slots || end >= t.n))
+        record_device_error(a.err, kDevInvalidArg);
+    if (c >= a.C || end < 0 || end >= t.n || sl < 0 || sl >= a.num_slots) return;
+    uint64_t path = path_of(a.ancestors[t.first + end], end);
+    const __nv_bfloat16 *x = pick(a.x, z) + t.first * a.C + c;
+    uint4 r[kHalo];
+    int carried = kHalo;
+#pragma unroll
+    for (int i = kHalo - 1; i >= 0; --i) {
+        const __nv_bfloat16 *src;
+        if (path != 0) {
+            const int j = top_bit(path);
+            path ^= uint64_t{1} << j;
+            src = x + static_cast<int64_t>(j) * a.C;
+        } else {
+            src = a.pool + state_index(sl, z, --carried, a.C, c);
+        }
+        r[i] = *reinterpret_cast<const uint4 *>(src);
+    }
+#pragma unroll
+    for (int i = 0; i < kHalo; ++i)
+        *reinterpret_cast<uint4 *>(a.pool + state_index(sl, z, i, a.C, c)) = r[i];
+}
+
 }  // namespace
+
+cudaError_t launch_tree_conv(const TreeConv &a, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.C + kWarpCh - 1) / kWarpCh), a.B, 3);
+    const int smem = (a.max_nodes + kHalo) * kWarpCh * 2;  // 33.5 KB at most
+    tree_conv_kernel<<<grid, kWarps * 32, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tree_conv_commit(const TreeConv &a, cudaStream_t s) {
+    const int per_block = kWarps * 32 * kLaneCh;
+    const dim3 grid(static_cast<unsigned>((a.C + per_block - 1) / per_block), a.B, 3);
+    tree_conv_commit_kernel<<<grid, kWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_short_conv(const __nv_bfloat16 *const x[3], const float *const w[3],
                               __nv_bfloat16 *const y[3], const int32_t *cu_seqlens, int B,

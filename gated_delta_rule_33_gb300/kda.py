@@ -130,6 +130,31 @@ def load():
         lib.kda_paged_decode.argtypes = [P, I64, P, P, I, P, I, I, F, P, I, P, P, ctypes.c_size_t,
                                          P]
         lib.kda_paged_decode.restype = I
+        Z = ctypes.c_size_t
+        lib.kda_recurrent_tree_decode.argtypes = [P, P, P, P, P, P, I, P, I, P, P, I, I64, I, I, I,
+                                                  I, F, P, I, P, P]
+        lib.kda_recurrent_tree_decode.restype = I
+        lib.kda_recurrent_tree_commit.argtypes = [P, P, P, P, I, P, I, P, P, P, I, I64, I, I, I, I,
+                                                  P]
+        lib.kda_recurrent_tree_commit.restype = I
+        lib.kda_short_conv_qkv_tree.argtypes = [P, P, P, P, P, P, P, P, I, P, P, I, I64, I, I, P, P,
+                                                P, P]
+        lib.kda_short_conv_qkv_tree.restype = I
+        lib.kda_short_conv_tree_commit.argtypes = [P, P, P, P, P, I, P, P, P, I, I64, I, I, P]
+        lib.kda_short_conv_tree_commit.restype = I
+        lib.kda_paged_tree_decode_workspace_size.argtypes = [I, I, I, I, I]
+        lib.kda_paged_tree_decode_workspace_size.restype = Z
+        lib.kda_paged_tree_decode.argtypes = [P, I64, P, P, I, P, P, P, I, I64, I, I, F, P, P, P, Z,
+                                              P]
+        lib.kda_paged_tree_decode.restype = I
+        lib.kda_paged_compact.argtypes = [P, P, I, P, P, P, P, I, I64, I, P, P]
+        lib.kda_paged_compact.restype = I
+        lib.kda_page_fork.argtypes = [P, P, I, P, P, I, P, I, I, I, I, P, P, P, P]
+        lib.kda_page_fork.restype = I
+        lib.kda_paged_copy.argtypes = [P, I, P, P]
+        lib.kda_paged_copy.restype = I
+        lib.kda_page_release.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P]
+        lib.kda_page_release.restype = I
         lib.kda_debug_check_gate_division.argtypes = [P, P]
         lib.kda_debug_check_gate_division.restype = I
         lib.kda_debug_set_wait_limit.argtypes = [I64, I64]

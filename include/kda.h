@@ -673,6 +673,232 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
                             float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Drafted tokens.  A serving loop may run several drafted tokens of a request through the
+ * layers at once, as a tree: each node is a token, its ancestors the tokens before it; then
+ * one path is accepted and the rest is dropped.  A step of both kinds of layers:
+ *
+ *   kda_page_plan, kda_paged_append    place the nodes' keys and values, as for any new tokens
+ *   kda_short_conv_qkv_tree            the KDA pre-step of every node
+ *   kda_recurrent_tree_decode          the KDA recurrence to every node, the state unchanged
+ *   kda_paged_tree_decode              attention of every node over the cache
+ *   kda_recurrent_tree_commit, kda_short_conv_tree_commit, kda_paged_compact
+ *                                      what the accepted path leaves in the three memories
+ *
+ * Arguments that these calls share:
+ *
+ *   cu_seqlens   int32 [B+1] device: request b's nodes are rows cu_seqlens[b] ..
+ *                cu_seqlens[b+1] - 1 of the token tensors (what kda_page_plan writes); N rows
+ *                in all.  Rows behind the last request's are neither read nor written.
+ *   max_nodes    1 .. KDA_TREE_MAX_NODES: no request has more
+ *   ancestors    uint64 [N] device: bit j of a node's word is set where it sees node j of its
+ *                request.  The bits below its own number are its ancestors in the recurrence
+ *                and the convolution, where the other bits are not looked at; attention takes
+ *                the bits as they are, so a node's own bit belongs there.  (With parent[i] < i:
+ *                word[i] = 1 << i | word[parent[i]].)
+ *   last         int32 [B] device: the accepted path's last node; -1: nothing is accepted.
+ *                The path is that node and its ancestors.
+ *
+ * A request whose offsets go back or leave the N rows is left out (its rows stay as they
+ * were); one of more than max_nodes rows counts as inactive: outputs of its rows are zeros,
+ * its memory stays as it is.  Both set INVALID_ARG in the device error word, and so does a
+ * `last` past the request's nodes, which accepts nothing.  B is at most 65535.
+ */
+#define KDA_TREE_MAX_NODES 64
+
+/*
+ * kda_recurrent_tree_decode -- the KDA recurrence over trees of drafted tokens (the fused
+ * recurrent regime for several tokens of a sequence that follow one another in more than one
+ * order; code-audit.json, finding "dual-kda-execution-regimes").  Node i's state is its
+ * parent's (the slot's, for a node without ancestors) after the update with i's k, v, g and
+ * beta, as in kda_recurrent_decode; o is read from it.  No state is written: what the nodes
+ * add to it is kept as one vector a node,
+ *
+ *   u_i = beta_i (v_i - S'^T k_i),  S' = Diag(exp g_i) S_parent
+ *
+ * from which kda_recurrent_tree_commit forms the state after any path.  fp32 throughout (a
+ * bf16 state is widened; unlike a chain of one-token decodes, it is not rounded between the
+ * nodes of a path).
+ *
+ *   q, k, v        bf16 [N, H, 128];  g fp32 [N, H, 128];  beta fp32 [N, H]
+ *   state_pool     [num_slots, H, 128, 128] of state_dtype (fp32 or bf16), read
+ *   state_indices  int32 [B] device: the slot of each request, or NULL for slot b (then
+ *                  num_slots >= B).  Negative: inactive, its rows of o and u are zeros; one
+ *                  >= num_slots is skipped the same way and sets INVALID_ARG.  Requests may
+ *                  share a slot here.
+ *   o              [N, H, 128] of o_dtype (bf16 or fp32), written
+ *   u              fp32 [N, H, 128] written, or NULL
+ * K and V must be 128.  No output may overlap an input or another output.  B == 0 is a no-op.
+ */
+kda_status kda_recurrent_tree_decode(const void *q, const void *k, const void *v, const float *g,
+                                     const float *beta, const void *state_pool,
+                                     kda_dtype state_dtype, const int32_t *state_indices,
+                                     int num_slots, const int32_t *cu_seqlens,
+                                     const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                     int H, int K, int V, float scale, void *o, kda_dtype o_dtype,
+                                     float *u, void *stream);
+
+/*
+ * kda_recurrent_tree_commit -- the state after the accepted path, in place: with E_j the decays
+ * of the path's nodes behind j multiplied up,
+ *
+ *   S <- Diag(prod exp g_j) S + sum_j (E_j k_j) u_j^T,   j over the path of node last[b]
+ *
+ *   k, g, u        of the kda_recurrent_tree_decode call (u as it was written there)
+ *   state_pool, state_indices, num_slots
+ *                  as there, but written; two requests must not share a slot
+ * A bf16 state is rounded once, after the whole path.
+ */
+kda_status kda_recurrent_tree_commit(const void *k, const float *g, const float *u,
+                                     void *state_pool, kda_dtype state_dtype,
+                                     const int32_t *state_indices, int num_slots,
+                                     const int32_t *cu_seqlens, const uint64_t *ancestors,
+                                     const int32_t *last, int B, int64_t N, int max_nodes, int H,
+                                     int K, int V, void *stream);
+
+/*
+ * kda_short_conv_qkv_tree -- kda_short_conv_qkv for trees of drafted tokens: the three inputs
+ * before a node's own are those of its nearest ancestors, and the carried ones of its request
+ * where it has fewer than three.  The pool is read, not changed.
+ *
+ *   x_q, x_k, x_v     bf16 [N, C];  w_q, w_k, w_v fp32 [C, 4]
+ *   conv_state_pool   bf16 [num_slots, 3, 3, C];  state_indices, num_slots as in
+ *                     kda_recurrent_tree_decode
+ *   q, k, v           bf16 [N, C] written (zeros for an inactive request); must not overlap
+ *                     an input or one another
+ *
+ * kda_short_conv_tree_commit -- the carried inputs after the path of node last[b], in place: the
+ * last three of the carried ones and the path's.  Two requests must not share a slot.
+ * C must be a positive multiple of 128.
+ */
+kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void *x_v,
+                                   const float *w_q, const float *w_k, const float *w_v,
+                                   const void *conv_state_pool, const int32_t *state_indices,
+                                   int num_slots, const int32_t *cu_seqlens,
+                                   const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                   int C, void *q, void *k, void *v, void *stream);
+
+kda_status kda_short_conv_tree_commit(const void *x_q, const void *x_k, const void *x_v,
+                                      void *conv_state_pool, const int32_t *state_indices,
+                                      int num_slots, const int32_t *cu_seqlens,
+                                      const uint64_t *ancestors, const int32_t *last, int B,
+                                      int64_t N, int max_nodes, int C, void *stream);
+
+/* Bytes of device workspace kda_paged_tree_decode needs (0 for sizes that it rejects). */
+size_t kda_paged_tree_decode_workspace_size(int B, int max_nodes, int q_heads, int kv_heads,
+                                            int head_dim);
+
+/*
+ * kda_paged_tree_decode -- softmax attention of a tree of drafted tokens per sequence over its
+ * cached keys, the drafted tokens' own among them (appended before).  With L = seq_lens[b], n
+ * nodes and C = L - n, node i sees the keys j < C and the keys C + j, j < n, whose bit j is set
+ * in ancestors[cu_seqlens[b] + i]; over those keys it is kda_paged_decode's attention.
+ *
+ *   q           bf16, node's [q_heads, head_dim] values from q + row * q_row_stride (elements, a
+ *               multiple of 8)
+ *   cache, block_table, max_pages, seq_lens (drafted tokens included), q_heads, scale
+ *               as in kda_paged_decode
+ *   o           bf16 [N, q_heads, head_dim] written; a softmax weight is kept to 16 bits (over
+ *               an 8-bit cache to 2^-38 of the largest, if that is coarser)
+ *   lse         fp32 [N, q_heads] written, or NULL
+ *   workspace   device scratch, >= kda_paged_tree_decode_workspace_size() bytes, 16-byte
+ *               aligned; not shared with a concurrent call
+ *
+ * A node that sees no key gives o = 0 and lse = -inf; what it does not see has no part in its
+ * output, whatever it holds.  A length below n or above max_pages * page_size counts as no keys
+ * for all the request's nodes, and keys on a page outside 0 .. num_pages-1 are left out; both
+ * set INVALID_ARG in the device error word.  A request with more than max_nodes rows gives zeros
+ * and -inf.  Infinities and NaN act as in fp32 arithmetic; a call that meets infinite or NaN
+ * values takes longer.  Two calls on the same inputs write the same bits.
+ */
+kda_status kda_paged_tree_decode(const void *q, int64_t q_row_stride, const kda_paged_cache *cache,
+                                 const int32_t *block_table, int max_pages,
+                                 const int32_t *seq_lens, const int32_t *cu_seqlens,
+                                 const uint64_t *ancestors, int B, int64_t N, int max_nodes,
+                                 int q_heads, float scale, void *o, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * kda_paged_compact -- keeps the accepted path's keys and values: the r-th node of the path of
+ * last[b], r = 0, 1, .., moves to position C + r, C = seq_lens[b] - n (each layer).
+ *
+ *   kept_lens   int32 [B] written, or NULL: C + the path's nodes (for a request that is left
+ *               out C, or 0 where its length is below its rows or does not fit its table);
+ *               must not overlap an input
+ * What lies behind kept_lens[b] afterwards is not defined; kda_page_release gives its pages
+ * back.  The pages that hold drafted tokens must be the request's own.  Rows on a page outside
+ * 0 .. num_pages-1 stay where they are and set INVALID_ARG.
+ */
+kda_status kda_paged_compact(const kda_paged_cache *cache, const int32_t *block_table,
+                             int max_pages, const int32_t *seq_lens, const int32_t *cu_seqlens,
+                             const uint64_t *ancestors, const int32_t *last, int B, int64_t N,
+                             int max_nodes, int32_t *kept_lens, void *stream);
+
+/*
+ * kda_page_fork -- requests that go on from others (several continuations of one prompt): fork
+ * f makes request dst[f] hold what request src[f] holds.  The source's full pages are shared;
+ * its last, partly filled one gets a copy of its own, since both will write there.  Once for
+ * all layers; kda_paged_copy then copies the listed pages in each.
+ *
+ *   src, dst     int32 [num_forks] device.  dst[f] must hold no pages (its row of the table is
+ *                written over), be no fork's source and no other fork's destination; sources
+ *                may repeat.
+ *   seq_lens     int32 [B] device: seq_lens[dst[f]] = seq_lens[src[f]] is written
+ *   free_pages   int32 [num_free] device, taken from the front in the order of the forks (4-byte
+ *                aligned is enough)
+ *   block_table  int32 [B, max_pages] device: rows dst[f] are written
+ *   shares       int32 [num_pages] device: holders of each page beyond the first, so zeros for
+ *                a pool that no fork has touched; + 1 for every page that is shared
+ *   copies       int32 [num_forks, 3] written: source page, destination page and number of
+ *                tokens (-1, -1, 0: nothing to copy)
+ *   pages_used   int32 [1] written: how many of free_pages were taken
+ *
+ * A fork is refused, with INVALID_ARG in the device error word, if src or dst is out of range,
+ * the source's length is negative or does not fit its row, dst[f] is a source or an earlier
+ * fork's destination, or no page is left: nothing is written for it but its entry of copies.
+ * (Where src and its length are good, the page that it would take counts as taken.)  A page
+ * outside 0 .. num_pages-1 is neither counted nor copied and sets INVALID_ARG.  No array may
+ * overlap another.  num_forks == 0 writes pages_used = 0.
+ */
+kda_status kda_page_fork(const int32_t *src, const int32_t *dst, int num_forks, int32_t *seq_lens,
+                         const int32_t *free_pages, int num_free, int32_t *block_table,
+                         int max_pages, int B, int page_size, int num_pages, int32_t *shares,
+                         int32_t *copies, int32_t *pages_used, void *stream);
+
+/*
+ * kda_paged_copy -- copies pages within a cache: for each entry (source page, destination page,
+ * tokens) of copies int32 [num_copies, 3] the first `tokens` keys and values of all heads.  For
+ * what kda_page_fork lists, or a caller's own list (pages moved together).  A page that one
+ * entry writes must not be in another.  An entry of 0 tokens is skipped; one with a page
+ * outside 0 .. num_pages-1 or tokens outside 0 .. page_size is skipped and sets INVALID_ARG.
+ */
+kda_status kda_paged_copy(const int32_t *copies, int num_copies, const kda_paged_cache *cache,
+                          void *stream);
+
+/*
+ * kda_page_release -- gives pages back: request b keeps its first kept_lens[b] tokens of
+ * seq_lens[b] (0: it has ended) and leaves the pages that only the others need.  A page with
+ * shares has one less; one without is free.
+ *
+ *   seq_lens, kept_lens  int32 [B] device
+ *   block_table  int32 [B, max_pages] device, read
+ *   shares       int32 [num_pages] device, as in kda_page_fork; updated
+ *   freed        int32 [max_freed] written: the pages that are free now, ascending; entries
+ *                past num_freed stay as they were (it may be the end of the free list: 4-byte
+ *                aligned is enough)
+ *   num_freed    int32 [1] written
+ *
+ * A request with kept_lens[b] < 0 or > seq_lens[b], or a length that does not fit its row, is
+ * refused and keeps its pages.  A page that is given back more often than it is held is freed
+ * once; a page outside 0 .. num_pages-1 is passed over; pages past max_freed are not listed
+ * (their shares are 0: they are lost to the caller).  Each sets INVALID_ARG in the device error
+ * word.  No array may overlap another.  B == 0 writes num_freed = 0.
+ */
+kda_status kda_page_release(const int32_t *seq_lens, const int32_t *kept_lens,
+                            const int32_t *block_table, int max_pages, int B, int page_size,
+                            int num_pages, int32_t *shares, int32_t *freed, int max_freed,
+                            int32_t *num_freed, void *stream);
+
+/*
  * kda_debug_check_gate_division -- test hook: the gate kernel's common path
  * (|f + dt_bias| < 87) divides with an fma-based correctly rounded division
  * (Markstein's method) instead of IEEE division; this call runs it against
