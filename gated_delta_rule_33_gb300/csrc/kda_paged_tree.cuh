@@ -1,0 +1,1004 @@
+// kda_paged_tree.cuh -- softmax attention of a tree of drafted tokens per sequence over a paged
+// key-value cache that holds the drafted tokens' keys and values too.
+//
+// Node i of a sequence with L keys, n of them drafted, sees the C = L - n keys of the context
+// and the drafted key j (at position C + j) where bit j of its word is set:
+//
+//   s_j = scale <q_i, k_j>,  m = max_j s_j,  l = sum_j e^{s_j - m}
+//   o = sum_j e^{s_j - m} v_j / l,  lse = m + log l
+//
+// over the keys j that it sees; a node that sees none has o = 0 and lse = -inf.  Powers of two
+// throughout: the scores carry log2 e.
+//
+// Bound: a key and a value are 4 D bytes (2 D in 8 bits) and meet R = n G rows (G query heads
+// to a key head) in 4 D R flops: HBM up to some R = 300 of them (150), the tensor cores' full
+// rate beyond.  That rate needs tcgen05: the rows are the 128 rows of a product, the keys
+// (then the channels) its columns.
+//
+// Split.  A unit is (sequence, key head, up to kM x 128 rows); its keys are cut in tiles of 128
+// (64 at 256 channels).  The tiles of all units form one list, of which each CTA, one an SM,
+// takes an equal, contiguous piece; what is cut between CTAs is joined by a second, small
+// kernel that is set up with the first.
+//
+// A CTA.  Warps 8..11 copy the keys and values of its piece into two rings, rows swizzled as
+// the products read them (an 8-bit cache: raw, then widened to fp16, which holds every e4m3
+// value).  One thread issues the products: S = Q K^T from shared memory into one of
+// two score buffers in tensor memory, O += P V with P from there and V from shared memory,
+// the next step's S ahead of this one's O.  Warps 0..7 turn scores into weights in
+// place: a row is a lane of tensor memory, the two warps of a lane quarter halve its keys and
+// exchange their maxima through shared memory.  O is rescaled where a row's maximum grows.
+//
+// Precision: scores, maxima and sums in fp32.  For the product with the values a weight is two
+// words: bf16 numbers, 16 bits together (one would leave up to 2^-8 of every weight, as much as
+// the output's own rounding); over an 8-bit cache fp16 numbers of the weight times 2^13, which
+// keep it to 2^-38 of the largest, with the queries scaled to fp16's range by a power of
+// two a row.  The products' sums in tensor memory are cut off at each step of 16 keys:
+// 2^-24 of the sum, below the output's rounding by far.
+//
+// What is not finite.  A weight of 0 times an infinite or NaN value is NaN, and so is 0 (a
+// weight's second word) times an infinite one.  So a row whose output is not finite although
+// its weights are is computed again, key by key, over the keys that it sees (row_exact).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kda_sm100.cuh"
+#include "kda_tree.cuh"
+
+namespace kda {
+namespace treeatt {
+
+using namespace sm100;
+
+constexpr int kMaxCtas = 160;  // sizes the workspace; more SMs stay idle
+constexpr int kSoftWarps = 8, kCopyWarps = 4;
+constexpr int kThreads = 512;   // four warpgroups: weights (two), copies, products (one thread)
+// Their registers, of the 512 x 128 that the block is launched with: 2 x 184 + 80 + 56 = 504.
+constexpr int kSoftRegs = 184, kCopyRegs = 80, kProductRegs = 56;
+static_assert(2 * kSoftRegs + kCopyRegs + kProductRegs <= 512, "registers of the block");
+constexpr int kMinTiles = 1;   // of a CTA's piece
+constexpr uint32_t kMaxPolls = 1u << 20;
+
+__host__ __device__ constexpr int min_of(int a, int b) { return a < b ? a : b; }
+
+// m tiles of a unit: two where a sequence may have more than 128 rows and tensor memory has
+// room (2 x 128 columns of scores, 128 a tile of outputs).
+inline int m_tiles(int max_nodes, int group, int head_dim) {
+    return head_dim <= 128 && static_cast<int64_t>(max_nodes) * group > 128 ? 2 : 1;
+}
+
+inline size_t slot_bytes(int m, int head_dim) {
+    return static_cast<size_t>(m) * 128 * (head_dim + 2) * 4;
+}
+
+struct Args {
+    TreeAttention t;
+    FastDiv group;
+    float *ml;   // [CTAs][2][rows][2]
+    float *cut;  // [CTAs][2][D / 4][rows][4]
+};
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int kD_, bool kFp8_, int kM_>
+struct Shape {
+    static constexpr int kD = kD_, kM = kM_;
+    static constexpr bool kFp8 = kFp8_;
+    static constexpr int kRows = kM * 128;
+    static constexpr int kKeys = kD == 256 ? 64 : 128, kHalf = kKeys / 2;
+    static constexpr int kTile = kKeys * kD * 2;  // as an operand
+    static constexpr int kRaw = kTile / 2;        // of an 8-bit cache, as copied
+    static constexpr int kQ = kRows * kD * 2;
+    static constexpr int kRoom = 224 * 1024 - kQ;
+    // rings of operands, and of raw halves, in flight between copy and widening
+    static constexpr int kOps = kRoom / kTile;
+    static constexpr int kNK = kFp8 ? (kD == 64 || (kM == 1 && kD == 128) ? 2 : 1) : min_of(6, (kOps + 1) / 2);
+    static constexpr int kNV = kFp8 ? (kD == 64 ? 2 : 1) : min_of(6, kOps / 2);
+    static constexpr int kNR = kFp8 ? min_of(8, (kRoom - (kNK + kNV) * kTile) / kRaw) : 0;
+    static constexpr int kOffK = kQ, kOffV = kOffK + kNK * kTile, kOffRaw = kOffV + kNV * kTile;
+    static constexpr int kOffSmall = kOffRaw + kNR * kRaw;
+    static constexpr int kColO = 2 * kKeys;
+    static constexpr float kShift = kFp8 ? 13.f : 0.f;  // weights are 2^kShift times themselves
+    static_assert(kColO + kM * kD <= 512, "tensor memory");
+    static_assert(!kFp8 || kNR >= 3, "halves in flight");
+
+    struct Small {  // what lies behind the tiles
+        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], drain;
+        int64_t warp_sum[kThreads / 32], place[2];
+        float top[2][2][128];            // a half row's maximum, by step, half and row
+        uint32_t valid[16][kCopyWarps];  // which rows of a tile are keys, by copy warp
+        uint32_t tmem;
+    };
+    static constexpr int kSmem = kOffSmall + static_cast<int>(sizeof(Small));
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (kF16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <bool kF16>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+    if constexpr (kF16) return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    else return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
+    return y;
+}
+
+// ---- a row, key by key ---------------------------------------------------------------------
+
+// A lane's kN neighbouring values of a row, widened.
+template <bool kFp8, int kN>
+__device__ __forceinline__ void load_values(const uint8_t *p, float (&x)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+        const float2 f = kFp8 ? unpack2<true>(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(p + i)))
+                              : unpack2<false>(*reinterpret_cast<const uint32_t *>(p + 2 * i));
+        x[i] = f.x;
+        x[i + 1] = f.y;
+    }
+}
+
+// Channels [c0, c1) of one row's output, by one warp, in fp32 arithmetic over the keys that the
+// row sees.  The sums are averages from the first key on, so they are as large as the values.
+template <int kD, bool kFp8>
+__device__ __noinline__ void row_exact(const TreeAttention &a, int b, int64_t row, int qh, int n,
+                                       int len, int c0, int c1) {
+    constexpr int kN = kD / 32;
+    const int lane = threadIdx.x & 31, h = qh / a.group, context = len - n;
+    const uint64_t word = a.ancestors[row];
+    float q[kN], acc[kN], m = -INFINITY, l = 0.f;
+    load_values<false, kN>(
+        reinterpret_cast<const uint8_t *>(a.q + row * a.q_row_stride + qh * kD + lane * kN), q);
+    const float c = a.scale * kLog2e * (a.cache.k_scale != nullptr ? a.cache.k_scale[h] : 1.f);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+    for (int j = 0; j < len; ++j) {
+        if (j >= context && !((word >> (j - context)) & 1)) continue;
+        uint32_t idx, in_page;
+        a.cache.page.divmod(j, idx, in_page);
+        const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + idx];
+        if (page < 0 || page >= a.cache.num_pages) continue;
+        const int64_t off = page * a.cache.page_stride + in_page * a.cache.token_stride +
+                            h * a.cache.head_stride + lane * kN * (kFp8 ? 1 : 2);
+        float k[kN], v[kN], s = 0.f;
+        load_values<kFp8, kN>(a.cache.k + off, k);
+        load_values<kFp8, kN>(a.cache.v + off, v);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) s += q[i] * k[i];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        s *= c;
+        const float to = s > m || s != s ? s : m;
+        const float ref = to == -INFINITY ? 0.f : to;
+        const float p = exp2f(s - ref), before = l * exp2f(m - ref);
+        m = to;
+        l = before + p;
+        if (l == 0.f) continue;
+        const float w = p / l, rest = before / l;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) acc[i] = acc[i] * rest + w * v[i];
+    }
+    const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[h] : 1.f;
+    __nv_bfloat16 *o = a.o + (row * a.q_heads + qh) * kD;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int d = lane * kN + i;
+        if (d >= c0 && d < c1) o[d] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[i] * vs);
+    }
+}
+
+// ---- the list of tiles ---------------------------------------------------------------------
+
+// A place in the list: a unit's tile t.
+template <class S>
+struct Cursor {
+    int b, h, rg, t;
+    int n, len, rows, groups, tiles;  // of the sequence; rows = n G
+    int64_t first;                    // its first row
+
+    __device__ __forceinline__ void request(const TreeAttention &a, int at) {
+        b = at;
+        const TreeRows r = tree_rows(a.cu, b, a.N, a.max_nodes);
+        len = a.seq_lens[b];
+        first = r.first;
+        n = r.n;
+        if (len < n || len > static_cast<int64_t>(a.max_pages) * a.cache.page.d) n = 0;
+        rows = n * a.group;
+        groups = (rows + S::kRows - 1) / S::kRows;
+        tiles = n == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(len) + S::kKeys - 1) / S::kKeys);
+    }
+    __device__ __forceinline__ int64_t list_tiles(const TreeAttention &a) const {
+        return static_cast<int64_t>(a.cache.heads) * groups * tiles;
+    }
+    // Tile `at` of the sequence's part of the list.
+    __device__ __forceinline__ void seek(int64_t at) {
+        const int64_t u = at / tiles;
+        t = static_cast<int>(at - u * tiles);
+        h = static_cast<int>(u / groups);
+        rg = static_cast<int>(u - static_cast<int64_t>(h) * groups);
+    }
+    __device__ __forceinline__ void next_unit(const TreeAttention &a) {
+        t = 0;
+        if (++rg < groups) return;
+        rg = 0;
+        if (++h < a.cache.heads) return;
+        h = 0;
+        for (int i = b + 1; i < a.B; ++i) {
+            request(a, i);
+            if (tiles > 0) return;
+        }
+        tiles = 0;
+        b = a.B;
+    }
+};
+
+// The block's way through the list; every thread of the block calls it.  begin(c): the first
+// tile of piece c.
+struct List {
+    int64_t total;
+    int pieces;
+
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return total * c / pieces; }
+    __device__ __forceinline__ int piece_of(int64_t at) const {
+        return static_cast<int>(((at + 1) * pieces - 1) / total);
+    }
+};
+
+template <class S, int kWarps>
+__device__ __forceinline__ int64_t scan_sum(int64_t x, int64_t *s_warp, int64_t &before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t sum = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    int64_t all = 0;
+    before = sum - x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int64_t y = s_warp[w];
+        if (w < warp) before += y;
+        all += y;
+    }
+    return all;
+}
+
+// The list, and in s_place (shared) the sequence and tile within it of list place `at(list)`
+// (b = -1: past the end).
+template <class S, int kWarps, class At>
+__device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int64_t *s_warp,
+                                           int64_t (&s_place)[2], At at) {
+    const int tid = threadIdx.x;
+    constexpr int kStep = kWarps * 32;
+    List list;
+    list.total = 0;
+    Cursor<S> c;
+    int64_t mine = 0, before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kStep) {
+        mine = 0;
+        if (b0 + tid < a.B) {
+            c.request(a, b0 + tid);
+            mine = c.list_tiles(a);
+        }
+        list.total += scan_sum<S, kWarps>(mine, s_warp, before);
+    }
+    const int64_t most = (list.total + kMinTiles - 1) / kMinTiles;
+    list.pieces = static_cast<int>(most < ctas ? (most < 1 ? 1 : most) : ctas);
+    if (tid == 0) s_place[0] = -1;
+    __syncthreads();
+    const int64_t place = at(list);
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kStep) {
+        if (a.B > kStep) {  // else the first pass's values stand
+            mine = 0;
+            if (b0 + tid < a.B) {
+                c.request(a, b0 + tid);
+                mine = c.list_tiles(a);
+            }
+            const int64_t all = scan_sum<S, kWarps>(mine, s_warp, before);
+            before += base;
+            base += all;
+        }
+        if (b0 + tid < a.B && place >= before && place < before + mine) {
+            s_place[0] = b0 + tid;
+            s_place[1] = place - before;
+        }
+    }
+    __syncthreads();
+    return list;
+}
+
+// ---- products ------------------------------------------------------------------------------
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands of one type, fp32 sums.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// 16 bytes to shared memory, or zeros (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void pair_barrier(int quarter) {
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void leave_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Which of the 64 keys from drafted place d (below 0: still context) on a word sees.
+__device__ __forceinline__ uint64_t seen_from(uint64_t word, int d) {
+    if (d <= -64) return ~uint64_t{0};
+    if (d < 0) return (word << -d) | bits_below(-d);
+    return d >= 64 ? 0 : word >> d;
+}
+
+// A wait that runs out is an error, and the role that waited ends (the others' waits run out
+// too).  kWarp: by a whole warp, whose lanes agree and go on together.
+template <bool kWarp>
+struct Waits {
+    unsigned int *err;
+    bool ok;
+
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait_bounded(bar, parity, kMaxPolls)) {
+            record_device_error(err, kDevTimeout);
+            ok = false;
+        }
+        if constexpr (kWarp) ok = __all_sync(0xffffffffu, ok);
+        return ok;
+    }
+};
+
+// ---- the kernel ------------------------------------------------------------------------------
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __grid_constant__ Args args) {
+    constexpr int kD = S::kD, kM = S::kM, kKeys = S::kKeys, kHalf = S::kHalf;
+    constexpr bool kFp8 = S::kFp8;
+    constexpr int kWarps = kThreads / 32;
+    extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles: 1024-byte groups of rows
+    typename S::Small &sm = *reinterpret_cast<typename S::Small *>(smem + S::kOffSmall);
+    const TreeAttention &a = args.t;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_addr(smem);
+
+    if (warp == kSoftWarps + kCopyWarps) tmem_alloc(&sm.tmem, 512);
+    if (tid == 0) {
+        mbar_init(&sm.qfull, kSoftWarps);
+        for (int i = 0; i < S::kNK; ++i) {
+            // widened by the threads of the copy warps; else their copies', and a word of `valid` each
+            mbar_init(&sm.kfull[i], kFp8 ? kCopyWarps * 32 : kCopyWarps * 32 + kCopyWarps);
+            mbar_init(&sm.kempty[i], 1);
+        }
+        for (int i = 0; i < S::kNV; ++i) {
+            mbar_init(&sm.vfull[i], kCopyWarps * 32);
+            mbar_init(&sm.vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.pfull[i], kSoftWarps);
+        }
+        for (int i = 0; i < kM; ++i) mbar_init(&sm.odone[i], 1);
+        mbar_init(&sm.drain, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    wait_for_kernel_before();
+
+    const List list = find_place<S, kWarps>(a, gridDim.x, sm.warp_sum, sm.place, [&](const List &l) {
+        return static_cast<int>(blockIdx.x) < l.pieces ? l.begin(blockIdx.x) : l.total;
+    });
+    int64_t left = 0;
+    Cursor<S> at = {};
+    if (sm.place[0] >= 0) {
+        left = list.begin(blockIdx.x + int64_t{1}) - list.begin(blockIdx.x);
+        at.request(a, static_cast<int>(sm.place[0]));
+        at.seek(sm.place[1]);
+    }
+
+    if (warp < kSoftWarps) {
+        // ---- queries in, weights, outputs ------------------------------------------------
+        take_registers<kSoftRegs>();
+        Waits<true> wait = {a.err, true};
+        const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint32_t step = 0, tiles_done = 0, o_count[kM] = {};
+        while (left > 0 && wait.ok) {
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+            const int row0 = at.rg * S::kRows;
+            const float ks = a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f;
+            bool real[kM], some[kM];
+            int64_t row[kM];
+            int qh[kM];
+            uint64_t word[kM];
+            float c[kM], m[kM], l[kM];
+#pragma unroll
+            for (int t = 0; t < kM; ++t) {
+                const int rr = row0 + t * 128 + lrow;
+                some[t] = row0 + t * 128 + quarter * 32 < at.rows;
+                real[t] = rr < at.rows;
+                uint32_t node, g;
+                args.group.divmod(rr, node, g);
+                row[t] = at.first + node;
+                qh[t] = at.h * a.group + static_cast<int>(g);
+                word[t] = 0;
+                m[t] = -INFINITY;
+                l[t] = 0.f;
+                c[t] = a.scale * kLog2e * ks;
+                if (!some[t]) continue;
+                constexpr int kPieces = kD / 16;  // 16-byte pieces of half a row
+                const uint4 *src = nullptr;
+                if (real[t]) {
+                    word[t] = a.ancestors[row[t]] & bits_below(at.n);
+                    src = reinterpret_cast<const uint4 *>(a.q + row[t] * a.q_row_stride + qh[t] * kD +
+                                                          wg * (kD / 2));
+                }
+                auto place = [&](int i) {  // of piece i
+                    const int ch = wg * kPieces + i;
+                    return smem + t * (128 * kD * 2) + (ch >> 3) * (128 * 128) + lrow * 128 +
+                           (((ch & 7) ^ (lrow & 7)) << 4);
+                };
+                if constexpr (!kFp8) {
+#pragma unroll
+                    for (int i0 = 0; i0 < kPieces; i0 += 8) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
+                            if (real[t]) x[i] = src[i0 + i];
+#pragma unroll
+                        for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
+                            if (real[t]) *reinterpret_cast<uint4 *>(place(i0 + i)) = x[i];
+                    }
+                } else {
+                    // scaled by a power of two that puts the row's largest value below 2^15
+                    uint32_t top = 0;
+                    if (real[t])
+                        for (int i = 0; i < kPieces; ++i) {
+                            const uint4 x = src[i];
+                            for (const uint32_t y : {x.x, x.y, x.z, x.w})
+                                top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
+                        }
+                    sm.top[0][wg][lrow] = __uint_as_float(top);
+                    pair_barrier(quarter);
+                    top = max(top, __float_as_uint(sm.top[0][wg ^ 1][lrow]));
+                    pair_barrier(quarter);
+                    const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127;  // its exponent
+                    // (two factors: neither leaves fp32's range)
+                    const float up0 = exp2f(static_cast<float>((14 - e) / 2));
+                    const float up1 = exp2f(static_cast<float>(14 - e - (14 - e) / 2));
+                    c[t] = c[t] * exp2f(static_cast<float>((e - 14) / 2)) *
+                           exp2f(static_cast<float>(e - 14 - (e - 14) / 2));
+                    if (real[t])
+                        for (int i = 0; i < kPieces; ++i) {
+                            uint4 x = src[i];
+                            uint32_t *y = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = unpack2<false>(y[k]);
+                                y[k] = pack2<true>(f.x * up0 * up1, f.y * up0 * up1);
+                            }
+                            *reinterpret_cast<uint4 *>(place(i)) = x;
+                        }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.qfull);
+            const int m_used = at.rows - row0 > 128 ? kM : 1;
+
+            for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++tiles_done) {
+#pragma unroll
+                for (int t = 0; t < kM; ++t) {
+                    if (t >= m_used) break;
+                    const uint32_t buf = step & 1;
+                    wait(&sm.sfull[buf], (step >> 1) & 1);
+                    ++step;
+                    __syncwarp();
+                    if (!wait.ok) break;
+                    if (some[t]) {
+                        tc_fence_after();
+                        const uint32_t cols = lanes + buf * kKeys + wg * kHalf;
+                        float s[kHalf / 32][32];
+#pragma unroll
+                        for (int i = 0; i < kHalf / 32; ++i) tmem_ld32(cols + 32 * i, s[i]);
+                        // the keys of this half that the row sees
+                        const uint32_t *v = sm.valid[tiles_done & 15] + 2 * wg;
+                        uint64_t seen = kHalf == 64 ? static_cast<uint64_t>(v[1]) << 32 | v[0]
+                                                    : static_cast<uint64_t>(v[1] << 16 | v[0]);
+                        const int d = tile * kKeys + wg * kHalf - (at.len - at.n);
+                        if (d + kHalf > 0) seen &= seen_from(word[t], d);
+                        constexpr uint64_t kAll = kHalf == 64 ? ~uint64_t{0} : 0xffffffffu;
+                        seen &= kAll;
+                        tmem_wait_ld();
+                        float top = -INFINITY;
+                        if (__all_sync(0xffffffffu, seen == kAll)) {
+#pragma unroll
+                            for (int i = 0; i < kHalf; ++i) {
+                                s[i / 32][i % 32] *= c[t];
+                                top = fmaxf(top, s[i / 32][i % 32]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kHalf; ++i) {
+                                const bool in = (seen >> i) & 1;
+                                s[i / 32][i % 32] = in ? s[i / 32][i % 32] * c[t] : -INFINITY;
+                                top = fmaxf(top, s[i / 32][i % 32]);
+                            }
+                        }
+                        sm.top[buf][wg][lrow] = top;
+                        pair_barrier(quarter);
+                        const float to = fmaxf(m[t], fmaxf(top, sm.top[buf][wg ^ 1][lrow]));
+                        const float ref = to == -INFINITY ? 0.f : to;
+                        if (tile > at.t && __any_sync(0xffffffffu, to > m[t])) {
+                            const float keep = ex2(m[t] - ref);
+                            l[t] *= keep;
+                            wait(&sm.odone[t], (o_count[t] - 1) & 1);
+                            __syncwarp();
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = 0; i < kD / 64; ++i) {
+                                float o[32];
+                                const uint32_t oc = lanes + S::kColO + t * kD + wg * (kD / 2) + 32 * i;
+                                tmem_ld32(oc, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= keep;
+                                tmem_st32(oc, o);
+                            }
+                        }
+                        m[t] = to;
+                        const float off = S::kShift - ref;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < kHalf / 32; ++i) {
+                            float hi[16], lo[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float p0 = ex2(s[i][2 * k] + off), p1 = ex2(s[i][2 * k + 1] + off);
+                                sum += p0 + p1;
+                                const uint32_t x = pack2<kFp8>(p0, p1);
+                                const float2 y = unpack2<kFp8>(x);
+                                hi[k] = __uint_as_float(x);
+                                lo[k] = __uint_as_float(pack2<kFp8>(p0 - y.x, p1 - y.y));
+                            }
+                            tmem_st16(cols + 16 * i, hi);
+                            tmem_st16(cols + kHalf / 2 + 16 * i, lo);
+                        }
+                        l[t] += sum;
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                    ++o_count[t];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+                }
+            }
+
+            // outputs: a whole unit's to o, a cut one's to the workspace
+            const bool whole = at.t == 0 && t1 == at.tiles;
+            const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
+            const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
+#pragma unroll
+            for (int t = 0; t < kM; ++t) {
+                if (t >= m_used || !some[t]) break;
+                wait(&sm.odone[t], (o_count[t] - 1) & 1);
+                __syncwarp();
+                if (!wait.ok) break;
+                tc_fence_after();
+                sm.top[0][wg][lrow] = l[t];
+                pair_barrier(quarter);
+                const float all = sm.top[0][0][lrow] + sm.top[0][1][lrow];
+                pair_barrier(quarter);
+                const float f = all == 0.f ? 0.f : 1.f / all;
+                float nan = 0.f;
+                const int64_t out = row[t] * a.q_heads + qh[t];
+#pragma unroll
+                for (int i = 0; i < kD / 64; ++i) {
+                    float o[32];
+                    const int d = wg * (kD / 2) + 32 * i;
+                    tmem_ld32(lanes + S::kColO + t * kD + d, o);
+                    tmem_wait_ld();
+                    if (whole) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            nan = fmaf(o[k], 0.f, fmaf(o[k + 1], 0.f, nan));
+                            y[k / 2] = all == 0.f ? 0u : pack2<false>(o[k] * f * vs, o[k + 1] * f * vs);
+                        }
+                        if (real[t])
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                reinterpret_cast<uint4 *>(a.o + out * kD + d)[k] =
+                                    make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            reinterpret_cast<float4 *>(args.cut)[(slot * (kD / 4) + d / 4 + k) * S::kRows +
+                                                                 t * 128 + lrow] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                tc_fence_before();
+                if (whole) {
+                    if (real[t] && wg == 0 && a.lse != nullptr)
+                        a.lse[out] = all == 0.f ? -INFINITY : (m[t] + log2f(all) - S::kShift) * kLn2;
+                    // what is not finite although the weights are
+                    uint32_t again = __ballot_sync(0xffffffffu, real[t] && nan != 0.f && all * 0.f == 0.f &&
+                                                                    all != 0.f);
+                    while (again != 0) {
+                        const int src = __ffs(static_cast<int>(again)) - 1;
+                        again &= again - 1;
+                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, row[t], src),
+                                            __shfl_sync(0xffffffffu, qh[t], src), at.n, at.len,
+                                            wg * (kD / 2), (wg + 1) * (kD / 2));
+                        __syncwarp();
+                    }
+                } else if (wg == 0) {
+                    reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + t * 128 + lrow] =
+                        make_float2(m[t], all);
+                }
+            }
+            left -= t1 - at.t;
+            if (left > 0) at.next_unit(a);
+        }
+    } else if (warp < kSoftWarps + kCopyWarps) {
+        // ---- keys and values in --------------------------------------------------------------
+        leave_registers<kCopyRegs>();
+        Waits<true> wait = {a.err, true};
+        const int cw = warp - kSoftWarps;
+        constexpr int kRowsOfWarp = kKeys / kCopyWarps;
+        constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
+        constexpr int kPieces = kRowBytes / 16;          // lanes to a row
+        constexpr int kAtOnce = 32 / kPieces;            // rows of a warp's copy
+        constexpr int kTurns = kRowsOfWarp / kAtOnce;
+        const int sub = lane / kPieces, ch = lane % kPieces;
+        uint32_t item = 0, landed = 0;                   // halves of tiles: copied, widened
+        uint32_t made = 0;                               // tiles
+        // this lane's row of the next tile
+        auto page_at = [&](int tile, uint32_t &in_page, bool &held) {
+            const uint32_t j = static_cast<uint32_t>(tile) * kKeys + cw * kRowsOfWarp + lane;
+            uint32_t idx;
+            a.cache.page.divmod(j, idx, in_page);
+            held = lane < kRowsOfWarp && j < static_cast<uint32_t>(at.len);
+            return held ? a.block_table[static_cast<int64_t>(at.b) * a.max_pages + idx] : -1;
+        };
+        // a raw half, widened into its place as an operand (8-bit cache)
+        auto widen = [&]() {
+            if constexpr (kFp8) {
+                const bool is_v = landed & 1;
+                const uint32_t i = landed >> 1, n = is_v ? S::kNV : S::kNK, slot = i % n;
+                if (!wait(is_v ? &sm.vempty[slot] : &sm.kempty[slot], ((i / n) & 1) ^ 1)) return;
+                const uint8_t *raw = smem + S::kOffRaw + (landed % S::kNR) * S::kRaw;
+                uint8_t *to = smem + (is_v ? S::kOffV : S::kOffK) + slot * S::kTile;
+#pragma unroll 4
+                for (int k = 0; k < kTurns; ++k) {
+                    const int r = cw * kRowsOfWarp + k * kAtOnce + sub;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(raw + (k * kAtOnce * kCopyWarps * kPieces + cw * 32 + lane) * 16);
+                    uint4 y0, y1;
+                    y0.x = e4m3x2_to_f16x2(x.x);
+                    y0.y = e4m3x2_to_f16x2(x.x >> 16);
+                    y0.z = e4m3x2_to_f16x2(x.y);
+                    y0.w = e4m3x2_to_f16x2(x.y >> 16);
+                    y1.x = e4m3x2_to_f16x2(x.z);
+                    y1.y = e4m3x2_to_f16x2(x.z >> 16);
+                    y1.z = e4m3x2_to_f16x2(x.w);
+                    y1.w = e4m3x2_to_f16x2(x.w >> 16);
+                    uint8_t *row = to + (ch >> 2) * (kKeys * 128) + r * 128;
+                    *reinterpret_cast<uint4 *>(row + ((((2 * ch) & 7) ^ (r & 7)) << 4)) = y0;
+                    *reinterpret_cast<uint4 *>(row + ((((2 * ch + 1) & 7) ^ (r & 7)) << 4)) = y1;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(is_v ? &sm.vfull[slot] : &sm.kfull[slot]);
+                ++landed;
+            }
+        };
+        int page = -1;
+        uint32_t in_page = 0;
+        bool held = false;
+        if (left > 0) page = page_at(at.t, in_page, held);
+        while (left > 0 && wait.ok) {
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+            left -= t1 - at.t;
+            for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++made) {
+                const bool ok = page >= 0 && page < a.cache.num_pages;
+                if (held && !ok) record_device_error(a.err, kDevInvalidArg);
+                const int64_t off = ok ? page * a.cache.page_stride + in_page * a.cache.token_stride +
+                                             at.h * a.cache.head_stride
+                                       : -1;
+                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                // the next tile's pages, ahead of this one's copies
+                if (tile + 1 < t1) {
+                    page = page_at(tile + 1, in_page, held);
+                } else if (left > 0) {
+                    at.next_unit(a);
+                    page = page_at(0, in_page, held);
+                    // (at.t is 0, and tile + 1 == t1 ends this loop)
+                }
+                auto copy = [&](const uint8_t *data, uint32_t to) {
+#pragma unroll 8
+                    for (int k = 0; k < kTurns; ++k) {
+                        const int r = k * kAtOnce + sub;
+                        const int64_t from = __shfl_sync(0xffffffffu, off, r);
+                        const int rr = cw * kRowsOfWarp + r;
+                        uint32_t dst;
+                        if constexpr (kFp8) dst = to + (k * kAtOnce * kCopyWarps * kPieces + cw * 32 + lane) * 16;
+                        else dst = to + (ch >> 3) * (kKeys * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+                        copy16(dst, data + (from < 0 ? 0 : from) + ch * 16, from >= 0);
+                    }
+                };
+                if constexpr (!kFp8) {
+                    const uint32_t ks = made % S::kNK, vs = made % S::kNV;
+                    if (!wait(&sm.kempty[ks], ((made / S::kNK) & 1) ^ 1)) break;
+                    __syncwarp();
+                    copy(a.cache.k, base + S::kOffK + ks * S::kTile);
+                    copies_arrive(&sm.kfull[ks]);
+                    if (lane == 0) {
+                        sm.valid[made & 15][cw] = valid;
+                        mbar_arrive(&sm.kfull[ks]);
+                    }
+                    if (!wait(&sm.vempty[vs], ((made / S::kNV) & 1) ^ 1)) break;
+                    __syncwarp();
+                    copy(a.cache.v, base + S::kOffV + vs * S::kTile);
+                    copies_arrive(&sm.vfull[vs]);
+                } else {
+                    if (lane == 0) sm.valid[made & 15][cw] = valid;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        copy(half ? a.cache.v : a.cache.k, base + S::kOffRaw + (item % S::kNR) * S::kRaw);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        if (++item >= S::kNR) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(S::kNR > 0 ? S::kNR - 1 : 0) : "memory");
+                            widen();
+                            if (!wait.ok) break;
+                            __syncwarp();
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        while (kFp8 && landed < item && wait.ok) widen();
+    } else {
+        // ---- products ------------------------------------------------------------------------
+        leave_registers<kProductRegs>();
+        if (warp == kSoftWarps + kCopyWarps && lane == 0) {
+            Waits<false> wait = {a.err, true};
+            constexpr uint32_t kFmt = kFp8 ? kFmtF16 : kFmtBF16;
+            constexpr uint32_t kIdS = instr_desc(128, kKeys, kFmt, 0, 0), kIdO = instr_desc(128, kD, kFmt, 0, 1);
+            uint32_t step_s = 0, step_p = 0, kt = 0, vt = 0, units = 0;
+            while (left > 0 && wait.ok) {
+                const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+                const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+                const int steps = (t1 - at.t) * m_used;
+                wait(&sm.qfull, units & 1);
+                ++units;
+                auto scores = [&](int i) {  // of step i of this unit
+                    const int t = m_used == 1 ? 0 : i & 1;
+                    const uint32_t ks = kt % S::kNK;
+                    if (t == 0) {
+                        if (!wait(&sm.kfull[ks], (kt / S::kNK) & 1)) return;
+                        // the copies wrote by the generic proxy, the product reads by the async one
+                        fence_proxy_async_smem();
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + (step_s & 1) * kKeys;
+                    const uint64_t qd = smem_desc(base + t * (128 * kD * 2), 16, 1024, kSwizzle128B);
+                    const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
+    #pragma unroll
+                    for (int k = 0; k < kD / 16; ++k)
+                        mma_f16_ss(d, qd + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                                   kd + ((k / 4) * (kKeys * 128) + (k % 4) * 32) / 16, kIdS, k > 0);
+                    mma_commit(&sm.sfull[step_s & 1]);
+                    if (t == m_used - 1) {
+                        mma_commit(&sm.kempty[ks]);
+                        ++kt;
+                    }
+                    ++step_s;
+                };
+                auto outputs = [&](int i) {
+                    const int t = m_used == 1 ? 0 : i & 1;
+                    const uint32_t vs = vt % S::kNV, buf = step_p & 1;
+                    if (t == 0) {
+                        if (!wait(&sm.vfull[vs], (vt / S::kNV) & 1)) return;
+                        fence_proxy_async_smem();
+                    }
+                    if (!wait(&sm.pfull[buf], (step_p >> 1) & 1)) return;
+                    tc_fence_after();
+                    const uint32_t d = tmem + S::kColO + t * kD;
+                    const uint64_t vd = smem_desc(base + S::kOffV + vs * S::kTile, kKeys * 128, 1024, kSwizzle128B);
+    #pragma unroll
+                    for (int k = 0; k < kKeys / 16 * 2; ++k) {
+                        const int part = k / (kKeys / 16), key = k % (kKeys / 16) * 16;  // word, keys
+                        const uint32_t p = tmem + buf * kKeys + key / kHalf * kHalf + key % kHalf / 2 + part * (kHalf / 2);
+                        mma_f16_ts(d, p, vd + key * 128 / 16, kIdO, k > 0 || i >= m_used);
+                    }
+                    mma_commit(&sm.odone[t]);
+                    if (t == m_used - 1) {
+                        mma_commit(&sm.vempty[vs]);
+                        ++vt;
+                    }
+                    ++step_p;
+                };
+                if (wait.ok) scores(0);
+                for (int i = 0; i < steps && wait.ok; ++i) {
+                    if (i + 1 < steps) scores(i + 1);
+                    if (wait.ok) outputs(i);
+                }
+                left -= t1 - at.t;
+                if (left > 0) at.next_unit(a);
+            }
+            // nothing is in flight when tensor memory is given back
+            mma_commit(&sm.drain);
+            mbar_wait_bounded(&sm.drain, 0, kMaxPolls);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps + kCopyWarps) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the unit that CTA blockIdx.x of the first kernel began and did not finish:
+// its slot 1, and slot 0 of the CTAs after it up to the last.  A thread has one row and 8
+// channels (blockIdx.y).  Blocks (c, 0) also look after sequences that have no keys.
+template <class S>
+__global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_constant__ Args args, int ctas) {
+    constexpr int kD = S::kD, kWarps = S::kRows / 32;
+    __shared__ int64_t s_warp[kWarps], s_place[2];
+    const TreeAttention &a = args.t;
+    const int tid = threadIdx.x, c0 = blockIdx.x;
+    // (this kernel is set up once the first one's blocks have all waited for what was before
+    // them, so the lengths, which the first one does not write, may be read here)
+    const List list = find_place<S, kWarps>(a, ctas, s_warp, s_place, [&](const List &l) {
+        return c0 < l.pieces ? l.begin(c0 + int64_t{1}) : l.total;
+    });
+    Cursor<S> cut = {};
+    int parts = 0;
+    if (s_place[0] >= 0) {
+        cut.request(a, static_cast<int>(s_place[0]));
+        cut.seek(s_place[1]);
+        const int64_t end = list.begin(c0 + int64_t{1}), start = end - cut.t;
+        if (cut.t > 0 && start >= list.begin(c0)) parts = list.piece_of(start + cut.tiles - 1) - c0 + 1;
+    }
+    wait_for_kernel_before();
+    const int r = cut.rg * S::kRows + tid;
+    if (parts > 0) {
+        const bool real = r < cut.rows;
+        uint32_t node, g;
+        args.group.divmod(r, node, g);
+        const int64_t row = cut.first + node;
+        const int qh = cut.h * a.group + static_cast<int>(g), d = blockIdx.y * 8;
+        auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+        float m = -INFINITY, l = 0.f, acc[8] = {}, nan = 0.f;
+        if (real) {
+#pragma unroll 8
+            for (int i = 0; i < parts; ++i)
+                m = fmaxf(m, reinterpret_cast<const float2 *>(args.ml)[slot(i) * S::kRows + tid].x);
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+            for (int i = 0; i < parts; ++i) {
+                const float2 x = reinterpret_cast<const float2 *>(args.ml)[slot(i) * S::kRows + tid];
+                const float w = ex2(x.x - ref);
+                l += w * x.y;
+                const float4 *p = reinterpret_cast<const float4 *>(args.cut) +
+                                  (slot(i) * (kD / 4) + d / 4) * S::kRows + tid;
+                const float4 y = p[0], z = p[S::kRows];
+                acc[0] += w * y.x;
+                acc[1] += w * y.y;
+                acc[2] += w * y.z;
+                acc[3] += w * y.w;
+                acc[4] += w * z.x;
+                acc[5] += w * z.y;
+                acc[6] += w * z.z;
+                acc[7] += w * z.w;
+            }
+            const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[cut.h] : 1.f;
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            const int64_t out = row * a.q_heads + qh;
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                nan = fmaf(acc[k], 0.f, fmaf(acc[k + 1], 0.f, nan));
+                y[k / 2] = l == 0.f ? 0u : pack2<false>(acc[k] * f * vs, acc[k + 1] * f * vs);
+            }
+            *reinterpret_cast<uint4 *>(a.o + out * kD + d) = make_uint4(y[0], y[1], y[2], y[3]);
+            if (a.lse != nullptr && blockIdx.y == 0)
+                a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - S::kShift) * kLn2;
+        }
+        uint32_t again = __ballot_sync(0xffffffffu, real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
+        while (again != 0) {
+            const int src = __ffs(static_cast<int>(again)) - 1;
+            again &= again - 1;
+            row_exact<kD, S::kFp8>(a, cut.b, __shfl_sync(0xffffffffu, row, src),
+                                   __shfl_sync(0xffffffffu, qh, src), cut.n, cut.len, d, d + 8);
+            __syncwarp();
+        }
+    }
+    if (blockIdx.y != 0) return;
+    for (int b = c0; b < a.B; b += gridDim.x) {
+        const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
+        const int len = a.seq_lens[b];
+        const bool fits = len >= t.rows && len <= static_cast<int64_t>(a.max_pages) * a.cache.page.d;
+        if (!t.bad && fits) continue;
+        if (tid == 0) record_device_error(a.err, kDevInvalidArg);
+        const int64_t rows = static_cast<int64_t>(t.rows) * a.q_heads, o0 = t.first * a.q_heads;
+        for (int64_t i = tid; i < rows * (kD / 8); i += S::kRows)
+            reinterpret_cast<uint4 *>(a.o + o0 * kD)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse != nullptr)
+            for (int64_t i = tid; i < rows; i += S::kRows) a.lse[o0 + i] = -INFINITY;
+    }
+}
+
+template <class S>
+cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
+    const cudaError_t e =
+        ensure_dynamic_smem(reinterpret_cast<const void *>(&tree_attention_kernel<S>), S::kSmem);
+    if (e != cudaSuccess) return e;
+    const cudaError_t e1 = launch_early(tree_attention_kernel<S>, dim3(ctas), kThreads, S::kSmem, s, a);
+    if (e1 != cudaSuccess) return e1;
+    return launch_early(tree_join_kernel<S>, dim3(ctas, S::kD / 8), S::kRows, 0, s, a, ctas);
+}
+
+}  // namespace
+
+// Instantiated for each head_dim in a file of its own: they compile side by side.
+template <int kD>
+cudaError_t launch_dim(const Args &a, int m, int ctas, cudaStream_t s) {
+    if constexpr (kD <= 128)
+        if (m == 2)
+            return a.t.cache.fp8 ? launch_shape<Shape<kD, true, 2>>(a, ctas, s)
+                                 : launch_shape<Shape<kD, false, 2>>(a, ctas, s);
+    return a.t.cache.fp8 ? launch_shape<Shape<kD, true, 1>>(a, ctas, s)
+                         : launch_shape<Shape<kD, false, 1>>(a, ctas, s);
+}
+
+}  // namespace treeatt
+}  // namespace kda
