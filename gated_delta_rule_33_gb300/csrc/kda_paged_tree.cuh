@@ -26,12 +26,15 @@
 // two score buffers in tensor memory, O += P V with P from there and V from shared memory,
 // the next step's S ahead of this one's O.  Warps 0..7 turn scores into weights in
 // place: a row is a lane of tensor memory, the two warps of a lane quarter halve its keys and
-// exchange their maxima through shared memory.  O is rescaled where a row's maximum grows.
+// exchange their maxima through shared memory.  A row's weights are relative to a reference
+// that follows its maximum only when that has grown by 2^7 (2^3 over an 8-bit cache): O is then
+// rescaled, which waits for the last product (at every growth, some row of a warp grows in most
+// tiles: MEASURE).
 //
 // Precision: scores, maxima and sums in fp32.  For the product with the values a weight is two
 // words: bf16 numbers, 16 bits together (one would leave up to 2^-8 of every weight, as much as
-// the output's own rounding); over an 8-bit cache fp16 numbers of the weight times 2^13, which
-// keep it to 2^-38 of the largest, with the queries scaled to fp16's range by a power of
+// the output's own rounding); over an 8-bit cache fp16 numbers of the weight times 2^12, which
+// keep it to 2^-37 of the largest, with the queries scaled to fp16's range by a power of
 // two a row.  The products' sums in tensor memory are cut off at each step of 16 keys:
 // 2^-24 of the sum, below the output's rounding by far.
 //
@@ -40,8 +43,11 @@
 // its weights are is computed again, key by key, over the keys that it sees (row_exact).
 #pragma once
 
+#include <cfloat>
+
 #include <cuda_fp16.h>
 
+#include "kda_f32x2.cuh"
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
@@ -101,12 +107,14 @@ struct Shape {
     static constexpr int kOffK = kQ, kOffV = kOffK + kNK * kTile, kOffRaw = kOffV + kNV * kTile;
     static constexpr int kOffSmall = kOffRaw + kNR * kRaw;
     static constexpr int kColO = 2 * kKeys;
-    static constexpr float kShift = kFp8 ? 13.f : 0.f;  // weights are 2^kShift times themselves
+    // a row's reference follows its maximum when that has grown by 2^kSlack; weights are
+    // 2^kShift times themselves (fp16 ends at 2^16)
+    static constexpr float kSlack = kFp8 ? 3.f : 7.f, kShift = kFp8 ? 12.f : 0.f;
     static_assert(kColO + kM * kD <= 512, "tensor memory");
     static_assert(!kFp8 || kNR >= 3, "halves in flight");
 
     struct Small {  // what lies behind the tiles
-        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], drain;
+        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], done, drain;
         int64_t warp_sum[kThreads / 32], place[2];
         float top[2][2][128];            // a half row's maximum, by step, half and row
         uint32_t valid[16][kCopyWarps];  // which rows of a tile are keys, by copy warp
@@ -121,6 +129,9 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// x, or the least normal number where x is below it; a NaN stays.
+__device__ __forceinline__ float at_least_normal(float x) { return x < FLT_MIN ? FLT_MIN : x; }
 
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -334,12 +345,13 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
 
 // ---- products ------------------------------------------------------------------------------
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands of one type, fp32 sums.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands of one type, fp32 sums; by one lane of a
+// converged warp.
+__device__ __forceinline__ void mma_f16_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -375,9 +387,8 @@ __device__ __forceinline__ uint64_t seen_from(uint64_t word, int d) {
     return d >= 64 ? 0 : word >> d;
 }
 
-// A wait that runs out is an error, and the role that waited ends (the others' waits run out
-// too).  kWarp: by a whole warp, whose lanes agree and go on together.
-template <bool kWarp>
+// A wait, by a whole warp, whose lanes agree and go on together.  One that runs out is an
+// error, and the role that waited ends (the others' waits run out too).
 struct Waits {
     unsigned int *err;
     bool ok;
@@ -387,7 +398,7 @@ struct Waits {
             record_device_error(err, kDevTimeout);
             ok = false;
         }
-        if constexpr (kWarp) ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, ok);
         return ok;
     }
 };
@@ -422,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             mbar_init(&sm.pfull[i], kSoftWarps);
         }
         for (int i = 0; i < kM; ++i) mbar_init(&sm.odone[i], 1);
+        mbar_init(&sm.done, 1);
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
     }
@@ -445,60 +457,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     if (warp < kSoftWarps) {
         // ---- queries in, weights, outputs ------------------------------------------------
         take_registers<kSoftRegs>();
-        Waits<true> wait = {a.err, true};
+        Waits wait = {a.err, true};
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t step = 0, tiles_done = 0, o_count[kM] = {};
-        while (left > 0 && wait.ok) {
-            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
-            const int row0 = at.rg * S::kRows;
-            const float ks = a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f;
-            bool real[kM], some[kM];
-            int64_t row[kM];
-            int qh[kM];
-            uint64_t word[kM];
-            float c[kM], m[kM], l[kM];
+        uint32_t step = 0, tiles_done = 0, units = 0, o_count[kM] = {};
+        // Row `lrow` of m tile t of a unit.
+        struct Row {
+            bool some, real;  // this warp has rows there; this lane's is one
+            int64_t row;
+            int qh;
+        };
+        auto row_of = [&](const Cursor<S> &u, int t) {
+            const int rr = u.rg * S::kRows + t * 128 + lrow;
+            uint32_t node, g;
+            args.group.divmod(rr, node, g);
+            return Row{rr - lane < u.rows, rr < u.rows, u.first + node, u.h * a.group + static_cast<int>(g)};
+        };
+        // A unit's queries to shared memory, this lane's half of its rows; c: what turns a row's
+        // products into scores, above 0 (queries of a negative scale change their sign).
+        auto queries = [&](const Cursor<S> &u, float (&c)[kM]) {
+            constexpr int kPieces = kD / 16;  // 16-byte pieces of half a row
+            const float ks = a.cache.k_scale != nullptr ? a.cache.k_scale[u.h] : 1.f;
+            const float cs = a.scale * kLog2e * ks;
 #pragma unroll
             for (int t = 0; t < kM; ++t) {
-                const int rr = row0 + t * 128 + lrow;
-                some[t] = row0 + t * 128 + quarter * 32 < at.rows;
-                real[t] = rr < at.rows;
-                uint32_t node, g;
-                args.group.divmod(rr, node, g);
-                row[t] = at.first + node;
-                qh[t] = at.h * a.group + static_cast<int>(g);
-                word[t] = 0;
-                m[t] = -INFINITY;
-                l[t] = 0.f;
-                c[t] = a.scale * kLog2e * ks;
-                if (!some[t]) continue;
-                constexpr int kPieces = kD / 16;  // 16-byte pieces of half a row
-                const uint4 *src = nullptr;
-                if (real[t]) {
-                    word[t] = a.ancestors[row[t]] & bits_below(at.n);
-                    src = reinterpret_cast<const uint4 *>(a.q + row[t] * a.q_row_stride + qh[t] * kD +
-                                                          wg * (kD / 2));
-                }
+                const Row r = row_of(u, t);
+                c[t] = fabsf(cs);
+                if (!r.some) continue;
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (r.real ? r.row * a.q_row_stride + r.qh * kD : 0) +
+                                                                   wg * (kD / 2));
                 auto place = [&](int i) {  // of piece i
                     const int ch = wg * kPieces + i;
                     return smem + t * (128 * kD * 2) + (ch >> 3) * (128 * 128) + lrow * 128 +
                            (((ch & 7) ^ (lrow & 7)) << 4);
                 };
                 if constexpr (!kFp8) {
+                    const uint32_t sign = cs < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                     for (int i0 = 0; i0 < kPieces; i0 += 8) {
                         uint4 x[8];
 #pragma unroll
                         for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
-                            if (real[t]) x[i] = src[i0 + i];
+                            if (r.real) x[i] = src[i0 + i];
 #pragma unroll
                         for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
-                            if (real[t]) *reinterpret_cast<uint4 *>(place(i0 + i)) = x[i];
+                            if (r.real)
+                                *reinterpret_cast<uint4 *>(place(i0 + i)) =
+                                    make_uint4(x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign, x[i].w ^ sign);
                     }
                 } else {
                     // scaled by a power of two that puts the row's largest value below 2^15
                     uint32_t top = 0;
-                    if (real[t])
+                    if (r.real)
                         for (int i = 0; i < kPieces; ++i) {
                             const uint4 x = src[i];
                             for (const uint32_t y : {x.x, x.y, x.z, x.w})
@@ -508,13 +518,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     pair_barrier(quarter);
                     top = max(top, __float_as_uint(sm.top[0][wg ^ 1][lrow]));
                     pair_barrier(quarter);
-                    const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127;  // its exponent
-                    // (two factors: neither leaves fp32's range)
-                    const float up0 = exp2f(static_cast<float>((14 - e) / 2));
-                    const float up1 = exp2f(static_cast<float>(14 - e - (14 - e) / 2));
-                    c[t] = c[t] * exp2f(static_cast<float>((e - 14) / 2)) *
-                           exp2f(static_cast<float>(e - 14 - (e - 14) / 2));
-                    if (real[t])
+                    // its exponent, taken back in two factors: neither leaves fp32's range
+                    const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127 - 14;
+                    const float up0 = exp2f(static_cast<float>(-e / 2)) * (cs < 0.f ? -1.f : 1.f);
+                    const float up1 = exp2f(static_cast<float>(-e - -e / 2));
+                    c[t] = c[t] * exp2f(static_cast<float>(e / 2)) * exp2f(static_cast<float>(e - e / 2));
+                    if (r.real)
                         for (int i = 0; i < kPieces; ++i) {
                             uint4 x = src[i];
                             uint32_t *y = reinterpret_cast<uint32_t *>(&x);
@@ -526,22 +535,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             *reinterpret_cast<uint4 *>(place(i)) = x;
                         }
                 }
+                c[t] = at_least_normal(c[t]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.qfull);
-            const int m_used = at.rows - row0 > 128 ? kM : 1;
+        };
+        float c[kM], c_next[kM];
+        if (left > 0) queries(at, c);
+        while (left > 0 && wait.ok) {
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+            const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+            Row r[kM];
+            uint64_t word[kM];
+            float m[kM], l[kM];
+#pragma unroll
+            for (int t = 0; t < kM; ++t) {
+                r[t] = row_of(at, t);
+                word[t] = r[t].real ? a.ancestors[r[t].row] & bits_below(at.n) : 0;
+                m[t] = -INFINITY;
+                l[t] = 0.f;
+            }
 
             for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++tiles_done) {
 #pragma unroll
                 for (int t = 0; t < kM; ++t) {
                     if (t >= m_used) break;
                     const uint32_t buf = step & 1;
-                    wait(&sm.sfull[buf], (step >> 1) & 1);
+                    if (!wait(&sm.sfull[buf], (step >> 1) & 1)) break;
                     ++step;
-                    __syncwarp();
-                    if (!wait.ok) break;
-                    if (some[t]) {
+                    if (r[t].some) {
                         tc_fence_after();
                         const uint32_t cols = lanes + buf * kKeys + wg * kHalf;
                         float s[kHalf / 32][32];
@@ -556,30 +579,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         constexpr uint64_t kAll = kHalf == 64 ? ~uint64_t{0} : 0xffffffffu;
                         seen &= kAll;
                         tmem_wait_ld();
-                        float top = -INFINITY;
-                        if (__all_sync(0xffffffffu, seen == kAll)) {
+                        if (!__all_sync(0xffffffffu, seen == kAll)) {
 #pragma unroll
-                            for (int i = 0; i < kHalf; ++i) {
-                                s[i / 32][i % 32] *= c[t];
-                                top = fmaxf(top, s[i / 32][i % 32]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kHalf; ++i) {
-                                const bool in = (seen >> i) & 1;
-                                s[i / 32][i % 32] = in ? s[i / 32][i % 32] * c[t] : -INFINITY;
-                                top = fmaxf(top, s[i / 32][i % 32]);
-                            }
+                            for (int i = 0; i < kHalf; ++i)
+                                if (!((seen >> i) & 1)) s[i / 32][i % 32] = -INFINITY;
                         }
+                        float top = s[0][0], top1 = s[0][1];
+#pragma unroll
+                        for (int i = 2; i < kHalf; i += 4) {
+                            top = fmaxf(fmaxf(top, s[i / 32][i % 32]), s[i / 32][i % 32 + 1]);
+                            if (i + 2 < kHalf)
+                                top1 = fmaxf(fmaxf(top1, s[(i + 2) / 32][(i + 2) % 32]), s[(i + 2) / 32][(i + 2) % 32 + 1]);
+                        }
+                        top = fmaxf(top, top1);
                         sm.top[buf][wg][lrow] = top;
                         pair_barrier(quarter);
-                        const float to = fmaxf(m[t], fmaxf(top, sm.top[buf][wg ^ 1][lrow]));
+                        top = fmaxf(top, sm.top[buf][wg ^ 1][lrow]) * c[t];
+                        const bool grown = top > m[t] + (tile > at.t ? S::kSlack : 0.f);
+                        const float to = grown ? top : m[t];
                         const float ref = to == -INFINITY ? 0.f : to;
-                        if (tile > at.t && __any_sync(0xffffffffu, to > m[t])) {
-                            const float keep = ex2(m[t] - ref);
+                        if (tile > at.t && __any_sync(0xffffffffu, grown)) {
+                            const float keep = grown ? ex2(m[t] - ref) : 1.f;
                             l[t] *= keep;
+                            // the last product of these rows; the one before it was complete
+                            // when this step's scores were (so one phase is open at most)
                             wait(&sm.odone[t], (o_count[t] - 1) & 1);
-                            __syncwarp();
                             tc_fence_after();
 #pragma unroll
                             for (int i = 0; i < kD / 64; ++i) {
@@ -593,24 +617,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             }
                         }
                         m[t] = to;
-                        const float off = S::kShift - ref;
-                        float sum = 0.f;
+                        const uint64_t c2 = f2(c[t], c[t]), off2 = f2(S::kShift - ref, S::kShift - ref);
+                        uint64_t sum2 = 0;
 #pragma unroll
                         for (int i = 0; i < kHalf / 32; ++i) {
                             float hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                const float p0 = ex2(s[i][2 * k] + off), p1 = ex2(s[i][2 * k + 1] + off);
-                                sum += p0 + p1;
-                                const uint32_t x = pack2<kFp8>(p0, p1);
-                                const float2 y = unpack2<kFp8>(x);
-                                hi[k] = __uint_as_float(x);
-                                lo[k] = __uint_as_float(pack2<kFp8>(p0 - y.x, p1 - y.y));
+                                const float2 x = f2_split(f2_fma(f2(s[i][2 * k], s[i][2 * k + 1]), c2, off2));
+                                const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                const uint64_t p2 = f2(p0, p1);
+                                sum2 = f2_add(sum2, p2);
+                                const uint32_t h = pack2<kFp8>(p0, p1);
+                                const float2 y = unpack2<kFp8>(h);
+                                const float2 rest = f2_split(f2_sub(p2, f2(y.x, y.y)));
+                                hi[k] = __uint_as_float(h);
+                                lo[k] = __uint_as_float(pack2<kFp8>(rest.x, rest.y));
                             }
                             tmem_st16(cols + 16 * i, hi);
                             tmem_st16(cols + kHalf / 2 + 16 * i, lo);
                         }
-                        l[t] += sum;
+                        const float2 sum = f2_split(sum2);
+                        l[t] += sum.x + sum.y;
                         tmem_wait_st();
                         tc_fence_before();
                     }
@@ -619,17 +647,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (lane == 0) mbar_arrive(&sm.pfull[buf]);
                 }
             }
+            left -= t1 - at.t;
+            // the next unit's queries, while this one's last products run: its scores are all
+            // there, so nothing reads these any more
+            Cursor<S> next = at;
+            if (left > 0 && wait.ok) {
+                next.next_unit(a);
+                queries(next, c_next);
+            }
 
             // outputs: a whole unit's to o, a cut one's to the workspace
+            wait(&sm.done, units & 1);
+            ++units;
             const bool whole = at.t == 0 && t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
 #pragma unroll
             for (int t = 0; t < kM; ++t) {
-                if (t >= m_used || !some[t]) break;
-                wait(&sm.odone[t], (o_count[t] - 1) & 1);
-                __syncwarp();
-                if (!wait.ok) break;
+                if (t >= m_used || !r[t].some || !wait.ok) break;
                 tc_fence_after();
                 sm.top[0][wg][lrow] = l[t];
                 pair_barrier(quarter);
@@ -637,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 pair_barrier(quarter);
                 const float f = all == 0.f ? 0.f : 1.f / all;
                 float nan = 0.f;
-                const int64_t out = row[t] * a.q_heads + qh[t];
+                const int64_t out = r[t].row * a.q_heads + r[t].qh;
 #pragma unroll
                 for (int i = 0; i < kD / 64; ++i) {
                     float o[32];
@@ -651,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             nan = fmaf(o[k], 0.f, fmaf(o[k + 1], 0.f, nan));
                             y[k / 2] = all == 0.f ? 0u : pack2<false>(o[k] * f * vs, o[k + 1] * f * vs);
                         }
-                        if (real[t])
+                        if (r[t].real)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 reinterpret_cast<uint4 *>(a.o + out * kD + d)[k] =
@@ -666,16 +701,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 tc_fence_before();
                 if (whole) {
-                    if (real[t] && wg == 0 && a.lse != nullptr)
+                    if (r[t].real && wg == 0 && a.lse != nullptr)
                         a.lse[out] = all == 0.f ? -INFINITY : (m[t] + log2f(all) - S::kShift) * kLn2;
                     // what is not finite although the weights are
-                    uint32_t again = __ballot_sync(0xffffffffu, real[t] && nan != 0.f && all * 0.f == 0.f &&
+                    uint32_t again = __ballot_sync(0xffffffffu, r[t].real && nan != 0.f && all * 0.f == 0.f &&
                                                                     all != 0.f);
                     while (again != 0) {
                         const int src = __ffs(static_cast<int>(again)) - 1;
                         again &= again - 1;
-                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, row[t], src),
-                                            __shfl_sync(0xffffffffu, qh[t], src), at.n, at.len,
+                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, r[t].row, src),
+                                            __shfl_sync(0xffffffffu, r[t].qh, src), at.n, at.len,
                                             wg * (kD / 2), (wg + 1) * (kD / 2));
                         __syncwarp();
                     }
@@ -684,13 +719,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         make_float2(m[t], all);
                 }
             }
-            left -= t1 - at.t;
-            if (left > 0) at.next_unit(a);
+            at = next;
+#pragma unroll
+            for (int t = 0; t < kM; ++t) c[t] = c_next[t];
         }
     } else if (warp < kSoftWarps + kCopyWarps) {
         // ---- keys and values in --------------------------------------------------------------
         leave_registers<kCopyRegs>();
-        Waits<true> wait = {a.err, true};
+        Waits wait = {a.err, true};
         const int cw = warp - kSoftWarps;
         constexpr int kRowsOfWarp = kKeys / kCopyWarps;
         constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
@@ -808,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     } else {
         // ---- products ------------------------------------------------------------------------
         leave_registers<kProductRegs>();
-        if (warp == kSoftWarps + kCopyWarps && lane == 0) {
-            Waits<false> wait = {a.err, true};
+        if (warp == kSoftWarps + kCopyWarps) {
+            Waits wait = {a.err, true};
             constexpr uint32_t kFmt = kFp8 ? kFmtF16 : kFmtBF16;
             constexpr uint32_t kIdS = instr_desc(128, kKeys, kFmt, 0, 0), kIdO = instr_desc(128, kD, kFmt, 0, 1);
             uint32_t step_s = 0, step_p = 0, kt = 0, vt = 0, units = 0;
@@ -833,11 +869,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
     #pragma unroll
                     for (int k = 0; k < kD / 16; ++k)
-                        mma_f16_ss(d, qd + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                        mma_f16_ss_w(d, qd + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
                                    kd + ((k / 4) * (kKeys * 128) + (k % 4) * 32) / 16, kIdS, k > 0);
-                    mma_commit(&sm.sfull[step_s & 1]);
+                    mma_commit_w(&sm.sfull[step_s & 1]);
                     if (t == m_used - 1) {
-                        mma_commit(&sm.kempty[ks]);
+                        mma_commit_w(&sm.kempty[ks]);
                         ++kt;
                     }
                     ++step_s;
@@ -857,11 +893,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     for (int k = 0; k < kKeys / 16 * 2; ++k) {
                         const int part = k / (kKeys / 16), key = k % (kKeys / 16) * 16;  // word, keys
                         const uint32_t p = tmem + buf * kKeys + key / kHalf * kHalf + key % kHalf / 2 + part * (kHalf / 2);
-                        mma_f16_ts(d, p, vd + key * 128 / 16, kIdO, k > 0 || i >= m_used);
+                        mma_f16_ts_w(d, p, vd + key * 128 / 16, kIdO, k > 0 || i >= m_used);
                     }
-                    mma_commit(&sm.odone[t]);
+                    mma_commit_w(&sm.odone[t]);
                     if (t == m_used - 1) {
-                        mma_commit(&sm.vempty[vs]);
+                        mma_commit_w(&sm.vempty[vs]);
                         ++vt;
                     }
                     ++step_p;
@@ -871,11 +907,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (i + 1 < steps) scores(i + 1);
                     if (wait.ok) outputs(i);
                 }
+                mma_commit_w(&sm.done);
                 left -= t1 - at.t;
                 if (left > 0) at.next_unit(a);
             }
             // nothing is in flight when tensor memory is given back
-            mma_commit(&sm.drain);
+            mma_commit_w(&sm.drain);
             mbar_wait_bounded(&sm.drain, 0, kMaxPolls);
         }
     }

@@ -798,7 +798,7 @@ size_t kda_paged_tree_decode_workspace_size(int B, int max_nodes, int q_heads, i
  *   cache, block_table, max_pages, seq_lens (drafted tokens included), q_heads, scale
  *               as in kda_paged_decode
  *   o           bf16 [N, q_heads, head_dim] written; a softmax weight is kept to 16 bits (over
- *               an 8-bit cache to 2^-38 of the largest, if that is coarser)
+ *               an 8-bit cache to 2^-37 of the largest, if that is coarser)
  *   lse         fp32 [N, q_heads] written, or NULL
  *   workspace   device scratch, >= kda_paged_tree_decode_workspace_size() bytes, 16-byte
  *               aligned; not shared with a concurrent call
