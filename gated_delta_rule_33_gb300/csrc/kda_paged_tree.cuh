@@ -24,12 +24,12 @@
 // the products read them (an 8-bit cache: raw, then widened to fp16, which holds every e4m3
 // value).  One thread issues the products: S = Q K^T from shared memory into one of
 // two score buffers in tensor memory, O += P V with P from there and V from shared memory,
-// the next step's S ahead of this one's O.  Warps 0..7 turn scores into weights in
-// place: a row is a lane of tensor memory, the two warps of a lane quarter halve its keys and
-// exchange their maxima through shared memory.  A row's weights are relative to a reference
-// that follows its maximum only when that has grown by 2^7 (2^3 over an 8-bit cache): O is then
-// rescaled, which waits for the last product (at every growth, some row of a warp grows in most
-// tiles: MEASURE).
+// the next step's S ahead of this one's O.  Two warpgroups turn scores into weights in place, a
+// thread a row (a lane of tensor memory), each every second step, so that one's exponentials run
+// beside the other's loads and maxima.  A row's weights are relative to a reference that
+// follows its maximum only when that has grown by 2^7 (2^3 over an 8-bit cache): O is then
+// rescaled, which waits for the last product (at every growth, some row of a warp would grow in
+// most tiles).
 //
 // Precision: scores, maxima and sums in fp32.  For the product with the values a weight is two
 // words: bf16 numbers, 16 bits together (one would leave up to 2^-8 of every weight, as much as
@@ -94,7 +94,7 @@ struct Shape {
     static constexpr int kD = kD_, kM = kM_;
     static constexpr bool kFp8 = kFp8_;
     static constexpr int kRows = kM * 128;
-    static constexpr int kKeys = kD == 256 ? 64 : 128, kHalf = kKeys / 2;
+    static constexpr int kKeys = kD == 256 ? 64 : 128;
     static constexpr int kTile = kKeys * kD * 2;  // as an operand
     static constexpr int kRaw = kTile / 2;        // of an 8-bit cache, as copied
     static constexpr int kQ = kRows * kD * 2;
@@ -114,9 +114,10 @@ struct Shape {
     static_assert(!kFp8 || kNR >= 3, "halves in flight");
 
     struct Small {  // what lies behind the tiles
-        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], done, drain;
+        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], scored, done, drain;
         int64_t warp_sum[kThreads / 32], place[2];
-        float top[2][2][128];            // a half row's maximum, by step, half and row
+        // by row: the reference that a warpgroup hands to the other, and what they exchange
+        float ref[128], top[2][128];
         uint32_t valid[16][kCopyWarps];  // which rows of a tile are keys, by copy warp
         uint32_t tmem;
     };
@@ -367,8 +368,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool re
                  : "memory");
 }
 
+// The two warps of a lane quarter.
 __device__ __forceinline__ void pair_barrier(int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+}
+// One of them (of warpgroup wg) waits for what the other has done; the other says so.
+__device__ __forceinline__ void pair_wait(int quarter, int wg) {
+    asm volatile("bar.sync %0, 64;" ::"r"(5 + wg * 4 + quarter) : "memory");
+}
+__device__ __forceinline__ void pair_arrive(int quarter, int wg) {
+    asm volatile("bar.arrive %0, 64;" ::"r"(5 + (wg ^ 1) * 4 + quarter) : "memory");
 }
 
 template <int kRegs>
@@ -407,7 +416,7 @@ struct Waits {
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __grid_constant__ Args args) {
-    constexpr int kD = S::kD, kM = S::kM, kKeys = S::kKeys, kHalf = S::kHalf;
+    constexpr int kD = S::kD, kM = S::kM, kKeys = S::kKeys;
     constexpr bool kFp8 = S::kFp8;
     constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles: 1024-byte groups of rows
@@ -430,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.pfull[i], kSoftWarps);
+            mbar_init(&sm.pfull[i], kSoftWarps / 2);
         }
         for (int i = 0; i < kM; ++i) mbar_init(&sm.odone[i], 1);
+        mbar_init(&sm.scored, 1);
         mbar_init(&sm.done, 1);
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
@@ -460,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         Waits wait = {a.err, true};
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t step = 0, tiles_done = 0, units = 0, o_count[kM] = {};
+        // steps, tiles and units so far, and the products into each O
+        uint32_t step = 0, tiles_done = 0, units = 0, products[kM] = {};
         // Row `lrow` of m tile t of a unit.
         struct Row {
             bool some, real;  // this warp has rows there; this lane's is one
@@ -514,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             for (const uint32_t y : {x.x, x.y, x.z, x.w})
                                 top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
                         }
-                    sm.top[0][wg][lrow] = __uint_as_float(top);
+                    sm.top[wg][lrow] = __uint_as_float(top);
                     pair_barrier(quarter);
-                    top = max(top, __float_as_uint(sm.top[0][wg ^ 1][lrow]));
+                    top = max(top, __float_as_uint(sm.top[wg ^ 1][lrow]));
                     pair_barrier(quarter);
                     // its exponent, taken back in two factors: neither leaves fp32's range
                     const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127 - 14;
@@ -546,147 +557,178 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         while (left > 0 && wait.ok) {
             const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
             const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
-            Row r[kM];
-            uint64_t word[kM];
-            float m[kM], l[kM];
-#pragma unroll
-            for (int t = 0; t < kM; ++t) {
-                r[t] = row_of(at, t);
-                word[t] = r[t].real ? a.ancestors[r[t].row] & bits_below(at.n) : 0;
-                m[t] = -INFINITY;
-                l[t] = 0.f;
-            }
+            const int steps = (t1 - at.t) * m_used;
+            // This warpgroup has every second step: of two m tiles always the same one, of one
+            // every second tile.
+            const int i0 = (step + wg) & 1, mt = m_used == 1 ? 0 : i0;
+            const Row r = row_of(at, mt);
+            const uint64_t word = r.real ? a.ancestors[r.row] & bits_below(at.n) : 0;
+            const float cr = kM == 1 || mt == 0 ? c[0] : c[kM - 1];
+            float m = -INFINITY, l = 0.f;
 
-            for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++tiles_done) {
+            for (int i = i0; i < steps && wait.ok; i += 2) {
+                const int tile = m_used == 1 ? i : i >> 1;
+                const uint32_t g = step + i;
+                if (!wait(&sm.sfull[wg], (g >> 1) & 1)) break;
+                if (r.some) {
+                    tc_fence_after();
+                    const uint32_t cols = lanes + wg * kKeys;
+                    // the keys that the row sees, where that is not all of them
+                    const uint32_t *v = sm.valid[(tiles_done + tile) & 15];
+                    const int d = (at.t + tile) * kKeys - (at.len - at.n);
+                    bool all = true;
 #pragma unroll
-                for (int t = 0; t < kM; ++t) {
-                    if (t >= m_used) break;
-                    const uint32_t buf = step & 1;
-                    if (!wait(&sm.sfull[buf], (step >> 1) & 1)) break;
-                    ++step;
-                    if (r[t].some) {
-                        tc_fence_after();
-                        const uint32_t cols = lanes + buf * kKeys + wg * kHalf;
-                        float s[kHalf / 32][32];
+                    for (int k = 0; k < kCopyWarps; ++k)
+                        all &= v[k] == (kKeys == 128 ? 0xffffffffu : 0xffffu);
+                    if (d + kKeys > 0 || !all) {
+#pragma unroll 1
+                        for (int k = 0; k < kKeys / 32; ++k) {
+                            uint32_t seen = kKeys == 128 ? v[k] : v[2 * k + 1] << 16 | v[2 * k];
+                            if (d + 32 * (k + 1) > 0) seen &= static_cast<uint32_t>(seen_from(word, d + 32 * k));
+                            float s[32];
+                            tmem_ld32(cols + 32 * k, s);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < kHalf / 32; ++i) tmem_ld32(cols + 32 * i, s[i]);
-                        // the keys of this half that the row sees
-                        const uint32_t *v = sm.valid[tiles_done & 15] + 2 * wg;
-                        uint64_t seen = kHalf == 64 ? static_cast<uint64_t>(v[1]) << 32 | v[0]
-                                                    : static_cast<uint64_t>(v[1] << 16 | v[0]);
-                        const int d = tile * kKeys + wg * kHalf - (at.len - at.n);
-                        if (d + kHalf > 0) seen &= seen_from(word[t], d);
-                        constexpr uint64_t kAll = kHalf == 64 ? ~uint64_t{0} : 0xffffffffu;
-                        seen &= kAll;
-                        tmem_wait_ld();
-                        if (!__all_sync(0xffffffffu, seen == kAll)) {
-#pragma unroll
-                            for (int i = 0; i < kHalf; ++i)
-                                if (!((seen >> i) & 1)) s[i / 32][i % 32] = -INFINITY;
+                            for (int x = 0; x < 32; ++x)
+                                if (!((seen >> x) & 1)) s[x] = -INFINITY;
+                            tmem_st32(cols + 32 * k, s);
                         }
-                        float top = s[0][0], top1 = s[0][1];
-#pragma unroll
-                        for (int i = 2; i < kHalf; i += 4) {
-                            top = fmaxf(fmaxf(top, s[i / 32][i % 32]), s[i / 32][i % 32 + 1]);
-                            if (i + 2 < kHalf)
-                                top1 = fmaxf(fmaxf(top1, s[(i + 2) / 32][(i + 2) % 32]), s[(i + 2) / 32][(i + 2) % 32 + 1]);
-                        }
-                        top = fmaxf(top, top1);
-                        sm.top[buf][wg][lrow] = top;
-                        pair_barrier(quarter);
-                        top = fmaxf(top, sm.top[buf][wg ^ 1][lrow]) * c[t];
-                        const bool grown = top > m[t] + (tile > at.t ? S::kSlack : 0.f);
-                        const float to = grown ? top : m[t];
-                        const float ref = to == -INFINITY ? 0.f : to;
-                        if (tile > at.t && __any_sync(0xffffffffu, grown)) {
-                            const float keep = grown ? ex2(m[t] - ref) : 1.f;
-                            l[t] *= keep;
-                            // the last product of these rows; the one before it was complete
-                            // when this step's scores were (so one phase is open at most)
-                            wait(&sm.odone[t], (o_count[t] - 1) & 1);
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 0; i < kD / 64; ++i) {
-                                float o[32];
-                                const uint32_t oc = lanes + S::kColO + t * kD + wg * (kD / 2) + 32 * i;
-                                tmem_ld32(oc, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= keep;
-                                tmem_st32(oc, o);
-                            }
-                        }
-                        m[t] = to;
-                        const uint64_t c2 = f2(c[t], c[t]), off2 = f2(S::kShift - ref, S::kShift - ref);
-                        uint64_t sum2 = 0;
-#pragma unroll
-                        for (int i = 0; i < kHalf / 32; ++i) {
-                            float hi[16], lo[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float2 x = f2_split(f2_fma(f2(s[i][2 * k], s[i][2 * k + 1]), c2, off2));
-                                const float p0 = ex2(x.x), p1 = ex2(x.y);
-                                const uint64_t p2 = f2(p0, p1);
-                                sum2 = f2_add(sum2, p2);
-                                const uint32_t h = pack2<kFp8>(p0, p1);
-                                const float2 y = unpack2<kFp8>(h);
-                                const float2 rest = f2_split(f2_sub(p2, f2(y.x, y.y)));
-                                hi[k] = __uint_as_float(h);
-                                lo[k] = __uint_as_float(pack2<kFp8>(rest.x, rest.y));
-                            }
-                            tmem_st16(cols + 16 * i, hi);
-                            tmem_st16(cols + kHalf / 2 + 16 * i, lo);
-                        }
-                        const float2 sum = f2_split(sum2);
-                        l[t] += sum.x + sum.y;
                         tmem_wait_st();
-                        tc_fence_before();
                     }
-                    ++o_count[t];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+                    float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kKeys / 64; ++k) {
+                        float s0[32], s1[32];
+                        tmem_ld32(cols + 64 * k, s0);
+                        tmem_ld32(cols + 64 * k + 32, s1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            top = fmaxf(fmaxf(top, s0[x]), s0[x + 1]);
+                            top1 = fmaxf(fmaxf(top1, s1[x]), s1[x + 1]);
+                        }
+                    }
+                    top = fmaxf(top, top1) * cr;
+                    // one m tile: the reference is the other warpgroup's of the step before
+                    if (m_used == 1 && i > 0) {
+                        pair_wait(quarter, wg);
+                        const float other = sm.ref[lrow];
+                        if (other > m) {
+                            if (i > 1) l *= ex2(m - other);
+                            m = other;
+                        }
+                    }
+                    const bool first = i < m_used;
+                    const bool grown = top > m + (first ? 0.f : S::kSlack);
+                    const float to = grown ? top : m;
+                    const float ref = to == -INFINITY ? 0.f : to;
+                    if (m_used == 1 && i + 1 < steps) {
+                        sm.ref[lrow] = to;
+                        pair_arrive(quarter, wg);
+                    }
+                    if (!first && __any_sync(0xffffffffu, grown)) {
+                        const float keep = grown ? ex2(m - ref) : 1.f;
+                        l *= keep;
+                        // the last product of these rows; the one before it was complete when
+                        // this step's scores were (so one phase is open at most)
+                        wait(&sm.odone[mt], (products[mt] + tile - 1) & 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < kD / 32; ++k) {
+                            float o[32];
+                            const uint32_t oc = lanes + S::kColO + mt * kD + 32 * k;
+                            tmem_ld32(oc, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] *= keep;
+                            tmem_st32(oc, o);
+                        }
+                    }
+                    m = to;
+                    const uint64_t c2 = f2(cr, cr), off2 = f2(S::kShift - ref, S::kShift - ref);
+                    uint64_t sum2 = 0;
+#pragma unroll 1
+                    for (int k = 0; k < kKeys / 32; ++k) {
+                        float s[32], hi[16], lo[16];
+                        tmem_ld32(cols + 32 * k, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float2 e = f2_split(f2_fma(f2(s[2 * x], s[2 * x + 1]), c2, off2));
+                            const float p0 = ex2(e.x), p1 = ex2(e.y);
+                            const uint64_t p2 = f2(p0, p1);
+                            sum2 = f2_add(sum2, p2);
+                            const uint32_t h = pack2<kFp8>(p0, p1);
+                            const float2 y = unpack2<kFp8>(h);
+                            const float2 rest = f2_split(f2_sub(p2, f2(y.x, y.y)));
+                            hi[x] = __uint_as_float(h);
+                            lo[x] = __uint_as_float(pack2<kFp8>(rest.x, rest.y));
+                        }
+                        // a weight's two words take its score's place
+                        tmem_st16(cols + 32 * k, hi);
+                        tmem_st16(cols + 32 * k + 16, lo);
+                    }
+                    const float2 sum = f2_split(sum2);
+                    l += sum.x + sum.y;
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.pfull[wg]);
             }
+            // (a warpgroup's last step may not be the unit's)
+            if (!wait(&sm.scored, units & 1)) break;
+            step += steps;
+            tiles_done += t1 - at.t;
+#pragma unroll
+            for (int t = 0; t < kM; ++t)
+                if (t < m_used) products[t] += t1 - at.t;
             left -= t1 - at.t;
             // the next unit's queries, while this one's last products run: its scores are all
             // there, so nothing reads these any more
             Cursor<S> next = at;
-            if (left > 0 && wait.ok) {
+            if (left > 0) {
                 next.next_unit(a);
                 queries(next, c_next);
             }
 
-            // outputs: a whole unit's to o, a cut one's to the workspace
-            wait(&sm.done, units & 1);
+            // outputs: a whole unit's to o, a cut one's to the workspace.  Of two m tiles a
+            // warpgroup has its own, of one half the channels.
+            if (!wait(&sm.done, units & 1)) break;
             ++units;
             const bool whole = at.t == 0 && t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
-#pragma unroll
-            for (int t = 0; t < kM; ++t) {
-                if (t >= m_used || !r[t].some || !wait.ok) break;
+            if (r.some) {
                 tc_fence_after();
-                sm.top[0][wg][lrow] = l[t];
-                pair_barrier(quarter);
-                const float all = sm.top[0][0][lrow] + sm.top[0][1][lrow];
-                pair_barrier(quarter);
-                const float f = all == 0.f ? 0.f : 1.f / all;
+                if (m_used == 1) {  // the two warpgroups' sums, by the later reference
+                    sm.top[wg][lrow] = m;
+                    pair_barrier(quarter);
+                    const float to = fmaxf(m, sm.top[wg ^ 1][lrow]);
+                    pair_barrier(quarter);
+                    sm.top[wg][lrow] = l * ex2(m - (to == -INFINITY ? 0.f : to));
+                    pair_barrier(quarter);
+                    l = sm.top[0][lrow] + sm.top[1][lrow];
+                    m = to;
+                    pair_barrier(quarter);
+                }
+                const int d0 = m_used == 1 ? wg * (kD / 2) : 0, d1 = m_used == 1 ? d0 + kD / 2 : kD;
+                const float f = l == 0.f ? 0.f : 1.f / l;
                 float nan = 0.f;
-                const int64_t out = r[t].row * a.q_heads + r[t].qh;
-#pragma unroll
-                for (int i = 0; i < kD / 64; ++i) {
+                const int64_t out = r.row * a.q_heads + r.qh;
+#pragma unroll 1
+                for (int d = d0; d < d1; d += 32) {
                     float o[32];
-                    const int d = wg * (kD / 2) + 32 * i;
-                    tmem_ld32(lanes + S::kColO + t * kD + d, o);
+                    tmem_ld32(lanes + S::kColO + mt * kD + d, o);
                     tmem_wait_ld();
                     if (whole) {
                         uint32_t y[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             nan = fmaf(o[k], 0.f, fmaf(o[k + 1], 0.f, nan));
-                            y[k / 2] = all == 0.f ? 0u : pack2<false>(o[k] * f * vs, o[k + 1] * f * vs);
+                            y[k / 2] = l == 0.f ? 0u : pack2<false>(o[k] * f * vs, o[k + 1] * f * vs);
                         }
-                        if (r[t].real)
+                        if (r.real)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 reinterpret_cast<uint4 *>(a.o + out * kD + d)[k] =
@@ -695,28 +737,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             reinterpret_cast<float4 *>(args.cut)[(slot * (kD / 4) + d / 4 + k) * S::kRows +
-                                                                 t * 128 + lrow] =
+                                                                 mt * 128 + lrow] =
                                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
                 tc_fence_before();
                 if (whole) {
-                    if (r[t].real && wg == 0 && a.lse != nullptr)
-                        a.lse[out] = all == 0.f ? -INFINITY : (m[t] + log2f(all) - S::kShift) * kLn2;
+                    if (r.real && d0 == 0 && a.lse != nullptr)
+                        a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - S::kShift) * kLn2;
                     // what is not finite although the weights are
-                    uint32_t again = __ballot_sync(0xffffffffu, r[t].real && nan != 0.f && all * 0.f == 0.f &&
-                                                                    all != 0.f);
+                    uint32_t again = __ballot_sync(0xffffffffu, r.real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
                     while (again != 0) {
                         const int src = __ffs(static_cast<int>(again)) - 1;
                         again &= again - 1;
-                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, r[t].row, src),
-                                            __shfl_sync(0xffffffffu, r[t].qh, src), at.n, at.len,
-                                            wg * (kD / 2), (wg + 1) * (kD / 2));
+                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, r.row, src),
+                                            __shfl_sync(0xffffffffu, r.qh, src), at.n, at.len, d0, d1);
                         __syncwarp();
                     }
-                } else if (wg == 0) {
-                    reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + t * 128 + lrow] =
-                        make_float2(m[t], all);
+                } else if (d0 == 0) {
+                    reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + mt * 128 + lrow] = make_float2(m, l);
                 }
             }
             at = next;
@@ -810,18 +849,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 };
                 if constexpr (!kFp8) {
                     const uint32_t ks = made % S::kNK, vs = made % S::kNV;
-                    if (!wait(&sm.kempty[ks], ((made / S::kNK) & 1) ^ 1)) break;
-                    __syncwarp();
-                    copy(a.cache.k, base + S::kOffK + ks * S::kTile);
-                    copies_arrive(&sm.kfull[ks]);
-                    if (lane == 0) {
-                        sm.valid[made & 15][cw] = valid;
-                        mbar_arrive(&sm.kfull[ks]);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint64_t *full = half ? &sm.vfull[vs] : &sm.kfull[ks];
+                        if (!wait(half ? &sm.vempty[vs] : &sm.kempty[ks],
+                                  ((made / (half ? S::kNV : S::kNK)) & 1) ^ 1))
+                            break;
+                        copy(half ? a.cache.v : a.cache.k,
+                             base + (half ? S::kOffV + vs * S::kTile : S::kOffK + ks * S::kTile));
+                        copies_arrive(full);
+                        if (half == 0 && lane == 0) {
+                            sm.valid[made & 15][cw] = valid;
+                            mbar_arrive(full);
+                        }
                     }
-                    if (!wait(&sm.vempty[vs], ((made / S::kNV) & 1) ^ 1)) break;
-                    __syncwarp();
-                    copy(a.cache.v, base + S::kOffV + vs * S::kTile);
-                    copies_arrive(&sm.vfull[vs]);
                 } else {
                     if (lane == 0) sm.valid[made & 15][cw] = valid;
                     __syncwarp();
@@ -867,10 +908,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     const uint32_t d = tmem + (step_s & 1) * kKeys;
                     const uint64_t qd = smem_desc(base + t * (128 * kD * 2), 16, 1024, kSwizzle128B);
                     const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
-    #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k)
-                        mma_f16_ss_w(d, qd + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
-                                   kd + ((k / 4) * (kKeys * 128) + (k % 4) * 32) / 16, kIdS, k > 0);
+    #pragma unroll 1
+                    for (int k = 0; k < kD / 64; ++k)  // (short code: the warps share its cache)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_f16_ss_w(d, qd + (k * (128 * 128) + j * 32) / 16, kd + (k * (kKeys * 128) + j * 32) / 16,
+                                         kIdS, k + j > 0);
                     mma_commit_w(&sm.sfull[step_s & 1]);
                     if (t == m_used - 1) {
                         mma_commit_w(&sm.kempty[ks]);
@@ -889,12 +932,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     tc_fence_after();
                     const uint32_t d = tmem + S::kColO + t * kD;
                     const uint64_t vd = smem_desc(base + S::kOffV + vs * S::kTile, kKeys * 128, 1024, kSwizzle128B);
-    #pragma unroll
-                    for (int k = 0; k < kKeys / 16 * 2; ++k) {
-                        const int part = k / (kKeys / 16), key = k % (kKeys / 16) * 16;  // word, keys
-                        const uint32_t p = tmem + buf * kKeys + key / kHalf * kHalf + key % kHalf / 2 + part * (kHalf / 2);
-                        mma_f16_ts_w(d, p, vd + key * 128 / 16, kIdO, k > 0 || i >= m_used);
-                    }
+    #pragma unroll 1
+                    for (int k = 0; k < kKeys / 32; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // two groups of 16 keys, two words
+                            mma_f16_ts_w(d, tmem + buf * kKeys + 32 * k + (j & 1) * 8 + (j >> 1) * 16,
+                                         vd + (32 * k + (j & 1) * 16) * 128 / 16, kIdO, k + j > 0 || i >= m_used);
                     mma_commit_w(&sm.odone[t]);
                     if (t == m_used - 1) {
                         mma_commit_w(&sm.vempty[vs]);
@@ -902,10 +945,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     }
                     ++step_p;
                 };
-                if (wait.ok) scores(0);
-                for (int i = 0; i < steps && wait.ok; ++i) {
+#pragma unroll 1
+                for (int i = -1; i < steps && wait.ok; ++i) {
                     if (i + 1 < steps) scores(i + 1);
-                    if (wait.ok) outputs(i);
+                    else mma_commit_w(&sm.scored);
+                    if (i >= 0 && wait.ok) outputs(i);
                 }
                 mma_commit_w(&sm.done);
                 left -= t1 - at.t;

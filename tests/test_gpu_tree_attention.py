@@ -119,6 +119,27 @@ def test_long(lib, shapes, cache, D, G):
     check(x, o, lse)
 
 
+@pytest.mark.parametrize("cache,D,H,G,shapes", [("bf16", 128, 8, 2, [(3, 30000), (1, 9000)]),
+                                                ("fp8", 128, 6, 3, [(2, 41003)]),
+                                                ("bf16", 64, 8, 1, [(4, 35000)]),
+                                                ("bf16", 256, 5, 2, [(2, 25000), (3, 1)]),
+                                                ("bf16", 128, 2, 48, [(3, 40000)]),
+                                                ("fp8", 64, 2, 70, [(2, 60000)])])
+def test_many_tiles_of_a_block(lib, cache, D, H, G, shapes):
+    """Pieces of many tiles, whose references grow on the way: the last keys score highest.  (A
+    part has at most 1500 keys.)"""
+    x = tree_case(shapes, H, G, D, 64, cache, seed=D + G, peak=2.0)
+    for b in range(len(shapes)):                           # keys grow towards the end
+        n = int(x["lens"][b])
+        for i in range(paged.pages(n, 64)):
+            p = int(x["table"][b, i])
+            up = 0.2 + 2.0 * i * 64 / n
+            x["k"][p] = (x["k"][p].float() * up).to(x["k"].dtype)
+    o, lse = run(lib, x)
+    assert lib.kda_get_last_device_error() == 0
+    check(x, o, lse)
+
+
 def test_many_requests(lib):
     """More requests than blocks, of no, one or a few nodes."""
     rng = np.random.default_rng(3)
