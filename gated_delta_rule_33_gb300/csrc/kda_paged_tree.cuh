@@ -22,11 +22,10 @@
 //
 // A CTA.  Warps 8..11 copy the keys and values of its piece into two rings, rows swizzled as
 // the products read them (an 8-bit cache: raw, then widened to fp16, which holds every e4m3
-// value).  One thread issues the products: S = Q K^T from shared memory into one of
-// two score buffers in tensor memory, O += P V with P from there and V from shared memory,
-// the next step's S ahead of this one's O.  Two warpgroups turn scores into weights in place, a
-// thread a row (a lane of tensor memory), each every second step, so that one's exponentials run
-// beside the other's loads and maxima.  A row's weights are relative to a reference that
+// value).  Two warps issue the products: S = Q K^T from shared memory into one of two score
+// buffers in tensor memory, and O += P V with P from there and V from shared memory.  Two
+// warpgroups turn scores into weights in place, a thread a row (a lane of tensor memory), each
+// every second step, so that one's exponentials run beside the other's loads and maxima.  A row's weights are relative to a reference that
 // follows its maximum only when that has grown by 2^7 (2^3 over an 8-bit cache): O is then
 // rescaled, which waits for the last product (at every growth, some row of a warp would grow in
 // most tiles).
@@ -62,7 +61,8 @@ constexpr int kThreads = 512;   // four warpgroups: weights (two), copies, produ
 // Their registers, of the 512 x 128 that the block is launched with: 2 x 184 + 80 + 56 = 504.
 constexpr int kSoftRegs = 184, kCopyRegs = 80, kProductRegs = 56;
 static_assert(2 * kSoftRegs + kCopyRegs + kProductRegs <= 512, "registers of the block");
-constexpr int kMinTiles = 1;   // of a CTA's piece
+constexpr int kUnitCost = 2;   // of beginning and ending a unit, in tiles
+constexpr int kMinPlaces = 1;  // of a CTA's piece
 constexpr uint32_t kMaxPolls = 1u << 20;
 
 __host__ __device__ constexpr int min_of(int a, int b) { return a < b ? a : b; }
@@ -114,7 +114,7 @@ struct Shape {
     static_assert(!kFp8 || kNR >= 3, "halves in flight");
 
     struct Small {  // what lies behind the tiles
-        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], scored, done, drain;
+        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], pfree[2], scored, done, ofree, drain[2];
         int64_t warp_sum[kThreads / 32], place[2];
         // by row: the reference that a warpgroup hands to the other, and what they exchange
         float ref[128], top[2][128];
@@ -221,15 +221,19 @@ __device__ __noinline__ void row_exact(const TreeAttention &a, int b, int64_t ro
 
 // ---- the list of tiles ---------------------------------------------------------------------
 
-// A place in the list: a unit's tile t.
+// A place in the list, and the way from there.  A unit takes kUnitCost places of the list before
+// those of its tiles: what it costs to begin and end one.
 template <class S>
 struct Cursor {
-    int b, h, rg, t;
+    int b, h, rg;
     int n, len, rows, groups, tiles;  // of the sequence; rows = n G
     int64_t first;                    // its first row
+    int at;                           // place in the unit
+    int t, t1;                        // the tiles taken of it
+    int64_t left;                     // places to take
 
-    __device__ __forceinline__ void request(const TreeAttention &a, int at) {
-        b = at;
+    __device__ __forceinline__ void request(const TreeAttention &a, int i) {
+        b = i;
         const TreeRows r = tree_rows(a.cu, b, a.N, a.max_nodes);
         len = a.seq_lens[b];
         first = r.first;
@@ -239,33 +243,46 @@ struct Cursor {
         groups = (rows + S::kRows - 1) / S::kRows;
         tiles = n == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(len) + S::kKeys - 1) / S::kKeys);
     }
-    __device__ __forceinline__ int64_t list_tiles(const TreeAttention &a) const {
-        return static_cast<int64_t>(a.cache.heads) * groups * tiles;
+    __device__ __forceinline__ int64_t places(const TreeAttention &a) const {
+        return tiles == 0 ? 0 : static_cast<int64_t>(a.cache.heads) * groups * (tiles + kUnitCost);
     }
-    // Tile `at` of the sequence's part of the list.
-    __device__ __forceinline__ void seek(int64_t at) {
-        const int64_t u = at / tiles;
-        t = static_cast<int>(at - u * tiles);
+    // Place `i` of the sequence's part of the list.
+    __device__ __forceinline__ void seek(int64_t i) {
+        const int64_t u = i / (tiles + kUnitCost);
+        at = static_cast<int>(i - u * (tiles + kUnitCost));
         h = static_cast<int>(u / groups);
         rg = static_cast<int>(u - static_cast<int64_t>(h) * groups);
     }
     __device__ __forceinline__ void next_unit(const TreeAttention &a) {
-        t = 0;
+        at = 0;
         if (++rg < groups) return;
         rg = 0;
         if (++h < a.cache.heads) return;
         h = 0;
-        for (int i = b + 1; i < a.B; ++i) {
-            request(a, i);
-            if (tiles > 0) return;
+        do request(a, b + 1);  // (there is one: places are left)
+        while (tiles == 0);
+    }
+    // The next tiles [t, t1) of one unit; false at the end.
+    __device__ __forceinline__ bool take(const TreeAttention &a) {
+        while (left > 0) {
+            const int end = tiles + kUnitCost;
+            if (at == end) {
+                next_unit(a);
+                continue;
+            }
+            const int to = static_cast<int>(min(static_cast<int64_t>(end), at + left));
+            t = max(at - kUnitCost, 0);
+            t1 = max(to - kUnitCost, 0);
+            left -= to - at;
+            at = to;
+            if (t1 > t) return true;
         }
-        tiles = 0;
-        b = a.B;
+        return false;
     }
 };
 
 // The block's way through the list; every thread of the block calls it.  begin(c): the first
-// tile of piece c.
+// place of piece c.
 struct List {
     int64_t total;
     int pieces;
@@ -314,11 +331,11 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
         mine = 0;
         if (b0 + tid < a.B) {
             c.request(a, b0 + tid);
-            mine = c.list_tiles(a);
+            mine = c.places(a);
         }
         list.total += scan_sum<S, kWarps>(mine, s_warp, before);
     }
-    const int64_t most = (list.total + kMinTiles - 1) / kMinTiles;
+    const int64_t most = (list.total + kMinPlaces - 1) / kMinPlaces;
     list.pieces = static_cast<int>(most < ctas ? (most < 1 ? 1 : most) : ctas);
     if (tid == 0) s_place[0] = -1;
     __syncthreads();
@@ -329,7 +346,7 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
             mine = 0;
             if (b0 + tid < a.B) {
                 c.request(a, b0 + tid);
-                mine = c.list_tiles(a);
+                mine = c.places(a);
             }
             const int64_t all = scan_sum<S, kWarps>(mine, s_warp, before);
             before += base;
@@ -440,11 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
             mbar_init(&sm.pfull[i], kSoftWarps / 2);
+            mbar_init(&sm.pfree[i], 1);
         }
         for (int i = 0; i < kM; ++i) mbar_init(&sm.odone[i], 1);
         mbar_init(&sm.scored, 1);
         mbar_init(&sm.done, 1);
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.ofree, kSoftWarps);
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -456,10 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     const List list = find_place<S, kWarps>(a, gridDim.x, sm.warp_sum, sm.place, [&](const List &l) {
         return static_cast<int>(blockIdx.x) < l.pieces ? l.begin(blockIdx.x) : l.total;
     });
-    int64_t left = 0;
     Cursor<S> at = {};
     if (sm.place[0] >= 0) {
-        left = list.begin(blockIdx.x + int64_t{1}) - list.begin(blockIdx.x);
+        at.left = list.begin(blockIdx.x + int64_t{1}) - list.begin(blockIdx.x);
         at.request(a, static_cast<int>(sm.place[0]));
         at.seek(sm.place[1]);
     }
@@ -553,11 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             if (lane == 0) mbar_arrive(&sm.qfull);
         };
         float c[kM], c_next[kM];
-        if (left > 0) queries(at, c);
-        while (left > 0 && wait.ok) {
-            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+        bool more = at.take(a);
+        if (more) queries(at, c);
+        while (more && wait.ok) {
             const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
-            const int steps = (t1 - at.t) * m_used;
+            const int tiles = at.t1 - at.t, steps = tiles * m_used;
             // This warpgroup has every second step: of two m tiles always the same one, of one
             // every second tile.
             const int i0 = (step + wg) & 1, mt = m_used == 1 ? 0 : i0;
@@ -679,24 +698,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             // (a warpgroup's last step may not be the unit's)
             if (!wait(&sm.scored, units & 1)) break;
             step += steps;
-            tiles_done += t1 - at.t;
+            tiles_done += tiles;
 #pragma unroll
             for (int t = 0; t < kM; ++t)
-                if (t < m_used) products[t] += t1 - at.t;
-            left -= t1 - at.t;
+                if (t < m_used) products[t] += tiles;
             // the next unit's queries, while this one's last products run: its scores are all
             // there, so nothing reads these any more
             Cursor<S> next = at;
-            if (left > 0) {
-                next.next_unit(a);
-                queries(next, c_next);
-            }
+            more = next.take(a);
+            if (more) queries(next, c_next);
 
             // outputs: a whole unit's to o, a cut one's to the workspace.  Of two m tiles a
             // warpgroup has its own, of one half the channels.
             if (!wait(&sm.done, units & 1)) break;
             ++units;
-            const bool whole = at.t == 0 && t1 == at.tiles;
+            const bool whole = at.t == 0 && at.t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
             if (r.some) {
@@ -758,6 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + mt * 128 + lrow] = make_float2(m, l);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ofree);
             at = next;
 #pragma unroll
             for (int t = 0; t < kM; ++t) c[t] = c_next[t];
@@ -816,10 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         int page = -1;
         uint32_t in_page = 0;
         bool held = false;
-        if (left > 0) page = page_at(at.t, in_page, held);
-        while (left > 0 && wait.ok) {
-            const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
-            left -= t1 - at.t;
+        bool more = at.take(a);
+        if (more) page = page_at(at.t, in_page, held);
+        while (more && wait.ok) {
+            const int t1 = at.t1;
             for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++made) {
                 const bool ok = page >= 0 && page < a.cache.num_pages;
                 if (held && !ok) record_device_error(a.err, kDevInvalidArg);
@@ -830,10 +848,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 // the next tile's pages, ahead of this one's copies
                 if (tile + 1 < t1) {
                     page = page_at(tile + 1, in_page, held);
-                } else if (left > 0) {
-                    at.next_unit(a);
-                    page = page_at(0, in_page, held);
-                    // (at.t is 0, and tile + 1 == t1 ends this loop)
+                } else {
+                    more = at.take(a);
+                    if (more) page = page_at(at.t, in_page, held);
                 }
                 auto copy = [&](const uint8_t *data, uint32_t to) {
 #pragma unroll 8
@@ -884,80 +901,79 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         while (kFp8 && landed < item && wait.ok) widen();
     } else {
         // ---- products ------------------------------------------------------------------------
+        // One warp issues the scores', the next the outputs': each spends more time on its waits
+        // and its instructions' way to the SM than a product takes.
         leave_registers<kProductRegs>();
+        constexpr uint32_t kFmt = kFp8 ? kFmtF16 : kFmtBF16;
+        Waits wait = {a.err, true};
         if (warp == kSoftWarps + kCopyWarps) {
-            Waits wait = {a.err, true};
-            constexpr uint32_t kFmt = kFp8 ? kFmtF16 : kFmtBF16;
-            constexpr uint32_t kIdS = instr_desc(128, kKeys, kFmt, 0, 0), kIdO = instr_desc(128, kD, kFmt, 0, 1);
-            uint32_t step_s = 0, step_p = 0, kt = 0, vt = 0, units = 0;
-            while (left > 0 && wait.ok) {
-                const int t1 = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.t + left));
+            constexpr uint32_t kId = instr_desc(128, kKeys, kFmt, 0, 0);
+            uint32_t step = 0, made = 0, units = 0;
+            while (at.take(a) && wait.ok) {
                 const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
-                const int steps = (t1 - at.t) * m_used;
                 wait(&sm.qfull, units & 1);
-                ++units;
-                auto scores = [&](int i) {  // of step i of this unit
-                    const int t = m_used == 1 ? 0 : i & 1;
-                    const uint32_t ks = kt % S::kNK;
-                    if (t == 0) {
-                        if (!wait(&sm.kfull[ks], (kt / S::kNK) & 1)) return;
-                        // the copies wrote by the generic proxy, the product reads by the async one
-                        fence_proxy_async_smem();
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + (step_s & 1) * kKeys;
-                    const uint64_t qd = smem_desc(base + t * (128 * kD * 2), 16, 1024, kSwizzle128B);
-                    const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
-    #pragma unroll 1
-                    for (int k = 0; k < kD / 64; ++k)  // (short code: the warps share its cache)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_f16_ss_w(d, qd + (k * (128 * 128) + j * 32) / 16, kd + (k * (kKeys * 128) + j * 32) / 16,
-                                         kIdS, k + j > 0);
-                    mma_commit_w(&sm.sfull[step_s & 1]);
-                    if (t == m_used - 1) {
-                        mma_commit_w(&sm.kempty[ks]);
-                        ++kt;
-                    }
-                    ++step_s;
-                };
-                auto outputs = [&](int i) {
-                    const int t = m_used == 1 ? 0 : i & 1;
-                    const uint32_t vs = vt % S::kNV, buf = step_p & 1;
-                    if (t == 0) {
-                        if (!wait(&sm.vfull[vs], (vt / S::kNV) & 1)) return;
-                        fence_proxy_async_smem();
-                    }
-                    if (!wait(&sm.pfull[buf], (step_p >> 1) & 1)) return;
-                    tc_fence_after();
-                    const uint32_t d = tmem + S::kColO + t * kD;
-                    const uint64_t vd = smem_desc(base + S::kOffV + vs * S::kTile, kKeys * 128, 1024, kSwizzle128B);
-    #pragma unroll 1
-                    for (int k = 0; k < kKeys / 32; ++k)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)  // two groups of 16 keys, two words
-                            mma_f16_ts_w(d, tmem + buf * kKeys + 32 * k + (j & 1) * 8 + (j >> 1) * 16,
-                                         vd + (32 * k + (j & 1) * 16) * 128 / 16, kIdO, k + j > 0 || i >= m_used);
-                    mma_commit_w(&sm.odone[t]);
-                    if (t == m_used - 1) {
-                        mma_commit_w(&sm.vempty[vs]);
-                        ++vt;
-                    }
-                    ++step_p;
-                };
+                for (int tile = at.t; tile < at.t1 && wait.ok; ++tile, ++made) {
+                    const uint32_t ks = made % S::kNK;
+                    if (!wait(&sm.kfull[ks], (made / S::kNK) & 1)) break;
+                    // the copies wrote by the generic proxy, the product reads by the async one
+                    fence_proxy_async_smem();
+                    for (int t = 0; t < m_used; ++t, ++step) {
+                        // the weights in this buffer have met their values
+                        if (!wait(&sm.pfree[step & 1], ((step >> 1) & 1) ^ 1)) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + (step & 1) * kKeys;
+                        const uint64_t qd = smem_desc(base + t * (128 * kD * 2), 16, 1024, kSwizzle128B);
+                        const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
 #pragma unroll 1
-                for (int i = -1; i < steps && wait.ok; ++i) {
-                    if (i + 1 < steps) scores(i + 1);
-                    else mma_commit_w(&sm.scored);
-                    if (i >= 0 && wait.ok) outputs(i);
+                        for (int k = 0; k < kD / 64; ++k)  // (short code: the warps share its cache)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma_f16_ss_w(d, qd + (k * (128 * 128) + j * 32) / 16,
+                                             kd + (k * (kKeys * 128) + j * 32) / 16, kId, k + j > 0);
+                        mma_commit_w(&sm.sfull[step & 1]);
+                    }
+                    mma_commit_w(&sm.kempty[ks]);
+                }
+                mma_commit_w(&sm.scored);
+                ++units;
+            }
+        } else if (warp == kSoftWarps + kCopyWarps + 1) {
+            constexpr uint32_t kId = instr_desc(128, kD, kFmt, 0, 1);
+            uint32_t step = 0, made = 0, units = 0;
+            while (at.take(a) && wait.ok) {
+                const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+                // the last unit's outputs have been read
+                if (!wait(&sm.ofree, (units & 1) ^ 1)) break;
+                ++units;
+                for (int tile = at.t; tile < at.t1 && wait.ok; ++tile, ++made) {
+                    const uint32_t vs = made % S::kNV;
+                    if (!wait(&sm.vfull[vs], (made / S::kNV) & 1)) break;
+                    fence_proxy_async_smem();
+                    for (int t = 0; t < m_used; ++t, ++step) {
+                        const uint32_t buf = step & 1;
+                        if (!wait(&sm.pfull[buf], (step >> 1) & 1)) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + S::kColO + t * kD, p = tmem + buf * kKeys;
+                        const uint64_t vd = smem_desc(base + S::kOffV + vs * S::kTile, kKeys * 128, 1024, kSwizzle128B);
+#pragma unroll 1
+                        for (int k = 0; k < kKeys / 32; ++k)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)  // two groups of 16 keys, two words
+                                mma_f16_ts_w(d, p + 32 * k + (j & 1) * 8 + (j >> 1) * 16,
+                                             vd + (32 * k + (j & 1) * 16) * 128 / 16, kId, k + j > 0 || tile > at.t);
+                        mma_commit_w(&sm.odone[t]);
+                        mma_commit_w(&sm.pfree[buf]);
+                    }
+                    mma_commit_w(&sm.vempty[vs]);
                 }
                 mma_commit_w(&sm.done);
-                left -= t1 - at.t;
-                if (left > 0) at.next_unit(a);
             }
+        }
+        if (warp <= kSoftWarps + kCopyWarps + 1) {
             // nothing is in flight when tensor memory is given back
-            mma_commit_w(&sm.drain);
-            mbar_wait_bounded(&sm.drain, 0, kMaxPolls);
+            uint64_t *drain = &sm.drain[warp - kSoftWarps - kCopyWarps];
+            mma_commit_w(drain);
+            mbar_wait_bounded(drain, 0, kMaxPolls);
         }
     }
     __syncwarp();
@@ -986,8 +1002,9 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
     if (s_place[0] >= 0) {
         cut.request(a, static_cast<int>(s_place[0]));
         cut.seek(s_place[1]);
-        const int64_t end = list.begin(c0 + int64_t{1}), start = end - cut.t;
-        if (cut.t > 0 && start >= list.begin(c0)) parts = list.piece_of(start + cut.tiles - 1) - c0 + 1;
+        // the places of the unit's first tile and of its last
+        const int64_t first = list.begin(c0 + int64_t{1}) - cut.at + kUnitCost, last = first + cut.tiles - 1;
+        if (cut.at > kUnitCost && first >= list.begin(c0)) parts = list.piece_of(last) - c0 + 1;
     }
     wait_for_kernel_before();
     const int r = cut.rg * S::kRows + tid;
