@@ -58,10 +58,10 @@ using namespace sm100;
 constexpr int kMaxCtas = 160;  // sizes the workspace; more SMs stay idle
 constexpr int kSoftWarps = 8, kCopyWarps = 4;
 constexpr int kThreads = 512;   // four warpgroups: weights (two), copies, products (one thread)
-// Their registers, of the 512 x 128 that the block is launched with: 2 x 184 + 80 + 56 = 504.
-constexpr int kSoftRegs = 184, kCopyRegs = 80, kProductRegs = 56;
+// Their registers, of the 512 x 128 that the block is launched with: 2 x 168 + 112 + 56 = 504.
+constexpr int kSoftRegs = 168, kCopyRegs = 112, kProductRegs = 56;
 static_assert(2 * kSoftRegs + kCopyRegs + kProductRegs <= 512, "registers of the block");
-constexpr int kUnitCost = 2;   // of beginning and ending a unit, in tiles
+constexpr int kUnitCost = 3;   // of beginning and ending a unit, in tiles
 constexpr int kMinPlaces = 1;  // of a CTA's piece
 constexpr uint32_t kMaxPolls = 1u << 20;
 
@@ -809,22 +809,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 if (!wait(is_v ? &sm.vempty[slot] : &sm.kempty[slot], ((i / n) & 1) ^ 1)) return;
                 const uint8_t *raw = smem + S::kOffRaw + (landed % S::kNR) * S::kRaw;
                 uint8_t *to = smem + (is_v ? S::kOffV : S::kOffK) + slot * S::kTile;
-#pragma unroll 4
+                uint4 x[kTurns];  // all loads first: a store might alias them
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k)
+                    x[k] = *reinterpret_cast<const uint4 *>(raw + (k * 32 * kCopyWarps + cw * 32 + lane) * 16);
+                // (neighbouring blocks of 64 channels in turn, so that 8 lanes meet every bank once)
+                const int swap = (ch >> 2) & 1;
+#pragma unroll
                 for (int k = 0; k < kTurns; ++k) {
                     const int r = cw * kRowsOfWarp + k * kAtOnce + sub;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(raw + (k * kAtOnce * kCopyWarps * kPieces + cw * 32 + lane) * 16);
                     uint4 y0, y1;
-                    y0.x = e4m3x2_to_f16x2(x.x);
-                    y0.y = e4m3x2_to_f16x2(x.x >> 16);
-                    y0.z = e4m3x2_to_f16x2(x.y);
-                    y0.w = e4m3x2_to_f16x2(x.y >> 16);
-                    y1.x = e4m3x2_to_f16x2(x.z);
-                    y1.y = e4m3x2_to_f16x2(x.z >> 16);
-                    y1.z = e4m3x2_to_f16x2(x.w);
-                    y1.w = e4m3x2_to_f16x2(x.w >> 16);
+                    y0.x = e4m3x2_to_f16x2(x[k].x);
+                    y0.y = e4m3x2_to_f16x2(x[k].x >> 16);
+                    y0.z = e4m3x2_to_f16x2(x[k].y);
+                    y0.w = e4m3x2_to_f16x2(x[k].y >> 16);
+                    y1.x = e4m3x2_to_f16x2(x[k].z);
+                    y1.y = e4m3x2_to_f16x2(x[k].z >> 16);
+                    y1.z = e4m3x2_to_f16x2(x[k].w);
+                    y1.w = e4m3x2_to_f16x2(x[k].w >> 16);
                     uint8_t *row = to + (ch >> 2) * (kKeys * 128) + r * 128;
-                    *reinterpret_cast<uint4 *>(row + ((((2 * ch) & 7) ^ (r & 7)) << 4)) = y0;
-                    *reinterpret_cast<uint4 *>(row + ((((2 * ch + 1) & 7) ^ (r & 7)) << 4)) = y1;
+                    const int c0 = ((2 * ch + swap) & 7) ^ (r & 7);
+                    *reinterpret_cast<uint4 *>(row + (c0 << 4)) = swap ? y1 : y0;
+                    *reinterpret_cast<uint4 *>(row + ((c0 ^ 1) << 4)) = swap ? y0 : y1;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(is_v ? &sm.vfull[slot] : &sm.kfull[slot]);
@@ -852,16 +858,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     more = at.take(a);
                     if (more) page = page_at(at.t, in_page, held);
                 }
+                int64_t from[kTurns];  // this lane's rows, -1: none
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k) from[k] = __shfl_sync(0xffffffffu, off, k * kAtOnce + sub);
                 auto copy = [&](const uint8_t *data, uint32_t to) {
-#pragma unroll 8
+                    data += ch * 16;
+#pragma unroll
                     for (int k = 0; k < kTurns; ++k) {
-                        const int r = k * kAtOnce + sub;
-                        const int64_t from = __shfl_sync(0xffffffffu, off, r);
-                        const int rr = cw * kRowsOfWarp + r;
+                        const int r = cw * kRowsOfWarp + k * kAtOnce + sub;
                         uint32_t dst;
-                        if constexpr (kFp8) dst = to + (k * kAtOnce * kCopyWarps * kPieces + cw * 32 + lane) * 16;
-                        else dst = to + (ch >> 3) * (kKeys * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-                        copy16(dst, data + (from < 0 ? 0 : from) + ch * 16, from >= 0);
+                        if constexpr (kFp8) dst = to + (k * 32 * kCopyWarps + cw * 32 + lane) * 16;
+                        else dst = to + (ch >> 3) * (kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                        copy16(dst, data + (from[k] < 0 ? 0 : from[k]), from[k] >= 0);
                     }
                 };
                 if constexpr (!kFp8) {
