@@ -20,9 +20,11 @@
 // takes an equal, contiguous piece; what is cut between CTAs is joined by a second, small
 // kernel that is set up with the first.
 //
-// A CTA.  Warps 8..11 copy the keys and values of its piece into two rings, rows swizzled as
-// the products read them (an 8-bit cache: raw, then widened to fp16, which holds every e4m3
-// value).  Two warps issue the products: S = Q K^T from shared memory into one of two score
+// A CTA.  Two warps copy the keys and two the values of its piece into two rings, rows swizzled
+// as the products read them: by TMA boxes of a page's keys, one instruction for up to 64 of
+// them (16-byte copies took the warps longer than a product), or 16 bytes at a time where pages
+// do not divide so or a tile is not full.  An 8-bit cache comes raw and is widened to fp16, which
+// holds every e4m3 value.  Two warps issue the products: S = Q K^T from shared memory into one of two score
 // buffers in tensor memory, and O += P V with P from there and V from shared memory.  Two
 // warpgroups turn scores into weights in place, a thread a row (a lane of tensor memory), each
 // every second step, so that one's exponentials run beside the other's loads and maxima.  A row's weights are relative to a reference that
@@ -46,6 +48,7 @@
 
 #include <cuda_fp16.h>
 
+#include "kda_chunk_common.cuh"
 #include "kda_f32x2.cuh"
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
@@ -58,8 +61,8 @@ using namespace sm100;
 constexpr int kMaxCtas = 160;  // sizes the workspace; more SMs stay idle
 constexpr int kSoftWarps = 8, kCopyWarps = 4;
 constexpr int kThreads = 512;   // four warpgroups: weights (two), copies, products (one thread)
-// Their registers, of the 512 x 128 that the block is launched with: 2 x 168 + 112 + 56 = 504.
-constexpr int kSoftRegs = 168, kCopyRegs = 112, kProductRegs = 56;
+// Their registers, of the 512 x 128 that the block is launched with: 2 x 176 + 96 + 56 = 504.
+constexpr int kSoftRegs = 176, kCopyRegs = 96, kProductRegs = 56;
 static_assert(2 * kSoftRegs + kCopyRegs + kProductRegs <= 512, "registers of the block");
 constexpr int kUnitCost = 3;   // of beginning and ending a unit, in tiles
 constexpr int kMinPlaces = 1;  // of a CTA's piece
@@ -82,6 +85,9 @@ struct Args {
     FastDiv group;
     float *ml;   // [CTAs][2][rows][2]
     float *cut;  // [CTAs][2][D / 4][rows][4]
+    // the cache's halves as [pages][heads][tokens][channels]: boxes of `box` tokens of a page
+    CUtensorMap map_k, map_v;
+    int box;
 };
 
 namespace {
@@ -99,26 +105,27 @@ struct Shape {
     static constexpr int kRaw = kTile / 2;        // of an 8-bit cache, as copied
     static constexpr int kQ = kRows * kD * 2;
     static constexpr int kRoom = 224 * 1024 - kQ;
-    // rings of operands, and of raw halves, in flight between copy and widening
+    // rings of operands, and of raw tiles of keys and of values, in flight between copy and widening
     static constexpr int kOps = kRoom / kTile;
     static constexpr int kNK = kFp8 ? (kD == 64 || (kM == 1 && kD == 128) ? 2 : 1) : min_of(6, (kOps + 1) / 2);
     static constexpr int kNV = kFp8 ? (kD == 64 ? 2 : 1) : min_of(6, kOps / 2);
-    static constexpr int kNR = kFp8 ? min_of(8, (kRoom - (kNK + kNV) * kTile) / kRaw) : 0;
+    static constexpr int kNR = kFp8 ? min_of(4, (kRoom - (kNK + kNV) * kTile) / kRaw / 2) : 0;
     static constexpr int kOffK = kQ, kOffV = kOffK + kNK * kTile, kOffRaw = kOffV + kNV * kTile;
-    static constexpr int kOffSmall = kOffRaw + kNR * kRaw;
+    static constexpr int kOffSmall = kOffRaw + 2 * kNR * kRaw;
     static constexpr int kColO = 2 * kKeys;
     // a row's reference follows its maximum when that has grown by 2^kSlack; weights are
     // 2^kShift times themselves (fp16 ends at 2^16)
     static constexpr float kSlack = kFp8 ? 3.f : 7.f, kShift = kFp8 ? 12.f : 0.f;
     static_assert(kColO + kM * kD <= 512, "tensor memory");
-    static_assert(!kFp8 || kNR >= 3, "halves in flight");
+    static_assert(!kFp8 || kNR >= 2, "tiles in flight");
 
     struct Small {  // what lies behind the tiles
         uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], pfree[2], scored, done, ofree, drain[2];
         int64_t warp_sum[kThreads / 32], place[2];
         // by row: the reference that a warpgroup hands to the other, and what they exchange
         float ref[128], top[2][128];
-        uint32_t valid[16][kCopyWarps];  // which rows of a tile are keys, by copy warp
+        uint64_t raw[2][2][kNR > 0 ? kNR : 1];  // keys and values, halves of rows
+        uint32_t valid[16][kKeys / 32];         // which rows of a tile are keys
         uint32_t tmem;
     };
     static constexpr int kSmem = kOffSmall + static_cast<int>(sizeof(Small));
@@ -385,6 +392,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool re
                  : "memory");
 }
 
+// A box of a page to shared memory; x a multiple of 64 elements.
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int token,
+                                         int head, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // The two warps of a lane quarter.
 __device__ __forceinline__ void pair_barrier(int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
@@ -446,14 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     if (tid == 0) {
         mbar_init(&sm.qfull, kSoftWarps);
         for (int i = 0; i < S::kNK; ++i) {
-            // widened by the threads of the copy warps; else their copies', and a word of `valid` each
-            mbar_init(&sm.kfull[i], kFp8 ? kCopyWarps * 32 : kCopyWarps * 32 + kCopyWarps);
+            // two warps' threads when they have widened their rows; else their copies, and a
+            // thread of each for what it has said beside them
+            mbar_init(&sm.kfull[i], kFp8 ? 64 : 66);
             mbar_init(&sm.kempty[i], 1);
         }
         for (int i = 0; i < S::kNV; ++i) {
-            mbar_init(&sm.vfull[i], kCopyWarps * 32);
+            mbar_init(&sm.vfull[i], kFp8 ? 64 : 66);
             mbar_init(&sm.vempty[i], 1);
         }
+        for (int i = 0; i < 4 * S::kNR; ++i) mbar_init(&sm.raw[0][0][0] + i, 33);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
             mbar_init(&sm.pfull[i], kSoftWarps / 2);
@@ -597,12 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     const int d = (at.t + tile) * kKeys - (at.len - at.n);
                     bool all = true;
 #pragma unroll
-                    for (int k = 0; k < kCopyWarps; ++k)
-                        all &= v[k] == (kKeys == 128 ? 0xffffffffu : 0xffffu);
+                    for (int k = 0; k < kKeys / 32; ++k) all &= v[k] == 0xffffffffu;
                     if (d + kKeys > 0 || !all) {
 #pragma unroll 1
                         for (int k = 0; k < kKeys / 32; ++k) {
-                            uint32_t seen = kKeys == 128 ? v[k] : v[2 * k + 1] << 16 | v[2 * k];
+                            uint32_t seen = v[k];
                             if (d + 32 * (k + 1) > 0) seen &= static_cast<uint32_t>(seen_from(word, d + 32 * k));
                             float s[32];
                             tmem_ld32(cols + 32 * k, s);
@@ -782,131 +800,170 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         }
     } else if (warp < kSoftWarps + kCopyWarps) {
         // ---- keys and values in --------------------------------------------------------------
+        // Two warps copy keys, two values; each half of a tile's rows.
         leave_registers<kCopyRegs>();
         Waits wait = {a.err, true};
-        const int cw = warp - kSoftWarps;
-        constexpr int kRowsOfWarp = kKeys / kCopyWarps;
+        const int cw = warp - kSoftWarps, half = cw & 1;
+        const bool is_v = cw >= 2;
+        const uint8_t *data = is_v ? a.cache.v : a.cache.k;
+        const CUtensorMap *map = is_v ? &args.map_v : &args.map_k;
+        uint64_t *full = is_v ? sm.vfull : sm.kfull, *empty = is_v ? sm.vempty : sm.kempty;
+        const uint32_t slots = is_v ? S::kNV : S::kNK, ops = is_v ? S::kOffV : S::kOffK;
+        constexpr int kRowsOfWarp = kKeys / 2, kLaneRows = kRowsOfWarp / 32;
         constexpr int kRowBytes = kD * (kFp8 ? 1 : 2);
         constexpr int kPieces = kRowBytes / 16;          // lanes to a row
         constexpr int kAtOnce = 32 / kPieces;            // rows of a warp's copy
         constexpr int kTurns = kRowsOfWarp / kAtOnce;
-        const int sub = lane / kPieces, ch = lane % kPieces;
-        uint32_t item = 0, landed = 0;                   // halves of tiles: copied, widened
-        uint32_t made = 0;                               // tiles
-        // this lane's row of the next tile
-        auto page_at = [&](int tile, uint32_t &in_page, bool &held) {
-            const uint32_t j = static_cast<uint32_t>(tile) * kKeys + cw * kRowsOfWarp + lane;
-            uint32_t idx;
-            a.cache.page.divmod(j, idx, in_page);
-            held = lane < kRowsOfWarp && j < static_cast<uint32_t>(at.len);
-            return held ? a.block_table[static_cast<int64_t>(at.b) * a.max_pages + idx] : -1;
-        };
-        // a raw half, widened into its place as an operand (8-bit cache)
-        auto widen = [&]() {
-            if constexpr (kFp8) {
-                const bool is_v = landed & 1;
-                const uint32_t i = landed >> 1, n = is_v ? S::kNV : S::kNK, slot = i % n;
-                if (!wait(is_v ? &sm.vempty[slot] : &sm.kempty[slot], ((i / n) & 1) ^ 1)) return;
-                const uint8_t *raw = smem + S::kOffRaw + (landed % S::kNR) * S::kRaw;
-                uint8_t *to = smem + (is_v ? S::kOffV : S::kOffK) + slot * S::kTile;
-                uint4 x[kTurns];  // all loads first: a store might alias them
+        constexpr int kBlocks = kFp8 ? 1 : kD / 64;      // boxes beside one another
+        const int sub = lane / kPieces, ch = lane % kPieces, row0 = half * kRowsOfWarp;
+        const int box = args.box;                        // keys of a box; 0: none
+        uint32_t made = 0, widened = 0;                  // tiles
+        int page[kLaneRows];                             // of this lane's rows of the next tile
+        uint32_t in_page[kLaneRows];
+        bool held[kLaneRows];
+        auto find_pages = [&](int tile) {
 #pragma unroll
-                for (int k = 0; k < kTurns; ++k)
-                    x[k] = *reinterpret_cast<const uint4 *>(raw + (k * 32 * kCopyWarps + cw * 32 + lane) * 16);
-                // (neighbouring blocks of 64 channels in turn, so that 8 lanes meet every bank once)
-                const int swap = (ch >> 2) & 1;
-#pragma unroll
-                for (int k = 0; k < kTurns; ++k) {
-                    const int r = cw * kRowsOfWarp + k * kAtOnce + sub;
-                    uint4 y0, y1;
-                    y0.x = e4m3x2_to_f16x2(x[k].x);
-                    y0.y = e4m3x2_to_f16x2(x[k].x >> 16);
-                    y0.z = e4m3x2_to_f16x2(x[k].y);
-                    y0.w = e4m3x2_to_f16x2(x[k].y >> 16);
-                    y1.x = e4m3x2_to_f16x2(x[k].z);
-                    y1.y = e4m3x2_to_f16x2(x[k].z >> 16);
-                    y1.z = e4m3x2_to_f16x2(x[k].w);
-                    y1.w = e4m3x2_to_f16x2(x[k].w >> 16);
-                    uint8_t *row = to + (ch >> 2) * (kKeys * 128) + r * 128;
-                    const int c0 = ((2 * ch + swap) & 7) ^ (r & 7);
-                    *reinterpret_cast<uint4 *>(row + (c0 << 4)) = swap ? y1 : y0;
-                    *reinterpret_cast<uint4 *>(row + ((c0 ^ 1) << 4)) = swap ? y0 : y1;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(is_v ? &sm.vfull[slot] : &sm.kfull[slot]);
-                ++landed;
+            for (int i = 0; i < kLaneRows; ++i) {
+                const uint32_t j = static_cast<uint32_t>(tile) * kKeys + row0 + lane + 32 * i;
+                uint32_t idx;
+                a.cache.page.divmod(j, idx, in_page[i]);
+                held[i] = j < static_cast<uint32_t>(at.len);
+                page[i] = held[i] ? a.block_table[static_cast<int64_t>(at.b) * a.max_pages + idx] : -1;
             }
         };
-        int page = -1;
-        uint32_t in_page = 0;
-        bool held = false;
+        // a raw tile's rows, widened into their place as an operand (8-bit cache)
+        auto widen = [&]() {
+            if constexpr (kFp8) {
+                const uint32_t slot = widened % slots, raw_slot = widened % S::kNR;
+                if (!wait(&sm.raw[is_v][half][raw_slot], (widened / S::kNR) & 1)) return;
+                if (!wait(&empty[slot], ((widened / slots) & 1) ^ 1)) return;
+                const uint8_t *raw = smem + S::kOffRaw + (is_v * S::kNR + raw_slot) * S::kRaw + half * (S::kRaw / 2);
+                uint8_t *to = smem + ops + slot * S::kTile;
+                // (neighbouring blocks of 64 channels in turn, so that 8 lanes meet every bank once)
+                const int swap = (ch >> 2) & 1;
+                constexpr int kBatch = kTurns < 8 ? kTurns : 8;
+#pragma unroll
+                for (int k0 = 0; k0 < kTurns; k0 += kBatch) {
+                    uint4 x[kBatch];  // loads first: a store might alias them
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        x[k] = *reinterpret_cast<const uint4 *>(raw + ((k0 + k) * 32 + lane) * 16);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int r = row0 + (k0 + k) * kAtOnce + sub;
+                        uint4 y0, y1;
+                        y0.x = e4m3x2_to_f16x2(x[k].x);
+                        y0.y = e4m3x2_to_f16x2(x[k].x >> 16);
+                        y0.z = e4m3x2_to_f16x2(x[k].y);
+                        y0.w = e4m3x2_to_f16x2(x[k].y >> 16);
+                        y1.x = e4m3x2_to_f16x2(x[k].z);
+                        y1.y = e4m3x2_to_f16x2(x[k].z >> 16);
+                        y1.z = e4m3x2_to_f16x2(x[k].w);
+                        y1.w = e4m3x2_to_f16x2(x[k].w >> 16);
+                        uint8_t *row = to + (ch >> 2) * (kKeys * 128) + r * 128;
+                        const int c0 = ((2 * ch + swap) & 7) ^ (r & 7);
+                        *reinterpret_cast<uint4 *>(row + (c0 << 4)) = swap ? y1 : y0;
+                        *reinterpret_cast<uint4 *>(row + ((c0 ^ 1) << 4)) = swap ? y0 : y1;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&full[slot]);
+                ++widened;
+                __syncwarp();
+            }
+        };
         bool more = at.take(a);
-        if (more) page = page_at(at.t, in_page, held);
+        if (more) find_pages(at.t);
         while (more && wait.ok) {
             const int t1 = at.t1;
             for (int tile = at.t; tile < t1 && wait.ok; ++tile, ++made) {
-                const bool ok = page >= 0 && page < a.cache.num_pages;
-                if (held && !ok) record_device_error(a.err, kDevInvalidArg);
-                const int64_t off = ok ? page * a.cache.page_stride + in_page * a.cache.token_stride +
-                                             at.h * a.cache.head_stride
-                                       : -1;
-                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                const int h = at.h;
+                bool whole = box > 0;
+                int64_t off[kLaneRows];
+                int box_page = 0, box_row = 0;  // of this lane's box
+                const int mine = lane / kBlocks * box;
+#pragma unroll
+                for (int i = 0; i < kLaneRows; ++i) {
+                    const bool ok = page[i] >= 0 && page[i] < a.cache.num_pages;
+                    if (held[i] && !ok) record_device_error(a.err, kDevInvalidArg);
+                    off[i] = ok ? page[i] * a.cache.page_stride + in_page[i] * a.cache.token_stride +
+                                      h * a.cache.head_stride
+                                : -1;
+                    const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                    whole &= valid == 0xffffffffu;
+                    if (!is_v && lane == 0) sm.valid[made & 15][half * kLaneRows + i] = valid;
+                    const int p = __shfl_sync(0xffffffffu, page[i], mine & 31);
+                    const int q = __shfl_sync(0xffffffffu, static_cast<int>(in_page[i]), mine & 31);
+                    if (i == mine >> 5) {
+                        box_page = p;
+                        box_row = q;
+                    }
+                }
                 // the next tile's pages, ahead of this one's copies
                 if (tile + 1 < t1) {
-                    page = page_at(tile + 1, in_page, held);
+                    find_pages(tile + 1);
                 } else {
                     more = at.take(a);
-                    if (more) page = page_at(at.t, in_page, held);
+                    if (more) find_pages(at.t);
                 }
-                int64_t from[kTurns];  // this lane's rows, -1: none
-#pragma unroll
-                for (int k = 0; k < kTurns; ++k) from[k] = __shfl_sync(0xffffffffu, off, k * kAtOnce + sub);
-                auto copy = [&](const uint8_t *data, uint32_t to) {
-                    data += ch * 16;
-#pragma unroll
-                    for (int k = 0; k < kTurns; ++k) {
-                        const int r = cw * kRowsOfWarp + k * kAtOnce + sub;
-                        uint32_t dst;
-                        if constexpr (kFp8) dst = to + (k * 32 * kCopyWarps + cw * 32 + lane) * 16;
-                        else dst = to + (ch >> 3) * (kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                        copy16(dst, data + (from[k] < 0 ? 0 : from[k]), from[k] >= 0);
-                    }
-                };
-                if constexpr (!kFp8) {
-                    const uint32_t ks = made % S::kNK, vs = made % S::kNV;
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        uint64_t *full = half ? &sm.vfull[vs] : &sm.kfull[ks];
-                        if (!wait(half ? &sm.vempty[vs] : &sm.kempty[ks],
-                                  ((made / (half ? S::kNV : S::kNK)) & 1) ^ 1))
-                            break;
-                        copy(half ? a.cache.v : a.cache.k,
-                             base + (half ? S::kOffV + vs * S::kTile : S::kOffK + ks * S::kTile));
-                        copies_arrive(full);
-                        if (half == 0 && lane == 0) {
-                            sm.valid[made & 15][cw] = valid;
-                            mbar_arrive(full);
-                        }
-                    }
+                uint64_t *bar;
+                uint32_t to, row_pitch;  // where the warp's rows go
+                if constexpr (kFp8) {
+                    const uint32_t slot = made % S::kNR;
+                    bar = &sm.raw[is_v][half][slot];
+                    to = S::kOffRaw + (is_v * S::kNR + slot) * S::kRaw + half * (S::kRaw / 2);
+                    row_pitch = kD;
                 } else {
-                    if (lane == 0) sm.valid[made & 15][cw] = valid;
+                    const uint32_t slot = made % slots;
+                    if (!wait(&empty[slot], ((made / slots) & 1) ^ 1)) break;
+                    bar = &full[slot];
+                    to = ops + slot * S::kTile + row0 * 128;
+                    row_pitch = 128;
+                }
+                if (whole) {
+                    // every row is a key: boxes of keys, by the tensor map
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kRowsOfWarp * kRowBytes);
                     __syncwarp();
+                    if (mine < kRowsOfWarp)
+                        load_box(smem + to + lane % kBlocks * (kKeys * 128) + mine * row_pitch, map, bar,
+                                 lane % kBlocks * 64, box_row, h, box_page);
+                    mbar_arrive(bar);
+                } else {
+                    // row by row, zeros where there is no key
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        copy(half ? a.cache.v : a.cache.k, base + S::kOffRaw + (item % S::kNR) * S::kRaw);
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        if (++item >= S::kNR) {
-                            asm volatile("cp.async.wait_group %0;" ::"n"(S::kNR > 0 ? S::kNR - 1 : 0) : "memory");
-                            widen();
-                            if (!wait.ok) break;
-                            __syncwarp();
+                    for (int k0 = 0; k0 < kTurns; k0 += 4) {
+                        int64_t from[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = (k0 + k) * kAtOnce + sub;
+                            from[k] = __shfl_sync(0xffffffffu, off[0], r & 31);
+                            if constexpr (kLaneRows == 2) {
+                                const int64_t x = __shfl_sync(0xffffffffu, off[1], r & 31);
+                                if (r >= 32) from[k] = x;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = (k0 + k) * kAtOnce + sub;
+                            uint32_t dst = base + to + r * row_pitch;
+                            if constexpr (kFp8) dst += ch * 16;
+                            else dst += (ch >> 3) * (kKeys * 128) + (((ch & 7) ^ (r & 7)) << 4);
+                            copy16(dst, data + (from[k] < 0 ? 0 : from[k] + ch * 16), from[k] >= 0);
                         }
                     }
+                    copies_arrive(bar);
+                    if (lane == 0) mbar_arrive(bar);
                 }
+                if (kFp8 && made + 1 >= S::kNR) widen();
             }
         }
+        while (kFp8 && widened < made && wait.ok) widen();
         asm volatile("cp.async.wait_all;" ::: "memory");
-        while (kFp8 && landed < item && wait.ok) widen();
+        if (!wait.ok) {  // boxes that nobody waits for any more
+            const uint32_t ring = kFp8 ? S::kNR : slots;
+            for (uint32_t i = made < ring ? 0 : made - ring; i < made; ++i)
+                mbar_wait_bounded(kFp8 ? &sm.raw[is_v][half][i % ring] : &full[i % ring], (i / ring) & 1, kMaxPolls);
+        }
     } else {
         // ---- products ------------------------------------------------------------------------
         // One warp issues the scores', the next the outputs': each spends more time on its waits
@@ -1083,8 +1140,36 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
     }
 }
 
+// The cache's halves for boxes of keys, where its pages can be cut in boxes of 8 keys (a swizzled
+// group of rows) or more.  Otherwise, and where the driver refuses, rows are copied one by one.
 template <class S>
-cudaError_t launch_shape(const Args &a, int ctas, cudaStream_t s) {
+void make_maps(Args &a) {
+    constexpr int kSize = S::kFp8 ? 1 : 2;
+    const PagedView &c = a.t.cache;
+    a.box = 0;
+    int box = S::kKeys / 2;
+    while (c.page.d % static_cast<uint32_t>(box) != 0) box /= 2;
+    const chunk::EncodeTiledFn fn = chunk::encode_fn();
+    if (box < 8 || fn == nullptr) return;
+    const cuuint64_t dims[4] = {S::kD, c.page.d, static_cast<cuuint64_t>(c.heads),
+                                static_cast<cuuint64_t>(c.num_pages)};
+    // (the stride of a single entry is not given, and never taken)
+    auto stride = [](int64_t x) { return static_cast<cuuint64_t>(x > 0 ? x : S::kD * kSize); };
+    const cuuint64_t strides[3] = {stride(c.token_stride), stride(c.head_stride), stride(c.page_stride)};
+    const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(S::kFp8 ? S::kD : 64), static_cast<cuuint32_t>(box), 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    auto make = [&](CUtensorMap *map, void *data) {
+        return fn(map, S::kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, data, dims,
+                  strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  S::kFp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (make(&a.map_k, c.k) && make(&a.map_v, c.v)) a.box = box;
+}
+
+template <class S>
+cudaError_t launch_shape(Args a, int ctas, cudaStream_t s) {
+    make_maps<S>(a);
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(&tree_attention_kernel<S>), S::kSmem);
     if (e != cudaSuccess) return e;
