@@ -112,15 +112,16 @@ struct Shape {
     static constexpr int kNR = kFp8 ? min_of(4, (kRoom - (kNK + kNV) * kTile) / kRaw / 2) : 0;
     static constexpr int kOffK = kQ, kOffV = kOffK + kNK * kTile, kOffRaw = kOffV + kNV * kTile;
     static constexpr int kOffSmall = kOffRaw + 2 * kNR * kRaw;
-    static constexpr int kColO = 2 * kKeys;
+    // score buffers in tensor memory, then the outputs
+    static constexpr int kBufs = min_of(4, (512 - kM * kD) / kKeys), kColO = kBufs * kKeys;
     // a row's reference follows its maximum when that has grown by 2^kSlack; weights are
     // 2^kShift times themselves (fp16 ends at 2^16)
     static constexpr float kSlack = kFp8 ? 3.f : 7.f, kShift = kFp8 ? 12.f : 0.f;
-    static_assert(kColO + kM * kD <= 512, "tensor memory");
+    static_assert(kBufs >= 2, "tensor memory");
     static_assert(!kFp8 || kNR >= 2, "tiles in flight");
 
     struct Small {  // what lies behind the tiles
-        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[2], pfull[2], odone[kM], pfree[2], scored, done, ofree, drain[2];
+        uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[kBufs], pfull[kBufs][2], pfree[kBufs], scored, done, ofree, drain[2];
         int64_t warp_sum[kThreads / 32], place[2];
         // by row: the reference that a warpgroup hands to the other, and what they exchange
         float ref[128], top[2][128];
@@ -473,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             mbar_init(&sm.vempty[i], 1);
         }
         for (int i = 0; i < 4 * S::kNR; ++i) mbar_init(&sm.raw[0][0][0] + i, 33);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.pfull[i], kSoftWarps / 2);
+            mbar_init(&sm.pfull[i][0], kSoftWarps / 2);
+            mbar_init(&sm.pfull[i][1], kSoftWarps / 2);
             mbar_init(&sm.pfree[i], 1);
         }
-        for (int i = 0; i < kM; ++i) mbar_init(&sm.odone[i], 1);
         mbar_init(&sm.scored, 1);
         mbar_init(&sm.done, 1);
         mbar_init(&sm.ofree, kSoftWarps);
@@ -508,8 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         Waits wait = {a.err, true};
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        // steps, tiles and units so far, and the products into each O
-        uint32_t step = 0, tiles_done = 0, units = 0, products[kM] = {};
+        uint32_t step = 0, tiles_done = 0, units = 0;
         // Row `lrow` of m tile t of a unit.
         struct Row {
             bool some, real;  // this warp has rows there; this lane's is one
@@ -606,11 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
 
             for (int i = i0; i < steps && wait.ok; i += 2) {
                 const int tile = m_used == 1 ? i : i >> 1;
-                const uint32_t g = step + i;
-                if (!wait(&sm.sfull[wg], (g >> 1) & 1)) break;
+                const uint32_t g = step + i, buf = g % S::kBufs;
+                if (!wait(&sm.sfull[buf], (g / S::kBufs) & 1)) break;
                 if (r.some) {
                     tc_fence_after();
-                    const uint32_t cols = lanes + wg * kKeys;
+                    const uint32_t cols = lanes + buf * kKeys;
                     // the keys that the row sees, where that is not all of them
                     const uint32_t *v = sm.valid[(tiles_done + tile) & 15];
                     const int d = (at.t + tile) * kKeys - (at.len - at.n);
@@ -666,9 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (!first && __any_sync(0xffffffffu, grown)) {
                         const float keep = grown ? ex2(m - ref) : 1.f;
                         l *= keep;
-                        // the last product of these rows; the one before it was complete when
-                        // this step's scores were (so one phase is open at most)
-                        wait(&sm.odone[mt], (products[mt] + tile - 1) & 1);
+                        const uint32_t q = g - m_used;  // the last product of these rows
+                        wait(&sm.pfree[q % S::kBufs], (q / S::kBufs) & 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int k = 0; k < kD / 32; ++k) {
@@ -695,8 +694,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             const float p0 = ex2(e.x), p1 = ex2(e.y);
                             const uint64_t p2 = f2(p0, p1);
                             sum2 = f2_add(sum2, p2);
-                            const uint32_t h = pack2<kFp8>(p0, p1);
-                            const float2 y = unpack2<kFp8>(h);
+                            uint32_t h;
+                            float2 y;  // the first words' values
+                            if constexpr (kFp8) {
+                                h = pack2<true>(p0, p1);
+                                y = unpack2<true>(h);
+                            } else {  // cut off: the second word holds what remains, and its rounding
+                                h = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                                y = make_float2(__uint_as_float(__float_as_uint(p0) & 0xffff0000u),
+                                                __uint_as_float(__float_as_uint(p1) & 0xffff0000u));
+                            }
                             const float2 rest = f2_split(f2_sub(p2, f2(y.x, y.y)));
                             hi[x] = __uint_as_float(h);
                             lo[x] = __uint_as_float(pack2<kFp8>(rest.x, rest.y));
@@ -704,22 +711,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         // a weight's two words take its score's place
                         tmem_st16(cols + 32 * k, hi);
                         tmem_st16(cols + 32 * k + 16, lo);
+                        if (k + 1 == kKeys / 64 || k + 1 == kKeys / 32) {
+                            // half the keys' weights: their product may begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.pfull[buf][k + 1 == kKeys / 64 ? 0 : 1]);
+                        }
                     }
                     const float2 sum = f2_split(sum2);
                     l += sum.x + sum.y;
-                    tmem_wait_st();
-                    tc_fence_before();
+                } else {
+                    if (lane < 2) mbar_arrive(&sm.pfull[buf][lane]);
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pfull[wg]);
             }
             // (a warpgroup's last step may not be the unit's)
             if (!wait(&sm.scored, units & 1)) break;
             step += steps;
             tiles_done += tiles;
-#pragma unroll
-            for (int t = 0; t < kM; ++t)
-                if (t < m_used) products[t] += tiles;
             // the next unit's queries, while this one's last products run: its scores are all
             // there, so nothing reads these any more
             Cursor<S> next = at;
@@ -984,9 +994,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     fence_proxy_async_smem();
                     for (int t = 0; t < m_used; ++t, ++step) {
                         // the weights in this buffer have met their values
-                        if (!wait(&sm.pfree[step & 1], ((step >> 1) & 1) ^ 1)) break;
+                        const uint32_t buf = step % S::kBufs;
+                        if (!wait(&sm.pfree[buf], ((step / S::kBufs) & 1) ^ 1)) break;
                         tc_fence_after();
-                        const uint32_t d = tmem + (step & 1) * kKeys;
+                        const uint32_t d = tmem + buf * kKeys;
                         const uint64_t qd = smem_desc(base + t * (128 * kD * 2), 16, 1024, kSwizzle128B);
                         const uint64_t kd = smem_desc(base + S::kOffK + ks * S::kTile, 16, 1024, kSwizzle128B);
 #pragma unroll 1
@@ -995,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             for (int j = 0; j < 4; ++j)
                                 mma_f16_ss_w(d, qd + (k * (128 * 128) + j * 32) / 16,
                                              kd + (k * (kKeys * 128) + j * 32) / 16, kId, k + j > 0);
-                        mma_commit_w(&sm.sfull[step & 1]);
+                        mma_commit_w(&sm.sfull[buf]);
                     }
                     mma_commit_w(&sm.kempty[ks]);
                 }
@@ -1015,18 +1026,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (!wait(&sm.vfull[vs], (made / S::kNV) & 1)) break;
                     fence_proxy_async_smem();
                     for (int t = 0; t < m_used; ++t, ++step) {
-                        const uint32_t buf = step & 1;
-                        if (!wait(&sm.pfull[buf], (step >> 1) & 1)) break;
-                        tc_fence_after();
+                        const uint32_t buf = step % S::kBufs;
                         const uint32_t d = tmem + S::kColO + t * kD, p = tmem + buf * kKeys;
                         const uint64_t vd = smem_desc(base + S::kOffV + vs * S::kTile, kKeys * 128, 1024, kSwizzle128B);
 #pragma unroll 1
-                        for (int k = 0; k < kKeys / 32; ++k)
+                        for (int k = 0; k < kKeys / 32; ++k) {
+                            if (k % (kKeys / 64) == 0) {
+                                if (!wait(&sm.pfull[buf][k / (kKeys / 64)], (step / S::kBufs) & 1)) break;
+                                tc_fence_after();
+                            }
 #pragma unroll
                             for (int j = 0; j < 4; ++j)  // two groups of 16 keys, two words
                                 mma_f16_ts_w(d, p + 32 * k + (j & 1) * 8 + (j >> 1) * 16,
                                              vd + (32 * k + (j & 1) * 16) * 128 / 16, kId, k + j > 0 || tile > at.t);
-                        mma_commit_w(&sm.odone[t]);
+                        }
+                        if (!wait.ok) break;
                         mma_commit_w(&sm.pfree[buf]);
                     }
                     mma_commit_w(&sm.vempty[vs]);
