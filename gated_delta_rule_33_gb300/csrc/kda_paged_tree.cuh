@@ -64,8 +64,6 @@ constexpr int kThreads = 512;   // four warpgroups: weights (two), copies, produ
 // Their registers, of the 512 x 128 that the block is launched with: 2 x 176 + 96 + 56 = 504.
 constexpr int kSoftRegs = 176, kCopyRegs = 96, kProductRegs = 56;
 static_assert(2 * kSoftRegs + kCopyRegs + kProductRegs <= 512, "registers of the block");
-constexpr int kUnitCost = 3;   // of beginning and ending a unit, in tiles
-constexpr int kMinPlaces = 1;  // of a CTA's piece
 constexpr uint32_t kMaxPolls = 1u << 20;
 
 __host__ __device__ constexpr int min_of(int a, int b) { return a < b ? a : b; }
@@ -102,13 +100,15 @@ struct Shape {
     static constexpr int kRows = kM * 128;
     static constexpr int kKeys = kD == 256 ? 64 : 128;
     static constexpr int kTile = kKeys * kD * 2;  // as an operand
+    // places in the list of a tile of one m tile, of two, and of beginning and ending a unit
+    static constexpr int kOneCost = kM == 1 ? 1 : 2, kTwoCost = 3, kUnitCost = kM == 1 ? 3 : 10;
     static constexpr int kRaw = kTile / 2;        // of an 8-bit cache, as copied
     static constexpr int kQ = kRows * kD * 2;
     static constexpr int kRoom = 224 * 1024 - kQ;
     // rings of operands, and of raw tiles of keys and of values, in flight between copy and widening
     static constexpr int kOps = kRoom / kTile;
-    static constexpr int kNK = kFp8 ? (kD == 64 || (kM == 1 && kD == 128) ? 2 : 1) : min_of(6, (kOps + 1) / 2);
-    static constexpr int kNV = kFp8 ? (kD == 64 ? 2 : 1) : min_of(6, kOps / 2);
+    static constexpr int kNK = kFp8 ? (kD == 256 ? 1 : 2) : min_of(6, (kOps + 1) / 2);
+    static constexpr int kNV = kFp8 ? (kTile <= 16 * 1024 ? 2 : 1) : min_of(6, kOps / 2);
     static constexpr int kNR = kFp8 ? min_of(4, (kRoom - (kNK + kNV) * kTile) / kRaw / 2) : 0;
     static constexpr int kOffK = kQ, kOffV = kOffK + kNK * kTile, kOffRaw = kOffV + kNV * kTile;
     static constexpr int kOffSmall = kOffRaw + 2 * kNR * kRaw;
@@ -120,13 +120,17 @@ struct Shape {
     static_assert(kBufs >= 2, "tensor memory");
     static_assert(!kFp8 || kNR >= 2, "tiles in flight");
 
+    // tiles whose rows' validity is kept: more than lie between a copy and its weights
+    static constexpr int kTilesAhead = 16;
+    static_assert(kTilesAhead > kNK + kNR + kBufs, "tiles ahead");
+
     struct Small {  // what lies behind the tiles
         uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[kBufs], pfull[kBufs][2], pfree[kBufs], scored, done, ofree, drain[2];
         int64_t warp_sum[kThreads / 32], place[2];
-        // by row: the reference that a warpgroup hands to the other, and what they exchange
-        float ref[128], top[2][128];
+        // by row: the reference that a warpgroup hands to the other (top[0]), and what they exchange in the end
+        float top[2][128];
         uint64_t raw[2][2][kNR > 0 ? kNR : 1];  // keys and values, halves of rows
-        uint32_t valid[16][kKeys / 32];         // which rows of a tile are keys
+        uint32_t valid[kTilesAhead][kKeys / 32];  // which rows of a tile are keys
         uint32_t tmem;
     };
     static constexpr int kSmem = kOffSmall + static_cast<int>(sizeof(Small));
@@ -138,6 +142,9 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// 2^e, -126 <= e <= 127 (a power further out is taken in two factors).
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
 // x, or the least normal number where x is below it; a NaN stays.
 __device__ __forceinline__ float at_least_normal(float x) { return x < FLT_MIN ? FLT_MIN : x; }
@@ -229,8 +236,9 @@ __device__ __noinline__ void row_exact(const TreeAttention &a, int b, int64_t ro
 
 // ---- the list of tiles ---------------------------------------------------------------------
 
-// A place in the list, and the way from there.  A unit takes kUnitCost places of the list before
-// those of its tiles: what it costs to begin and end one.
+// A place in the list, and the way from there.  A unit takes kUnitCost places of the list, then as
+// many for each of its tiles as they cost (measured: a tile of two m tiles takes one and a half
+// times one's; beginning and ending a unit takes three).
 template <class S>
 struct Cursor {
     int b, h, rg;
@@ -251,15 +259,24 @@ struct Cursor {
         groups = (rows + S::kRows - 1) / S::kRows;
         tiles = n == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(len) + S::kKeys - 1) / S::kKeys);
     }
+    // m tiles of the sequence's i-th group of rows, places of a tile of them and of their unit
+    __device__ __forceinline__ int m_tiles(int i) const { return S::kM == 2 && rows - i * S::kRows > 128 ? 2 : 1; }
+    __device__ __forceinline__ int cost(int i) const { return m_tiles(i) == 2 ? S::kTwoCost : S::kOneCost; }
+    __device__ __forceinline__ int64_t unit(int i) const {
+        return static_cast<int64_t>(tiles) * cost(i) + S::kUnitCost;
+    }
+    __device__ __forceinline__ int64_t head() const {
+        return (groups - 1) * unit(0) + unit(groups - 1);  // all groups but the last are full
+    }
     __device__ __forceinline__ int64_t places(const TreeAttention &a) const {
-        return tiles == 0 ? 0 : static_cast<int64_t>(a.cache.heads) * groups * (tiles + kUnitCost);
+        return tiles == 0 ? 0 : a.cache.heads * head();
     }
     // Place `i` of the sequence's part of the list.
     __device__ __forceinline__ void seek(int64_t i) {
-        const int64_t u = i / (tiles + kUnitCost);
-        at = static_cast<int>(i - u * (tiles + kUnitCost));
-        h = static_cast<int>(u / groups);
-        rg = static_cast<int>(u - static_cast<int64_t>(h) * groups);
+        h = static_cast<int>(i / head());
+        i -= h * head();
+        rg = min(static_cast<int>(i / unit(0)), groups - 1);
+        at = static_cast<int>(i - rg * unit(0));
     }
     __device__ __forceinline__ void next_unit(const TreeAttention &a) {
         at = 0;
@@ -270,17 +287,21 @@ struct Cursor {
         do request(a, b + 1);  // (there is one: places are left)
         while (tiles == 0);
     }
+    // The first tile that begins at place i of the unit or behind it.
+    __device__ __forceinline__ int tile_at(int i) const {
+        return (max(i - S::kUnitCost, 0) + cost(rg) - 1) / cost(rg);
+    }
     // The next tiles [t, t1) of one unit; false at the end.
     __device__ __forceinline__ bool take(const TreeAttention &a) {
         while (left > 0) {
-            const int end = tiles + kUnitCost;
+            const int end = static_cast<int>(unit(rg));
             if (at == end) {
                 next_unit(a);
                 continue;
             }
             const int to = static_cast<int>(min(static_cast<int64_t>(end), at + left));
-            t = max(at - kUnitCost, 0);
-            t1 = max(to - kUnitCost, 0);
+            t = tile_at(at);
+            t1 = tile_at(to);
             left -= to - at;
             at = to;
             if (t1 > t) return true;
@@ -343,7 +364,8 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
         }
         list.total += scan_sum<S, kWarps>(mine, s_warp, before);
     }
-    const int64_t most = (list.total + kMinPlaces - 1) / kMinPlaces;
+    // (a tile begins in every piece that lies within a unit's tiles: the join counts on it)
+    const int64_t most = list.total / (S::kM == 1 ? S::kOneCost : S::kTwoCost);
     list.pieces = static_cast<int>(most < ctas ? (most < 1 ? 1 : most) : ctas);
     if (tid == 0) s_place[0] = -1;
     __syncthreads();
@@ -461,8 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     const uint32_t base = smem_addr(smem);
 
     if (warp == kSoftWarps + kCopyWarps) tmem_alloc(&sm.tmem, 512);
+    if (tid == 32 && args.box > 0) {
+        prefetch_tmap(&args.map_k);
+        prefetch_tmap(&args.map_v);
+    }
     if (tid == 0) {
-        mbar_init(&sm.qfull, kSoftWarps);
+        mbar_init(&sm.qfull, kFp8 ? kSoftWarps : 64);
         for (int i = 0; i < S::kNK; ++i) {
             // two warps' threads when they have widened their rows; else their copies, and a
             // thread of each for what it has said beside them
@@ -510,109 +536,87 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t step = 0, tiles_done = 0, units = 0;
-        // Row `lrow` of m tile t of a unit.
-        struct Row {
-            bool some, real;  // this warp has rows there; this lane's is one
-            int64_t row;
-            int qh;
-        };
-        auto row_of = [&](const Cursor<S> &u, int t) {
-            const int rr = u.rg * S::kRows + t * 128 + lrow;
-            uint32_t node, g;
-            args.group.divmod(rr, node, g);
-            return Row{rr - lane < u.rows, rr < u.rows, u.first + node, u.h * a.group + static_cast<int>(g)};
-        };
-        // A unit's queries to shared memory, this lane's half of its rows; c: what turns a row's
-        // products into scores, above 0 (queries of a negative scale change their sign).
-        auto queries = [&](const Cursor<S> &u, float (&c)[kM]) {
+        // Queries for an 8-bit cache, as fp16: a unit's, this lane's half of its rows, scaled by a
+        // power of two that puts a row's largest value below 2^15; exps: those powers.
+        int exps[kM], exps_next[kM];
+        auto queries = [&](const Cursor<S> &u, int (&exps)[kM]) {
             constexpr int kPieces = kD / 16;  // 16-byte pieces of half a row
-            const float ks = a.cache.k_scale != nullptr ? a.cache.k_scale[u.h] : 1.f;
-            const float cs = a.scale * kLog2e * ks;
 #pragma unroll
             for (int t = 0; t < kM; ++t) {
-                const Row r = row_of(u, t);
-                c[t] = fabsf(cs);
-                if (!r.some) continue;
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (r.real ? r.row * a.q_row_stride + r.qh * kD : 0) +
-                                                                   wg * (kD / 2));
-                auto place = [&](int i) {  // of piece i
-                    const int ch = wg * kPieces + i;
-                    return smem + t * (128 * kD * 2) + (ch >> 3) * (128 * 128) + lrow * 128 +
-                           (((ch & 7) ^ (lrow & 7)) << 4);
-                };
-                if constexpr (!kFp8) {
-                    const uint32_t sign = cs < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-                    for (int i0 = 0; i0 < kPieces; i0 += 8) {
-                        uint4 x[8];
-#pragma unroll
-                        for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
-                            if (r.real) x[i] = src[i0 + i];
-#pragma unroll
-                        for (int i = 0; i < 8 && i0 + i < kPieces; ++i)
-                            if (r.real)
-                                *reinterpret_cast<uint4 *>(place(i0 + i)) =
-                                    make_uint4(x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign, x[i].w ^ sign);
+                const int rr = u.rg * S::kRows + t * 128 + lrow;
+                exps[t] = 0;
+                if (rr - lane >= u.rows) continue;
+                const bool real = rr < u.rows;
+                uint32_t node, head;
+                args.group.divmod(rr, node, head);
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (real ? (u.first + node) * a.q_row_stride + (u.h * a.group + static_cast<int>(head)) * kD : 0) +
+                    wg * (kD / 2));
+                uint32_t top = 0;
+                if (real)
+#pragma unroll 4
+                    for (int i = 0; i < kPieces; ++i) {
+                        const uint4 x = src[i];
+                        for (const uint32_t y : {x.x, x.y, x.z, x.w})
+                            top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
                     }
-                } else {
-                    // scaled by a power of two that puts the row's largest value below 2^15
-                    uint32_t top = 0;
-                    if (r.real)
-                        for (int i = 0; i < kPieces; ++i) {
-                            const uint4 x = src[i];
-                            for (const uint32_t y : {x.x, x.y, x.z, x.w})
-                                top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
-                        }
-                    sm.top[wg][lrow] = __uint_as_float(top);
-                    pair_barrier(quarter);
-                    top = max(top, __float_as_uint(sm.top[wg ^ 1][lrow]));
-                    pair_barrier(quarter);
-                    // its exponent, taken back in two factors: neither leaves fp32's range
-                    const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127 - 14;
-                    const float up0 = exp2f(static_cast<float>(-e / 2)) * (cs < 0.f ? -1.f : 1.f);
-                    const float up1 = exp2f(static_cast<float>(-e - -e / 2));
-                    c[t] = c[t] * exp2f(static_cast<float>(e / 2)) * exp2f(static_cast<float>(e - e / 2));
-                    if (r.real)
-                        for (int i = 0; i < kPieces; ++i) {
-                            uint4 x = src[i];
-                            uint32_t *y = reinterpret_cast<uint32_t *>(&x);
+                sm.top[wg][lrow] = __uint_as_float(top);
+                pair_barrier(quarter);
+                top = max(top, __float_as_uint(sm.top[wg ^ 1][lrow]));
+                pair_barrier(quarter);
+                exps[t] = min(max(static_cast<int>(top >> 23), 15), 254) - 127 - 14;
+                const float up = power_of_two(-exps[t]);
+                if (real)
+#pragma unroll 4
+                    for (int i = 0; i < kPieces; ++i) {
+                        uint4 x = src[i];
+                        uint32_t *y = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = unpack2<false>(y[k]);
-                                y[k] = pack2<true>(f.x * up0 * up1, f.y * up0 * up1);
-                            }
-                            *reinterpret_cast<uint4 *>(place(i)) = x;
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack2<false>(y[k]);
+                            y[k] = pack2<true>(f.x * up, f.y * up);
                         }
-                }
-                c[t] = at_least_normal(c[t]);
+                        const int ch = wg * kPieces + i;
+                        *reinterpret_cast<uint4 *>(smem + t * (128 * kD * 2) + (ch >> 3) * (128 * 128) + lrow * 128 +
+                                                   (((ch & 7) ^ (lrow & 7)) << 4)) = x;
+                    }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.qfull);
         };
-        float c[kM], c_next[kM];
         bool more = at.take(a);
-        if (more) queries(at, c);
+        if (kFp8 && more) queries(at, exps);
         while (more && wait.ok) {
-            const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+            const int m_used = at.m_tiles(at.rg);
             const int tiles = at.t1 - at.t, steps = tiles * m_used;
             // This warpgroup has every second step: of two m tiles always the same one, of one
             // every second tile.
             const int i0 = (step + wg) & 1, mt = m_used == 1 ? 0 : i0;
-            const Row r = row_of(at, mt);
-            const uint64_t word = r.real ? a.ancestors[r.row] & bits_below(at.n) : 0;
-            const float cr = kM == 1 || mt == 0 ? c[0] : c[kM - 1];
+            const int rr = at.rg * S::kRows + mt * 128 + lrow;  // this lane's row
+            const bool some = rr - lane < at.rows, real = rr < at.rows;
+            uint32_t node, head;
+            args.group.divmod(rr, node, head);
+            const int64_t row = at.first + node;
+            const int qh = at.h * a.group + static_cast<int>(head);
+            const uint64_t word = real ? a.ancestors[row] & bits_below(at.n) : 0;
+            // what turns the row's products into scores: above 0 (the queries of a negative scale
+            // are negated by the product)
+            float c = at_least_normal(fabsf(a.scale * kLog2e * (a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f)));
+            if constexpr (kFp8) c = at_least_normal(c * power_of_two(mt == 0 ? exps[0] : exps[kM - 1]));
             float m = -INFINITY, l = 0.f;
+            Cursor<S> next = at;
+            more = next.take(a);
 
             for (int i = i0; i < steps && wait.ok; i += 2) {
                 const int tile = m_used == 1 ? i : i >> 1;
                 const uint32_t g = step + i, buf = g % S::kBufs;
                 if (!wait(&sm.sfull[buf], (g / S::kBufs) & 1)) break;
-                if (r.some) {
+                if (some) {
                     tc_fence_after();
                     const uint32_t cols = lanes + buf * kKeys;
                     // the keys that the row sees, where that is not all of them
-                    const uint32_t *v = sm.valid[(tiles_done + tile) & 15];
+                    const uint32_t *v = sm.valid[(tiles_done + tile) % S::kTilesAhead];
                     const int d = (at.t + tile) * kKeys - (at.len - at.n);
                     bool all = true;
 #pragma unroll
@@ -645,11 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             top1 = fmaxf(fmaxf(top1, s1[x]), s1[x + 1]);
                         }
                     }
-                    top = fmaxf(top, top1) * cr;
+                    top = fmaxf(top, top1) * c;
                     // one m tile: the reference is the other warpgroup's of the step before
                     if (m_used == 1 && i > 0) {
                         pair_wait(quarter, wg);
-                        const float other = sm.ref[lrow];
+                        const float other = sm.top[0][lrow];
                         if (other > m) {
                             if (i > 1) l *= ex2(m - other);
                             m = other;
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     const float to = grown ? top : m;
                     const float ref = to == -INFINITY ? 0.f : to;
                     if (m_used == 1 && i + 1 < steps) {
-                        sm.ref[lrow] = to;
+                        sm.top[0][lrow] = to;
                         pair_arrive(quarter, wg);
                     }
                     if (!first && __any_sync(0xffffffffu, grown)) {
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         }
                     }
                     m = to;
-                    const uint64_t c2 = f2(cr, cr), off2 = f2(S::kShift - ref, S::kShift - ref);
+                    const uint64_t c2 = f2(c, c), off2 = f2(S::kShift - ref, S::kShift - ref);
                     uint64_t sum2 = 0;
 #pragma unroll 1
                     for (int k = 0; k < kKeys / 32; ++k) {
@@ -726,15 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     __syncwarp();
                 }
             }
-            // (a warpgroup's last step may not be the unit's)
-            if (!wait(&sm.scored, units & 1)) break;
             step += steps;
             tiles_done += tiles;
-            // the next unit's queries, while this one's last products run: its scores are all
-            // there, so nothing reads these any more
-            Cursor<S> next = at;
-            more = next.take(a);
-            if (more) queries(next, c_next);
+            if constexpr (kFp8) {
+                // while this unit's last products run: its scores are all there, so nothing reads
+                // its queries any more
+                if (!wait(&sm.scored, units & 1)) break;
+                if (more) queries(next, exps_next);
+            }
 
             // outputs: a whole unit's to o, a cut one's to the workspace.  Of two m tiles a
             // warpgroup has its own, of one half the channels.
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             const bool whole = at.t == 0 && at.t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
-            if (r.some) {
+            if (some) {
                 tc_fence_after();
                 if (m_used == 1) {  // the two warpgroups' sums, by the later reference
                     sm.top[wg][lrow] = m;
@@ -759,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 const int d0 = m_used == 1 ? wg * (kD / 2) : 0, d1 = m_used == 1 ? d0 + kD / 2 : kD;
                 const float f = l == 0.f ? 0.f : 1.f / l;
                 float nan = 0.f;
-                const int64_t out = r.row * a.q_heads + r.qh;
+                const int64_t out = row * a.q_heads + qh;
 #pragma unroll 1
                 for (int d = d0; d < d1; d += 32) {
                     float o[32];
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             nan = fmaf(o[k], 0.f, fmaf(o[k + 1], 0.f, nan));
                             y[k / 2] = l == 0.f ? 0u : pack2<false>(o[k] * f * vs, o[k + 1] * f * vs);
                         }
-                        if (r.real)
+                        if (real)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 reinterpret_cast<uint4 *>(a.o + out * kD + d)[k] =
@@ -787,15 +790,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 tc_fence_before();
                 if (whole) {
-                    if (r.real && d0 == 0 && a.lse != nullptr)
+                    if (real && d0 == 0 && a.lse != nullptr)
                         a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - S::kShift) * kLn2;
                     // what is not finite although the weights are
-                    uint32_t again = __ballot_sync(0xffffffffu, r.real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
+                    uint32_t again = __ballot_sync(0xffffffffu, real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
                     while (again != 0) {
                         const int src = __ffs(static_cast<int>(again)) - 1;
                         again &= again - 1;
-                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, r.row, src),
-                                            __shfl_sync(0xffffffffu, r.qh, src), at.n, at.len, d0, d1);
+                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, row, src),
+                                            __shfl_sync(0xffffffffu, qh, src), at.n, at.len, d0, d1);
                         __syncwarp();
                     }
                 } else if (d0 == 0) {
@@ -805,8 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.ofree);
             at = next;
+            if constexpr (kFp8)
 #pragma unroll
-            for (int t = 0; t < kM; ++t) c[t] = c_next[t];
+                for (int t = 0; t < kM; ++t) exps[t] = exps_next[t];
         }
     } else if (warp < kSoftWarps + kCopyWarps) {
         // ---- keys and values in --------------------------------------------------------------
@@ -901,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                                 : -1;
                     const uint32_t valid = __ballot_sync(0xffffffffu, ok);
                     whole &= valid == 0xffffffffu;
-                    if (!is_v && lane == 0) sm.valid[made & 15][half * kLaneRows + i] = valid;
+                    if (!is_v && lane == 0) sm.valid[made % S::kTilesAhead][half * kLaneRows + i] = valid;
                     const int p = __shfl_sync(0xffffffffu, page[i], mine & 31);
                     const int q = __shfl_sync(0xffffffffu, static_cast<int>(in_page[i]), mine & 31);
                     if (i == mine >> 5) {
@@ -982,10 +986,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         constexpr uint32_t kFmt = kFp8 ? kFmtF16 : kFmtBF16;
         Waits wait = {a.err, true};
         if (warp == kSoftWarps + kCopyWarps) {
-            constexpr uint32_t kId = instr_desc(128, kKeys, kFmt, 0, 0);
             uint32_t step = 0, made = 0, units = 0;
             while (at.take(a) && wait.ok) {
-                const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+                const bool negate = a.scale * (a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f) < 0.f;
+                const uint32_t id = negate ? instr_desc(128, kKeys, kFmt, 0, 0, 1) : instr_desc(128, kKeys, kFmt, 0, 0);
+                const int m_used = at.m_tiles(at.rg);
                 wait(&sm.qfull, units & 1);
                 for (int tile = at.t; tile < at.t1 && wait.ok; ++tile, ++made) {
                     const uint32_t ks = made % S::kNK;
@@ -1005,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 mma_f16_ss_w(d, qd + (k * (128 * 128) + j * 32) / 16,
-                                             kd + (k * (kKeys * 128) + j * 32) / 16, kId, k + j > 0);
+                                             kd + (k * (kKeys * 128) + j * 32) / 16, id, k + j > 0);
                         mma_commit_w(&sm.sfull[buf]);
                     }
                     mma_commit_w(&sm.kempty[ks]);
@@ -1017,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             constexpr uint32_t kId = instr_desc(128, kD, kFmt, 0, 1);
             uint32_t step = 0, made = 0, units = 0;
             while (at.take(a) && wait.ok) {
-                const int m_used = at.rows - at.rg * S::kRows > 128 ? kM : 1;
+                const int m_used = at.m_tiles(at.rg);
                 // the last unit's outputs have been read
                 if (!wait(&sm.ofree, (units & 1) ^ 1)) break;
                 ++units;
@@ -1047,6 +1052,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 mma_commit_w(&sm.done);
             }
+        } else if (!kFp8) {
+            // Queries in, by two warps: a unit's when the last one's scores are all there; their
+            // rows are called into L2 before.
+            const int qw = warp - kSoftWarps - kCopyWarps - 2;
+            constexpr int kLanes = kD / 8, kAtOnce = 32 / kLanes;  // lanes to a row, rows of a warp
+            const int sub = lane / kLanes, ch = lane % kLanes;     // ch: 16-byte piece
+            uint32_t units = 0;
+            while (at.take(a) && wait.ok) {
+                const int row0 = at.rg * S::kRows, rows = min(at.rows - row0, S::kRows);
+                auto source = [&](int r) {  // this lane's piece of row r
+                    uint32_t node, head;
+                    args.group.divmod(row0 + r, node, head);
+                    return reinterpret_cast<const uint4 *>(a.q + (at.first + node) * a.q_row_stride +
+                                                           (at.h * a.group + static_cast<int>(head)) * kD) + ch;
+                };
+                auto place = [&](int r) {
+                    return (r >> 7) * (128 * kD * 2) + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                };
+                if (ch % 8 == 0)
+                    for (int r = qw * kAtOnce + sub; r < rows; r += 2 * kAtOnce)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(source(r)));
+                if (units > 0 && !wait(&sm.scored, (units - 1) & 1)) break;
+#pragma unroll 4
+                for (int r = qw * kAtOnce + sub; r < rows; r += 2 * kAtOnce)
+                    copy16(base + place(r), reinterpret_cast<const uint8_t *>(source(r)), true);
+                copies_arrive(&sm.qfull);
+                ++units;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         if (warp <= kSoftWarps + kCopyWarps + 1) {
             // nothing is in flight when tensor memory is given back
@@ -1081,9 +1115,11 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
     if (s_place[0] >= 0) {
         cut.request(a, static_cast<int>(s_place[0]));
         cut.seek(s_place[1]);
-        // the places of the unit's first tile and of its last
-        const int64_t first = list.begin(c0 + int64_t{1}) - cut.at + kUnitCost, last = first + cut.tiles - 1;
-        if (cut.at > kUnitCost && first >= list.begin(c0)) parts = list.piece_of(last) - c0 + 1;
+        // the places where the unit's first and last tiles begin
+        const int64_t first = list.begin(c0 + int64_t{1}) - cut.at + S::kUnitCost,
+                      last = first + static_cast<int64_t>(cut.tiles - 1) * cut.cost(cut.rg);
+        const int done = cut.tile_at(cut.at);  // tiles that begin before the next piece
+        if (done > 0 && done < cut.tiles && first >= list.begin(c0)) parts = list.piece_of(last) - c0 + 1;
     }
     wait_for_kernel_before();
     const int r = cut.rg * S::kRows + tid;
