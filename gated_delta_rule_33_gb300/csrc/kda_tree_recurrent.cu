@@ -12,6 +12,16 @@
 // and after the path of node e the state is Diag(E_e) S_0 + sum_{j in path(e)} (E_ej k_j) u_j^T.
 // E_ij is formed by products along the path, from node i upwards: no decay is divided out, so
 // none is too strong.
+//
+// Decode.  Bound: the state is read once (64 KB of fp32 a head, 32 KB of bf16) and meets 2 n
+// vectors, 4 n 128^2 flops: HBM up to some 16 nodes, then the fp32 pipe (all sums are fp32 on
+// CUDA cores: a product on the tensor cores' 10-bit words would take three for each and the
+// update's result becomes state).  One block a (request, head), two blocks an SM, so that one's
+// state arrives while the other computes: the state comes by one bulk copy; meanwhile a warp a
+// node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i; then the
+// 2 n x 128 by 128 x 128 product, 16 rows x 4 columns a thread, split over k where there are
+// fewer rows than warps; then each thread solves its column of the updates, 8 nodes in
+// registers, and the outputs follow.
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
@@ -21,12 +31,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
-template <bool kBf16>
-__device__ __forceinline__ float state_at(const void *pool, int64_t i) {
-    if constexpr (kBf16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(pool)[i]);
-    else return static_cast<const float *>(pool)[i];
-}
+constexpr uint32_t kMaxPolls = 1u << 20;
 
 template <bool kBf16>
 __device__ __forceinline__ void write_out(void *o, int64_t i, float x) {
@@ -42,21 +47,72 @@ __device__ __forceinline__ int64_t slot_of(const TreeStep &a, int b) {
     return s < 0 || s >= a.num_slots ? -1 : s;
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
+__device__ __forceinline__ float4 widen4(uint2 x) {
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
 }
 
-// One block a (request, head).
+// ---- decode --------------------------------------------------------------------------------
+
+// Shared memory: nodes in eights (kc of them, nc nodes).
+struct TreeSmem {
+    int nc;
+    float *parts;     // the state, then the products' parts: [k groups][eights][16][128], 64 KB
+    float *rows;      // [eights][k 128][16]: E_i k_i of eight nodes, E_i scale q_i of the same; by
+                      // fours of a row, exchanged by k (see row_at)
+    float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
+    float *decay;     // [n][128] a_i; then u_i
+    float *beta;
+    __nv_bfloat16 *k, *v;  // [n][128]
+    uint64_t *bar;
+
+    __host__ __device__ static int nodes(int max_nodes) { return (max_nodes + 7) / 8 * 8; }
+    __host__ __device__ static int bytes(int nc) {
+        return 64 * 1024 + nc / 8 * (kD * 16 * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2 + 2) + nc * 4 + 16;
+    }
+    __device__ TreeSmem(uint8_t *base, int max_nodes) {
+        nc = nodes(max_nodes);
+        parts = reinterpret_cast<float *>(base);
+        rows = parts + 16 * 1024;
+        ak = rows + nc / 8 * (kD * 16);
+        aq = ak + nc * nc;
+        decay = aq + nc * nc;
+        k = reinterpret_cast<__nv_bfloat16 *>(decay + nc * kD);
+        v = k + nc * kD;
+        beta = reinterpret_cast<float *>(v + nc * kD);
+        bar = reinterpret_cast<uint64_t *>(beta + nc);
+    }
+};
+
+// Place of row r (0 .. 15) at k in an eight's rows: fours of rows exchanged, so that neighbouring
+// k's rows lie in different banks.
+__device__ __forceinline__ int row_at(int k, int r) { return k * 16 + ((((r >> 2) ^ (k >> 1)) & 3) << 2) + (r & 3); }
+
+// Eight values of each lane summed over the warp: lane l returns the sum of value (l >> 2) & 7.
+__device__ __forceinline__ float sum_eight(float (&x)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int step = 4, bit = 16; step >= 1; step >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < step; ++i) {
+            const float send = up ? x[i] : x[i + step], keep = up ? x[i + step] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
+    }
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+    return x[0];
+}
+
 template <bool kStateBf16, bool kOutBf16>
-__global__ void __launch_bounds__(kThreads) tree_decode_kernel(const TreeStep a) {
-    extern __shared__ float smem[];
+__global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep a) {
+    extern __shared__ __align__(128) uint8_t smem[];
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
-    if (t.bad && tid == 0) record_device_error(a.err, kDevInvalidArg);
     const int64_t slot = slot_of(a, b);
+    if (t.bad && tid == 0) record_device_error(a.err, kDevInvalidArg);
     const int n = t.n;
     if (n == 0 || slot < 0) {
         for (int64_t i = tid; i < static_cast<int64_t>(t.rows) * kD; i += kThreads) {
@@ -66,142 +122,293 @@ __global__ void __launch_bounds__(kThreads) tree_decode_kernel(const TreeStep a)
         }
         return;
     }
-    float *s_kb = smem;                      // [n][128] E_i k_i
-    float *s_qb = s_kb + a.max_nodes * kD;   // [n][128] scale E_i q_i
-    float *s_u = s_qb + a.max_nodes * kD;    // [n][128]
-    float *s_ak = s_u + a.max_nodes * kD;    // [n][n] (E_ij k_j) . k_i
-    float *s_aq = s_ak + a.max_nodes * a.max_nodes;
+    const TreeSmem s(smem, a.max_nodes);
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
+    constexpr uint32_t kBytes = kD * kD * (kStateBf16 ? 2 : 4);
+    if (tid == 0) {
+        sm100::mbar_init(s.bar, 1);
+        sm100::fence_mbar_init();
+        sm100::mbar_arrive_expect_tx(s.bar, kBytes);
+        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * kBytes;
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         sm100::smem_addr(s.parts)),
+                     "l"(src), "r"(kBytes), "r"(sm100::smem_addr(s.bar))
+                     : "memory");
+    }
+    // the nodes' vectors: 16 bytes a thread
+    for (int i = tid; i < n * 16; i += kThreads) {
+        const int64_t src = at(i >> 4) + (i & 15) * 8;
+        sm100::cp_async_16(s.k + i * 8, a.k + src, true);
+        sm100::cp_async_16(s.v + i * 8, a.v + src, true);
+    }
+    for (int i = tid; i < n * 32; i += kThreads) {
+        float4 g = *reinterpret_cast<const float4 *>(a.g + at(i >> 5) + (i & 31) * 4);
+        g = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+        reinterpret_cast<float4 *>(s.decay)[i] = g;
+    }
+    for (int i = tid; i < n * s.nc / 4; i += kThreads)
+        reinterpret_cast<float4 *>(s.ak)[i] = reinterpret_cast<float4 *>(s.aq)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < n) s.beta[tid] = a.beta[(t.first + tid) * a.H + h];
+    sm100::cp_async_wait_all();
+    __syncthreads();
 
-    for (int i = warp; i < n; i += kWarps) {
+    // A warp a node: four channels a lane, four nodes of the path at a time.
+    const int eights = (n + 7) / 8;
+    for (int i = warp; i < 8 * eights; i += kWarps) {
+        float *rows = s.rows + (i >> 3) * (kD * 16);
+        if (i >= n) {  // rows of the last eight that are no node
+#pragma unroll
+            for (int c = 0; c < 4; ++c) rows[row_at(4 * lane + c, i & 7)] = rows[row_at(4 * lane + c, 8 + (i & 7))] = 0.f;
+            continue;
+        }
         uint64_t path = path_of(a.ancestors[t.first + i], i);
-        float e[4] = {1.f, 1.f, 1.f, 1.f}, k[4], q[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            k[c] = __bfloat162float(a.k[at(i) + lane + 32 * c]);
-            q[c] = a.scale * __bfloat162float(a.q[at(i) + lane + 32 * c]);
-        }
+        float4 e = make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 k = widen4(*reinterpret_cast<const uint2 *>(s.k + i * kD + 4 * lane));
+        float4 q = widen4(*reinterpret_cast<const uint2 *>(a.q + at(i) + 4 * lane));
+        q = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
         while (path != 0) {
-            const int j = top_bit(path);
-            path ^= uint64_t{1} << j;
-            float dk = 0.f, dq = 0.f;
+            float x[8];
+            int js[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float x = e[c] * __bfloat162float(a.k[at(j) + lane + 32 * c]);
-                dk += x * k[c];
-                dq += x * q[c];
-                e[c] *= expf(a.g[at(j) + lane + 32 * c]);
+            for (int m = 0; m < 4; ++m) {
+                const bool some = path != 0;
+                const int j = some ? top_bit(path) : 0;
+                js[m] = some ? j : -1;
+                if (some) path ^= uint64_t{1} << j;
+                const float4 kj = widen4(*reinterpret_cast<const uint2 *>(s.k + j * kD + 4 * lane));
+                const float4 d = *reinterpret_cast<const float4 *>(s.decay + j * kD + 4 * lane);
+                const float4 y = make_float4(e.x * kj.x, e.y * kj.y, e.z * kj.z, e.w * kj.w);
+                x[2 * m] = y.x * k.x + y.y * k.y + (y.z * k.z + y.w * k.w);
+                x[2 * m + 1] = y.x * q.x + y.y * q.y + (y.z * q.z + y.w * q.w);
+                if (some) e = make_float4(e.x * d.x, e.y * d.y, e.z * d.z, e.w * d.w);
             }
-            dk = warp_sum(dk);
-            dq = warp_sum(dq);
-            if (lane == 0) {
-                s_ak[i * a.max_nodes + j] = dk;
-                s_aq[i * a.max_nodes + j] = dq;
+            const float sum = sum_eight(x);
+            const int m = lane >> 3, j = m == 0 ? js[0] : m == 1 ? js[1] : m == 2 ? js[2] : js[3];
+            if ((lane & 3) == 0 && j >= 0) {
+                if (lane & 4) s.aq[j * s.nc + i] = sum;
+                else if (j != i) s.ak[j * s.nc + i] = sum;
             }
         }
+        const float ke[4] = {e.x * k.x, e.y * k.y, e.z * k.z, e.w * k.w};
+        const float qe[4] = {e.x * q.x, e.y * q.y, e.z * q.z, e.w * q.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            s_kb[i * kD + lane + 32 * c] = e[c] * k[c];
-            s_qb[i * kD + lane + 32 * c] = e[c] * q[c];
+            rows[row_at(4 * lane + c, i & 7)] = ke[c];
+            rows[row_at(4 * lane + c, 8 + (i & 7))] = qe[c];
+        }
+    }
+    // (every thread sees the copy's bytes through the barrier)
+    const bool ok = sm100::mbar_wait_bounded(s.bar, 0, kMaxPolls);
+    if (!ok) record_device_error(a.err, kDevTimeout);
+    if (__syncthreads_or(!ok)) return;
+
+    // The product: a warp has the 16 rows of an eight, the lanes 4 columns each, for a part of k.
+    const int groups = eights <= 4 ? (eights == 3 ? 2 : 8 / eights) : 1;
+    const int eight = warp % eights, group = warp / eights;
+    float acc[16][4];
+    if (group < groups) {
+        const int k0 = group * (kD / groups), k1 = k0 + kD / groups;
+        const float *rows = s.rows + eight * (kD * 16);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.f;
+#pragma unroll 2
+        for (int k = k0; k < k1; ++k) {
+            float4 x;
+            if constexpr (kStateBf16) x = widen4(reinterpret_cast<const uint2 *>(s.parts)[k * 32 + lane]);
+            else x = reinterpret_cast<const float4 *>(s.parts)[k * 32 + lane];
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(rows + row_at(k, r));
+                const float w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    acc[r + m][0] += w[m] * x.x;
+                    acc[r + m][1] += w[m] * x.y;
+                    acc[r + m][2] += w[m] * x.z;
+                    acc[r + m][3] += w[m] * x.w;
+                }
+            }
         }
     }
     __syncthreads();
-    // threads 0 .. 127 the k products and the updates, the others the q products
+    if (group < groups) {
+        float4 *to = reinterpret_cast<float4 *>(s.parts) + (group * eights + eight) * (16 * 32) + lane;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) to[r * 32] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    }
+    __syncthreads();
+    auto product = [&](int m, int r, int c) {  // row r of eight m, column c
+        float x = 0.f;
+        for (int g = 0; g < groups; ++g) x += s.parts[((g * eights + m) * 16 + r) * kD + c];
+        return x;
+    };
+
+    // The updates: a thread a column, eight nodes in registers.
     const int c = tid & (kD - 1);
-    const bool is_q = tid >= kD;
-    const int64_t S = (slot * a.H + h) * (kD * kD) + c;
-    for (int i = 0; i < n; ++i) {
-        const float *row = (is_q ? s_qb : s_kb) + i * kD;
-        float acc = 0.f;
-        for (int r = 0; r < kD; ++r) acc += row[r] * state_at<kStateBf16>(a.pool, S + r * kD);
-        uint64_t path = a.ancestors[t.first + i] & bits_below(i);
-        while (path != 0) {
-            const int j = top_bit(path);
-            path ^= uint64_t{1} << j;
-            acc += (is_q ? s_aq : s_ak)[i * a.max_nodes + j] * s_u[j * kD + c];
+    if (tid < kD) {
+        for (int m = 0; m < eights; ++m) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = product(m, i, c);
+            for (int j = 0; j < 8 * m; ++j) {
+                const float u = s.decay[j * kD + c];
+                const float4 x = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m);
+                const float4 y = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m + 4);
+                w[0] += x.x * u;
+                w[1] += x.y * u;
+                w[2] += x.z * u;
+                w[3] += x.w * u;
+                w[4] += y.x * u;
+                w[5] += y.y * u;
+                w[6] += y.z * u;
+                w[7] += y.w * u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int node = 8 * m + i;
+                if (node >= n) break;
+                const float u = s.beta[node] * (__bfloat162float(s.v[node * kD + c]) - w[i]);
+                s.decay[node * kD + c] = u;
+                if (a.u != nullptr) a.u[at(node) + c] = u;
+#pragma unroll
+                for (int l = i + 1; l < 8; ++l) w[l] += s.ak[node * s.nc + 8 * m + l] * u;
+            }
         }
-        if (!is_q) {
-            const float u = a.beta[(t.first + i) * a.H + h] * (__bfloat162float(a.v[at(i) + c]) - acc);
-            s_u[i * kD + c] = u;
-            if (a.u != nullptr) a.u[at(i) + c] = u;
+    }
+    __syncthreads();
+    // The outputs: half of an eight's nodes for each half of the threads.
+    const int half = tid / kD;
+    for (int m = 0; m < eights; ++m) {
+        float w[4];
+        const int i0 = 8 * m + 4 * half;
+        if (i0 >= n) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = product(m, 8 + 4 * half + i, c);
+        const int end = min(i0 + 4, n);
+        for (int j = 0; j < end; ++j) {
+            const float u = s.decay[j * kD + c];
+            const float4 x = *reinterpret_cast<const float4 *>(s.aq + j * s.nc + i0);
+            w[0] += x.x * u;
+            w[1] += x.y * u;
+            w[2] += x.z * u;
+            w[3] += x.w * u;
         }
-        __syncthreads();
-        if (is_q)
-            write_out<kOutBf16>(a.o, at(i) + c, acc + s_aq[i * a.max_nodes + i] * s_u[i * kD + c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < n) write_out<kOutBf16>(a.o, at(i0 + i) + c, w[i]);
     }
 }
 
-// One block a (request, head): warp w owns rows w, w + 8, .. of the state, lane l the columns
-// 4 l .. 4 l + 3, so a warp moves whole 512-byte rows.
+// ---- commit --------------------------------------------------------------------------------
+
+// One block a (request, head); the state stays in registers between its read and its write: warp
+// w owns rows w, w + 8, .., lane l the columns 4 l .. 4 l + 3, so a warp moves whole rows.  The
+// path's nodes act sixteen at a time: S <- Diag(E) S + sum_j (E_j k_j) u_j^T, E and E_j the decays
+// of the sixteen, and of those behind j.
+constexpr int kCommitNodes = 16;
+constexpr int kRows = kD / kWarps;
+
 template <bool kStateBf16>
-__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeStep a) {
-    extern __shared__ float smem[];
+__global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep a) {
+    __shared__ __align__(16) float s_w[kCommitNodes][kD], s_u[kCommitNodes][kD];
+    __shared__ float s_decay[kD];
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
     const int end = a.last[b];
-    if ((t.bad || end >= t.n) && tid == 0) record_device_error(a.err, kDevInvalidArg);
     const int64_t slot = slot_of(a, b);
+    if ((t.bad || end >= t.n) && tid == 0) record_device_error(a.err, kDevInvalidArg);
     if (end < 0 || end >= t.n || slot < 0) return;
-    float *s_w = smem;                             // [nodes of the path][128] E_ej k_j
-    float *s_u = smem + a.max_nodes * kD;          // [nodes of the path][128]
-    __shared__ float s_decay[kD];
+    // the whole state in flight first
+    const int64_t base = (slot * a.H + h) * (kD * kD) + warp * kD + 4 * lane;
+    float4 x[kRows];
+    uint2 raw[kStateBf16 ? kRows : 1];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t i = base + r * kWarps * kD;
+        if constexpr (kStateBf16) raw[r] = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.pool) + i));
+        else x[r] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.pool) + i));
+    }
     uint64_t path = path_of(a.ancestors[t.first + end], end);
-    const int m = __popcll(path);
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
-    if (tid < kD) {
-        float e = 1.f;
-        for (int r = 0; r < m; ++r) {
-            const int j = top_bit(path);
-            path ^= uint64_t{1} << j;
-            s_w[r * kD + tid] = e * __bfloat162float(a.k[at(j) + tid]);
-            e *= expf(a.g[at(j) + tid]);
+    bool first = true;
+    while (path != 0) {
+        // the next sixteen nodes from the root, and their last
+        uint64_t some = 0, rest = path;
+        int m = 0;
+        for (; m < kCommitNodes && rest != 0; ++m) {
+            some |= rest & (~rest + 1);
+            rest &= rest - 1;
         }
-        s_decay[tid] = e;
-    } else {
-        for (int r = 0; r < m; ++r) {
-            const int j = top_bit(path);
-            path ^= uint64_t{1} << j;
-            s_u[r * kD + tid - kD] = a.u[at(j) + tid - kD];
+        path = rest;
+        if (!first) __syncthreads();
+        if (tid < kD) {
+            float e = 1.f;
+            int r = 0;
+            for (uint64_t p = some; p != 0; ++r) {
+                const int j = top_bit(p);
+                p ^= uint64_t{1} << j;
+                s_w[r][tid] = e * __bfloat162float(a.k[at(j) + tid]);
+                e *= expf(a.g[at(j) + tid]);
+            }
+            s_decay[tid] = e;
+        } else {
+            int r = 0;
+            for (uint64_t p = some; p != 0; ++r) {
+                const int j = top_bit(p);
+                p ^= uint64_t{1} << j;
+                s_u[r][tid - kD] = a.u[at(j) + tid - kD];
+            }
+        }
+        __syncthreads();
+        if constexpr (kStateBf16)
+            if (first)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) x[r] = widen4(raw[r]);
+        first = false;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float d = s_decay[warp + kWarps * r];
+            x[r] = make_float4(x[r].x * d, x[r].y * d, x[r].z * d, x[r].w * d);
+        }
+        for (int j = 0; j < m; ++j) {
+            const float4 u = *reinterpret_cast<const float4 *>(&s_u[j][4 * lane]);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float w = s_w[j][warp + kWarps * r];
+                x[r].x += w * u.x;
+                x[r].y += w * u.y;
+                x[r].z += w * u.z;
+                x[r].w += w * u.w;
+            }
         }
     }
-    __syncthreads();
-    const int64_t S = (slot * a.H + h) * (kD * kD);
-    for (int r = warp; r < kD; r += kWarps) {
-        const int64_t i = S + r * kD + 4 * lane;
-        float x[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = s_decay[r] * state_at<kStateBf16>(a.pool, i + c);
-        for (int j = 0; j < m; ++j) {
-            const float w = s_w[j * kD + r];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] += w * s_u[j * kD + 4 * lane + c];
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t i = base + r * kWarps * kD;
+        if constexpr (kStateBf16) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[r].x, x[r].y), hi = __floats2bfloat162_rn(x[r].z, x[r].w);
+            __stcs(reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.pool) + i),
+                   make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi)));
+        } else {
+            __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + i), x[r]);
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) write_out<kStateBf16>(a.pool, i + c, x[c]);
     }
 }
-
-int decode_smem(int n) { return (3 * n * kD + 2 * n * n) * 4; }
-int commit_smem(int n) { return 2 * n * kD * 4; }
 
 template <bool kStateBf16, bool kOutBf16>
 cudaError_t decode_t(const TreeStep &a, cudaStream_t s) {
     const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16>;
     const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), decode_smem(kTreeNodes));
+        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem::bytes(kTreeNodes));
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, decode_smem(a.max_nodes), s>>>(a);
+    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, TreeSmem::bytes(TreeSmem::nodes(a.max_nodes)), s>>>(a);
     return cudaGetLastError();
 }
 
 template <bool kStateBf16>
 cudaError_t commit_t(const TreeStep &a, cudaStream_t s) {
-    const auto kernel = &tree_commit_kernel<kStateBf16>;
-    const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), commit_smem(kTreeNodes));
-    if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, commit_smem(a.max_nodes), s>>>(a);
+    tree_commit_kernel<kStateBf16><<<static_cast<unsigned>(a.B * a.H), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
