@@ -14,14 +14,14 @@
 // none is too strong.
 //
 // Decode.  Bound: the state is read once (64 KB of fp32 a head, 32 KB of bf16) and meets 2 n
-// vectors, 4 n 128^2 flops: HBM up to some 16 nodes, then the fp32 pipe (all sums are fp32 on
-// CUDA cores: a product on the tensor cores' 10-bit words would take three for each and the
-// update's result becomes state).  One block a (request, head), two blocks an SM, so that one's
-// state arrives while the other computes: the state comes by one bulk copy; meanwhile a warp a
-// node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i; then the
-// 2 n x 128 by 128 x 128 product, 16 rows x 4 columns a thread, split over k where there are
-// fewer rows than warps; then each thread solves its column of the updates, 8 nodes in
-// registers, and the outputs follow.
+// vectors, 4 n 128^2 flops: HBM.  On the fp32 pipe that product alone takes as long (337 us where
+// the bytes take 82); so it runs on the matrix instructions, every operand as two words of 11
+// bits (tf32) and three products, which keeps 2^-20 of it: u becomes state.  One block a
+// (request, head), two blocks an SM, so that one's state arrives while the other computes.  The
+// state comes by bulk copies, a row each, to rows 8 words apart in the banks; meanwhile a warp a
+// node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp
+// has 16 columns of the product for all rows; then each thread solves its column of the
+// updates, 8 nodes in registers, and the outputs follow.
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
@@ -54,39 +54,57 @@ __device__ __forceinline__ float4 widen4(uint2 x) {
 
 // ---- decode --------------------------------------------------------------------------------
 
-// Shared memory: nodes in eights (kc of them, nc nodes).
+constexpr int kPitch = 136;            // floats of a state's or product's row
+constexpr int kBlock = 132;            // floats of an eight's rows at 8 k's (see TreeSmem)
+constexpr int kEight = 16 * kBlock;    // and at all
+
+// Shared memory: nodes in eights, as many as nc nodes fill.
 struct TreeSmem {
     int nc;
-    float *parts;     // the state, then the products' parts: [k groups][eights][16][128], 64 KB
-    float *rows;      // [eights][k 128][16]: E_i k_i of eight nodes, E_i scale q_i of the same; by
-                      // fours of a row, exchanged by k (see row_at)
+    float *state;     // [k 128][kPitch]; then the products [eight][16][kPitch]: of its nodes' E_i k_i
+                      // with the state, then of their E_i scale q_i
+    float *rows;      // [eight][k / 8][kBlock]: those vectors as left operands of 16 rows x 8 k's:
+                      // lane (g, t) has (k_g, q_g) at k = t, then at k = t + 4
     float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
     float *decay;     // [n][128] a_i; then u_i
     float *beta;
-    __nv_bfloat16 *k, *v;  // [n][128]
+    __nv_bfloat16 *k; // [n][128]; then v_i
     uint64_t *bar;
 
     __host__ __device__ static int nodes(int max_nodes) { return (max_nodes + 7) / 8 * 8; }
     __host__ __device__ static int bytes(int nc) {
-        return 64 * 1024 + nc / 8 * (kD * 16 * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2 + 2) + nc * 4 + 16;
+        return kD * kPitch * 4 + nc / 8 * (kEight * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4 + 16;
     }
     __device__ TreeSmem(uint8_t *base, int max_nodes) {
         nc = nodes(max_nodes);
-        parts = reinterpret_cast<float *>(base);
-        rows = parts + 16 * 1024;
-        ak = rows + nc / 8 * (kD * 16);
+        state = reinterpret_cast<float *>(base);
+        rows = state + kD * kPitch;
+        ak = rows + nc / 8 * kEight;
         aq = ak + nc * nc;
         decay = aq + nc * nc;
         k = reinterpret_cast<__nv_bfloat16 *>(decay + nc * kD);
-        v = k + nc * kD;
-        beta = reinterpret_cast<float *>(v + nc * kD);
+        beta = reinterpret_cast<float *>(k + nc * kD);
         bar = reinterpret_cast<uint64_t *>(beta + nc);
     }
 };
 
-// Place of row r (0 .. 15) at k in an eight's rows: fours of rows exchanged, so that neighbouring
-// k's rows lie in different banks.
-__device__ __forceinline__ int row_at(int k, int r) { return k * 16 + ((((r >> 2) ^ (k >> 1)) & 3) << 2) + (r & 3); }
+// c (16 x 8) += a (16 x 8) b (8 x 8), tf32 words (an fp32 value's 13 low bits are not looked at).
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], const float (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+          "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b[0])), "r"(__float_as_uint(b[1])));
+}
+
+// x as a sum of two tf32 words: the first cut off, the second what remains (its own 11 bits of it).
+template <int kN>
+__device__ __forceinline__ void split(const float (&x)[kN], float (&hi)[kN], float (&lo)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        hi[i] = __uint_as_float(__float_as_uint(x[i]) & 0xffffe000u);
+        lo[i] = x[i] - hi[i];
+    }
+}
 
 // Eight values of each lane summed over the warp: lane l returns the sum of value (l >> 2) & 7.
 __device__ __forceinline__ float sum_eight(float (&x)[8]) {
@@ -105,8 +123,9 @@ __device__ __forceinline__ float sum_eight(float (&x)[8]) {
     return x[0];
 }
 
-template <bool kStateBf16, bool kOutBf16>
-__global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep a) {
+// kEights: eights of nodes that the accumulators hold.
+template <bool kStateBf16, bool kOutBf16, int kEights>
+__global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_kernel(const TreeStep a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
@@ -124,23 +143,24 @@ __global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep
     }
     const TreeSmem s(smem, a.max_nodes);
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
-    constexpr uint32_t kBytes = kD * kD * (kStateBf16 ? 2 : 4);
+    constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
     if (tid == 0) {
         sm100::mbar_init(s.bar, 1);
         sm100::fence_mbar_init();
-        sm100::mbar_arrive_expect_tx(s.bar, kBytes);
-        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * kBytes;
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         sm100::smem_addr(s.parts)),
-                     "l"(src), "r"(kBytes), "r"(sm100::smem_addr(s.bar))
-                     : "memory");
+        sm100::mbar_arrive_expect_tx(s.bar, kD * kRow);
+    }
+    if (warp == 0) {
+        __syncwarp();
+        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * (kD * kRow);
+        for (int k = lane; k < kD; k += 32)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             sm100::smem_addr(s.state + k * kPitch)),
+                         "l"(src + k * kRow), "r"(kRow), "r"(sm100::smem_addr(s.bar))
+                         : "memory");
     }
     // the nodes' vectors: 16 bytes a thread
-    for (int i = tid; i < n * 16; i += kThreads) {
-        const int64_t src = at(i >> 4) + (i & 15) * 8;
-        sm100::cp_async_16(s.k + i * 8, a.k + src, true);
-        sm100::cp_async_16(s.v + i * 8, a.v + src, true);
-    }
+    for (int i = tid; i < n * 16; i += kThreads)
+        sm100::cp_async_16(s.k + i * 8, a.k + at(i >> 4) + (i & 15) * 8, true);
     for (int i = tid; i < n * 32; i += kThreads) {
         float4 g = *reinterpret_cast<const float4 *>(a.g + at(i >> 5) + (i & 31) * 4);
         g = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
@@ -155,10 +175,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep
     // A warp a node: four channels a lane, four nodes of the path at a time.
     const int eights = (n + 7) / 8;
     for (int i = warp; i < 8 * eights; i += kWarps) {
-        float *rows = s.rows + (i >> 3) * (kD * 16);
+        // (k = 4 lane + c: lane (i & 7, c) of the operand at k / 8 = lane / 2)
+        float2 *rows = reinterpret_cast<float2 *>(s.rows + (i >> 3) * kEight + (lane >> 1) * kBlock + (i & 7) * 16) + (lane & 1);
         if (i >= n) {  // rows of the last eight that are no node
 #pragma unroll
-            for (int c = 0; c < 4; ++c) rows[row_at(4 * lane + c, i & 7)] = rows[row_at(4 * lane + c, 8 + (i & 7))] = 0.f;
+            for (int c = 0; c < 4; ++c) rows[2 * c] = make_float2(0.f, 0.f);
             continue;
         }
         uint64_t path = path_of(a.ancestors[t.first + i], i);
@@ -189,59 +210,74 @@ __global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep
                 else if (j != i) s.ak[j * s.nc + i] = sum;
             }
         }
-        const float ke[4] = {e.x * k.x, e.y * k.y, e.z * k.z, e.w * k.w};
-        const float qe[4] = {e.x * q.x, e.y * q.y, e.z * q.z, e.w * q.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            rows[row_at(4 * lane + c, i & 7)] = ke[c];
-            rows[row_at(4 * lane + c, 8 + (i & 7))] = qe[c];
-        }
+        rows[0] = make_float2(e.x * k.x, e.x * q.x);
+        rows[2] = make_float2(e.y * k.y, e.y * q.y);
+        rows[4] = make_float2(e.z * k.z, e.z * q.z);
+        rows[6] = make_float2(e.w * k.w, e.w * q.w);
     }
     // (every thread sees the copy's bytes through the barrier)
     const bool ok = sm100::mbar_wait_bounded(s.bar, 0, kMaxPolls);
     if (!ok) record_device_error(a.err, kDevTimeout);
     if (__syncthreads_or(!ok)) return;
 
-    // The product: a warp has the 16 rows of an eight, the lanes 4 columns each, for a part of k.
-    const int groups = eights <= 4 ? (eights == 3 ? 2 : 8 / eights) : 1;
-    const int eight = warp % eights, group = warp / eights;
-    float acc[16][4];
-    if (group < groups) {
-        const int k0 = group * (kD / groups), k1 = k0 + kD / groups;
-        const float *rows = s.rows + eight * (kD * 16);
+    for (int i = tid; i < n * 16; i += kThreads)  // the values in the keys' place
+        sm100::cp_async_16(s.k + i * 8, a.v + at(i >> 4) + (i & 15) * 8, true);
+
+    // The product: a warp has columns 16 warp .. + 15 of all rows.
+    const int g = lane >> 2, tq = lane & 3;
+    float acc[kEights][2][4];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.f;
+    for (int m = 0; m < kEights; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = 0.f;
 #pragma unroll 2
-        for (int k = k0; k < k1; ++k) {
-            float4 x;
-            if constexpr (kStateBf16) x = widen4(reinterpret_cast<const uint2 *>(s.parts)[k * 32 + lane]);
-            else x = reinterpret_cast<const float4 *>(s.parts)[k * 32 + lane];
+    for (int ks = 0; ks < kD / 8; ++ks) {
+        float bh[2][2], bl[2][2];
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(rows + row_at(k, r));
-                const float w[4] = {y.x, y.y, y.z, y.w};
+        for (int c = 0; c < 2; ++c) {
+            float x[2];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    acc[r + m][0] += w[m] * x.x;
-                    acc[r + m][1] += w[m] * x.y;
-                    acc[r + m][2] += w[m] * x.z;
-                    acc[r + m][3] += w[m] * x.w;
-                }
+            for (int i = 0; i < 2; ++i) {
+                const int k = 8 * ks + tq + 4 * i, col = 16 * warp + 8 * c + g;
+                if constexpr (kStateBf16) x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(s.state + k * kPitch)[col]);
+                else x[i] = s.state[k * kPitch + col];
+            }
+            if constexpr (kStateBf16) {  // one word
+                bh[c][0] = x[0];
+                bh[c][1] = x[1];
+            } else {
+                split(x, bh[c], bl[c]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kEights; ++m) {
+            if (m >= eights) break;
+            const float4 y = *reinterpret_cast<const float4 *>(s.rows + m * kEight + ks * kBlock + lane * 4);
+            const float x[4] = {y.x, y.y, y.z, y.w};
+            float ah[4], al[4];
+            split(x, ah, al);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mma_tf32(acc[m][c], al, bh[c]);
+                if constexpr (!kStateBf16) mma_tf32(acc[m][c], ah, bl[c]);
+                mma_tf32(acc[m][c], ah, bh[c]);
             }
         }
     }
+    sm100::cp_async_wait_all();
     __syncthreads();
-    if (group < groups) {
-        float4 *to = reinterpret_cast<float4 *>(s.parts) + (group * eights + eight) * (16 * 32) + lane;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) to[r * 32] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    for (int m = 0; m < kEights; ++m) {
+        if (m >= eights) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float *to = s.state + (m * 16 + g) * kPitch + 16 * warp + 8 * c + 2 * tq;
+            *reinterpret_cast<float2 *>(to) = make_float2(acc[m][c][0], acc[m][c][1]);
+            *reinterpret_cast<float2 *>(to + 8 * kPitch) = make_float2(acc[m][c][2], acc[m][c][3]);
+        }
     }
     __syncthreads();
-    auto product = [&](int m, int r, int c) {  // row r of eight m, column c
-        float x = 0.f;
-        for (int g = 0; g < groups; ++g) x += s.parts[((g * eights + m) * 16 + r) * kD + c];
-        return x;
-    };
+    auto product = [&](int m, int r, int c) { return s.state[(m * 16 + r) * kPitch + c]; };
 
     // The updates: a thread a column, eight nodes in registers.
     const int c = tid & (kD - 1);
@@ -267,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_decode_kernel(const TreeStep
             for (int i = 0; i < 8; ++i) {
                 const int node = 8 * m + i;
                 if (node >= n) break;
-                const float u = s.beta[node] * (__bfloat162float(s.v[node * kD + c]) - w[i]);
+                const float u = s.beta[node] * (__bfloat162float(s.k[node * kD + c]) - w[i]);
                 s.decay[node * kD + c] = u;
                 if (a.u != nullptr) a.u[at(node) + c] = u;
 #pragma unroll
@@ -396,14 +432,19 @@ __global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep
     }
 }
 
-template <bool kStateBf16, bool kOutBf16>
-cudaError_t decode_t(const TreeStep &a, cudaStream_t s) {
-    const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16>;
+template <bool kStateBf16, bool kOutBf16, int kEights>
+cudaError_t decode_n(const TreeStep &a, cudaStream_t s) {
+    const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16, kEights>;
     const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem::bytes(kTreeNodes));
+        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem::bytes(8 * kEights));
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, TreeSmem::bytes(TreeSmem::nodes(a.max_nodes)), s>>>(a);
     return cudaGetLastError();
+}
+
+template <bool kStateBf16, bool kOutBf16>
+cudaError_t decode_t(const TreeStep &a, cudaStream_t s) {
+    return a.max_nodes <= 16 ? decode_n<kStateBf16, kOutBf16, 2>(a, s) : decode_n<kStateBf16, kOutBf16, 8>(a, s);
 }
 
 template <bool kStateBf16>
