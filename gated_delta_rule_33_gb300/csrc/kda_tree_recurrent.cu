@@ -18,7 +18,8 @@
 // the bytes take 82); so it runs on the matrix instructions, every operand as two words of 11
 // bits (tf32) and three products, which keeps 2^-20 of it: u becomes state.  One block a
 // (request, head), two blocks an SM, so that one's state arrives while the other computes.  The
-// state comes by bulk copies, a row each, to rows 8 words apart in the banks; meanwhile a warp a
+// state comes by 16-byte copies, to rows 8 words apart in the banks (bulk copies of a row each took
+// 5 us to issue); meanwhile a warp a
 // node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp
 // has 16 columns of the product for all rows; then each thread solves its column of the
 // updates, 8 nodes in registers, and the outputs follow.
@@ -31,7 +32,6 @@ namespace {
 constexpr int kD = 128;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kMaxPolls = 1u << 20;
 
 template <bool kBf16>
 __device__ __forceinline__ void write_out(void *o, int64_t i, float x) {
@@ -69,11 +69,10 @@ struct TreeSmem {
     float *decay;     // [n][128] a_i; then u_i
     float *beta;
     __nv_bfloat16 *k; // [n][128]; then v_i
-    uint64_t *bar;
 
     __host__ __device__ static int nodes(int max_nodes) { return (max_nodes + 7) / 8 * 8; }
     __host__ __device__ static int bytes(int nc) {
-        return kD * kPitch * 4 + nc / 8 * (kEight * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4 + 16;
+        return kD * kPitch * 4 + nc / 8 * (kEight * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4;
     }
     __device__ TreeSmem(uint8_t *base, int max_nodes) {
         nc = nodes(max_nodes);
@@ -84,7 +83,6 @@ struct TreeSmem {
         decay = aq + nc * nc;
         k = reinterpret_cast<__nv_bfloat16 *>(decay + nc * kD);
         beta = reinterpret_cast<float *>(k + nc * kD);
-        bar = reinterpret_cast<uint64_t *>(beta + nc);
     }
 };
 
@@ -144,23 +142,19 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     const TreeSmem s(smem, a.max_nodes);
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
     constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
-    if (tid == 0) {
-        sm100::mbar_init(s.bar, 1);
-        sm100::fence_mbar_init();
-        sm100::mbar_arrive_expect_tx(s.bar, kD * kRow);
-    }
-    if (warp == 0) {
-        __syncwarp();
-        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * (kD * kRow);
-        for (int k = lane; k < kD; k += 32)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             sm100::smem_addr(s.state + k * kPitch)),
-                         "l"(src + k * kRow), "r"(kRow), "r"(sm100::smem_addr(s.bar))
-                         : "memory");
-    }
-    // the nodes' vectors: 16 bytes a thread
+    auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    // the keys, and behind them the state: 16 bytes a copy
     for (int i = tid; i < n * 16; i += kThreads)
         sm100::cp_async_16(s.k + i * 8, a.k + at(i >> 4) + (i & 15) * 8, true);
+    group();
+    const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * (kD * kRow);
+    constexpr int kPieces = kRow / 16;
+#pragma unroll
+    for (int i = 0; i < kD * kPieces / kThreads; ++i) {
+        const int k = (tid + i * kThreads) / kPieces, c = (tid + i * kThreads) % kPieces;
+        sm100::cp_async_16(reinterpret_cast<uint8_t *>(s.state + k * kPitch) + c * 16, src + k * kRow + c * 16, true);
+    }
+    group();
     for (int i = tid; i < n * 32; i += kThreads) {
         float4 g = *reinterpret_cast<const float4 *>(a.g + at(i >> 5) + (i & 31) * 4);
         g = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
@@ -169,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     for (int i = tid; i < n * s.nc / 4; i += kThreads)
         reinterpret_cast<float4 *>(s.ak)[i] = reinterpret_cast<float4 *>(s.aq)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (tid < n) s.beta[tid] = a.beta[(t.first + tid) * a.H + h];
-    sm100::cp_async_wait_all();
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
 
     // A warp a node: four channels a lane, four nodes of the path at a time.
@@ -215,11 +209,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
         rows[4] = make_float2(e.z * k.z, e.z * q.z);
         rows[6] = make_float2(e.w * k.w, e.w * q.w);
     }
-    // (every thread sees the copy's bytes through the barrier)
-    const bool ok = sm100::mbar_wait_bounded(s.bar, 0, kMaxPolls);
-    if (!ok) record_device_error(a.err, kDevTimeout);
-    if (__syncthreads_or(!ok)) return;
-
+    sm100::cp_async_wait_all();
+    __syncthreads();
     for (int i = tid; i < n * 16; i += kThreads)  // the values in the keys' place
         sm100::cp_async_16(s.k + i * 8, a.v + at(i >> 4) + (i & 15) * 8, true);
 
@@ -257,11 +248,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             float ah[4], al[4];
             split(x, ah, al);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                mma_tf32(acc[m][c], al, bh[c]);
-                if constexpr (!kStateBf16) mma_tf32(acc[m][c], ah, bl[c]);
-                mma_tf32(acc[m][c], ah, bh[c]);
-            }
+            for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], al, bh[c]);
+            if constexpr (!kStateBf16)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], ah, bl[c]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], ah, bh[c]);
         }
     }
     sm100::cp_async_wait_all();
