@@ -23,6 +23,9 @@
 // node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp
 // has 16 columns of the product for all rows; then each thread solves its column of the
 // updates, 8 nodes in registers, and the outputs follow.
+#include <type_traits>
+
+#include "kda_f32x2.cuh"
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
@@ -104,6 +107,17 @@ __device__ __forceinline__ void split(const float (&x)[kN], float (&hi)[kN], flo
     }
 }
 
+struct Pairs {  // four channels
+    uint64_t x, y;
+};
+__device__ __forceinline__ Pairs pairs(uint2 v) {
+    const float4 f = widen4(v);
+    return {f2(f.x, f.y), f2(f.z, f.w)};
+}
+
+__device__ __forceinline__ int count_leading(uint32_t x) { return __clz(static_cast<int>(x)); }
+__device__ __forceinline__ int count_leading(uint64_t x) { return __clzll(static_cast<long long>(x)); }
+
 // Eight values of each lane summed over the warp: lane l returns the sum of value (l >> 2) & 7.
 __device__ __forceinline__ float sum_eight(float (&x)[8]) {
     const int lane = threadIdx.x & 31;
@@ -143,6 +157,11 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
     constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
     auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    float4 g4[kEights];  // the gates, ahead of all copies
+#pragma unroll
+    for (int i = 0; i < kEights; ++i)
+        if (tid + i * kThreads < n * 32)
+            g4[i] = *reinterpret_cast<const float4 *>(a.g + at((tid >> 5) + 8 * i) + lane * 4);
     // the keys, and behind them the state: 16 bytes a copy
     for (int i = tid; i < n * 16; i += kThreads)
         sm100::cp_async_16(s.k + i * 8, a.k + at(i >> 4) + (i & 15) * 8, true);
@@ -155,18 +174,20 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
         sm100::cp_async_16(reinterpret_cast<uint8_t *>(s.state + k * kPitch) + c * 16, src + k * kRow + c * 16, true);
     }
     group();
-    for (int i = tid; i < n * 32; i += kThreads) {
-        float4 g = *reinterpret_cast<const float4 *>(a.g + at(i >> 5) + (i & 31) * 4);
-        g = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
-        reinterpret_cast<float4 *>(s.decay)[i] = g;
-    }
     for (int i = tid; i < n * s.nc / 4; i += kThreads)
         reinterpret_cast<float4 *>(s.ak)[i] = reinterpret_cast<float4 *>(s.aq)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (tid < n) s.beta[tid] = a.beta[(t.first + tid) * a.H + h];
+#pragma unroll
+    for (int i = 0; i < kEights; ++i)
+        if (tid + i * kThreads < n * 32)
+            reinterpret_cast<float4 *>(s.decay)[tid + i * kThreads] =
+                make_float4(expf(g4[i].x), expf(g4[i].y), expf(g4[i].z), expf(g4[i].w));
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
 
     // A warp a node: four channels a lane, four nodes of the path at a time.
+    using Word = std::conditional_t<kEights <= 4, uint32_t, uint64_t>;
+    constexpr int kBits = 8 * sizeof(Word);
     const int eights = (n + 7) / 8;
     for (int i = warp; i < 8 * eights; i += kWarps) {
         // (k = 4 lane + c: lane (i & 7, c) of the operand at k / 8 = lane / 2)
@@ -176,26 +197,29 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             for (int c = 0; c < 4; ++c) rows[2 * c] = make_float2(0.f, 0.f);
             continue;
         }
-        uint64_t path = path_of(a.ancestors[t.first + i], i);
-        float4 e = make_float4(1.f, 1.f, 1.f, 1.f);
-        const float4 k = widen4(*reinterpret_cast<const uint2 *>(s.k + i * kD + 4 * lane));
-        float4 q = widen4(*reinterpret_cast<const uint2 *>(a.q + at(i) + 4 * lane));
-        q = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
+        Word path = static_cast<Word>(path_of(a.ancestors[t.first + i], i));
+        const Pairs k = pairs(*reinterpret_cast<const uint2 *>(s.k + i * kD + 4 * lane));
+        Pairs q = pairs(*reinterpret_cast<const uint2 *>(a.q + at(i) + 4 * lane));
+        const uint64_t scale = f2(a.scale, a.scale), one = f2(1.f, 1.f);
+        q = {f2_mul(q.x, scale), f2_mul(q.y, scale)};
+        Pairs e = {one, one};
         while (path != 0) {
             float x[8];
             int js[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const bool some = path != 0;
-                const int j = some ? top_bit(path) : 0;
+                const int j = some ? kBits - 1 - count_leading(path) : 0;
                 js[m] = some ? j : -1;
-                if (some) path ^= uint64_t{1} << j;
-                const float4 kj = widen4(*reinterpret_cast<const uint2 *>(s.k + j * kD + 4 * lane));
+                path &= (Word{1} << j) - 1;  // (nothing is left of none)
+                const Pairs kj = pairs(*reinterpret_cast<const uint2 *>(s.k + j * kD + 4 * lane));
                 const float4 d = *reinterpret_cast<const float4 *>(s.decay + j * kD + 4 * lane);
-                const float4 y = make_float4(e.x * kj.x, e.y * kj.y, e.z * kj.z, e.w * kj.w);
-                x[2 * m] = y.x * k.x + y.y * k.y + (y.z * k.z + y.w * k.w);
-                x[2 * m + 1] = y.x * q.x + y.y * q.y + (y.z * q.z + y.w * q.w);
-                if (some) e = make_float4(e.x * d.x, e.y * d.y, e.z * d.z, e.w * d.w);
+                const Pairs y = {f2_mul(e.x, kj.x), f2_mul(e.y, kj.y)};
+                const float2 dk = f2_split(f2_fma(y.y, k.y, f2_mul(y.x, k.x)));
+                const float2 dq = f2_split(f2_fma(y.y, q.y, f2_mul(y.x, q.x)));
+                x[2 * m] = dk.x + dk.y;
+                x[2 * m + 1] = dq.x + dq.y;
+                if (some) e = {f2_mul(e.x, f2(d.x, d.y)), f2_mul(e.y, f2(d.z, d.w))};
             }
             const float sum = sum_eight(x);
             const int m = lane >> 3, j = m == 0 ? js[0] : m == 1 ? js[1] : m == 2 ? js[2] : js[3];
@@ -204,10 +228,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
                 else if (j != i) s.ak[j * s.nc + i] = sum;
             }
         }
-        rows[0] = make_float2(e.x * k.x, e.x * q.x);
-        rows[2] = make_float2(e.y * k.y, e.y * q.y);
-        rows[4] = make_float2(e.z * k.z, e.z * q.z);
-        rows[6] = make_float2(e.w * k.w, e.w * q.w);
+        const float2 k0 = f2_split(f2_mul(e.x, k.x)), k1 = f2_split(f2_mul(e.y, k.y));
+        const float2 q0 = f2_split(f2_mul(e.x, q.x)), q1 = f2_split(f2_mul(e.y, q.y));
+        rows[0] = make_float2(k0.x, q0.x);
+        rows[2] = make_float2(k0.y, q0.y);
+        rows[4] = make_float2(k1.x, q1.x);
+        rows[6] = make_float2(k1.y, q1.y);
     }
     sm100::cp_async_wait_all();
     __syncthreads();
@@ -216,12 +242,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
 
     // The product: a warp has columns 16 warp .. + 15 of all rows.
     const int g = lane >> 2, tq = lane & 3;
-    float acc[kEights][2][4];
+    float acc[kEights][2][4], low[kEights][2][4];  // (the second words' products apart: shorter chains)
 #pragma unroll
     for (int m = 0; m < kEights; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = 0.f;
-#pragma unroll 2
+        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
+#pragma unroll 4
     for (int ks = 0; ks < kD / 8; ++ks) {
         float bh[2][2], bl[2][2];
 #pragma unroll
@@ -248,12 +274,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             float ah[4], al[4];
             split(x, ah, al);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], al, bh[c]);
-            if constexpr (!kStateBf16)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], ah, bl[c]);
+            for (int c = 0; c < 2; ++c) mma_tf32(low[m][c], al, bh[c]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], ah, bh[c]);
+            if constexpr (!kStateBf16)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mma_tf32(low[m][c], ah, bl[c]);
         }
     }
     sm100::cp_async_wait_all();
@@ -264,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float *to = s.state + (m * 16 + g) * kPitch + 16 * warp + 8 * c + 2 * tq;
-            *reinterpret_cast<float2 *>(to) = make_float2(acc[m][c][0], acc[m][c][1]);
-            *reinterpret_cast<float2 *>(to + 8 * kPitch) = make_float2(acc[m][c][2], acc[m][c][3]);
+            *reinterpret_cast<float2 *>(to) = make_float2(acc[m][c][0] + low[m][c][0], acc[m][c][1] + low[m][c][1]);
+            *reinterpret_cast<float2 *>(to + 8 * kPitch) = make_float2(acc[m][c][2] + low[m][c][2], acc[m][c][3] + low[m][c][3]);
         }
     }
     __syncthreads();
