@@ -15,8 +15,9 @@
 //
 // Decode.  Bound: the state is read once (64 KB of fp32 a head, 32 KB of bf16) and meets 2 n
 // vectors, 4 n 128^2 flops: HBM.  On the fp32 pipe that product alone takes as long (337 us where
-// the bytes take 82); so it runs on the matrix instructions, every operand as two words of 11
-// bits (tf32) and three products, which keeps 2^-20 of it: u becomes state.  One block a
+// the bytes take 82); so it runs on the matrix instructions, every operand as three bf16 words, 24
+// bits together, and the six products that reach 2^-24 (u becomes state; two tf32 words and
+// three products hold less and took twice as long).  One block a
 // (request, head), two blocks an SM, so that one's state arrives while the other computes.  The
 // state comes by 16-byte copies, to rows 8 words apart in the banks (bulk copies of a row each took
 // 5 us to issue); meanwhile a warp a
@@ -57,17 +58,25 @@ __device__ __forceinline__ float4 widen4(uint2 x) {
 
 // ---- decode --------------------------------------------------------------------------------
 
-constexpr int kPitch = 136;            // floats of a state's or product's row
-constexpr int kBlock = 132;            // floats of an eight's rows at 8 k's (see TreeSmem)
-constexpr int kEight = 16 * kBlock;    // and at all
+constexpr int kPitch = 132;  // floats of a state's or product's row: eight banks between every second
+
+// Left operands of 16 rows x 16 k's, for eight nodes: rows g are E_i k_i, rows 8 + g their E_i q_i.
+// Up to 16 nodes they lie as bf16 words, a block of 32 lanes' registers and a gap for the banks;
+// more of them as fp32, which each warp splits.
+template <int kEights>
+struct LeftOperands {
+    static constexpr bool kWords = kEights <= 2;
+    static constexpr int kBlock = kWords ? 3 * 512 + 32 : 32 * 32 + 32;  // bytes at 16 k's
+    static constexpr int kEight = kD / 16 * kBlock;                      // and at all
+};
 
 // Shared memory: nodes in eights, as many as nc nodes fill.
+template <int kEights>
 struct TreeSmem {
     int nc;
     float *state;     // [k 128][kPitch]; then the products [eight][16][kPitch]: of its nodes' E_i k_i
                       // with the state, then of their E_i scale q_i
-    float *rows;      // [eight][k / 8][kBlock]: those vectors as left operands of 16 rows x 8 k's:
-                      // lane (g, t) has (k_g, q_g) at k = t, then at k = t + 4
+    uint8_t *rows;    // [eight][k / 16]: LeftOperands
     float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
     float *decay;     // [n][128] a_i; then u_i
     float *beta;
@@ -75,13 +84,13 @@ struct TreeSmem {
 
     __host__ __device__ static int nodes(int max_nodes) { return (max_nodes + 7) / 8 * 8; }
     __host__ __device__ static int bytes(int nc) {
-        return kD * kPitch * 4 + nc / 8 * (kEight * 4) + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4;
+        return kD * kPitch * 4 + nc / 8 * LeftOperands<kEights>::kEight + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4;
     }
     __device__ TreeSmem(uint8_t *base, int max_nodes) {
         nc = nodes(max_nodes);
         state = reinterpret_cast<float *>(base);
-        rows = state + kD * kPitch;
-        ak = rows + nc / 8 * kEight;
+        rows = base + kD * kPitch * 4;
+        ak = reinterpret_cast<float *>(rows + nc / 8 * LeftOperands<kEights>::kEight);
         aq = ak + nc * nc;
         decay = aq + nc * nc;
         k = reinterpret_cast<__nv_bfloat16 *>(decay + nc * kD);
@@ -89,22 +98,26 @@ struct TreeSmem {
     }
 };
 
-// c (16 x 8) += a (16 x 8) b (8 x 8), tf32 words (an fp32 value's 13 low bits are not looked at).
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], const float (&b)[2]) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+// c (16 x 8) += a (16 x 16) b (16 x 8), bf16 operands.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
-          "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b[0])), "r"(__float_as_uint(b[1])));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// x as a sum of two tf32 words: the first cut off, the second what remains (its own 11 bits of it).
-template <int kN>
-__device__ __forceinline__ void split(const float (&x)[kN], float (&hi)[kN], float (&lo)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        hi[i] = __uint_as_float(__float_as_uint(x[i]) & 0xffffe000u);
-        lo[i] = x[i] - hi[i];
-    }
+// Two values as sums of three bf16 words each.
+__device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l) {
+    auto pack = [](float x, float y) {
+        const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&w);
+    };
+    h = pack(a, b);
+    a -= __uint_as_float(h << 16);
+    b -= __uint_as_float(h & 0xffff0000u);
+    m = pack(a, b);
+    a -= __uint_as_float(m << 16);
+    b -= __uint_as_float(m & 0xffff0000u);
+    l = pack(a, b);
 }
 
 struct Pairs {  // four channels
@@ -153,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
         }
         return;
     }
-    const TreeSmem s(smem, a.max_nodes);
+    const TreeSmem<kEights> s(smem, a.max_nodes);
+    using Left = LeftOperands<kEights>;
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
     constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
     auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
@@ -190,11 +204,32 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     constexpr int kBits = 8 * sizeof(Word);
     const int eights = (n + 7) / 8;
     for (int i = warp; i < 8 * eights; i += kWarps) {
-        // (k = 4 lane + c: lane (i & 7, c) of the operand at k / 8 = lane / 2)
-        float2 *rows = reinterpret_cast<float2 *>(s.rows + (i >> 3) * kEight + (lane >> 1) * kBlock + (i & 7) * 16) + (lane & 1);
-        if (i >= n) {  // rows of the last eight that are no node
+        // this lane's k's, 4 lane ..: for lane lane0 and the next of the operand at lane / 4,
+        // their first or second pair
+        const int lane0 = (i & 7) * 4 + 2 * (lane & 1), pair = (lane >> 1) & 1;
+        uint8_t *rows = s.rows + (i >> 3) * Left::kEight + (lane >> 2) * Left::kBlock;
+        auto write = [&](float2 k0, float2 k1, float2 q0, float2 q1) {
+            if constexpr (Left::kWords) {
+                uint32_t k[2][3], q[2][3];
+                split3(k0.x, k0.y, k[0][0], k[0][1], k[0][2]);
+                split3(k1.x, k1.y, k[1][0], k[1][1], k[1][2]);
+                split3(q0.x, q0.y, q[0][0], q[0][1], q[0][2]);
+                split3(q1.x, q1.y, q[1][0], q[1][1], q[1][2]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) rows[2 * c] = make_float2(0.f, 0.f);
+                for (int w = 0; w < 3; ++w) {
+                    uint2 *to = reinterpret_cast<uint2 *>(rows + w * 512) + lane0 * 2 + pair;
+                    to[0] = make_uint2(k[0][w], q[0][w]);
+                    to[2] = make_uint2(k[1][w], q[1][w]);
+                }
+            } else {
+                float4 *to = reinterpret_cast<float4 *>(rows) + lane0 * 2 + pair;
+                to[0] = make_float4(k0.x, k0.y, q0.x, q0.y);
+                to[2] = make_float4(k1.x, k1.y, q1.x, q1.y);
+            }
+        };
+        if (i >= n) {  // rows of the last eight that are no node
+            const float2 zero = make_float2(0.f, 0.f);
+            write(zero, zero, zero, zero);
             continue;
         }
         Word path = static_cast<Word>(path_of(a.ancestors[t.first + i], i));
@@ -228,12 +263,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
                 else if (j != i) s.ak[j * s.nc + i] = sum;
             }
         }
-        const float2 k0 = f2_split(f2_mul(e.x, k.x)), k1 = f2_split(f2_mul(e.y, k.y));
-        const float2 q0 = f2_split(f2_mul(e.x, q.x)), q1 = f2_split(f2_mul(e.y, q.y));
-        rows[0] = make_float2(k0.x, q0.x);
-        rows[2] = make_float2(k0.y, q0.y);
-        rows[4] = make_float2(k1.x, q1.x);
-        rows[6] = make_float2(k1.y, q1.y);
+        write(f2_split(f2_mul(e.x, k.x)), f2_split(f2_mul(e.y, k.y)), f2_split(f2_mul(e.x, q.x)),
+              f2_split(f2_mul(e.y, q.y)));
     }
     sm100::cp_async_wait_all();
     __syncthreads();
@@ -242,44 +273,57 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
 
     // The product: a warp has columns 16 warp .. + 15 of all rows.
     const int g = lane >> 2, tq = lane & 3;
-    float acc[kEights][2][4], low[kEights][2][4];  // (the second words' products apart: shorter chains)
+    float acc[kEights][2][4], low[kEights][2][4];  // (the lower words' products apart: shorter chains)
 #pragma unroll
     for (int m = 0; m < kEights; ++m)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
-#pragma unroll 4
-    for (int ks = 0; ks < kD / 8; ++ks) {
-        float bh[2][2], bl[2][2];
+#pragma unroll 2
+    for (int ks = 0; ks < kD / 16; ++ks) {
+        uint32_t b[3][2][2];  // word, tile, pair of k's
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float x[2];
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int k = 8 * ks + tq + 4 * i, col = 16 * warp + 8 * c + g;
-                if constexpr (kStateBf16) x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(s.state + k * kPitch)[col]);
-                else x[i] = s.state[k * kPitch + col];
+                const int k = 16 * ks + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
+                if constexpr (kStateBf16) {
+                    const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * kPitch) + col;
+                    b[0][c][i] = x[0] | static_cast<uint32_t>(x[2 * kPitch]) << 16;
+                } else {
+                    const float *x = s.state + k * kPitch + col;
+                    split3(x[0], x[kPitch], b[0][c][i], b[1][c][i], b[2][c][i]);
+                }
             }
-            if constexpr (kStateBf16) {  // one word
-                bh[c][0] = x[0];
-                bh[c][1] = x[1];
-            } else {
-                split(x, bh[c], bl[c]);
-            }
-        }
 #pragma unroll
         for (int m = 0; m < kEights; ++m) {
             if (m >= eights) break;
-            const float4 y = *reinterpret_cast<const float4 *>(s.rows + m * kEight + ks * kBlock + lane * 4);
-            const float x[4] = {y.x, y.y, y.z, y.w};
-            float ah[4], al[4];
-            split(x, ah, al);
+            uint32_t w[3][4];
+            const uint8_t *rows = s.rows + m * Left::kEight + ks * Left::kBlock;
+            if constexpr (Left::kWords) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) mma_tf32(low[m][c], al, bh[c]);
+                for (int i = 0; i < 3; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(rows + i * 512 + lane * 16);
+                    w[i][0] = x.x;
+                    w[i][1] = x.y;
+                    w[i][2] = x.z;
+                    w[i][3] = x.w;
+                }
+            } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) mma_tf32(acc[m][c], ah, bh[c]);
-            if constexpr (!kStateBf16)
+                for (int i = 0; i < 2; ++i) {
+                    const float4 x = reinterpret_cast<const float4 *>(rows)[lane * 2 + i];
+                    split3(x.x, x.y, w[0][2 * i], w[1][2 * i], w[2][2 * i]);
+                    split3(x.z, x.w, w[0][2 * i + 1], w[1][2 * i + 1], w[2][2 * i + 1]);
+                }
+            }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) mma_tf32(low[m][c], ah, bl[c]);
+            for (int i = 2; i >= 0; --i)  // word of the left operand
+#pragma unroll
+                for (int k = 2 - i; k >= 0; --k) {
+                    if (kStateBf16 && k > 0) continue;  // its state is one word
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) mma_bf16(i + k == 0 ? acc[m][c] : low[m][c], w[i], b[k][c]);
+                }
         }
     }
     sm100::cp_async_wait_all();
@@ -454,9 +498,9 @@ template <bool kStateBf16, bool kOutBf16, int kEights>
 cudaError_t decode_n(const TreeStep &a, cudaStream_t s) {
     const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16, kEights>;
     const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem::bytes(8 * kEights));
+        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem<kEights>::bytes(8 * kEights));
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, TreeSmem::bytes(TreeSmem::nodes(a.max_nodes)), s>>>(a);
+    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, TreeSmem<kEights>::bytes(TreeSmem<kEights>::nodes(a.max_nodes)), s>>>(a);
     return cudaGetLastError();
 }
 
