@@ -848,7 +848,7 @@ kda_status kda_recurrent_tree_decode(const void *q, const void *k, const void *v
     a.u = u;
     a.err = dev->error_word;
     try {
-        return from_cuda(kda::launch_tree_decode(a, state_dtype == KDA_BF16, o_dtype == KDA_BF16,
+        return from_cuda(kda::launch_tree_decode(a, state_dtype == KDA_BF16, o_dtype == KDA_BF16, dev->num_sms,
                                                  static_cast<cudaStream_t>(stream)));
     } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
         return KDA_ERR_CUDA;

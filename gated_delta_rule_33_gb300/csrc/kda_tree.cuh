@@ -58,7 +58,8 @@ struct TreeStep {   // the operands of the recurrence over trees
     unsigned int *err;
 };
 
-cudaError_t launch_tree_decode(const TreeStep &a, bool state_bf16, bool o_bf16, cudaStream_t s);
+cudaError_t launch_tree_decode(const TreeStep &a, bool state_bf16, bool o_bf16, int num_sms,
+                               cudaStream_t s);
 cudaError_t launch_tree_commit(const TreeStep &a, bool state_bf16, cudaStream_t s);
 
 struct TreeConv {

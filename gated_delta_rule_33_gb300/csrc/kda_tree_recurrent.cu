@@ -68,15 +68,16 @@ struct LeftOperands {
     static constexpr bool kWords = kEights <= 2;
     static constexpr int kBlock = kWords ? 3 * 512 + 32 : 32 * 32 + 32;  // bytes at 16 k's
     static constexpr int kEight = kD / 16 * kBlock;                      // and at all
+    static_assert(kEight >= 16 * kPitch * 4, "the products take their place");
 };
 
 // Shared memory: nodes in eights, as many as nc nodes fill.
 template <int kEights>
 struct TreeSmem {
     int nc;
-    float *state;     // [k 128][kPitch]; then the products [eight][16][kPitch]: of its nodes' E_i k_i
-                      // with the state, then of their E_i scale q_i
-    uint8_t *rows;    // [eight][k / 16]: LeftOperands
+    float *state;     // [k 128][kPitch]
+    uint8_t *rows;    // [eight][k / 16]: LeftOperands; then the products [eight][16][kPitch] of the
+                      // eight's E_i k_i with the state, and of its E_i scale q_i
     float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
     float *decay;     // [n][128] a_i; then u_i
     float *beta;
@@ -148,252 +149,314 @@ __device__ __forceinline__ float sum_eight(float (&x)[8]) {
     return x[0];
 }
 
-// kEights: eights of nodes that the accumulators hold.
+// A (request, head) of a block.
+struct TreeUnit {
+    int64_t first, slot;
+    int n, rows, h;
+
+    __device__ __forceinline__ TreeUnit(const TreeStep &a, int64_t unit) {
+        const int b = static_cast<int>(unit / a.H);
+        h = static_cast<int>(unit - static_cast<int64_t>(b) * a.H);
+        const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
+        if (t.bad && threadIdx.x == 0) record_device_error(a.err, kDevInvalidArg);
+        slot = slot_of(a, b);
+        first = t.first;
+        rows = t.rows;
+        n = slot < 0 ? 0 : t.n;
+    }
+    __device__ __forceinline__ int64_t at(const TreeStep &a, int i) const { return ((first + i) * a.H + h) * kD; }
+};
+
+// kEights: eights of nodes that the accumulators hold.  A block walks over units, gridDim.x apart.
 template <bool kStateBf16, bool kOutBf16, int kEights>
 __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_kernel(const TreeStep a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
-    const int warp = tid >> 5, lane = tid & 31;
-    const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
-    const int64_t slot = slot_of(a, b);
-    if (t.bad && tid == 0) record_device_error(a.err, kDevInvalidArg);
-    const int n = t.n;
-    if (n == 0 || slot < 0) {
-        for (int64_t i = tid; i < static_cast<int64_t>(t.rows) * kD; i += kThreads) {
-            const int64_t at = ((t.first + i / kD) * a.H + h) * kD + i % kD;
-            write_out<kOutBf16>(a.o, at, 0.f);
-            if (a.u != nullptr) a.u[at] = 0.f;
-        }
-        return;
-    }
-    const TreeSmem<kEights> s(smem, a.max_nodes);
     using Left = LeftOperands<kEights>;
-    auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
-    constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
-    auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    float4 g4[kEights];  // the gates, ahead of all copies
-#pragma unroll
-    for (int i = 0; i < kEights; ++i)
-        if (tid + i * kThreads < n * 32)
-            g4[i] = *reinterpret_cast<const float4 *>(a.g + at((tid >> 5) + 8 * i) + lane * 4);
-    // the keys, and behind them the state: 16 bytes a copy
-    for (int i = tid; i < n * 16; i += kThreads)
-        sm100::cp_async_16(s.k + i * 8, a.k + at(i >> 4) + (i & 15) * 8, true);
-    group();
-    const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (slot * a.H + h) * (kD * kRow);
-    constexpr int kPieces = kRow / 16;
-#pragma unroll
-    for (int i = 0; i < kD * kPieces / kThreads; ++i) {
-        const int k = (tid + i * kThreads) / kPieces, c = (tid + i * kThreads) % kPieces;
-        sm100::cp_async_16(reinterpret_cast<uint8_t *>(s.state + k * kPitch) + c * 16, src + k * kRow + c * 16, true);
-    }
-    group();
-    for (int i = tid; i < n * s.nc / 4; i += kThreads)
-        reinterpret_cast<float4 *>(s.ak)[i] = reinterpret_cast<float4 *>(s.aq)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < n) s.beta[tid] = a.beta[(t.first + tid) * a.H + h];
-#pragma unroll
-    for (int i = 0; i < kEights; ++i)
-        if (tid + i * kThreads < n * 32)
-            reinterpret_cast<float4 *>(s.decay)[tid + i * kThreads] =
-                make_float4(expf(g4[i].x), expf(g4[i].y), expf(g4[i].z), expf(g4[i].w));
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
-
-    // A warp a node: four channels a lane, four nodes of the path at a time.
     using Word = std::conditional_t<kEights <= 4, uint32_t, uint64_t>;
     constexpr int kBits = 8 * sizeof(Word);
-    const int eights = (n + 7) / 8;
-    for (int i = warp; i < 8 * eights; i += kWarps) {
-        // this lane's k's, 4 lane ..: for lane lane0 and the next of the operand at lane / 4,
-        // their first or second pair
-        const int lane0 = (i & 7) * 4 + 2 * (lane & 1), pair = (lane >> 1) & 1;
-        uint8_t *rows = s.rows + (i >> 3) * Left::kEight + (lane >> 2) * Left::kBlock;
-        auto write = [&](float2 k0, float2 k1, float2 q0, float2 q1) {
-            if constexpr (Left::kWords) {
-                uint32_t k[2][3], q[2][3];
-                split3(k0.x, k0.y, k[0][0], k[0][1], k[0][2]);
-                split3(k1.x, k1.y, k[1][0], k[1][1], k[1][2]);
-                split3(q0.x, q0.y, q[0][0], q[0][1], q[0][2]);
-                split3(q1.x, q1.y, q[1][0], q[1][1], q[1][2]);
+    constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const TreeSmem<kEights> s(smem, a.max_nodes);
+    const int64_t units = static_cast<int64_t>(a.B) * a.H;
+
+    // What a unit brings from memory, ahead of its turn: the state and the keys to shared memory,
+    // and in registers the gates (four channels of nodes warp, warp + 8, ..), the queries of the
+    // same nodes, their words and (of the first threads) beta.
+    float4 g4[kEights];
+    uint2 q2[kEights];
+    uint64_t words[kEights];
+    float beta = 0.f;
+    auto fetch_state = [&](const TreeUnit &u) {
+        if (u.n == 0) return;
 #pragma unroll
-                for (int w = 0; w < 3; ++w) {
-                    uint2 *to = reinterpret_cast<uint2 *>(rows + w * 512) + lane0 * 2 + pair;
-                    to[0] = make_uint2(k[0][w], q[0][w]);
-                    to[2] = make_uint2(k[1][w], q[1][w]);
-                }
-            } else {
-                float4 *to = reinterpret_cast<float4 *>(rows) + lane0 * 2 + pair;
-                to[0] = make_float4(k0.x, k0.y, q0.x, q0.y);
-                to[2] = make_float4(k1.x, k1.y, q1.x, q1.y);
+        for (int i = 0; i < kEights; ++i) {
+            const int node = warp + kWarps * i;
+            if (node < u.n) {
+                g4[i] = *reinterpret_cast<const float4 *>(a.g + u.at(a, node) + lane * 4);
+                q2[i] = *reinterpret_cast<const uint2 *>(a.q + u.at(a, node) + lane * 4);
+                words[i] = a.ancestors[u.first + node];
             }
-        };
-        if (i >= n) {  // rows of the last eight that are no node
-            const float2 zero = make_float2(0.f, 0.f);
-            write(zero, zero, zero, zero);
+        }
+        if (tid < u.n) beta = a.beta[(u.first + tid) * a.H + u.h];
+        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (u.slot * a.H + u.h) * (kD * kRow);
+        constexpr int kPieces = kRow / 16;
+#pragma unroll
+        for (int i = 0; i < kD * kPieces / kThreads; ++i) {
+            const int k = (tid + i * kThreads) / kPieces, c = (tid + i * kThreads) % kPieces;
+            sm100::cp_async_16(reinterpret_cast<uint8_t *>(s.state + k * kPitch) + c * 16, src + k * kRow + c * 16, true);
+        }
+    };
+    auto fetch_rows = [&](const TreeUnit &u, const __nv_bfloat16 *x) {  // keys, or values in their place
+        for (int i = tid; i < u.n * 16; i += kThreads)
+            sm100::cp_async_16(s.k + i * 8, x + u.at(a, i >> 4) + (i & 15) * 8, true);
+    };
+
+    TreeUnit u(a, blockIdx.x);
+    fetch_state(u);
+    fetch_rows(u, a.k);
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const TreeUnit next(a, min(unit + gridDim.x, units - 1));
+        const bool more = unit + gridDim.x < units;
+        const int n = u.n;
+        if (n == 0) {
+            for (int64_t i = tid; i < static_cast<int64_t>(u.rows) * kD; i += kThreads) {
+                const int64_t at = ((u.first + i / kD) * a.H + u.h) * kD + i % kD;
+                write_out<kOutBf16>(a.o, at, 0.f);
+                if (a.u != nullptr) a.u[at] = 0.f;
+            }
+            u = next;
+            if (more) {
+                fetch_state(u);
+                fetch_rows(u, a.k);
+            }
             continue;
         }
-        Word path = static_cast<Word>(path_of(a.ancestors[t.first + i], i));
-        const Pairs k = pairs(*reinterpret_cast<const uint2 *>(s.k + i * kD + 4 * lane));
-        Pairs q = pairs(*reinterpret_cast<const uint2 *>(a.q + at(i) + 4 * lane));
-        const uint64_t scale = f2(a.scale, a.scale), one = f2(1.f, 1.f);
-        q = {f2_mul(q.x, scale), f2_mul(q.y, scale)};
-        Pairs e = {one, one};
-        while (path != 0) {
-            float x[8];
-            int js[4];
+        const int eights = (n + 7) / 8;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const bool some = path != 0;
-                const int j = some ? kBits - 1 - count_leading(path) : 0;
-                js[m] = some ? j : -1;
-                path &= (Word{1} << j) - 1;  // (nothing is left of none)
-                const Pairs kj = pairs(*reinterpret_cast<const uint2 *>(s.k + j * kD + 4 * lane));
-                const float4 d = *reinterpret_cast<const float4 *>(s.decay + j * kD + 4 * lane);
-                const Pairs y = {f2_mul(e.x, kj.x), f2_mul(e.y, kj.y)};
-                const float2 dk = f2_split(f2_fma(y.y, k.y, f2_mul(y.x, k.x)));
-                const float2 dq = f2_split(f2_fma(y.y, q.y, f2_mul(y.x, q.x)));
-                x[2 * m] = dk.x + dk.y;
-                x[2 * m + 1] = dq.x + dq.y;
-                if (some) e = {f2_mul(e.x, f2(d.x, d.y)), f2_mul(e.y, f2(d.z, d.w))};
-            }
-            const float sum = sum_eight(x);
-            const int m = lane >> 3, j = m == 0 ? js[0] : m == 1 ? js[1] : m == 2 ? js[2] : js[3];
-            if ((lane & 3) == 0 && j >= 0) {
-                if (lane & 4) s.aq[j * s.nc + i] = sum;
-                else if (j != i) s.ak[j * s.nc + i] = sum;
-            }
+        for (int i = 0; i < kEights; ++i) {
+            const int node = warp + kWarps * i;
+            if (node < n)
+                *reinterpret_cast<float4 *>(s.decay + node * kD + lane * 4) =
+                    make_float4(expf(g4[i].x), expf(g4[i].y), expf(g4[i].z), expf(g4[i].w));
         }
-        write(f2_split(f2_mul(e.x, k.x)), f2_split(f2_mul(e.y, k.y)), f2_split(f2_mul(e.x, q.x)),
-              f2_split(f2_mul(e.y, q.y)));
-    }
-    sm100::cp_async_wait_all();
-    __syncthreads();
-    for (int i = tid; i < n * 16; i += kThreads)  // the values in the keys' place
-        sm100::cp_async_16(s.k + i * 8, a.v + at(i >> 4) + (i & 15) * 8, true);
+        for (int i = tid; i < n * s.nc / 4; i += kThreads)
+            reinterpret_cast<float4 *>(s.ak)[i] = reinterpret_cast<float4 *>(s.aq)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tid < n) s.beta[tid] = beta;
+        sm100::cp_async_wait_all();
+        __syncthreads();
 
-    // The product: a warp has columns 16 warp .. + 15 of all rows.
-    const int g = lane >> 2, tq = lane & 3;
-    float acc[kEights][2][4], low[kEights][2][4];  // (the lower words' products apart: shorter chains)
+        // A warp a node: four channels a lane, four nodes of the path at a time.
 #pragma unroll
-    for (int m = 0; m < kEights; ++m)
+        for (int eight = 0; eight < kEights; ++eight) {
+            if (eight >= eights) break;
+            const int i = warp + kWarps * eight;
+            // this lane's k's, 4 lane ..: for lane lane0 and the next of the operand at lane / 4, their
+            // first or second pair
+            const int lane0 = (i & 7) * 4 + 2 * (lane & 1), pair = (lane >> 1) & 1;
+            uint8_t *rows = s.rows + eight * Left::kEight + (lane >> 2) * Left::kBlock;
+            auto write = [&](float2 k0, float2 k1, float2 q0, float2 q1) {
+                if constexpr (Left::kWords) {
+                    uint32_t k[2][3], q[2][3];
+                    split3(k0.x, k0.y, k[0][0], k[0][1], k[0][2]);
+                    split3(k1.x, k1.y, k[1][0], k[1][1], k[1][2]);
+                    split3(q0.x, q0.y, q[0][0], q[0][1], q[0][2]);
+                    split3(q1.x, q1.y, q[1][0], q[1][1], q[1][2]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
-#pragma unroll 2
-    for (int ks = 0; ks < kD / 16; ++ks) {
-        uint32_t b[3][2][2];  // word, tile, pair of k's
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = 16 * ks + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
-                if constexpr (kStateBf16) {
-                    const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * kPitch) + col;
-                    b[0][c][i] = x[0] | static_cast<uint32_t>(x[2 * kPitch]) << 16;
+                    for (int w = 0; w < 3; ++w) {
+                        uint2 *to = reinterpret_cast<uint2 *>(rows + w * 512) + lane0 * 2 + pair;
+                        to[0] = make_uint2(k[0][w], q[0][w]);
+                        to[2] = make_uint2(k[1][w], q[1][w]);
+                    }
                 } else {
-                    const float *x = s.state + k * kPitch + col;
-                    split3(x[0], x[kPitch], b[0][c][i], b[1][c][i], b[2][c][i]);
+                    float4 *to = reinterpret_cast<float4 *>(rows) + lane0 * 2 + pair;
+                    to[0] = make_float4(k0.x, k0.y, q0.x, q0.y);
+                    to[2] = make_float4(k1.x, k1.y, q1.x, q1.y);
+                }
+            };
+            if (i >= n) {  // rows of the last eight that are no node
+                const float2 zero = make_float2(0.f, 0.f);
+                write(zero, zero, zero, zero);
+                continue;
+            }
+            Word path = static_cast<Word>(path_of(words[eight], i));
+            const Pairs k = pairs(*reinterpret_cast<const uint2 *>(s.k + i * kD + 4 * lane));
+            Pairs q = pairs(q2[eight]);
+            const uint64_t scale = f2(a.scale, a.scale), one = f2(1.f, 1.f);
+            q = {f2_mul(q.x, scale), f2_mul(q.y, scale)};
+            Pairs e = {one, one};
+            while (path != 0) {
+                float x[8];
+                int js[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const bool some = path != 0;
+                    const int j = some ? kBits - 1 - count_leading(path) : 0;
+                    js[m] = some ? j : -1;
+                    path &= (Word{1} << j) - 1;  // (nothing is left of none)
+                    const Pairs kj = pairs(*reinterpret_cast<const uint2 *>(s.k + j * kD + 4 * lane));
+                    const float4 d = *reinterpret_cast<const float4 *>(s.decay + j * kD + 4 * lane);
+                    const Pairs y = {f2_mul(e.x, kj.x), f2_mul(e.y, kj.y)};
+                    const float2 dk = f2_split(f2_fma(y.y, k.y, f2_mul(y.x, k.x)));
+                    const float2 dq = f2_split(f2_fma(y.y, q.y, f2_mul(y.x, q.x)));
+                    x[2 * m] = dk.x + dk.y;
+                    x[2 * m + 1] = dq.x + dq.y;
+                    if (some) e = {f2_mul(e.x, f2(d.x, d.y)), f2_mul(e.y, f2(d.z, d.w))};
+                }
+                const float sum = sum_eight(x);
+                const int m = lane >> 3, j = m == 0 ? js[0] : m == 1 ? js[1] : m == 2 ? js[2] : js[3];
+                if ((lane & 3) == 0 && j >= 0) {
+                    if (lane & 4) s.aq[j * s.nc + i] = sum;
+                    else if (j != i) s.ak[j * s.nc + i] = sum;
                 }
             }
+            write(f2_split(f2_mul(e.x, k.x)), f2_split(f2_mul(e.y, k.y)), f2_split(f2_mul(e.x, q.x)),
+                  f2_split(f2_mul(e.y, q.y)));
+        }
+        __syncthreads();
+        fetch_rows(u, a.v);
+
+        // The product: a warp has columns 16 warp .. + 15 of all rows.
+        const int g = lane >> 2, tq = lane & 3;
+        float acc[kEights][2][4], low[kEights][2][4];  // (the lower words' products apart: shorter chains)
+#pragma unroll
+        for (int m = 0; m < kEights; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
+#pragma unroll 2
+        for (int ks = 0; ks < kD / 16; ++ks) {
+            uint32_t b[3][2][2];  // word, tile, pair of k's
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k = 16 * ks + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
+                    if constexpr (kStateBf16) {
+                        const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * kPitch) + col;
+                        b[0][c][i] = x[0] | static_cast<uint32_t>(x[2 * kPitch]) << 16;
+                    } else {
+                        const float *x = s.state + k * kPitch + col;
+                        split3(x[0], x[kPitch], b[0][c][i], b[1][c][i], b[2][c][i]);
+                    }
+                }
+            // two eights at a time, their products in turn
+#pragma unroll
+            for (int m0 = 0; m0 < kEights; m0 += 2) {
+                if (m0 >= eights) break;
+                uint32_t w[2][3][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint8_t *rows = s.rows + (m0 + m) * Left::kEight + ks * Left::kBlock;
+                    if (m0 + m >= eights) break;
+                    if constexpr (Left::kWords) {
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(rows + i * 512 + lane * 16);
+                            w[m][i][0] = x.x;
+                            w[m][i][1] = x.y;
+                            w[m][i][2] = x.z;
+                            w[m][i][3] = x.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 x = reinterpret_cast<const float4 *>(rows)[lane * 2 + i];
+                            split3(x.x, x.y, w[m][0][2 * i], w[m][1][2 * i], w[m][2][2 * i]);
+                            split3(x.z, x.w, w[m][0][2 * i + 1], w[m][1][2 * i + 1], w[m][2][2 * i + 1]);
+                        }
+                    }
+                }
+                // words (i, k) of the two operands, i + k <= 2; a bf16 state is one word
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int k = 0; k < (kStateBf16 ? 1 : 3 - i); ++k)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            if (m0 + m >= eights) break;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                mma_bf16(i + k == 0 ? acc[m0 + m][c] : low[m0 + m][c], w[m][i], b[k][c]);
+                        }
+            }
+        }
+        sm100::cp_async_wait_all();
+        __syncthreads();
+        // nobody reads the state or the left operands any more: the next unit's state may come, and
+        // the products go where the operands were
+        if (more) fetch_state(next);
+        float *products = reinterpret_cast<float *>(s.rows);
 #pragma unroll
         for (int m = 0; m < kEights; ++m) {
             if (m >= eights) break;
-            uint32_t w[3][4];
-            const uint8_t *rows = s.rows + m * Left::kEight + ks * Left::kBlock;
-            if constexpr (Left::kWords) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(rows + i * 512 + lane * 16);
-                    w[i][0] = x.x;
-                    w[i][1] = x.y;
-                    w[i][2] = x.z;
-                    w[i][3] = x.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 x = reinterpret_cast<const float4 *>(rows)[lane * 2 + i];
-                    split3(x.x, x.y, w[0][2 * i], w[1][2 * i], w[2][2 * i]);
-                    split3(x.z, x.w, w[0][2 * i + 1], w[1][2 * i + 1], w[2][2 * i + 1]);
-                }
+            for (int c = 0; c < 2; ++c) {
+                float *to = products + (m * 16 + g) * kPitch + 16 * warp + 8 * c + 2 * tq;
+                *reinterpret_cast<float2 *>(to) = make_float2(acc[m][c][0] + low[m][c][0], acc[m][c][1] + low[m][c][1]);
+                *reinterpret_cast<float2 *>(to + 8 * kPitch) =
+                    make_float2(acc[m][c][2] + low[m][c][2], acc[m][c][3] + low[m][c][3]);
             }
-#pragma unroll
-            for (int i = 2; i >= 0; --i)  // word of the left operand
-#pragma unroll
-                for (int k = 2 - i; k >= 0; --k) {
-                    if (kStateBf16 && k > 0) continue;  // its state is one word
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) mma_bf16(i + k == 0 ? acc[m][c] : low[m][c], w[i], b[k][c]);
-                }
         }
-    }
-    sm100::cp_async_wait_all();
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < kEights; ++m) {
-        if (m >= eights) break;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float *to = s.state + (m * 16 + g) * kPitch + 16 * warp + 8 * c + 2 * tq;
-            *reinterpret_cast<float2 *>(to) = make_float2(acc[m][c][0] + low[m][c][0], acc[m][c][1] + low[m][c][1]);
-            *reinterpret_cast<float2 *>(to + 8 * kPitch) = make_float2(acc[m][c][2] + low[m][c][2], acc[m][c][3] + low[m][c][3]);
-        }
-    }
-    __syncthreads();
-    auto product = [&](int m, int r, int c) { return s.state[(m * 16 + r) * kPitch + c]; };
+        __syncthreads();
+        auto product = [&](int m, int r, int c) { return products[(m * 16 + r) * kPitch + c]; };
 
-    // The updates: a thread a column, eight nodes in registers.
-    const int c = tid & (kD - 1);
-    if (tid < kD) {
+        // The updates: a thread a column, eight nodes in registers.
+        const int c = tid & (kD - 1);
+        if (tid < kD) {
+            for (int m = 0; m < eights; ++m) {
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = product(m, i, c);
+#pragma unroll 4
+                for (int j = 0; j < 8 * m; ++j) {
+                    const float x = s.decay[j * kD + c];
+                    const float4 y = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m);
+                    const float4 z = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m + 4);
+                    w[0] += y.x * x;
+                    w[1] += y.y * x;
+                    w[2] += y.z * x;
+                    w[3] += y.w * x;
+                    w[4] += z.x * x;
+                    w[5] += z.y * x;
+                    w[6] += z.z * x;
+                    w[7] += z.w * x;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int node = 8 * m + i;
+                    if (node >= n) break;
+                    const float x = s.beta[node] * (__bfloat162float(s.k[node * kD + c]) - w[i]);
+                    s.decay[node * kD + c] = x;
+                    if (a.u != nullptr) a.u[u.at(a, node) + c] = x;
+#pragma unroll
+                    for (int l = i + 1; l < 8; ++l) w[l] += s.ak[node * s.nc + 8 * m + l] * x;
+                }
+            }
+        }
+        __syncthreads();
+        if (more) fetch_rows(next, a.k);
+        // The outputs: half of an eight's nodes for each half of the threads.
         for (int m = 0; m < eights; ++m) {
-            float w[8];
+            float w[4];
+            const int i0 = 8 * m + 4 * (tid / kD);
+            if (i0 >= n) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = product(m, i, c);
-            for (int j = 0; j < 8 * m; ++j) {
-                const float u = s.decay[j * kD + c];
-                const float4 x = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m);
-                const float4 y = *reinterpret_cast<const float4 *>(s.ak + j * s.nc + 8 * m + 4);
-                w[0] += x.x * u;
-                w[1] += x.y * u;
-                w[2] += x.z * u;
-                w[3] += x.w * u;
-                w[4] += y.x * u;
-                w[5] += y.y * u;
-                w[6] += y.z * u;
-                w[7] += y.w * u;
+            for (int i = 0; i < 4; ++i) w[i] = product(m, 8 + (i0 & 7) + i, c);
+            const int end = min(i0 + 4, n);
+#pragma unroll 4
+            for (int j = 0; j < end; ++j) {
+                const float x = s.decay[j * kD + c];
+                const float4 y = *reinterpret_cast<const float4 *>(s.aq + j * s.nc + i0);
+                w[0] += y.x * x;
+                w[1] += y.y * x;
+                w[2] += y.z * x;
+                w[3] += y.w * x;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int node = 8 * m + i;
-                if (node >= n) break;
-                const float u = s.beta[node] * (__bfloat162float(s.k[node * kD + c]) - w[i]);
-                s.decay[node * kD + c] = u;
-                if (a.u != nullptr) a.u[at(node) + c] = u;
-#pragma unroll
-                for (int l = i + 1; l < 8; ++l) w[l] += s.ak[node * s.nc + 8 * m + l] * u;
-            }
+            for (int i = 0; i < 4; ++i)
+                if (i0 + i < n) write_out<kOutBf16>(a.o, u.at(a, i0 + i) + c, w[i]);
         }
-    }
-    __syncthreads();
-    // The outputs: half of an eight's nodes for each half of the threads.
-    const int half = tid / kD;
-    for (int m = 0; m < eights; ++m) {
-        float w[4];
-        const int i0 = 8 * m + 4 * half;
-        if (i0 >= n) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = product(m, 8 + 4 * half + i, c);
-        const int end = min(i0 + 4, n);
-        for (int j = 0; j < end; ++j) {
-            const float u = s.decay[j * kD + c];
-            const float4 x = *reinterpret_cast<const float4 *>(s.aq + j * s.nc + i0);
-            w[0] += x.x * u;
-            w[1] += x.y * u;
-            w[2] += x.z * u;
-            w[3] += x.w * u;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i0 + i < n) write_out<kOutBf16>(a.o, at(i0 + i) + c, w[i]);
+        __syncthreads();
+        u = next;
     }
 }
 
@@ -495,18 +558,21 @@ __global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep
 }
 
 template <bool kStateBf16, bool kOutBf16, int kEights>
-cudaError_t decode_n(const TreeStep &a, cudaStream_t s) {
+cudaError_t decode_n(const TreeStep &a, int num_sms, cudaStream_t s) {
     const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16, kEights>;
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem<kEights>::bytes(8 * kEights));
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.B * a.H), kThreads, TreeSmem<kEights>::bytes(TreeSmem<kEights>::nodes(a.max_nodes)), s>>>(a);
+    const int64_t units = static_cast<int64_t>(a.B) * a.H, most = static_cast<int64_t>(num_sms) * (kEights <= 2 ? 2 : 1);
+    kernel<<<static_cast<unsigned>(units < most ? units : most), kThreads,
+             TreeSmem<kEights>::bytes(TreeSmem<kEights>::nodes(a.max_nodes)), s>>>(a);
     return cudaGetLastError();
 }
 
 template <bool kStateBf16, bool kOutBf16>
-cudaError_t decode_t(const TreeStep &a, cudaStream_t s) {
-    return a.max_nodes <= 16 ? decode_n<kStateBf16, kOutBf16, 2>(a, s) : decode_n<kStateBf16, kOutBf16, 8>(a, s);
+cudaError_t decode_t(const TreeStep &a, int num_sms, cudaStream_t s) {
+    return a.max_nodes <= 16 ? decode_n<kStateBf16, kOutBf16, 2>(a, num_sms, s)
+                             : decode_n<kStateBf16, kOutBf16, 8>(a, num_sms, s);
 }
 
 template <bool kStateBf16>
@@ -517,9 +583,9 @@ cudaError_t commit_t(const TreeStep &a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_tree_decode(const TreeStep &a, bool state_bf16, bool o_bf16, cudaStream_t s) {
-    if (state_bf16) return o_bf16 ? decode_t<true, true>(a, s) : decode_t<true, false>(a, s);
-    return o_bf16 ? decode_t<false, true>(a, s) : decode_t<false, false>(a, s);
+cudaError_t launch_tree_decode(const TreeStep &a, bool state_bf16, bool o_bf16, int num_sms, cudaStream_t s) {
+    if (state_bf16) return o_bf16 ? decode_t<true, true>(a, num_sms, s) : decode_t<true, false>(a, num_sms, s);
+    return o_bf16 ? decode_t<false, true>(a, num_sms, s) : decode_t<false, false>(a, num_sms, s);
 }
 
 cudaError_t launch_tree_commit(const TreeStep &a, bool state_bf16, cudaStream_t s) {
