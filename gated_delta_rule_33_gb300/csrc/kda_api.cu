@@ -951,7 +951,7 @@ kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void 
     a.max_nodes = max_nodes;
     a.N = N;
     a.err = dev->error_word;
-    return from_cuda(kda::launch_tree_conv(a, static_cast<cudaStream_t>(stream)));
+    return from_cuda(kda::launch_tree_conv(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_short_conv_tree_commit(const void *x_q, const void *x_k, const void *x_v,

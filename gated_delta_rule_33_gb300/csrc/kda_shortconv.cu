@@ -28,6 +28,8 @@
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -39,6 +41,7 @@ constexpr int kWarpCh = 32 * kLaneCh;      // 256 channels per warp
 constexpr int kWarps = 8;
 constexpr int kTT = 128;                   // tokens per warp
 constexpr int kBatch = 4;                  // rows requested together
+constexpr int kTreeBlocks = 3;             // blocks an SM over trees: 68 KB each at 64 nodes
 constexpr float kNormEps = 1e-6f;
 
 static_assert(kWarpCh == 2 * kHeadDim, "a warp covers two heads; the norm reduces 16 lanes");
@@ -327,60 +330,82 @@ __global__ void __launch_bounds__(kWarps * 32) short_conv_step_kernel(
     }
 }
 
-// A tree of drafted tokens per request; the pool is read, not changed.  grid = (channel
-// groups of kWarpCh, B, 3 streams).  The three inputs before a node's own are those of its
-// nearest ancestors, then the carried ones, the last of them first.  The block stages the
-// request's rows of its channels, and its carried rows, in shared memory: each is an input of
-// every node below it, and comes from memory once.
-__global__ void __launch_bounds__(kWarps * 32) tree_conv_kernel(const TreeConv a) {
-    extern __shared__ __align__(16) uint8_t s_rows[];  // [max_nodes + 3][kWarpCh] bf16
-    const int z = blockIdx.z, b = blockIdx.y;
+// A tree of drafted tokens per request; the pool is read, not changed.  The three inputs before
+// a node's own are those of its nearest ancestors, then the carried ones, the last of them
+// first.  The block stages the request's rows of its channels, and its carried rows, in shared
+// memory: each is an input of every node below it, and comes from memory once.
+//
+// grid = (channel groups of kWarpCh, parts, 3 streams); a block takes requests blockIdx.y,
+// + parts, ..  A group's taps are 16 bytes a channel, as much as 8 rows of it, so a block that
+// held one request's 21 rows read them again for every request; one that walks over requests
+// reads them once, and the next request's rows arrive while this one's are worked on.
+__global__ void __launch_bounds__(kWarps * 32, kTreeBlocks) tree_conv_kernel(const TreeConv a) {
+    extern __shared__ __align__(16) uint8_t s_rows[];  // [2][max_nodes + 3][kWarpCh] bf16
+    const int z = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * kWarpCh + lane * kLaneCh;
     const bool active = c < a.C;
-    const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
-    const int sl = a.slots != nullptr ? a.slots[b] : b;
-    if (threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && (t.bad || sl >= a.num_slots))
-        record_device_error(a.err, kDevInvalidArg);
-    __nv_bfloat16 *y = pick(a.y, z) + t.first * a.C + c;
-    if (t.n == 0 || sl < 0 || sl >= a.num_slots) {
-        Pair zero[kLanePairs];
-        zero_row(zero);
-        for (int i = warp; i < t.rows; i += kWarps)
-            if (active) store_row(y + static_cast<int64_t>(i) * a.C, zero);
-        return;
-    }
-    const __nv_bfloat16 *x = pick(a.x, z) + t.first * a.C + c;
+    const int half = (a.max_nodes + kHalo) * kWarpCh * 2;
+    const __nv_bfloat16 *xs = pick(a.x, z) + c;
+
+    TreeRows now{0, 0, 0, false}, next;
+    uint64_t words = 0, words_next;  // lane i: the word of node warp + kWarps i
+    auto fetch = [&](int b, uint8_t *mine, TreeRows &t, uint64_t &own) {
+        t = tree_rows(a.cu, b, a.N, a.max_nodes);
+        own = 0;
+        const int sl = a.slots != nullptr ? a.slots[b] : b;
+        if (threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && (t.bad || sl >= a.num_slots))
+            record_device_error(a.err, kDevInvalidArg);
+        if (sl < 0 || sl >= a.num_slots) t.n = 0;
+        if (t.n == 0) return;
+        const __nv_bfloat16 *x = xs + t.first * a.C;
+        for (int i = warp; i < t.n + kHalo; i += kWarps) {
+            const __nv_bfloat16 *src = i < t.n ? x + static_cast<int64_t>(i) * a.C
+                                               : a.pool + state_index(sl, z, i - t.n, a.C, c);
+            sm100::cp_async_16(mine + i * kWarpCh * 2, active ? src : a.pool, active);
+        }
+        if (warp + kWarps * lane < t.n) own = a.ancestors[t.first + warp + kWarps * lane];
+    };
     uint8_t *mine = s_rows + lane * kLaneCh * 2;
-    for (int i = warp; i < t.n + kHalo; i += kWarps) {
-        const __nv_bfloat16 *src = i < t.n ? x + static_cast<int64_t>(i) * a.C
-                                           : a.pool + state_index(sl, z, i - t.n, a.C, c);
-        sm100::cp_async_16(mine + i * kWarpCh * 2, active ? src : a.pool, active);
-    }
+    fetch(blockIdx.y, mine, now, words);
     Pair w[kLanePairs][kTaps];
     load_taps(pick(a.w, z), c, active, w);
-    sm100::cp_async_wait_all();
-    __syncthreads();
-    auto row = [&](int i, Pair (&r)[kLanePairs]) {
-        unpack_row(*reinterpret_cast<const uint4 *>(mine + i * kWarpCh * 2), r);
-    };
-    for (int i = warp; i < t.n; i += kWarps) {
-        uint64_t above = a.ancestors[t.first + i] & bits_below(i);
-        Pair win[kHalo][kLanePairs], xt[kLanePairs], out[kLanePairs];
-        row(i, xt);
-        int carried = t.n + kHalo;
-#pragma unroll
-        for (int r = kHalo - 1; r >= 0; --r) {
-            if (above != 0) {
-                const int j = top_bit(above);
-                above ^= uint64_t{1} << j;
-                row(j, win[r]);
-            } else {
-                row(--carried, win[r]);
-            }
+    for (int b = blockIdx.y, buf = 0; b < a.B; b += gridDim.y, buf ^= 1) {
+        sm100::cp_async_wait_all();
+        __syncthreads();  // this request's rows are there, and the other half has been read
+        next.n = next.rows = 0;
+        if (b + static_cast<int>(gridDim.y) < a.B)
+            fetch(b + gridDim.y, mine + (buf ^ 1) * half, next, words_next);
+        __nv_bfloat16 *y = pick(a.y, z) + now.first * a.C + c;
+        if (now.n == 0) {
+            Pair zero[kLanePairs];
+            zero_row(zero);
+            for (int i = warp; i < now.rows; i += kWarps)
+                if (active) store_row(y + static_cast<int64_t>(i) * a.C, zero);
         }
-        conv_row(w, win, xt, z < 2, out);
-        if (active) store_row(y + static_cast<int64_t>(i) * a.C, out);
+        auto row = [&](int i, Pair (&r)[kLanePairs]) {
+            unpack_row(*reinterpret_cast<const uint4 *>(mine + buf * half + i * kWarpCh * 2), r);
+        };
+        for (int i = warp, k = 0; i < now.n; i += kWarps, ++k) {
+            uint64_t above = __shfl_sync(0xffffffffu, words, k) & bits_below(i);
+            Pair win[kHalo][kLanePairs], xt[kLanePairs], out[kLanePairs];
+            row(i, xt);
+            int carried = now.n + kHalo;
+#pragma unroll
+            for (int r = kHalo - 1; r >= 0; --r) {
+                if (above != 0) {
+                    const int j = top_bit(above);
+                    above ^= uint64_t{1} << j;
+                    row(j, win[r]);
+                } else {
+                    row(--carried, win[r]);
+                }
+            }
+            conv_row(w, win, xt, z < 2, out);
+            if (active) store_row(y + static_cast<int64_t>(i) * a.C, out);
+        }
+        now = next;
+        words = words_next;
     }
 }
 
@@ -417,9 +442,16 @@ __global__ void __launch_bounds__(kWarps * 32) tree_conv_commit_kernel(const Tre
 
 }  // namespace
 
-cudaError_t launch_tree_conv(const TreeConv &a, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((a.C + kWarpCh - 1) / kWarpCh), a.B, 3);
-    const int smem = (a.max_nodes + kHalo) * kWarpCh * 2;  // 33.5 KB at most
+cudaError_t launch_tree_conv(const TreeConv &a, int num_sms, cudaStream_t s) {
+    const int groups = (a.C + kWarpCh - 1) / kWarpCh;
+    const int parts = std::min(a.B, std::max(1, kTreeBlocks * num_sms / (groups * 3)));
+    const dim3 grid(groups, parts, 3);
+    constexpr int kRowBytes = 2 * kWarpCh * 2;
+    const int smem = (a.max_nodes + kHalo) * kRowBytes;  // 67 KB at most
+    const cudaError_t e = cudaFuncSetAttribute(tree_conv_kernel,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kTreeNodes + kHalo) * kRowBytes);
+    if (e != cudaSuccess) return e;
     tree_conv_kernel<<<grid, kWarps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }

@@ -77,7 +77,7 @@ struct TreeConv {
     unsigned int *err;
 };
 
-cudaError_t launch_tree_conv(const TreeConv &a, cudaStream_t s);
+cudaError_t launch_tree_conv(const TreeConv &a, int num_sms, cudaStream_t s);
 cudaError_t launch_tree_conv_commit(const TreeConv &a, cudaStream_t s);
 
 struct TreeAttention {
