@@ -41,6 +41,7 @@ constexpr int kWarpCh = 32 * kLaneCh;      // 256 channels per warp
 constexpr int kWarps = 8;
 constexpr int kTT = 128;                   // tokens per warp
 constexpr int kBatch = 4;                  // rows requested together
+constexpr int kTreeWarps = 8;              // warps of a block over trees
 constexpr int kTreeBlocks = 3;             // blocks an SM over trees: 68 KB each at 64 nodes
 constexpr float kNormEps = 1e-6f;
 
@@ -339,73 +340,95 @@ __global__ void __launch_bounds__(kWarps * 32) short_conv_step_kernel(
 // + parts, ..  A group's taps are 16 bytes a channel, as much as 8 rows of it, so a block that
 // held one request's 21 rows read them again for every request; one that walks over requests
 // reads them once, and the next request's rows arrive while this one's are worked on.
-__global__ void __launch_bounds__(kWarps * 32, kTreeBlocks) tree_conv_kernel(const TreeConv a) {
+//
+// Each row is a few hundred instructions, so what all rows share is kept out of them: two warps
+// find the rows of every node's window while the others still work on the request before.
+__global__ void __launch_bounds__(kTreeWarps * 32, kTreeBlocks) tree_conv_kernel(const TreeConv a) {
     extern __shared__ __align__(16) uint8_t s_rows[];  // [2][max_nodes + 3][kWarpCh] bf16
+    __shared__ uint32_t s_window[2][kTreeNodes];       // offsets of a window's rows, 7 bits each
+    constexpr int kRow = kWarpCh * 2, kRowBits = 9;
+    static_assert(kRow == 1 << kRowBits && kTreeNodes + kHalo < 128 && kRowBits + 21 <= 32, "packed");
     const int z = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * kWarpCh + lane * kLaneCh;
     const bool active = c < a.C;
-    const int half = (a.max_nodes + kHalo) * kWarpCh * 2;
+    const int half = (a.max_nodes + kHalo) * kRow;
     const __nv_bfloat16 *xs = pick(a.x, z) + c;
+    const int64_t step = static_cast<int64_t>(kTreeWarps) * a.C;
 
     TreeRows now{0, 0, 0, false}, next;
-    uint64_t words = 0, words_next;  // lane i: the word of node warp + kWarps i
-    auto fetch = [&](int b, uint8_t *mine, TreeRows &t, uint64_t &own) {
+    uint64_t word = 0;  // thread i < 64: of node i of the request last fetched
+    auto fetch = [&](int b, uint8_t *mine, TreeRows &t) {
         t = tree_rows(a.cu, b, a.N, a.max_nodes);
-        own = 0;
         const int sl = a.slots != nullptr ? a.slots[b] : b;
         if (threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && (t.bad || sl >= a.num_slots))
             record_device_error(a.err, kDevInvalidArg);
         if (sl < 0 || sl >= a.num_slots) t.n = 0;
         if (t.n == 0) return;
-        const __nv_bfloat16 *x = xs + t.first * a.C;
-        for (int i = warp; i < t.n + kHalo; i += kWarps) {
-            const __nv_bfloat16 *src = i < t.n ? x + static_cast<int64_t>(i) * a.C
-                                               : a.pool + state_index(sl, z, i - t.n, a.C, c);
-            sm100::cp_async_16(mine + i * kWarpCh * 2, active ? src : a.pool, active);
+        const __nv_bfloat16 *x = active ? xs + (t.first + warp) * a.C : a.pool;
+        uint8_t *to = mine + warp * kRow;
+        for (int i = warp; i < t.n; i += kTreeWarps, to += kTreeWarps * kRow, x += active ? step : 0)
+            sm100::cp_async_16(to, x, active);
+        if (warp >= kTreeWarps - kHalo) {
+            const int r = warp - (kTreeWarps - kHalo);
+            sm100::cp_async_16(mine + (t.n + r) * kRow,
+                               active ? a.pool + state_index(sl, z, r, a.C, c) : a.pool, active);
         }
-        if (warp + kWarps * lane < t.n) own = a.ancestors[t.first + warp + kWarps * lane];
+        if (static_cast<int>(threadIdx.x) < t.n) word = a.ancestors[t.first + threadIdx.x];
+    };
+    // The rows before node i's own, nearest last.
+    auto find_window = [&](int n, uint32_t *window) {
+        const int i = threadIdx.x;
+        if (i >= n) return;
+        uint64_t above = word & bits_below(i);
+        int carried = n + kHalo;
+        uint32_t packed = 0;
+#pragma unroll
+        for (int r = kHalo - 1; r >= 0; --r) {
+            int j;
+            if (above != 0) {
+                j = top_bit(above);
+                above ^= uint64_t{1} << j;
+            } else {
+                j = --carried;
+            }
+            packed |= static_cast<uint32_t>(j) << (kRowBits + 7 * r);
+        }
+        window[i] = packed;
     };
     uint8_t *mine = s_rows + lane * kLaneCh * 2;
-    fetch(blockIdx.y, mine, now, words);
+    fetch(blockIdx.y, mine, now);
     Pair w[kLanePairs][kTaps];
     load_taps(pick(a.w, z), c, active, w);
+    find_window(now.n, s_window[0]);
     for (int b = blockIdx.y, buf = 0; b < a.B; b += gridDim.y, buf ^= 1) {
         sm100::cp_async_wait_all();
         __syncthreads();  // this request's rows are there, and the other half has been read
         next.n = next.rows = 0;
         if (b + static_cast<int>(gridDim.y) < a.B)
-            fetch(b + gridDim.y, mine + (buf ^ 1) * half, next, words_next);
-        __nv_bfloat16 *y = pick(a.y, z) + now.first * a.C + c;
+            fetch(b + gridDim.y, mine + (buf ^ 1) * half, next);
+        __nv_bfloat16 *y = pick(a.y, z) + (now.first + warp) * a.C + c;
         if (now.n == 0) {
             Pair zero[kLanePairs];
             zero_row(zero);
-            for (int i = warp; i < now.rows; i += kWarps)
-                if (active) store_row(y + static_cast<int64_t>(i) * a.C, zero);
+            for (int i = warp; i < now.rows; i += kTreeWarps, y += step)
+                if (active) store_row(y, zero);
         }
-        auto row = [&](int i, Pair (&r)[kLanePairs]) {
-            unpack_row(*reinterpret_cast<const uint4 *>(mine + buf * half + i * kWarpCh * 2), r);
+        const uint8_t *rows = mine + buf * half;
+        auto row = [&](int offset, Pair (&r)[kLanePairs]) {
+            unpack_row(*reinterpret_cast<const uint4 *>(rows + offset), r);
         };
-        for (int i = warp, k = 0; i < now.n; i += kWarps, ++k) {
-            uint64_t above = __shfl_sync(0xffffffffu, words, k) & bits_below(i);
+        for (int i = warp; i < now.n; i += kTreeWarps, y += step) {
+            const uint32_t packed = s_window[buf][i];
             Pair win[kHalo][kLanePairs], xt[kLanePairs], out[kLanePairs];
-            row(i, xt);
-            int carried = now.n + kHalo;
 #pragma unroll
-            for (int r = kHalo - 1; r >= 0; --r) {
-                if (above != 0) {
-                    const int j = top_bit(above);
-                    above ^= uint64_t{1} << j;
-                    row(j, win[r]);
-                } else {
-                    row(--carried, win[r]);
-                }
-            }
+            for (int r = 0; r < kHalo; ++r) row((packed >> (7 * r)) & (127u << kRowBits), win[r]);
+            row(i * kRow, xt);
             conv_row(w, win, xt, z < 2, out);
-            if (active) store_row(y + static_cast<int64_t>(i) * a.C, out);
+            if (active) store_row(y, out);
         }
+        find_window(next.n, s_window[buf ^ 1]);
         now = next;
-        words = words_next;
     }
 }
 
@@ -452,7 +475,7 @@ cudaError_t launch_tree_conv(const TreeConv &a, int num_sms, cudaStream_t s) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (kTreeNodes + kHalo) * kRowBytes);
     if (e != cudaSuccess) return e;
-    tree_conv_kernel<<<grid, kWarps * 32, smem, s>>>(a);
+    tree_conv_kernel<<<grid, kTreeWarps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 
