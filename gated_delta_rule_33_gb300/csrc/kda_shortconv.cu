@@ -41,8 +41,8 @@ constexpr int kWarpCh = 32 * kLaneCh;      // 256 channels per warp
 constexpr int kWarps = 8;
 constexpr int kTT = 128;                   // tokens per warp
 constexpr int kBatch = 4;                  // rows requested together
-constexpr int kTreeWarps = 8;              // warps of a block over trees
-constexpr int kTreeBlocks = 3;             // blocks an SM over trees: 68 KB each at 64 nodes
+constexpr int kTreeWarps = 4;              // warps of a block over trees
+constexpr int kTreeBlocks = 6;             // blocks an SM, where shared memory lets them
 constexpr float kNormEps = 1e-6f;
 
 static_assert(kWarpCh == 2 * kHeadDim, "a warp covers two heads; the norm reduces 16 lanes");
@@ -339,10 +339,13 @@ __global__ void __launch_bounds__(kWarps * 32) short_conv_step_kernel(
 // grid = (channel groups of kWarpCh, parts, 3 streams); a block takes requests blockIdx.y,
 // + parts, ..  A group's taps are 16 bytes a channel, as much as 8 rows of it, so a block that
 // held one request's 21 rows read them again for every request; one that walks over requests
-// reads them once, and the next request's rows arrive while this one's are worked on.
+// reads them once, and the next request's rows arrive while this one's are worked on: 240 us ->
+// 162 at 128 requests of 9 to 33 nodes and 12288 channels a stream (63 at the rate of a copy).
 //
 // Each row is a few hundred instructions, so what all rows share is kept out of them: two warps
-// find the rows of every node's window while the others still work on the request before.
+// find the rows of every node's window for all of them (162 -> 111 us).  Six blocks of 4 warps
+// (90 us) beat three of 8 (111) and four of 6 (102): a warp's share of what a request costs
+// beside its rows is spread over more of them.  Issue slots bound it, not memory.
 __global__ void __launch_bounds__(kTreeWarps * 32, kTreeBlocks) tree_conv_kernel(const TreeConv a) {
     extern __shared__ __align__(16) uint8_t s_rows[];  // [2][max_nodes + 3][kWarpCh] bf16
     __shared__ uint32_t s_window[2][kTreeNodes];       // offsets of a window's rows, 7 bits each
@@ -466,11 +469,12 @@ __global__ void __launch_bounds__(kWarps * 32) tree_conv_commit_kernel(const Tre
 }  // namespace
 
 cudaError_t launch_tree_conv(const TreeConv &a, int num_sms, cudaStream_t s) {
-    const int groups = (a.C + kWarpCh - 1) / kWarpCh;
-    const int parts = std::min(a.B, std::max(1, kTreeBlocks * num_sms / (groups * 3)));
-    const dim3 grid(groups, parts, 3);
     constexpr int kRowBytes = 2 * kWarpCh * 2;
     const int smem = (a.max_nodes + kHalo) * kRowBytes;  // 67 KB at most
+    const int blocks = std::min(kTreeBlocks, (228 << 10) / (smem + 1536));
+    const int groups = (a.C + kWarpCh - 1) / kWarpCh;
+    const int parts = std::min(a.B, std::max(1, blocks * num_sms / (groups * 3)));
+    const dim3 grid(groups, parts, 3);
     const cudaError_t e = cudaFuncSetAttribute(tree_conv_kernel,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (kTreeNodes + kHalo) * kRowBytes);

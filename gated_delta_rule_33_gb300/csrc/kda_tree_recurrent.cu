@@ -470,7 +470,7 @@ constexpr int kCommitNodes = 16;
 constexpr int kRows = kD / kWarps;
 
 template <bool kStateBf16>
-__global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep a) {
+__global__ void __launch_bounds__(kThreads, 3) tree_commit_kernel(const TreeStep a) {
     __shared__ __align__(16) float s_w[kCommitNodes][kD], s_u[kCommitNodes][kD];
     __shared__ float s_decay[kD];
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
@@ -483,12 +483,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep
     // the whole state in flight first
     const int64_t base = (slot * a.H + h) * (kD * kD) + warp * kD + 4 * lane;
     float4 x[kRows];
-    uint2 raw[kStateBf16 ? kRows : 1];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         const int64_t i = base + r * kWarps * kD;
-        if constexpr (kStateBf16) raw[r] = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.pool) + i));
-        else x[r] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.pool) + i));
+        if constexpr (kStateBf16) {
+            // four bf16 in the first two floats: one set of registers for both forms
+            const float2 raw = __ldcs(reinterpret_cast<const float2 *>(static_cast<const __nv_bfloat16 *>(a.pool) + i));
+            x[r].x = raw.x;
+            x[r].y = raw.y;
+        } else {
+            x[r] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.pool) + i));
+        }
     }
     uint64_t path = path_of(a.ancestors[t.first + end], end);
     auto at = [&](int i) { return ((t.first + i) * a.H + h) * kD; };
@@ -525,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_commit_kernel(const TreeStep
         if constexpr (kStateBf16)
             if (first)
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) x[r] = widen4(raw[r]);
+                for (int r = 0; r < kRows; ++r)
+                    x[r] = widen4(make_uint2(__float_as_uint(x[r].x), __float_as_uint(x[r].y)));
         first = false;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
