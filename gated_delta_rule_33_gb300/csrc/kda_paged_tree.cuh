@@ -127,7 +127,8 @@ struct Shape {
     struct Small {  // what lies behind the tiles
         uint64_t qfull, kfull[kNK], kempty[kNK], vfull[kNV], vempty[kNV], sfull[kBufs], pfull[kBufs][2], pfree[kBufs], scored, done, ofree, drain[2];
         int64_t warp_sum[kThreads / 32], place[2];
-        float top[2][2][128];  // by row: what the two warpgroups tell one another, every second time
+        // by row: the reference that a warpgroup hands to the other (top[0]), and what they exchange in the end
+        float top[2][128];
         uint64_t raw[2][2][kNR > 0 ? kNR : 1];  // keys and values, halves of rows
         uint32_t valid[kTilesAhead][kKeys / 32];  // which rows of a tile are keys
         uint32_t tmem;
@@ -428,6 +429,13 @@ __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, uint
 __device__ __forceinline__ void pair_barrier(int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
 }
+// One of them (of warpgroup wg) waits for what the other has done; the other says so.
+__device__ __forceinline__ void pair_wait(int quarter, int wg) {
+    asm volatile("bar.sync %0, 64;" ::"r"(5 + wg * 4 + quarter) : "memory");
+}
+__device__ __forceinline__ void pair_arrive(int quarter, int wg) {
+    asm volatile("bar.arrive %0, 64;" ::"r"(5 + (wg ^ 1) * 4 + quarter) : "memory");
+}
 
 template <int kRegs>
 __device__ __forceinline__ void take_registers() {
@@ -467,7 +475,6 @@ template <class S>
 __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __grid_constant__ Args args) {
     constexpr int kD = S::kD, kM = S::kM, kKeys = S::kKeys;
     constexpr bool kFp8 = S::kFp8;
-    constexpr int kHalf = kKeys / 2;
     constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles: 1024-byte groups of rows
     typename S::Small &sm = *reinterpret_cast<typename S::Small *>(smem + S::kOffSmall);
@@ -525,21 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     if (warp < kSoftWarps) {
         // ---- queries in, weights, outputs ------------------------------------------------
         take_registers<kSoftRegs>();
-        // (A wait that runs out ends no loop here: the warp still meets the other warpgroup's.)
         Waits wait = {a.err, true};
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t step = 0, tiles_done = 0, units = 0;
-        // What the other warpgroup has for this lane's row, for what this one has.  (Two places in
-        // turn: who writes the first again has met the other since it read it.)
-        uint32_t told = 0;
-        auto exchange = [&](float x) {
-            sm.top[told][wg][lrow] = x;
-            pair_barrier(quarter);
-            x = sm.top[told][wg ^ 1][lrow];
-            told ^= 1;
-            return x;
-        };
         // Queries for an 8-bit cache, as fp16: a unit's, this lane's half of its rows, scaled by a
         // power of two that puts a row's largest value below 2^15; exps: those powers.
         int exps[kM], exps_next[kM];
@@ -564,7 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         for (const uint32_t y : {x.x, x.y, x.z, x.w})
                             top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
                     }
-                top = max(top, __float_as_uint(exchange(__uint_as_float(top))));
+                sm.top[wg][lrow] = __uint_as_float(top);
+                pair_barrier(quarter);
+                top = max(top, __float_as_uint(sm.top[wg ^ 1][lrow]));
+                pair_barrier(quarter);
                 exps[t] = min(max(static_cast<int>(top >> 23), 15), 254) - 127 - 14;
                 const float up = power_of_two(-exps[t]);
                 if (real)
@@ -588,108 +587,114 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         };
         bool more = at.take(a);
         if (kFp8 && more) queries(at, exps);
-        while (more) {
+        while (more && wait.ok) {
             const int m_used = at.m_tiles(at.rg);
             const int tiles = at.t1 - at.t, steps = tiles * m_used;
-            // A lane has a row of each m tile: the one of this step, and the other's.
-            struct Row {
-                bool some;      // a row of this warp is one
-                uint64_t word;
-                float c, m, l;  // what turns its products into scores; reference; sum of weights
-            };
-            auto begin = [&](int mt) {
-                const int rr = at.rg * S::kRows + mt * 128 + lrow;
-                Row r = {rr - lane < at.rows && mt < m_used, 0, 0.f, -INFINITY, 0.f};
-                uint32_t node, head;
-                args.group.divmod(rr, node, head);
-                if (rr < at.rows) r.word = a.ancestors[at.first + node] & bits_below(at.n);
-                // above 0 (the queries of a negative scale are negated by the product)
-                r.c = at_least_normal(fabsf(a.scale * kLog2e * (a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f)));
-                if constexpr (kFp8) r.c = at_least_normal(r.c * power_of_two(mt == 0 ? exps[0] : exps[kM - 1]));
-                return r;
-            };
-            Row r = begin(0), r1;
-            if constexpr (kM == 2) r1 = begin(1);
-            auto change_rows = [&]() {
-                if constexpr (kM == 2)
-                    if (m_used == 2) {
-                        const Row x = r;
-                        r = r1;
-                        r1 = x;
-                    }
-            };
+            // This warpgroup has every second step: of two m tiles always the same one, of one
+            // every second tile.
+            const int i0 = (step + wg) & 1, mt = m_used == 1 ? 0 : i0;
+            const int rr = at.rg * S::kRows + mt * 128 + lrow;  // this lane's row
+            const bool some = rr - lane < at.rows, real = rr < at.rows;
+            uint32_t node, head;
+            args.group.divmod(rr, node, head);
+            const int64_t row = at.first + node;
+            const int qh = at.h * a.group + static_cast<int>(head);
+            const uint64_t word = real ? a.ancestors[row] & bits_below(at.n) : 0;
+            // what turns the row's products into scores: above 0 (the queries of a negative scale
+            // are negated by the product)
+            float c = at_least_normal(fabsf(a.scale * kLog2e * (a.cache.k_scale != nullptr ? a.cache.k_scale[at.h] : 1.f)));
+            if constexpr (kFp8) c = at_least_normal(c * power_of_two(mt == 0 ? exps[0] : exps[kM - 1]));
+            float m = -INFINITY, l = 0.f;
             Cursor<S> next = at;
             more = next.take(a);
 
-            for (int i = 0; i < steps; ++i, change_rows()) {
+            for (int i = i0; i < steps && wait.ok; i += 2) {
                 const int tile = m_used == 1 ? i : i >> 1;
                 const uint32_t g = step + i, buf = g % S::kBufs;
-                wait(&sm.sfull[buf], (g / S::kBufs) & 1);
-                if (r.some) {
+                if (!wait(&sm.sfull[buf], (g / S::kBufs) & 1)) break;
+                if (some) {
                     tc_fence_after();
-                    // this warpgroup's half of the keys
-                    const uint32_t cols = lanes + buf * kKeys + wg * kHalf;
-                    float s[kHalf];
+                    const uint32_t cols = lanes + buf * kKeys;
+                    // the keys that the row sees, where that is not all of them
+                    const uint32_t *v = sm.valid[(tiles_done + tile) % S::kTilesAhead];
+                    const int d = (at.t + tile) * kKeys - (at.len - at.n);
+                    bool all = true;
 #pragma unroll
-                    for (int k = 0; k < kHalf / 32; ++k) tmem_ld32(cols + 32 * k, *reinterpret_cast<float (*)[32]>(s + 32 * k));
-                    // which of them the row sees, where that is not all of them
-                    const uint32_t *v = sm.valid[(tiles_done + tile) % S::kTilesAhead] + wg * (kHalf / 32);
-                    const int d = (at.t + tile) * kKeys + wg * kHalf - (at.len - at.n);
-                    bool all = d + kHalf <= 0;
-#pragma unroll
-                    for (int k = 0; k < kHalf / 32; ++k) all &= v[k] == 0xffffffffu;
-                    tmem_wait_ld();
-                    if (!all)
-#pragma unroll
-                        for (int k = 0; k < kHalf / 32; ++k) {
-                            const uint32_t seen = v[k] & static_cast<uint32_t>(seen_from(r.word, d + 32 * k));
+                    for (int k = 0; k < kKeys / 32; ++k) all &= v[k] == 0xffffffffu;
+                    if (d + kKeys > 0 || !all) {
+#pragma unroll 1
+                        for (int k = 0; k < kKeys / 32; ++k) {
+                            uint32_t seen = v[k];
+                            if (d + 32 * (k + 1) > 0) seen &= static_cast<uint32_t>(seen_from(word, d + 32 * k));
+                            float s[32];
+                            tmem_ld32(cols + 32 * k, s);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
-                                if (!((seen >> x) & 1)) s[32 * k + x] = -INFINITY;
+                                if (!((seen >> x) & 1)) s[x] = -INFINITY;
+                            tmem_st32(cols + 32 * k, s);
                         }
+                        tmem_wait_st();
+                    }
                     float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < kHalf; x += 4) {
-                        top = fmaxf(fmaxf(top, s[x]), s[x + 1]);
-                        top1 = fmaxf(fmaxf(top1, s[x + 2]), s[x + 3]);
+                    for (int k = 0; k < kKeys / 64; ++k) {
+                        float s0[32], s1[32];
+                        tmem_ld32(cols + 64 * k, s0);
+                        tmem_ld32(cols + 64 * k + 32, s1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            top = fmaxf(fmaxf(top, s0[x]), s0[x + 1]);
+                            top1 = fmaxf(fmaxf(top1, s1[x]), s1[x + 1]);
+                        }
                     }
-                    top = fmaxf(top, top1);
-                    top = fmaxf(top, exchange(top)) * r.c;
-                    // (both warpgroups find the same)
+                    top = fmaxf(top, top1) * c;
+                    // one m tile: the reference is the other warpgroup's of the step before
+                    if (m_used == 1 && i > 0) {
+                        pair_wait(quarter, wg);
+                        const float other = sm.top[0][lrow];
+                        if (other > m) {
+                            if (i > 1) l *= ex2(m - other);
+                            m = other;
+                        }
+                    }
                     const bool first = i < m_used;
-                    const bool grown = top > r.m + (first ? 0.f : S::kSlack);
-                    const float to = grown ? top : r.m;
+                    const bool grown = top > m + (first ? 0.f : S::kSlack);
+                    const float to = grown ? top : m;
                     const float ref = to == -INFINITY ? 0.f : to;
+                    if (m_used == 1 && i + 1 < steps) {
+                        sm.top[0][lrow] = to;
+                        pair_arrive(quarter, wg);
+                    }
                     if (!first && __any_sync(0xffffffffu, grown)) {
-                        const float keep = grown ? ex2(r.m - ref) : 1.f;
-                        r.l *= keep;
+                        const float keep = grown ? ex2(m - ref) : 1.f;
+                        l *= keep;
                         const uint32_t q = g - m_used;  // the last product of these rows
                         wait(&sm.pfree[q % S::kBufs], (q / S::kBufs) & 1);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int k = 0; k < kD / 64; ++k) {  // half the channels
+                        for (int k = 0; k < kD / 32; ++k) {
                             float o[32];
-                            const uint32_t oc = lanes + S::kColO + (m_used == 1 ? 0 : i & 1) * kD + wg * (kD / 2) + 32 * k;
+                            const uint32_t oc = lanes + S::kColO + mt * kD + 32 * k;
                             tmem_ld32(oc, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int x = 0; x < 32; ++x) o[x] *= keep;
                             tmem_st32(oc, o);
                         }
-                        // the other's half too, before a product adds to it
-                        tmem_wait_st();
-                        tc_fence_before();
-                        pair_barrier(quarter);
                     }
-                    r.m = to;
-                    const uint64_t c2 = f2(r.c, r.c), off2 = f2(S::kShift - ref, S::kShift - ref);
+                    m = to;
+                    const uint64_t c2 = f2(c, c), off2 = f2(S::kShift - ref, S::kShift - ref);
                     uint64_t sum2 = 0;
-#pragma unroll
-                    for (int k = 0; k < kHalf / 32; ++k) {
-                        float hi[16], lo[16];
+#pragma unroll 1
+                    for (int k = 0; k < kKeys / 32; ++k) {
+                        float s[32], hi[16], lo[16];
+                        tmem_ld32(cols + 32 * k, s);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            const float2 e = f2_split(f2_fma(f2(s[32 * k + 2 * x], s[32 * k + 2 * x + 1]), c2, off2));
+                            const float2 e = f2_split(f2_fma(f2(s[2 * x], s[2 * x + 1]), c2, off2));
                             const float p0 = ex2(e.x), p1 = ex2(e.y);
                             const uint64_t p2 = f2(p0, p1);
                             sum2 = f2_add(sum2, p2);
@@ -710,42 +715,51 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         // a weight's two words take its score's place
                         tmem_st16(cols + 32 * k, hi);
                         tmem_st16(cols + 32 * k + 16, lo);
+                        if (k + 1 == kKeys / 64 || k + 1 == kKeys / 32) {
+                            // half the keys' weights: their product may begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.pfull[buf][k + 1 == kKeys / 64 ? 0 : 1]);
+                        }
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
                     const float2 sum = f2_split(sum2);
-                    r.l += sum.x + sum.y;
+                    l += sum.x + sum.y;
+                } else {
+                    if (lane < 2) mbar_arrive(&sm.pfull[buf][lane]);
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pfull[buf][wg]);
             }
             step += steps;
             tiles_done += tiles;
             if constexpr (kFp8) {
                 // while this unit's last products run: its scores are all there, so nothing reads
                 // its queries any more
-                wait(&sm.scored, units & 1);
+                if (!wait(&sm.scored, units & 1)) break;
                 if (more) queries(next, exps_next);
             }
 
-            // outputs: a whole unit's to o, a cut one's to the workspace; a warpgroup half the
-            // channels
-            wait(&sm.done, units & 1);
+            // outputs: a whole unit's to o, a cut one's to the workspace.  Of two m tiles a
+            // warpgroup has its own, of one half the channels.
+            if (!wait(&sm.done, units & 1)) break;
             ++units;
-            tc_fence_after();
             const bool whole = at.t == 0 && at.t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[at.h] : 1.f;
-            const int d0 = wg * (kD / 2), d1 = d0 + kD / 2;
-            for (int mt = 0; mt < m_used; ++mt, change_rows()) {
-                if (!r.some) continue;
-                const float l = r.l + exchange(r.l);
-                const int rr = at.rg * S::kRows + mt * 128 + lrow;
-                const bool real = rr < at.rows;
-                uint32_t node, head;
-                args.group.divmod(rr, node, head);
-                const int64_t row = at.first + node;
-                const int qh = at.h * a.group + static_cast<int>(head);
+            if (some) {
+                tc_fence_after();
+                if (m_used == 1) {  // the two warpgroups' sums, by the later reference
+                    sm.top[wg][lrow] = m;
+                    pair_barrier(quarter);
+                    const float to = fmaxf(m, sm.top[wg ^ 1][lrow]);
+                    pair_barrier(quarter);
+                    sm.top[wg][lrow] = l * ex2(m - (to == -INFINITY ? 0.f : to));
+                    pair_barrier(quarter);
+                    l = sm.top[0][lrow] + sm.top[1][lrow];
+                    m = to;
+                    pair_barrier(quarter);
+                }
+                const int d0 = m_used == 1 ? wg * (kD / 2) : 0, d1 = m_used == 1 ? d0 + kD / 2 : kD;
                 const float f = l == 0.f ? 0.f : 1.f / l;
                 float nan = 0.f;
                 const int64_t out = row * a.q_heads + qh;
@@ -774,9 +788,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
+                tc_fence_before();
                 if (whole) {
-                    if (real && wg == 0 && a.lse != nullptr)
-                        a.lse[out] = l == 0.f ? -INFINITY : (r.m + log2f(l) - S::kShift) * kLn2;
+                    if (real && d0 == 0 && a.lse != nullptr)
+                        a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - S::kShift) * kLn2;
                     // what is not finite although the weights are
                     uint32_t again = __ballot_sync(0xffffffffu, real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
                     while (again != 0) {
@@ -786,11 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                                             __shfl_sync(0xffffffffu, qh, src), at.n, at.len, d0, d1);
                         __syncwarp();
                     }
-                } else if (wg == 0) {
-                    reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + mt * 128 + lrow] = make_float2(r.m, l);
+                } else if (d0 == 0) {
+                    reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + mt * 128 + lrow] = make_float2(m, l);
                 }
             }
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.ofree);
             at = next;
