@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     if (warp < kSoftWarps) {
         // ---- queries in, weights, outputs ------------------------------------------------
         take_registers<kSoftRegs>();
+        // (A wait that runs out ends no loop here: the other warpgroup's warps count on this one's.)
         Waits wait = {a.err, true};
         const int wg = warp >> 2, quarter = warp & 3, lrow = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         };
         bool more = at.take(a);
         if (kFp8 && more) queries(at, exps);
-        while (more && wait.ok) {
+        while (more) {
             const int m_used = at.m_tiles(at.rg);
             const int tiles = at.t1 - at.t, steps = tiles * m_used;
             // This warpgroup has every second step: of two m tiles always the same one, of one
@@ -608,10 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             Cursor<S> next = at;
             more = next.take(a);
 
-            for (int i = i0; i < steps && wait.ok; i += 2) {
+            for (int i = i0; i < steps; i += 2) {
                 const int tile = m_used == 1 ? i : i >> 1;
                 const uint32_t g = step + i, buf = g % S::kBufs;
-                if (!wait(&sm.sfull[buf], (g / S::kBufs) & 1)) break;
+                wait(&sm.sfull[buf], (g / S::kBufs) & 1);
                 if (some) {
                     tc_fence_after();
                     const uint32_t cols = lanes + buf * kKeys;
@@ -735,13 +736,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             if constexpr (kFp8) {
                 // while this unit's last products run: its scores are all there, so nothing reads
                 // its queries any more
-                if (!wait(&sm.scored, units & 1)) break;
+                wait(&sm.scored, units & 1);
                 if (more) queries(next, exps_next);
             }
 
             // outputs: a whole unit's to o, a cut one's to the workspace.  Of two m tiles a
             // warpgroup has its own, of one half the channels.
-            if (!wait(&sm.done, units & 1)) break;
+            wait(&sm.done, units & 1);
             ++units;
             const bool whole = at.t == 0 && at.t1 == at.tiles;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (at.t == 0 ? 1 : 0);

@@ -475,9 +475,8 @@ cudaError_t launch_tree_conv(const TreeConv &a, int num_sms, cudaStream_t s) {
     const int groups = (a.C + kWarpCh - 1) / kWarpCh;
     const int parts = std::min(a.B, std::max(1, blocks * num_sms / (groups * 3)));
     const dim3 grid(groups, parts, 3);
-    const cudaError_t e = cudaFuncSetAttribute(tree_conv_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kTreeNodes + kHalo) * kRowBytes);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(&tree_conv_kernel),
+                                              (kTreeNodes + kHalo) * kRowBytes);
     if (e != cudaSuccess) return e;
     tree_conv_kernel<<<grid, kTreeWarps * 32, smem, s>>>(a);
     return cudaGetLastError();

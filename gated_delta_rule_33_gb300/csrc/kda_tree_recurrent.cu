@@ -17,13 +17,21 @@
 // vectors, 4 n 128^2 flops: HBM.  On the fp32 pipe that product alone takes as long (337 us where
 // the bytes take 82); so it runs on the matrix instructions, every operand as three bf16 words, 24
 // bits together, and the six products that reach 2^-24 (u becomes state; two tf32 words and
-// three products hold less and took twice as long).  One block a
-// (request, head), two blocks an SM, so that one's state arrives while the other computes.  The
-// state comes by 16-byte copies, to rows 8 words apart in the banks (bulk copies of a row each took
-// 5 us to issue); meanwhile a warp a
-// node walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp
-// has 16 columns of the product for all rows; then each thread solves its column of the
-// updates, 8 nodes in registers, and the outputs follow.
+// three products hold less and took twice as long).  A block walks over units, each a
+// (request, head); up to 16 nodes two blocks share an SM, so that one computes while the other's
+// state arrives.  The state comes by 16-byte copies, to rows 8 words apart in the banks (bulk copies
+// of a row each took 5 us to issue), the next unit's while this one's updates run; a warp a node
+// walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp has
+// 16 columns of the product for all rows; then each thread solves its column of the updates, 8
+// nodes in registers, and the outputs follow.
+//
+// Measured, 64 requests of 7 to 16 nodes, 96 heads, fp32 state: 211 us (82 at a copy's rate).  337
+// with the product on the fp32 pipe, 280 as two tf32 words, 226 with 16-byte copies, 213 with
+// paths in packed pairs (219 as three bf16 words, which hold more), 211 walking over units.
+// A unit takes a block 20k cycles: 6.0k decays and paths, 6.8k the product, 4.8k updates and
+// outputs, the rest waits.  The product's matrix instructions are 3.1k of its cycles (2.03 a bf16
+// instruction and SM); what bounds the kernel is the way through these phases, each a chain with
+// a barrier behind it, with two blocks to fill the gaps.
 #include <type_traits>
 
 #include "kda_f32x2.cuh"
@@ -465,7 +473,9 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
 // One block a (request, head); the state stays in registers between its read and its write: warp
 // w owns rows w, w + 8, .., lane l the columns 4 l .. 4 l + 3, so a warp moves whole rows.  The
 // path's nodes act sixteen at a time: S <- Diag(E) S + sum_j (E_j k_j) u_j^T, E and E_j the decays
-// of the sixteen, and of those behind j.
+// of the sixteen, and of those behind j.  Bound: the state is read and written once: 150 us for
+// 6144 heads of fp32 (5.4 TB/s; 120 at a copy's rate).  With the two other memories' commits 161 us;
+// at two blocks an SM 165, with four nodes' loads in flight, in registers that the state needs, 169.
 constexpr int kCommitNodes = 16;
 constexpr int kRows = kD / kWarps;
 

@@ -23,20 +23,25 @@ def _library():
     return _kda._lib or _kda.load()
 
 
-def _same_gpu(*tensors: Optional[torch.Tensor]) -> int:
+def _same_gpu(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """The GPU that all of a call's tensors are on."""
-    have = [t for t in tensors if t is not None]
-    gpu = have[0].get_device()
-    if gpu < 0 or any(t.get_device() != gpu for t in have):
-        raise _elsewhere(gpu, *have)
+    gpu = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != gpu:
+            raise _elsewhere(gpu, first, *(x for x in others if x is not None))
+    if gpu < 0:
+        raise _elsewhere(gpu)
     return gpu
 
 
 def _tree(cu_seqlens, ancestors, *per_request) -> Tuple[int, int]:
     """Requests and rows of a batch of trees."""
     B = cu_seqlens.numel() - 1
-    if B < 0 or any(t is not None and t.numel() != B for t in per_request):
-        raise ValueError("cu_seqlens is [B+1], what is given for each request [B]")
+    for t in per_request:
+        if t is not None and t.numel() != B:
+            raise ValueError("cu_seqlens is [B+1], what is given for each request [B]")
+    if B < 0:
+        raise ValueError("cu_seqlens is [B+1]")
     return B, ancestors.numel()
 
 
@@ -62,10 +67,13 @@ def kda_recurrent_tree_decode(q, k, v, g, beta, state_pool, state_indices, cu_se
     128] read; state_indices [B] or None; o [N, H, 128] and u (fp32, alike, or None) written."""
     B, N = _tree(cu_seqlens, ancestors, state_indices)
     slots, H, K, V = state_pool.shape
-    for t in (q, k, v, g, o, u):
-        if t is not None and tuple(t.shape) != (N, H, K):
+    shape = (N, H, K)
+    for t in (q, k, v, g, o):
+        if t.shape != shape:
             raise ValueError("q, k, v, g, o and u are [N, H, 128], N the number of words")
-    if tuple(beta.shape) != (N, H):
+    if u is not None and u.shape != shape:
+        raise ValueError("q, k, v, g, o and u are [N, H, 128], N the number of words")
+    if beta.shape != shape[:2]:
         raise ValueError("beta is [N, H]")
     gpu = _same_gpu(q, k, v, g, beta, state_pool, state_indices, cu_seqlens, ancestors, o, u)
     st = _library().kda_recurrent_tree_decode(
@@ -84,7 +92,7 @@ def kda_recurrent_tree_commit(k, g, u, state_pool, state_indices, cu_seqlens, an
     B, N = _tree(cu_seqlens, ancestors, state_indices, last)
     slots, H, K, V = state_pool.shape
     for t in (k, g, u):
-        if tuple(t.shape) != (N, H, K):
+        if t.shape != (N, H, K):
             raise ValueError("k, g and u are [N, H, 128], N the number of words")
     gpu = _same_gpu(k, g, u, state_pool, state_indices, cu_seqlens, ancestors, last)
     st = _library().kda_recurrent_tree_commit(
@@ -96,11 +104,13 @@ def kda_recurrent_tree_commit(k, g, u, state_pool, state_indices, cu_seqlens, an
 
 
 def _conv_sizes(pool, rows, N):
-    if pool.dim() != 4 or tuple(pool.shape[1:3]) != (3, 3):
+    shape = pool.shape
+    if len(shape) != 4 or shape[1] != 3 or shape[2] != 3:
         raise ValueError("conv_state_pool is [num_slots, 3, 3, C]")
-    slots, C = pool.shape[0], pool.shape[3]
-    if any(tuple(x.shape) != (N, C) for x in rows):
-        raise ValueError("x_q, x_k, x_v and the outputs are [N, C], N the number of words")
+    slots, _, _, C = shape
+    for x in rows:
+        if x.shape != (N, C):
+            raise ValueError("x_q, x_k, x_v and the outputs are [N, C], N the number of words")
     return slots, C
 
 

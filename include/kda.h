@@ -715,9 +715,9 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
  *
  *   u_i = beta_i (v_i - S'^T k_i),  S' = Diag(exp g_i) S_parent
  *
- * from which kda_recurrent_tree_commit forms the state after any path.  fp32 throughout (a
- * bf16 state is widened; unlike a chain of one-token decodes, it is not rounded between the
- * nodes of a path).
+ * from which kda_recurrent_tree_commit forms the state after any path.  Sums are fp32, and
+ * operands are kept to 24 bits (a bf16 state is widened; unlike a chain of one-token decodes, it
+ * is not rounded between the nodes of a path).
  *
  *   q, k, v        bf16 [N, H, 128];  g fp32 [N, H, 128];  beta fp32 [N, H]
  *   state_pool     [num_slots, H, 128, 128] of state_dtype (fp32 or bf16), read
