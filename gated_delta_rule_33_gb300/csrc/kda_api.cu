@@ -951,7 +951,11 @@ kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void 
     a.max_nodes = max_nodes;
     a.N = N;
     a.err = dev->error_word;
-    return from_cuda(kda::launch_tree_conv(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+    try {
+        return from_cuda(kda::launch_tree_conv(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
+        return KDA_ERR_CUDA;
+    }
 }
 
 kda_status kda_short_conv_tree_commit(const void *x_q, const void *x_k, const void *x_v,

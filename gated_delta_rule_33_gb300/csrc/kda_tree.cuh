@@ -22,12 +22,14 @@ struct TreeRows {
 
 // Offsets that lie outside the N rows, or go back, leave their request out; one of more than
 // max_nodes rows has no nodes.
-__device__ __forceinline__ TreeRows tree_rows(const int32_t *cu, int b, int64_t N, int max_nodes) {
-    const int64_t lo = cu[b], hi = cu[b + 1];
+__device__ __forceinline__ TreeRows tree_rows_between(int64_t lo, int64_t hi, int64_t N, int max_nodes) {
     if (lo < 0 || hi < lo || hi > N) return {0, 0, 0, true};
     const int64_t n = hi - lo;
     const bool ok = n <= max_nodes;
     return {lo, ok ? static_cast<int>(n) : 0, static_cast<int>(n), !ok};
+}
+__device__ __forceinline__ TreeRows tree_rows(const int32_t *cu, int b, int64_t N, int max_nodes) {
+    return tree_rows_between(cu[b], cu[b + 1], N, max_nodes);
 }
 
 __device__ __forceinline__ uint64_t bits_below(int i) {

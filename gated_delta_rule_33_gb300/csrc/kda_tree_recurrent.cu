@@ -157,17 +157,30 @@ __device__ __forceinline__ float sum_eight(float (&x)[8]) {
     return x[0];
 }
 
+// What says where a (request, head) lies: loaded early, looked at when it is needed.
+struct TreePlace {
+    int h, lo, hi, slot;
+
+    __device__ __forceinline__ TreePlace(const TreeStep &a, uint32_t unit) {
+        const uint32_t b = unit / static_cast<uint32_t>(a.H);
+        h = static_cast<int>(unit - b * static_cast<uint32_t>(a.H));
+        lo = a.cu[b];
+        hi = a.cu[b + 1];
+        slot = a.slots != nullptr ? a.slots[b] : static_cast<int>(b);
+    }
+};
+
 // A (request, head) of a block.
 struct TreeUnit {
-    int64_t first, slot;
-    int n, rows, h;
+    int64_t first;
+    int slot, n, rows, h;
 
-    __device__ __forceinline__ TreeUnit(const TreeStep &a, int64_t unit) {
-        const int b = static_cast<int>(unit / a.H);
-        h = static_cast<int>(unit - static_cast<int64_t>(b) * a.H);
-        const TreeRows t = tree_rows(a.cu, b, a.N, a.max_nodes);
-        if (t.bad && threadIdx.x == 0) record_device_error(a.err, kDevInvalidArg);
-        slot = slot_of(a, b);
+    __device__ __forceinline__ TreeUnit(const TreeStep &a, const TreePlace &p) {
+        h = p.h;
+        const TreeRows t = tree_rows_between(p.lo, p.hi, a.N, a.max_nodes);
+        const bool outside = a.slots != nullptr && p.slot >= a.num_slots;
+        if ((t.bad || outside) && threadIdx.x == 0) record_device_error(a.err, kDevInvalidArg);
+        slot = outside ? -1 : p.slot;
         first = t.first;
         rows = t.rows;
         n = slot < 0 ? 0 : t.n;
@@ -185,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TreeSmem<kEights> s(smem, a.max_nodes);
-    const int64_t units = static_cast<int64_t>(a.B) * a.H;
+    const uint32_t units = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.H);
 
     // What a unit brings from memory, ahead of its turn: the state and the keys to shared memory,
     // and in registers the gates (four channels of nodes warp, warp + 8, ..), the queries of the
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             }
         }
         if (tid < u.n) beta = a.beta[(u.first + tid) * a.H + u.h];
-        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (u.slot * a.H + u.h) * (kD * kRow);
+        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (static_cast<int64_t>(u.slot) * a.H + u.h) * (kD * kRow);
         constexpr int kPieces = kRow / 16;
 #pragma unroll
         for (int i = 0; i < kD * kPieces / kThreads; ++i) {
@@ -219,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             sm100::cp_async_16(s.k + i * 8, x + u.at(a, i >> 4) + (i & 15) * 8, true);
     };
 
-    TreeUnit u(a, blockIdx.x);
+    TreeUnit u(a, TreePlace(a, blockIdx.x));
     fetch_state(u);
     fetch_rows(u, a.k);
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const TreeUnit next(a, min(unit + gridDim.x, units - 1));
+    for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const bool more = unit + gridDim.x < units;
+        const TreePlace place(a, more ? unit + gridDim.x : unit);
         const int n = u.n;
         if (n == 0) {
             for (int64_t i = tid; i < static_cast<int64_t>(u.rows) * kD; i += kThreads) {
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
                 write_out<kOutBf16>(a.o, at, 0.f);
                 if (a.u != nullptr) a.u[at] = 0.f;
             }
-            u = next;
+            u = TreeUnit(a, place);
             if (more) {
                 fetch_state(u);
                 fetch_rows(u, a.k);
@@ -391,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
         __syncthreads();
         // nobody reads the state or the left operands any more: the next unit's state may come, and
         // the products go where the operands were
+        const TreeUnit next(a, place);
         if (more) fetch_state(next);
         float *products = reinterpret_cast<float *>(s.rows);
 #pragma unroll
