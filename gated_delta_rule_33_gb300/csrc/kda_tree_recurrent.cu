@@ -80,10 +80,15 @@ struct LeftOperands {
 };
 
 // Shared memory: nodes in eights, as many as nc nodes fill.
-template <int kEights>
+template <int kEights, bool kStateBf16>
 struct TreeSmem {
+    // The state comes in parts of kPartRows rows, one after another, where that lets a third block
+    // share the SM.  (A bf16 row's pitch: 8 banks between every second, as of an fp32 one.)
+    static constexpr int kParts = kEights <= 2 && !kStateBf16 ? 2 : 1;
+    static constexpr int kPartRows = kD / kParts, kStatePitch = kStateBf16 ? kD * 2 + 16 : kPitch * 4;
+    static constexpr int kState = kPartRows * kStatePitch;
     int nc;
-    float *state;     // [k 128][kPitch]
+    uint8_t *state;   // [kPartRows][kStatePitch]
     uint8_t *rows;    // [eight][k / 16]: LeftOperands; then the products [eight][16][kPitch] of the
                       // eight's E_i k_i with the state, and of its E_i scale q_i
     float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
@@ -93,12 +98,12 @@ struct TreeSmem {
 
     __host__ __device__ static int nodes(int max_nodes) { return (max_nodes + 7) / 8 * 8; }
     __host__ __device__ static int bytes(int nc) {
-        return kD * kPitch * 4 + nc / 8 * LeftOperands<kEights>::kEight + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4;
+        return kState + nc / 8 * LeftOperands<kEights>::kEight + 2 * nc * nc * 4 + nc * kD * (4 + 2) + nc * 4;
     }
     __device__ TreeSmem(uint8_t *base, int max_nodes) {
         nc = nodes(max_nodes);
-        state = reinterpret_cast<float *>(base);
-        rows = base + kD * kPitch * 4;
+        state = base;
+        rows = base + kState;
         ak = reinterpret_cast<float *>(rows + nc / 8 * LeftOperands<kEights>::kEight);
         aq = ak + nc * nc;
         decay = aq + nc * nc;
@@ -190,14 +195,15 @@ struct TreeUnit {
 
 // kEights: eights of nodes that the accumulators hold.  A block walks over units, gridDim.x apart.
 template <bool kStateBf16, bool kOutBf16, int kEights>
-__global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_kernel(const TreeStep a) {
+__global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_kernel(const TreeStep a) {
     using Left = LeftOperands<kEights>;
+    using Smem = TreeSmem<kEights, kStateBf16>;
     using Word = std::conditional_t<kEights <= 4, uint32_t, uint64_t>;
     constexpr int kBits = 8 * sizeof(Word);
     constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const TreeSmem<kEights> s(smem, a.max_nodes);
+    const Smem s(smem, a.max_nodes);
     const uint32_t units = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.H);
 
     // What a unit brings from memory, ahead of its turn: the state and the keys to shared memory,
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     uint2 q2[kEights];
     uint64_t words[kEights];
     float beta = 0.f;
-    auto fetch_state = [&](const TreeUnit &u) {
+    auto fetch_inputs = [&](const TreeUnit &u) {
         if (u.n == 0) return;
 #pragma unroll
         for (int i = 0; i < kEights; ++i) {
@@ -219,12 +225,16 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             }
         }
         if (tid < u.n) beta = a.beta[(u.first + tid) * a.H + u.h];
-        const uint8_t *src = static_cast<const uint8_t *>(a.pool) + (static_cast<int64_t>(u.slot) * a.H + u.h) * (kD * kRow);
+    };
+    auto fetch_part = [&](const TreeUnit &u, int part) {
+        if (u.n == 0) return;
+        const uint8_t *src = static_cast<const uint8_t *>(a.pool) +
+                             (static_cast<int64_t>(u.slot) * a.H + u.h) * (kD * kRow) + part * (Smem::kPartRows * kRow);
         constexpr int kPieces = kRow / 16;
 #pragma unroll
-        for (int i = 0; i < kD * kPieces / kThreads; ++i) {
+        for (int i = 0; i < Smem::kPartRows * kPieces / kThreads; ++i) {
             const int k = (tid + i * kThreads) / kPieces, c = (tid + i * kThreads) % kPieces;
-            sm100::cp_async_16(reinterpret_cast<uint8_t *>(s.state + k * kPitch) + c * 16, src + k * kRow + c * 16, true);
+            sm100::cp_async_16(s.state + k * Smem::kStatePitch + c * 16, src + k * kRow + c * 16, true);
         }
     };
     auto fetch_rows = [&](const TreeUnit &u, const __nv_bfloat16 *x) {  // keys, or values in their place
@@ -233,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
     };
 
     TreeUnit u(a, TreePlace(a, blockIdx.x));
-    fetch_state(u);
+    fetch_inputs(u);
+    fetch_part(u, 0);
     fetch_rows(u, a.k);
     for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const bool more = unit + gridDim.x < units;
@@ -247,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
             }
             u = TreeUnit(a, place);
             if (more) {
-                fetch_state(u);
+                fetch_inputs(u);
+                fetch_part(u, 0);
                 fetch_rows(u, a.k);
             }
             continue;
@@ -343,19 +355,18 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
         for (int m = 0; m < kEights; ++m)
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
-#pragma unroll 2
-        for (int ks = 0; ks < kD / 16; ++ks) {
+        auto product_of = [&](int ks, int row0) {  // 16 k's; the first row of the state's part
             uint32_t b[3][2][2];  // word, tile, pair of k's
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int k = 16 * ks + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
+                    const int k = 16 * ks - row0 + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
                     if constexpr (kStateBf16) {
-                        const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * kPitch) + col;
-                        b[0][c][i] = x[0] | static_cast<uint32_t>(x[2 * kPitch]) << 16;
+                        const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * Smem::kStatePitch) + col;
+                        b[0][c][i] = x[0] | static_cast<uint32_t>(x[Smem::kStatePitch / 2]) << 16;
                     } else {
-                        const float *x = s.state + k * kPitch + col;
+                        const float *x = reinterpret_cast<const float *>(s.state + k * Smem::kStatePitch) + col;
                         split3(x[0], x[kPitch], b[0][c][i], b[1][c][i], b[2][c][i]);
                     }
                 }
@@ -399,13 +410,26 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 2 : 1) tree_decode_ke
                                 mma_bf16(i + k == 0 ? acc[m0 + m][c] : low[m0 + m][c], w[m][i], b[k][c]);
                         }
             }
+        };
+        for (int part = 0;; ++part) {
+            const int row0 = part * Smem::kPartRows;
+#pragma unroll 2
+            for (int ks = row0 / 16; ks < (row0 + Smem::kPartRows) / 16; ++ks) product_of(ks, row0);
+            if (part + 1 == Smem::kParts) break;
+            __syncthreads();
+            fetch_part(u, part + 1);
+            sm100::cp_async_wait_all();
+            __syncthreads();
         }
         sm100::cp_async_wait_all();
         __syncthreads();
         // nobody reads the state or the left operands any more: the next unit's state may come, and
         // the products go where the operands were
         const TreeUnit next(a, place);
-        if (more) fetch_state(next);
+        if (more) {
+            fetch_inputs(next);
+            fetch_part(next, 0);
+        }
         float *products = reinterpret_cast<float *>(s.rows);
 #pragma unroll
         for (int m = 0; m < kEights; ++m) {
@@ -589,13 +613,14 @@ __global__ void __launch_bounds__(kThreads, 3) tree_commit_kernel(const TreeStep
 
 template <bool kStateBf16, bool kOutBf16, int kEights>
 cudaError_t decode_n(const TreeStep &a, int num_sms, cudaStream_t s) {
+    using Smem = TreeSmem<kEights, kStateBf16>;
     const auto kernel = &tree_decode_kernel<kStateBf16, kOutBf16, kEights>;
     const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), TreeSmem<kEights>::bytes(8 * kEights));
+        ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), Smem::bytes(8 * kEights));
     if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(a.B) * a.H, most = static_cast<int64_t>(num_sms) * (kEights <= 2 ? 2 : 1);
+    const int64_t units = static_cast<int64_t>(a.B) * a.H, most = static_cast<int64_t>(num_sms) * (kEights <= 2 ? 3 : 1);
     kernel<<<static_cast<unsigned>(units < most ? units : most), kThreads,
-             TreeSmem<kEights>::bytes(TreeSmem<kEights>::nodes(a.max_nodes)), s>>>(a);
+             Smem::bytes(Smem::nodes(a.max_nodes)), s>>>(a);
     return cudaGetLastError();
 }
 
