@@ -18,20 +18,21 @@
 // the bytes take 82); so it runs on the matrix instructions, every operand as three bf16 words, 24
 // bits together, and the six products that reach 2^-24 (u becomes state; two tf32 words and
 // three products hold less and took twice as long).  A block walks over units, each a
-// (request, head); up to 16 nodes two blocks share an SM, so that one computes while the other's
-// state arrives.  The state comes by 16-byte copies, to rows 8 words apart in the banks (bulk copies
-// of a row each took 5 us to issue), the next unit's while this one's updates run; a warp a node
+// (request, head); up to 16 nodes three blocks share an SM, so that some compute while others wait.
+// The state comes by 16-byte copies (bulk copies of a row each took 5 us to issue), to rows 8 words
+// apart in the banks, in quarters of which two are there at a time: one meets the vectors while the
+// next arrives, and the next unit's first two come while this one's updates run.  A warp a node
 // walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp has
 // 16 columns of the product for all rows; then each thread solves its column of the updates, 8
 // nodes in registers, and the outputs follow.
 //
-// Measured, 64 requests of 7 to 16 nodes, 96 heads, fp32 state: 211 us (82 at a copy's rate).  337
+// Measured, 64 requests of 7 to 16 nodes, 96 heads, fp32 state: 188 us (82 at a copy's rate).  337
 // with the product on the fp32 pipe, 280 as two tf32 words, 226 with 16-byte copies, 213 with
-// paths in packed pairs (219 as three bf16 words, which hold more), 211 walking over units.
-// A unit takes a block 20k cycles: 6.0k decays and paths, 6.8k the product, 4.8k updates and
-// outputs, the rest waits.  The product's matrix instructions are 3.1k of its cycles (2.03 a bf16
-// instruction and SM); what bounds the kernel is the way through these phases, each a chain with
-// a barrier behind it, with two blocks to fill the gaps.
+// paths in packed pairs (219 as three bf16 words, which hold more), 211 walking over units, 207 with
+// a unit's place loaded ahead, 197 with the state in halves and a third block, 188 in quarters.
+// (512 threads a block: 244.)  What bounds it: some 2300 instructions a warp and unit, which fill
+// half of the issue slots; a unit's phases (decays, paths, product, updates, outputs) are chains
+// with barriers between them, and three blocks do not fill all of their gaps.
 #include <type_traits>
 
 #include "kda_f32x2.cuh"
@@ -82,13 +83,13 @@ struct LeftOperands {
 // Shared memory: nodes in eights, as many as nc nodes fill.
 template <int kEights, bool kStateBf16>
 struct TreeSmem {
-    // The state comes in parts of kPartRows rows, one after another, where that lets a third block
+    // The state comes in parts of kPartRows rows, two at a time, where that lets a third block
     // share the SM.  (A bf16 row's pitch: 8 banks between every second, as of an fp32 one.)
-    static constexpr int kParts = kEights <= 2 && !kStateBf16 ? 2 : 1;
+    static constexpr int kParts = kEights <= 2 && !kStateBf16 ? 4 : 1, kSlots = kParts < 2 ? 1 : 2;
     static constexpr int kPartRows = kD / kParts, kStatePitch = kStateBf16 ? kD * 2 + 16 : kPitch * 4;
-    static constexpr int kState = kPartRows * kStatePitch;
+    static constexpr int kPart = kPartRows * kStatePitch, kState = kSlots * kPart;
     int nc;
-    uint8_t *state;   // [kPartRows][kStatePitch]
+    uint8_t *state;   // [kSlots][kPartRows][kStatePitch]
     uint8_t *rows;    // [eight][k / 16]: LeftOperands; then the products [eight][16][kPitch] of the
                       // eight's E_i k_i with the state, and of its E_i scale q_i
     float *ak, *aq;   // [j][i]: (E_ij k_j) . k_i (0 where j is not above i), (E_ij k_j) . scale q_i
@@ -234,8 +235,12 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
 #pragma unroll
         for (int i = 0; i < Smem::kPartRows * kPieces / kThreads; ++i) {
             const int k = (tid + i * kThreads) / kPieces, c = (tid + i * kThreads) % kPieces;
-            sm100::cp_async_16(s.state + k * Smem::kStatePitch + c * 16, src + k * kRow + c * 16, true);
+            sm100::cp_async_16(s.state + part % Smem::kSlots * Smem::kPart + k * Smem::kStatePitch + c * 16, src + k * kRow + c * 16, true);
         }
+    };
+    auto fetch_first_parts = [&](const TreeUnit &u) {
+        fetch_part(u, 0);
+        if constexpr (Smem::kSlots == 2) fetch_part(u, 1);
     };
     auto fetch_rows = [&](const TreeUnit &u, const __nv_bfloat16 *x) {  // keys, or values in their place
         for (int i = tid; i < u.n * 16; i += kThreads)
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
 
     TreeUnit u(a, TreePlace(a, blockIdx.x));
     fetch_inputs(u);
-    fetch_part(u, 0);
+    fetch_first_parts(u);
     fetch_rows(u, a.k);
     for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const bool more = unit + gridDim.x < units;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
             u = TreeUnit(a, place);
             if (more) {
                 fetch_inputs(u);
-                fetch_part(u, 0);
+                fetch_first_parts(u);
                 fetch_rows(u, a.k);
             }
             continue;
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
                   f2_split(f2_mul(e.y, q.y)));
         }
         __syncthreads();
-        fetch_rows(u, a.v);
+        if constexpr (Smem::kParts == 1) fetch_rows(u, a.v);
 
         // The product: a warp has columns 16 warp .. + 15 of all rows.
         const int g = lane >> 2, tq = lane & 3;
@@ -355,18 +360,18 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
         for (int m = 0; m < kEights; ++m)
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] = low[m][i >> 2][i & 3] = 0.f;
-        auto product_of = [&](int ks, int row0) {  // 16 k's; the first row of the state's part
+        auto product_of = [&](int ks, const uint8_t *state) {  // 16 k's; where the first k's row would lie
             uint32_t b[3][2][2];  // word, tile, pair of k's
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int k = 16 * ks - row0 + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
+                    const int k = 16 * ks + 2 * tq + 8 * i, col = 16 * warp + 8 * c + g;
                     if constexpr (kStateBf16) {
-                        const uint16_t *x = reinterpret_cast<const uint16_t *>(s.state + k * Smem::kStatePitch) + col;
+                        const uint16_t *x = reinterpret_cast<const uint16_t *>(state + k * Smem::kStatePitch) + col;
                         b[0][c][i] = x[0] | static_cast<uint32_t>(x[Smem::kStatePitch / 2]) << 16;
                     } else {
-                        const float *x = reinterpret_cast<const float *>(s.state + k * Smem::kStatePitch) + col;
+                        const float *x = reinterpret_cast<const float *>(state + k * Smem::kStatePitch) + col;
                         split3(x[0], x[kPitch], b[0][c][i], b[1][c][i], b[2][c][i]);
                     }
                 }
@@ -412,14 +417,15 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
             }
         };
         for (int part = 0;; ++part) {
-            const int row0 = part * Smem::kPartRows;
+            const uint8_t *state = s.state + part % Smem::kSlots * Smem::kPart - part * Smem::kPart;
 #pragma unroll 2
-            for (int ks = row0 / 16; ks < (row0 + Smem::kPartRows) / 16; ++ks) product_of(ks, row0);
+            for (int ks = part * Smem::kPartRows / 16; ks < (part + 1) * Smem::kPartRows / 16; ++ks)
+                product_of(ks, state);
             if (part + 1 == Smem::kParts) break;
-            __syncthreads();
-            fetch_part(u, part + 1);
             sm100::cp_async_wait_all();
-            __syncthreads();
+            __syncthreads();  // the next part is there, and this one's place is free
+            if (part + 2 < Smem::kParts) fetch_part(u, part + 2);
+            if (part == 0) fetch_rows(u, a.v);
         }
         sm100::cp_async_wait_all();
         __syncthreads();
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
         const TreeUnit next(a, place);
         if (more) {
             fetch_inputs(next);
-            fetch_part(next, 0);
+            fetch_first_parts(next);
         }
         float *products = reinterpret_cast<float *>(s.rows);
 #pragma unroll
