@@ -517,15 +517,17 @@ __global__ void __launch_bounds__(kThreads, kEights <= 2 ? 3 : 1) tree_decode_ke
 // One block a (request, head); the state stays in registers between its read and its write: warp
 // w owns rows w, w + 8, .., lane l the columns 4 l .. 4 l + 3, so a warp moves whole rows.  The
 // path's nodes act sixteen at a time: S <- Diag(E) S + sum_j (E_j k_j) u_j^T, E and E_j the decays
-// of the sixteen, and of those behind j.  Bound: the state is read and written once: 150 us for
-// 6144 heads of fp32 (5.4 TB/s; 120 at a copy's rate).  With the two other memories' commits 161 us;
-// at two blocks an SM 165, with four nodes' loads in flight, in registers that the state needs, 169.
+// of the sixteen, and of those behind j.  Bound: the state is read and written once, 121 us for
+// 6144 heads of fp32 at a copy's rate.  With the two other memories' commits 132 us; 161 with the
+// path's rows loaded one after another, which waited behind the state each time (165 at two
+// blocks an SM).
 constexpr int kCommitNodes = 16;
 constexpr int kRows = kD / kWarps;
 
 template <bool kStateBf16>
 __global__ void __launch_bounds__(kThreads, 3) tree_commit_kernel(const TreeStep a) {
-    __shared__ __align__(16) float s_w[kCommitNodes][kD], s_u[kCommitNodes][kD];
+    __shared__ __align__(16) float s_w[kCommitNodes][kD], s_u[kCommitNodes][kD], s_g[kCommitNodes][kD];
+    __shared__ __align__(16) __nv_bfloat16 s_k[kCommitNodes][kD];
     __shared__ float s_decay[kD];
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
@@ -562,23 +564,25 @@ __global__ void __launch_bounds__(kThreads, 3) tree_commit_kernel(const TreeStep
         }
         path = rest;
         if (!first) __syncthreads();
+        // their rows, all on their way at once, from the last node up
+        int r = 0;
+        for (uint64_t p = some; p != 0; ++r) {
+            const int j = top_bit(p);
+            p ^= uint64_t{1} << j;
+            if (r % kWarps != warp) continue;
+            if (lane < 16) sm100::cp_async_16(&s_k[r][8 * lane], a.k + at(j) + 8 * lane, true);
+            sm100::cp_async_16(&s_g[r][4 * lane], a.g + at(j) + 4 * lane, true);
+            sm100::cp_async_16(&s_u[r][4 * lane], a.u + at(j) + 4 * lane, true);
+        }
+        sm100::cp_async_wait_all();
+        __syncthreads();
         if (tid < kD) {
             float e = 1.f;
-            int r = 0;
-            for (uint64_t p = some; p != 0; ++r) {
-                const int j = top_bit(p);
-                p ^= uint64_t{1} << j;
-                s_w[r][tid] = e * __bfloat162float(a.k[at(j) + tid]);
-                e *= expf(a.g[at(j) + tid]);
+            for (r = 0; r < m; ++r) {
+                s_w[r][tid] = e * __bfloat162float(s_k[r][tid]);
+                e *= expf(s_g[r][tid]);
             }
             s_decay[tid] = e;
-        } else {
-            int r = 0;
-            for (uint64_t p = some; p != 0; ++r) {
-                const int j = top_bit(p);
-                p ^= uint64_t{1} << j;
-                s_u[r][tid - kD] = a.u[at(j) + tid - kD];
-            }
         }
         __syncthreads();
         if constexpr (kStateBf16)
