@@ -161,8 +161,8 @@ NCU_TRAFFIC = {
                         "778d78a20aa1906029a458cd4637581380c9c9720ad6861eb5dfc943faf9199d",
                         "c5455d461a5735fe8529d24adc80e51f03cd6f12a6b4cb7c406826b40c47bd2d"],
              "note": "T=4096 capture (profiles/gate_T4096_H96.md)"},
-    "short_conv": {"src": ["kda_shortconv.cu"], "bytes": 552.45e6,
-                   "sha256": ["d69ef349b594f9f5be7de9855c96ce080dc0c0fb1d58e2a9aa31d2fd7cc2d4a6"],
+    "short_conv": {"src": ["kda_shortconv.cu"], "bytes": 552.52e6,
+                   "sha256": ["52b886c5c63b3d72c3b2a6da2a9a3d383e8670e3f0f011e02affd8fd18c6f7b9"],
                    "note": "T=4096 capture (profiles/short_conv_T4096_H96.md)"},
     "backward": {"src": ["kda_backward.cu"], "bytes": 16 * 2.067e9,
                  "sha256": ["58f242b881fc2d1b1acb1532ced68f7c8a83e5dd92b3b19f71833997525eacc1"],
