@@ -236,6 +236,12 @@ __device__ __noinline__ void row_exact(const TreeAttention &a, int b, int64_t ro
 
 // ---- the list of tiles ---------------------------------------------------------------------
 
+// a / b, both 0 or above: in 32 bits where they fit, which nearly all lists do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // A place in the list, and the way from there.  A unit takes kUnitCost places of the list, then as
 // many for each of its tiles as they cost (measured: a tile of two m tiles takes one and a half
 // times one's; beginning and ending a unit takes three).
@@ -255,6 +261,17 @@ struct Cursor {
         first = r.first;
         n = r.n;
         if (len < n || len > static_cast<int64_t>(a.max_pages) * a.cache.page.d) n = 0;
+        measure(a);
+    }
+    // The request of lane `src`'s cursor.
+    __device__ __forceinline__ void request_of(const TreeAttention &a, int src, int i) {
+        b = i;
+        first = __shfl_sync(0xffffffffu, static_cast<int>(first), src);
+        n = __shfl_sync(0xffffffffu, n, src);
+        len = __shfl_sync(0xffffffffu, len, src);
+        measure(a);
+    }
+    __device__ __forceinline__ void measure(const TreeAttention &a) {
         rows = n * a.group;
         groups = (rows + S::kRows - 1) / S::kRows;
         tiles = n == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(len) + S::kKeys - 1) / S::kKeys);
@@ -273,9 +290,9 @@ struct Cursor {
     }
     // Place `i` of the sequence's part of the list.
     __device__ __forceinline__ void seek(int64_t i) {
-        h = static_cast<int>(i / head());
+        h = static_cast<int>(quotient(i, head()));
         i -= h * head();
-        rg = min(static_cast<int>(i / unit(0)), groups - 1);
+        rg = groups == 1 ? 0 : min(static_cast<int>(quotient(i, unit(0))), groups - 1);
         at = static_cast<int>(i - rg * unit(0));
     }
     __device__ __forceinline__ void next_unit(const TreeAttention &a) {
@@ -316,9 +333,9 @@ struct List {
     int64_t total;
     int pieces;
 
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return total * c / pieces; }
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return quotient(total * c, pieces); }
     __device__ __forceinline__ int piece_of(int64_t at) const {
-        return static_cast<int>(((at + 1) * pieces - 1) / total);
+        return static_cast<int>(quotient((at + 1) * pieces - 1, total));
     }
 };
 
@@ -345,16 +362,45 @@ __device__ __forceinline__ int64_t scan_sum(int64_t x, int64_t *s_warp, int64_t 
     return all;
 }
 
-// The list, and in s_place (shared) the sequence and tile within it of list place `at(list)`
-// (b = -1: past the end).
+// A tile begins in every piece that lies within a unit's tiles: the join counts on it.
+template <class S>
+__device__ __forceinline__ void cut_list(List &list, int ctas) {
+    const int64_t most = quotient(list.total, S::kM == 1 ? S::kOneCost : S::kTwoCost);
+    list.pieces = static_cast<int>(most < ctas ? (most < 1 ? 1 : most) : ctas);
+}
+
+// The list, and where place `at(list)` of it lies: c, or false past the end.  s_place: shared.
 template <class S, int kWarps, class At>
-__device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int64_t *s_warp,
-                                           int64_t (&s_place)[2], At at) {
-    const int tid = threadIdx.x;
-    constexpr int kStep = kWarps * 32;
-    List list;
+__device__ __forceinline__ bool find_place(const TreeAttention &a, int ctas, int64_t *s_warp,
+                                           int64_t (&s_place)[2], At at, List &list, Cursor<S> &c) {
+    const int tid = threadIdx.x, lane = tid & 31;
     list.total = 0;
-    Cursor<S> c;
+    if (a.B <= 32) {  // every warp by itself, a lane a request: no barriers, one trip to memory
+        int64_t mine = 0;
+        c.n = c.len = 0;
+        c.first = 0;
+        if (lane < a.B) {
+            c.request(a, lane);
+            mine = c.places(a);
+        }
+        int64_t end = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end += y;
+        }
+        list.total = __shfl_sync(0xffffffffu, end, 31);
+        cut_list<S>(list, ctas);
+        const int64_t place = at(list);
+        const uint32_t there = __ballot_sync(0xffffffffu, place >= end - mine && place < end);
+        if (there == 0) return false;
+        const int src = __ffs(static_cast<int>(there)) - 1;
+        const int64_t before = __shfl_sync(0xffffffffu, end - mine, src);
+        c.request_of(a, src, src);
+        c.seek(place - before);
+        return true;
+    }
+    constexpr int kStep = kWarps * 32;
     int64_t mine = 0, before = 0;
     for (int b0 = 0; b0 < a.B; b0 += kStep) {
         mine = 0;
@@ -364,9 +410,7 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
         }
         list.total += scan_sum<S, kWarps>(mine, s_warp, before);
     }
-    // (a tile begins in every piece that lies within a unit's tiles: the join counts on it)
-    const int64_t most = list.total / (S::kM == 1 ? S::kOneCost : S::kTwoCost);
-    list.pieces = static_cast<int>(most < ctas ? (most < 1 ? 1 : most) : ctas);
+    cut_list<S>(list, ctas);
     if (tid == 0) s_place[0] = -1;
     __syncthreads();
     const int64_t place = at(list);
@@ -388,7 +432,10 @@ __device__ __forceinline__ List find_place(const TreeAttention &a, int ctas, int
         }
     }
     __syncthreads();
-    return list;
+    if (s_place[0] < 0) return false;
+    c.request(a, static_cast<int>(s_place[0]));
+    c.seek(s_place[1]);
+    return true;
 }
 
 // ---- products ------------------------------------------------------------------------------
@@ -519,15 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     const uint32_t tmem = sm.tmem;
     wait_for_kernel_before();
 
-    const List list = find_place<S, kWarps>(a, gridDim.x, sm.warp_sum, sm.place, [&](const List &l) {
-        return static_cast<int>(blockIdx.x) < l.pieces ? l.begin(blockIdx.x) : l.total;
-    });
+    List list;
     Cursor<S> at = {};
-    if (sm.place[0] >= 0) {
+    if (find_place<S, kWarps>(a, gridDim.x, sm.warp_sum, sm.place, [&](const List &l) {
+            return static_cast<int>(blockIdx.x) < l.pieces ? l.begin(blockIdx.x) : l.total;
+        }, list, at))
         at.left = list.begin(blockIdx.x + int64_t{1}) - list.begin(blockIdx.x);
-        at.request(a, static_cast<int>(sm.place[0]));
-        at.seek(sm.place[1]);
-    }
 
     if (warp < kSoftWarps) {
         // ---- queries in, weights, outputs ------------------------------------------------
@@ -1108,14 +1152,12 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
     const int tid = threadIdx.x, c0 = blockIdx.x;
     // (this kernel is set up once the first one's blocks have all waited for what was before
     // them, so the lengths, which the first one does not write, may be read here)
-    const List list = find_place<S, kWarps>(a, ctas, s_warp, s_place, [&](const List &l) {
-        return c0 < l.pieces ? l.begin(c0 + int64_t{1}) : l.total;
-    });
+    List list;
     Cursor<S> cut = {};
     int parts = 0;
-    if (s_place[0] >= 0) {
-        cut.request(a, static_cast<int>(s_place[0]));
-        cut.seek(s_place[1]);
+    if (find_place<S, kWarps>(a, ctas, s_warp, s_place, [&](const List &l) {
+            return c0 < l.pieces ? l.begin(c0 + int64_t{1}) : l.total;
+        }, list, cut)) {
         // the places where the unit's first and last tiles begin
         const int64_t first = list.begin(c0 + int64_t{1}) - cut.at + S::kUnitCost,
                       last = first + static_cast<int64_t>(cut.tiles - 1) * cut.cost(cut.rg);
