@@ -24,13 +24,20 @@
 // as the products read them: by TMA boxes of a page's keys, one instruction for up to 64 of
 // them (16-byte copies took the warps longer than a product), or 16 bytes at a time where pages
 // do not divide so or a tile is not full.  An 8-bit cache comes raw and is widened to fp16, which
-// holds every e4m3 value.  Two warps issue the products: S = Q K^T from shared memory into one of two score
-// buffers in tensor memory, and O += P V with P from there and V from shared memory.  Two
-// warpgroups turn scores into weights in place, a thread a row (a lane of tensor memory), each
-// every second step, so that one's exponentials run beside the other's loads and maxima.  A row's weights are relative to a reference that
-// follows its maximum only when that has grown by 2^7 (2^3 over an 8-bit cache): O is then
-// rescaled, which waits for the last product (at every growth, some row of a warp would grow in
-// most tiles).
+// holds every e4m3 value.  Two warps issue the products: S = Q K^T from shared memory into one of
+// two to four score buffers in tensor memory, and O += P V with P from there and V from shared
+// memory.  Two warpgroups turn scores into weights in place, a thread a row (a lane of tensor
+// memory), each every second step, so that one's exponentials run beside the other's loads and
+// maxima.  A row's weights are relative to a reference that follows its maximum only when that has
+// grown by 2^7 (2^3 over an 8-bit cache): O is then rescaled, which waits for the last product (at
+// every growth, some row of a warp would grow in most tiles).
+//
+// Measured (floor): 1 request of 8 nodes, 301 keys 15 us; 32 requests of 16 nodes, 500-6000 keys, 8
+// heads to each of 8 key heads 82 us (48); 64 of 1-21 nodes over 8 bits 266 us (68); 12 of 64 nodes,
+// 12 heads to a key head 228 us (87).  The tensor cores are busy for 40 to 50 % of it: what bounds
+// it is the chain from scores over weights (2.4k cycles a tile) to outputs, as long as two products,
+// with the score buffers that tensor memory has room for.  Half of a step's keys for each warpgroup, or a
+// quarter for each of four, was slower (85 and 93 us in the second case).
 //
 // Precision: scores, maxima and sums in fp32.  For the product with the values a weight is two
 // words: bf16 numbers, 16 bits together (one would leave up to 2^-8 of every weight, as much as
@@ -1175,26 +1182,40 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
         auto slot = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
         float m = -INFINITY, l = 0.f, acc[8] = {}, nan = 0.f;
         if (real) {
-#pragma unroll 8
-            for (int i = 0; i < parts; ++i)
-                m = fmaxf(m, reinterpret_cast<const float2 *>(args.ml)[slot(i) * S::kRows + tid].x);
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-            for (int i = 0; i < parts; ++i) {
-                const float2 x = reinterpret_cast<const float2 *>(args.ml)[slot(i) * S::kRows + tid];
-                const float w = ex2(x.x - ref);
-                l += w * x.y;
-                const float4 *p = reinterpret_cast<const float4 *>(args.cut) +
-                                  (slot(i) * (kD / 4) + d / 4) * S::kRows + tid;
-                const float4 y = p[0], z = p[S::kRows];
-                acc[0] += w * y.x;
-                acc[1] += w * y.y;
-                acc[2] += w * y.z;
-                acc[3] += w * y.w;
-                acc[4] += w * z.x;
-                acc[5] += w * z.y;
-                acc[6] += w * z.z;
-                acc[7] += w * z.w;
+            // four parts at a time, one trip to memory for them
+            for (int i0 = 0; i0 < parts; i0 += 4) {
+                float2 x[4];
+                float4 y[4], z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = make_float2(-INFINITY, 0.f);
+                    y[i] = z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i0 + i >= parts) continue;
+                    x[i] = reinterpret_cast<const float2 *>(args.ml)[slot(i0 + i) * S::kRows + tid];
+                    const float4 *p = reinterpret_cast<const float4 *>(args.cut) +
+                                      (slot(i0 + i) * (kD / 4) + d / 4) * S::kRows + tid;
+                    y[i] = p[0];
+                    z[i] = p[S::kRows];
+                }
+                const float to = fmaxf(fmaxf(fmaxf(m, x[0].x), x[1].x), fmaxf(x[2].x, x[3].x));
+                const float ref = to == -INFINITY ? 0.f : to, keep = ex2(m - ref);
+                m = to;
+                l *= keep;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] *= keep;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = ex2(x[i].x - ref);
+                    l += w * x[i].y;
+                    acc[0] += w * y[i].x;
+                    acc[1] += w * y[i].y;
+                    acc[2] += w * y[i].z;
+                    acc[3] += w * y[i].w;
+                    acc[4] += w * z[i].x;
+                    acc[5] += w * z[i].y;
+                    acc[6] += w * z[i].z;
+                    acc[7] += w * z[i].w;
+                }
             }
             const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[cut.h] : 1.f;
             const float f = l == 0.f ? 0.f : 1.f / l;
