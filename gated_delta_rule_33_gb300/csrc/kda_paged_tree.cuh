@@ -712,14 +712,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         }
                     }
                     const bool first = i < m_used;
-                    const bool grown = top > m + (first ? 0.f : S::kSlack);
+                    // (where one row of the warp is rescaled, all that have grown at all are)
+                    const bool rescale = __any_sync(0xffffffffu, top > m + S::kSlack) && !first;
+                    const bool grown = top > m && (first || rescale);
                     const float to = grown ? top : m;
                     const float ref = to == -INFINITY ? 0.f : to;
                     if (m_used == 1 && i + 1 < steps) {
                         sm.top[0][lrow] = to;
                         pair_arrive(quarter, wg);
                     }
-                    if (!first && __any_sync(0xffffffffu, grown)) {
+                    if (rescale) {
                         const float keep = grown ? ex2(m - ref) : 1.f;
                         l *= keep;
                         const uint32_t q = g - m_used;  // the last product of these rows
