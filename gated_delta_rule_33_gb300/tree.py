@@ -24,13 +24,15 @@ def _library():
 
 
 def _same_gpu(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The GPU that all of a call's tensors are on."""
+    """The GPU that all of a call's tensors are on: the current one, whose kernels are launched."""
     gpu = first.get_device()
     for t in others:
         if t is not None and t.get_device() != gpu:
             raise _elsewhere(gpu, first, *(x for x in others if x is not None))
     if gpu < 0:
         raise _elsewhere(gpu)
+    if torch.cuda.is_initialized() and gpu != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{gpu}, but the current device is cuda:{torch._C._cuda_getDevice()}")
     return gpu
 
 
