@@ -31,8 +31,12 @@ def _same_gpu(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
             raise _elsewhere(gpu, first, *(x for x in others if x is not None))
     if gpu < 0:
         raise _elsewhere(gpu)
-    if torch.cuda.is_initialized() and gpu != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on cuda:{gpu}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    try:
+        current = torch._C._cuda_getDevice()
+    except RuntimeError:  # no driver: the library says so
+        return gpu
+    if gpu != current:
+        raise ValueError(f"tensors on cuda:{gpu}, but the current device is cuda:{current}")
     return gpu
 
 
