@@ -712,8 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         }
                     }
                     const bool first = i < m_used;
-                    // (where one row of the warp is rescaled, all that have grown at all are)
-                    const bool rescale = __any_sync(0xffffffffu, top > m + S::kSlack) && !first;
+                    // (where one row of the warp is rescaled, all that have grown at all are; lanes without a
+                    // row have scores of whatever lay where their queries would)
+                    const bool rescale = __any_sync(0xffffffffu, real && top > m + S::kSlack) && !first;
                     const bool grown = top > m && (first || rescale);
                     const float to = grown ? top : m;
                     const float ref = to == -INFINITY ? 0.f : to;
