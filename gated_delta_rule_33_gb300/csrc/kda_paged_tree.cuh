@@ -136,6 +136,9 @@ struct Shape {
         int64_t warp_sum[kThreads / 32], place[2];
         // by row: the reference that a warpgroup hands to the other (top[0]), and what they exchange in the end
         float top[2][128];
+        // by row: the halves' largest queries of the next unit.  Apart from `top`: one warpgroup comes to
+        // them while the other still reads its last step's reference.
+        float q_top[2][128];
         uint64_t raw[2][2][kNR > 0 ? kNR : 1];  // keys and values, halves of rows
         uint32_t valid[kTilesAhead][kKeys / 32];  // which rows of a tile are keys
         uint32_t tmem;
@@ -612,9 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         for (const uint32_t y : {x.x, x.y, x.z, x.w})
                             top = max(top, max(y & 0x7fff0000u, (y << 16) & 0x7fff0000u));
                     }
-                sm.top[wg][lrow] = __uint_as_float(top);
+                sm.q_top[wg][lrow] = __uint_as_float(top);
                 pair_barrier(quarter);
-                top = max(top, __float_as_uint(sm.top[wg ^ 1][lrow]));
+                top = max(top, __float_as_uint(sm.q_top[wg ^ 1][lrow]));
                 pair_barrier(quarter);
                 exps[t] = min(max(static_cast<int>(top >> 23), 15), 254) - 127 - 14;
                 const float up = power_of_two(-exps[t]);

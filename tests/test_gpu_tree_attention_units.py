@@ -64,7 +64,7 @@ def many_units(D, H, G, wide, cache, longest, seed):
     return x
 
 
-@pytest.mark.parametrize("cache", ["bf16"])
+@pytest.mark.parametrize("cache", ["fp8", "bf16"])
 @pytest.mark.parametrize("D,H,G,wide", [(128, 8, 8, 4), (64, 8, 8, 4), (256, 8, 8, 4), (128, 8, 8, 0),
                                         (64, 6, 12, 3), (256, 10, 1, 0)])
 def test_units_one_after_another(lib, D, H, G, wide, cache):
@@ -81,7 +81,7 @@ def test_units_one_after_another(lib, D, H, G, wide, cache):
     assert lib.kda_get_last_device_error() == 0
 
 
-@pytest.mark.parametrize("cache", ["bf16"])
+@pytest.mark.parametrize("cache", ["fp8", "bf16"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_bits_do_not_depend_on_the_call_before(lib, D, cache):
     """Requests of a few rows, after a call with large queries in every row of a block and after one
