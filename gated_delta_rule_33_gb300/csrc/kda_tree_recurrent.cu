@@ -26,13 +26,20 @@
 // 16 columns of the product for all rows; then each thread solves its column of the updates, 8
 // nodes in registers, and the outputs follow.
 //
-// Measured, 64 requests of 7 to 16 nodes, 96 heads, fp32 state: 188 us (82 at a copy's rate).  337
+// Measured, 64 requests of 7 to 16 nodes, 96 heads, fp32 state: 192 us (82 at a copy's rate).  337
 // with the product on the fp32 pipe, 280 as two tf32 words, 226 with 16-byte copies, 213 with
 // paths in packed pairs (219 as three bf16 words, which hold more), 211 walking over units, 207 with
 // a unit's place loaded ahead, 197 with the state in halves and a third block, 188 in quarters.
 // (512 threads a block: 244.)  What bounds it: some 2300 instructions a warp and unit, which fill
 // half of the issue slots; a unit's phases (decays, paths, product, updates, outputs) are chains
 // with barriers between them, and three blocks do not fill all of their gaps.
+//
+// What is not finite.  In the tables of products a node that is not above another has a 0, and 0 times
+// an update that is not finite is NaN; an infinite operand has no second word either (inf - inf).  So
+// a block that met an output that is not finite goes over its units again in the end and solves what
+// is not finite in them in fp32 arithmetic, the nodes chosen by their words (solve_again).  To look for
+// it costs 1 to 2 % (192 us where there were 189).
+#include <cfloat>
 #include <type_traits>
 
 #include "kda_f32x2.cuh"
@@ -194,6 +201,91 @@ struct TreeUnit {
     __device__ __forceinline__ int64_t at(const TreeStep &a, int i) const { return ((first + i) * a.H + h) * kD; }
 };
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+
+// What of a unit's updates and outputs is not finite, once more, in fp32 arithmetic and with the
+// nodes chosen by their words.  What is finite stays as it is.  By the whole block, which has nothing
+// else to do and nothing on its way to shared memory.  (Inlined: as a function it took the kernel
+// registers that the loop needs, 193 us.)
+template <bool kStateBf16, bool kOutBf16, int kEights>
+__device__ __forceinline__ void solve_again(const TreeStep &a, uint32_t which, uint8_t *smem) {
+    const TreeUnit unit(a, TreePlace(a, which));
+    if (unit.n == 0) return;
+    const TreeSmem<kEights, kStateBf16> s(smem, a.max_nodes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = unit.n, nc = s.nc;
+    float *rows = reinterpret_cast<float *>(s.rows), *u = s.decay;  // [n][2][kD]: E_i k_i, E_i scale q_i
+    auto output = [&](int64_t at) {
+        if constexpr (kOutBf16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(a.o)[at]);
+        else return static_cast<const float *>(a.o)[at];
+    };
+    bool all = true;
+    for (int i = tid; i < n * kD; i += kThreads) {
+        const int64_t at = unit.at(a, i / kD) + i % kD;
+        all &= finite(output(at)) && (a.u == nullptr || finite(a.u[at]));
+        s.decay[i] = expf(a.g[at]);
+        s.k[i] = a.k[at];
+    }
+    if (!__syncthreads_or(!all)) return;
+    for (int i = warp; i < n; i += kWarps) {  // a warp a node, up its path
+        const int64_t at = unit.at(a, i) + lane * 4;
+        const float4 k = widen4(*reinterpret_cast<const uint2 *>(s.k + i * kD + lane * 4));
+        float4 q = widen4(*reinterpret_cast<const uint2 *>(a.q + at)), e = make_float4(1.f, 1.f, 1.f, 1.f);
+        q = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
+        for (uint64_t path = path_of(a.ancestors[unit.first + i], i); path != 0;) {
+            const int j = top_bit(path);
+            path ^= uint64_t{1} << j;
+            const float4 kj = widen4(*reinterpret_cast<const uint2 *>(s.k + j * kD + lane * 4));
+            const float4 d = *reinterpret_cast<const float4 *>(s.decay + j * kD + lane * 4);
+            const float4 y = make_float4(e.x * kj.x, e.y * kj.y, e.z * kj.z, e.w * kj.w);
+            float dk = y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
+            float dq = y.x * q.x + y.y * q.y + y.z * q.z + y.w * q.w;
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) {
+                dk += __shfl_xor_sync(0xffffffffu, dk, m);
+                dq += __shfl_xor_sync(0xffffffffu, dq, m);
+            }
+            if (lane == 0) {
+                s.ak[j * nc + i] = dk;
+                s.aq[j * nc + i] = dq;
+            }
+            e = make_float4(e.x * d.x, e.y * d.y, e.z * d.z, e.w * d.w);
+        }
+        float4 *row = reinterpret_cast<float4 *>(rows + i * 2 * kD) + lane;
+        row[0] = make_float4(e.x * k.x, e.y * k.y, e.z * k.z, e.w * k.w);
+        row[kD / 4] = make_float4(e.x * q.x, e.y * q.y, e.z * q.z, e.w * q.w);
+    }
+    __syncthreads();
+    if (tid < kD) {  // a thread a column
+        const int64_t state = (static_cast<int64_t>(unit.slot) * a.H + unit.h) * (kD * kD) + tid;
+        for (int i = 0; i < n; ++i) {
+            const int64_t at = unit.at(a, i) + tid;
+            const float *row = rows + i * 2 * kD;
+            float w = 0.f, z = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < kD; ++k) {
+                float x;
+                if constexpr (kStateBf16) x = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.pool)[state + k * kD]);
+                else x = static_cast<const float *>(a.pool)[state + k * kD];
+                w += row[k] * x;
+                z += row[kD + k] * x;
+            }
+            for (uint64_t p = a.ancestors[unit.first + i] & bits_below(i); p != 0; p &= p - 1) {
+                const int j = __ffsll(static_cast<long long>(p)) - 1;
+                w += s.ak[j * nc + i] * u[j * kD + tid];
+                z += s.aq[j * nc + i] * u[j * kD + tid];
+            }
+            float x = a.beta[(unit.first + i) * a.H + unit.h] * (__bfloat162float(a.v[at]) - w);
+            if (a.u != nullptr) {
+                if (finite(a.u[at])) x = a.u[at];
+                else a.u[at] = x;
+            }
+            u[i * kD + tid] = x;
+            if (!finite(output(at))) write_out<kOutBf16>(a.o, at, z + s.aq[i * nc + i] * x);
+        }
+    }
+    __syncthreads();
+}
+
 // By registers (the accumulators of a warp are 16 an eight) and shared memory.
 constexpr int blocks_an_sm(int eights) { return eights <= 2 ? 3 : eights <= 4 ? 2 : 1; }
 
@@ -206,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, blocks_an_sm(kEights)) tree_decode_k
     constexpr int kBits = 8 * sizeof(Word);
     constexpr uint32_t kRow = kD * (kStateBf16 ? 2 : 4);
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_again;  // some unit of the block's has an output that is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Smem s(smem, a.max_nodes);
     const uint32_t units = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.H);
@@ -250,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, blocks_an_sm(kEights)) tree_decode_k
             sm100::cp_async_16(s.k + i * 8, x + u.at(a, i >> 4) + (i & 15) * 8, true);
     };
 
+    if (tid == 0) s_again = 0;  // (the first unit's barriers come before it is written again)
     TreeUnit u(a, TreePlace(a, blockIdx.x));
     fetch_inputs(u);
     fetch_first_parts(u);
@@ -509,10 +603,16 @@ __global__ void __launch_bounds__(kThreads, blocks_an_sm(kEights)) tree_decode_k
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i0 + i < n) write_out<kOutBf16>(a.o, u.at(a, i0 + i) + c, w[i]);
+            // (an update that is not finite shows in its own node's output)
+            if (!finite((w[0] + w[1]) + (w[2] + w[3]))) s_again = 1;
         }
         __syncthreads();
         u = next;
     }
+    __syncthreads();  // (there may have been no unit with nodes)
+    if (s_again == 0) return;
+    for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x)
+        solve_again<kStateBf16, kOutBf16, kEights>(a, unit, smem);
 }
 
 // ---- commit --------------------------------------------------------------------------------

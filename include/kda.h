@@ -717,7 +717,9 @@ kda_status kda_paged_decode(const void *q, int64_t q_row_stride, const kda_paged
  *
  * from which kda_recurrent_tree_commit forms the state after any path.  Sums are fp32, and
  * operands are kept to 24 bits (a bf16 state is widened; unlike a chain of one-token decodes, it
- * is not rounded between the nodes of a path).
+ * is not rounded between the nodes of a path).  What a node does not see has no part in its output
+ * and update, whatever it holds.  Infinities and NaN act as in fp32 arithmetic; a call that meets
+ * them takes longer.  Two calls on the same inputs write the same bits.
  *
  *   q, k, v        bf16 [N, H, 128];  g fp32 [N, H, 128];  beta fp32 [N, H]
  *   state_pool     [num_slots, H, 128, 128] of state_dtype (fp32 or bf16), read
