@@ -48,7 +48,10 @@
 //
 // What is not finite.  A weight of 0 times an infinite or NaN value is NaN, and so is 0 (a
 // weight's second word) times an infinite one.  So a row whose output is not finite although
-// its weights are is computed again, key by key, over the keys that it sees (row_exact).
+// its weights are is computed again over the keys that it sees (row_again), in 8 channels at a time:
+// that of a whole unit by the warps that had it, once the CTA has nothing else to do, that of
+// a cut one by the second kernel.  In neither place does another warp wait for it with a limit.  (One NaN
+// that 64 nodes x 8 heads see in 8192 keys, beside 64 short requests: 45 ms.)
 #pragma once
 
 #include <cfloat>
@@ -142,6 +145,8 @@ struct Shape {
         uint64_t raw[2][2][kNR > 0 ? kNR : 1];  // keys and values, halves of rows
         uint32_t valid[kTilesAhead][kKeys / 32];  // which rows of a tile are keys
         uint32_t tmem;
+        int begin[kSoftWarps][4];                 // where the CTA's piece begins: a warp's copy
+        int64_t places[kSoftWarps];
     };
     static constexpr int kSmem = kOffSmall + static_cast<int>(sizeof(Small));
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -181,67 +186,95 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
     return y;
 }
 
-// ---- a row, key by key ---------------------------------------------------------------------
+// ---- a row in fp32 arithmetic --------------------------------------------------------------
 
-// A lane's kN neighbouring values of a row, widened.
-template <bool kFp8, int kN>
-__device__ __forceinline__ void load_values(const uint8_t *p, float (&x)[kN]) {
+// Eight neighbouring values of a row, widened.
+template <bool kFp8>
+__device__ __forceinline__ void load_eight(const uint8_t *p, float (&y)[8]) {
+    uint32_t w[4];
+    if constexpr (kFp8) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = e4m3x2_to_f16x2(x.x);
+        w[1] = e4m3x2_to_f16x2(x.x >> 16);
+        w[2] = e4m3x2_to_f16x2(x.y);
+        w[3] = e4m3x2_to_f16x2(x.y >> 16);
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
+    }
 #pragma unroll
-    for (int i = 0; i < kN; i += 2) {
-        const float2 f = kFp8 ? unpack2<true>(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(p + i)))
-                              : unpack2<false>(*reinterpret_cast<const uint32_t *>(p + 2 * i));
-        x[i] = f.x;
-        x[i + 1] = f.y;
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<kFp8>(w[i]);
+        y[2 * i] = f.x;
+        y[2 * i + 1] = f.y;
     }
 }
 
-// Channels [c0, c1) of one row's output, by one warp, in fp32 arithmetic over the keys that the
-// row sees.  The sums are averages from the first key on, so they are as large as the values.
+// The average of values over two sets of keys, weights relative to references.  (Averages, so that they
+// are as large as the values.)
+__device__ __forceinline__ void join_averages(float &m, float &l, float (&acc)[8], float m1, float l1, const float (&acc1)[8]) {
+    const float to = m1 > m || m1 != m1 ? m1 : m, ref = to == -INFINITY ? 0.f : to;
+    const float w = l * exp2f(m - ref), w1 = l1 * exp2f(m1 - ref);
+    m = to;
+    l = w + w1;
+    if (l == 0.f) return;
+    const float part = w / l, part1 = w1 / l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = part * acc[i] + part1 * acc1[i];
+}
+
+// Channels d .. d + 7 of a row's output, by one warp, in fp32 arithmetic over the keys that the row
+// sees: each lane has every 32nd of them.  s_q: [kD], the warp's.
 template <int kD, bool kFp8>
-__device__ __noinline__ void row_exact(const TreeAttention &a, int b, int64_t row, int qh, int n,
-                                       int len, int c0, int c1) {
-    constexpr int kN = kD / 32;
+__device__ __noinline__ void row_again(const TreeAttention &a, int b, int64_t row, int qh, int n, int len, int d,
+                                       float *s_q) {
+    constexpr int kSize = kFp8 ? 1 : 2;
     const int lane = threadIdx.x & 31, h = qh / a.group, context = len - n;
     const uint64_t word = a.ancestors[row];
-    float q[kN], acc[kN], m = -INFINITY, l = 0.f;
-    load_values<false, kN>(
-        reinterpret_cast<const uint8_t *>(a.q + row * a.q_row_stride + qh * kD + lane * kN), q);
     const float c = a.scale * kLog2e * (a.cache.k_scale != nullptr ? a.cache.k_scale[h] : 1.f);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-    for (int j = 0; j < len; ++j) {
-        if (j >= context && !((word >> (j - context)) & 1)) continue;
+    for (int i = lane; i < kD; i += 32)
+        s_q[i] = __bfloat162float(a.q[row * a.q_row_stride + qh * kD + i]);
+    __syncwarp();
+    float m = -INFINITY, l = 0.f, acc[8] = {};
+    for (uint32_t j = lane; j < static_cast<uint32_t>(len); j += 32) {
+        const int drafted = static_cast<int>(j) - context;
+        if (drafted >= 0 && !((word >> drafted) & 1)) continue;
         uint32_t idx, in_page;
         a.cache.page.divmod(j, idx, in_page);
         const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + idx];
         if (page < 0 || page >= a.cache.num_pages) continue;
-        const int64_t off = page * a.cache.page_stride + in_page * a.cache.token_stride +
-                            h * a.cache.head_stride + lane * kN * (kFp8 ? 1 : 2);
-        float k[kN], v[kN], s = 0.f;
-        load_values<kFp8, kN>(a.cache.k + off, k);
-        load_values<kFp8, kN>(a.cache.v + off, v);
+        const int64_t off = page * a.cache.page_stride + in_page * a.cache.token_stride + h * a.cache.head_stride;
+        float s = 0.f, x[8];
+#pragma unroll 4
+        for (int i = 0; i < kD; i += 8) {
+            load_eight<kFp8>(a.cache.k + off + i * kSize, x);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) s += q[i] * k[i];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            for (int k = 0; k < 8; ++k) s += s_q[i + k] * x[k];
+        }
+        load_eight<kFp8>(a.cache.v + off + d * kSize, x);
         s *= c;
-        const float to = s > m || s != s ? s : m;
-        const float ref = to == -INFINITY ? 0.f : to;
-        const float p = exp2f(s - ref), before = l * exp2f(m - ref);
-        m = to;
-        l = before + p;
-        if (l == 0.f) continue;
-        const float w = p / l, rest = before / l;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) acc[i] = acc[i] * rest + w * v[i];
+        // (a score of -inf has no weight)
+        join_averages(m, l, acc, s, s == -INFINITY ? 0.f : 1.f, x);
     }
-    const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[h] : 1.f;
-    __nv_bfloat16 *o = a.o + (row * a.q_heads + qh) * kD;
+#pragma unroll 1
+    for (int x = 16; x > 0; x >>= 1) {
+        float other[8];
+        const float m1 = __shfl_xor_sync(0xffffffffu, m, x), l1 = __shfl_xor_sync(0xffffffffu, l, x);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int d = lane * kN + i;
-        if (d >= c0 && d < c1) o[d] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[i] * vs);
+        for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, acc[i], x);
+        join_averages(m, l, acc, m1, l1, other);
     }
+    if (lane == 0) {
+        const float vs = a.cache.v_scale != nullptr ? a.cache.v_scale[h] : 1.f;
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) y[i / 2] = l == 0.f ? 0u : pack2<false>(acc[i] * vs, acc[i + 1] * vs);
+        *reinterpret_cast<uint4 *>(a.o + (row * a.q_heads + qh) * kD + d) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    __syncwarp();
 }
 
 // ---- the list of tiles ---------------------------------------------------------------------
@@ -640,6 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.qfull);
         };
+        if (lane == 0) {
+            int *begin = sm.begin[warp];
+            begin[0] = at.b;
+            begin[1] = at.h;
+            begin[2] = at.rg;
+            begin[3] = at.at;
+            sm.places[warp] = at.left;
+        }
+        bool again = false;  // a row of the warp's, of a whole unit, is not finite although its weights are
         bool more = at.take(a);
         if (kFp8 && more) queries(at, exps);
         while (more) {
@@ -850,15 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 if (whole) {
                     if (real && d0 == 0 && a.lse != nullptr)
                         a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - S::kShift) * kLn2;
-                    // what is not finite although the weights are
-                    uint32_t again = __ballot_sync(0xffffffffu, real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
-                    while (again != 0) {
-                        const int src = __ffs(static_cast<int>(again)) - 1;
-                        again &= again - 1;
-                        row_exact<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, row, src),
-                                            __shfl_sync(0xffffffffu, qh, src), at.n, at.len, d0, d1);
-                        __syncwarp();
-                    }
+                    again |= __any_sync(0xffffffffu, real && nan != 0.f && l * 0.f == 0.f && l != 0.f);
                 } else if (d0 == 0) {
                     reinterpret_cast<float2 *>(args.ml)[slot * S::kRows + mt * 128 + lrow] = make_float2(m, l);
                 }
@@ -869,6 +903,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             if constexpr (kFp8)
 #pragma unroll
                 for (int t = 0; t < kM; ++t) exps[t] = exps_next[t];
+        }
+        // What is not finite is computed again when the piece is done: it may take long, and no other
+        // warp waits with a limit now.  (The queries' place is free.)
+        if (again) {
+            const int *begin = sm.begin[warp];
+            at.request(a, begin[0]);
+            at.h = begin[1];
+            at.rg = begin[2];
+            at.at = begin[3];
+            at.left = sm.places[warp];
+            step = 0;
+            while (at.take(a)) {
+                const int m_used = at.m_tiles(at.rg), mt = m_used == 1 ? 0 : (step + wg) & 1;
+                step += (at.t1 - at.t) * m_used;
+                if (at.t != 0 || at.t1 != at.tiles) continue;
+                const int d0 = m_used == 1 ? wg * (kD / 2) : 0, d1 = m_used == 1 ? d0 + kD / 2 : kD;
+                const int rr = at.rg * S::kRows + mt * 128 + lrow;
+                uint32_t node, head;
+                args.group.divmod(rr, node, head);
+                const int64_t row = at.first + node;
+                const int qh = at.h * a.group + static_cast<int>(head);
+                for (int d = d0; d < d1; d += 8) {
+                    bool bad = false;
+                    if (rr < at.rows) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(a.o + (row * a.q_heads + qh) * kD + d);
+                        for (const uint32_t y : {x.x, x.y, x.z, x.w})
+                            bad |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+                    }
+                    for (uint32_t rows = __ballot_sync(0xffffffffu, bad); rows != 0; rows &= rows - 1) {
+                        const int src = __ffs(static_cast<int>(rows)) - 1;
+                        row_again<kD, kFp8>(a, at.b, __shfl_sync(0xffffffffu, row, src),
+                                            __shfl_sync(0xffffffffu, qh, src), at.n, at.len, d,
+                                            reinterpret_cast<float *>(smem) + warp * kD);
+                    }
+                }
+            }
         }
     } else if (warp < kSoftWarps + kCopyWarps) {
         // ---- keys and values in --------------------------------------------------------------
@@ -1161,6 +1231,7 @@ template <class S>
 __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_constant__ Args args, int ctas) {
     constexpr int kD = S::kD, kWarps = S::kRows / 32;
     __shared__ int64_t s_warp[kWarps], s_place[2];
+    __shared__ float s_q[kWarps][kD];
     const TreeAttention &a = args.t;
     const int tid = threadIdx.x, c0 = blockIdx.x;
     // (this kernel is set up once the first one's blocks have all waited for what was before
@@ -1240,9 +1311,8 @@ __global__ void __launch_bounds__(S::kRows) tree_join_kernel(const __grid_consta
         while (again != 0) {
             const int src = __ffs(static_cast<int>(again)) - 1;
             again &= again - 1;
-            row_exact<kD, S::kFp8>(a, cut.b, __shfl_sync(0xffffffffu, row, src),
-                                   __shfl_sync(0xffffffffu, qh, src), cut.n, cut.len, d, d + 8);
-            __syncwarp();
+            row_again<kD, S::kFp8>(a, cut.b, __shfl_sync(0xffffffffu, row, src),
+                                   __shfl_sync(0xffffffffu, qh, src), cut.n, cut.len, d, s_q[tid >> 5]);
         }
     }
     if (blockIdx.y != 0) return;
