@@ -233,7 +233,8 @@ def kda_paged_copy(copies, cache, stream=None):
 def kda_page_release(seq_lens, kept_lens, block_table, page_size, shares, freed, num_freed,
                      stream=None):
     """Gives back the pages that requests of seq_lens [B] tokens no longer need for kept_lens [B];
-    shares [num_pages] is updated, freed [max_freed] and num_freed [1] written."""
+    shares [num_pages] is updated, freed [max_freed] and num_freed [1] written.  A request that keeps
+    part of a shared page must be forked before anything is appended to it."""
     B, max_pages = block_table.shape
     if seq_lens.numel() != B or kept_lens.numel() != B or num_freed.numel() != 1:
         raise ValueError("seq_lens and kept_lens [B], num_freed [1]")

@@ -858,8 +858,9 @@ kda_status kda_paged_compact(const kda_paged_cache *cache, const int32_t *block_
  * the source's length is negative or does not fit its row, dst[f] is a source or an earlier
  * fork's destination, or no page is left: nothing is written for it but its entry of copies.
  * (Where src and its length are good, the page that it would take counts as taken.)  A page
- * outside 0 .. num_pages-1 is neither counted nor copied and sets INVALID_ARG.  No array may
- * overlap another.  num_forks == 0 writes pages_used = 0.
+ * outside 0 .. num_pages-1 is neither counted nor copied and sets INVALID_ARG.  A source's last,
+ * partly filled page may be shared itself.  No array may overlap another.  num_forks == 0 writes
+ * pages_used = 0.
  */
 kda_status kda_page_fork(const int32_t *src, const int32_t *dst, int num_forks, int32_t *seq_lens,
                          const int32_t *free_pages, int num_free, int32_t *block_table,
@@ -888,6 +889,12 @@ kda_status kda_paged_copy(const int32_t *copies, int num_copies, const kda_paged
  *                past num_freed stay as they were (it may be the end of the free list: 4-byte
  *                aligned is enough)
  *   num_freed    int32 [1] written
+ *
+ * A kept length may end inside a page that another request holds too (shares > 0: a fork, or
+ * its source, that goes back behind the point where they parted).  The page stays shared, so the
+ * request may be read, shortened, forked and released, but nothing may be appended to it or
+ * compacted in it: that would write into the other's keys.  To go on from it, kda_page_fork it into an
+ * empty row, which gives the last page a copy of its own, kda_paged_copy, and release the old row.
  *
  * A request with kept_lens[b] < 0 or > seq_lens[b], or a length that does not fit its row, is
  * refused and keeps its pages.  A page that is given back more often than it is held is freed
