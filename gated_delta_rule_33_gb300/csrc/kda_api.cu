@@ -66,6 +66,21 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return a != nullptr && b != nullptr && na > 0 && nb > 0 && pa < pb + nb && pb < pa + na;
 }
 
+struct Buffer {
+    const void *p;
+    size_t bytes;
+};
+
+// Whether [a, a + na) meets one of n rows of `row` bytes, `stride` bytes (not below `row`) apart.
+inline bool overlaps_rows(const void *a, size_t na, const void *b, size_t row, size_t stride, int64_t n) {
+    if (n <= 1) return n == 1 && overlaps(a, na, b, row);
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    if (a == nullptr || b == nullptr || na == 0 || row == 0) return false;
+    // the first row that ends behind a's begin
+    const size_t first = pa < pb + row ? 0 : (pa - pb - row) / stride + 1;
+    return first < static_cast<size_t>(n) && pb + first * stride < pa + na;
+}
+
 kda_status from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return KDA_OK;
     cudaGetLastError();
@@ -818,11 +833,12 @@ kda_status kda_recurrent_tree_decode(const void *q, const void *k, const void *v
         return KDA_ERR_MISALIGNED;
     const size_t values = static_cast<size_t>(N) * H * 128;
     const size_t o_bytes = values * (o_dtype == KDA_BF16 ? 2 : 4);
-    const void *ins[5] = {q, k, v, g, state_pool};
     const size_t pool = static_cast<size_t>(num_slots) * H * 16384 * (state_dtype == KDA_BF16 ? 2 : 4);
-    const size_t in_bytes[5] = {values * 2, values * 2, values * 2, values * 4, pool};
-    for (int i = 0; i < 5; ++i)
-        if (overlaps(o, o_bytes, ins[i], in_bytes[i]) || overlaps(u, values * 4, ins[i], in_bytes[i]))
+    const Buffer ins[] = {{q, values * 2}, {k, values * 2}, {v, values * 2}, {g, values * 4}, {state_pool, pool},
+                          {beta, static_cast<size_t>(N) * H * 4}, {state_indices, static_cast<size_t>(B) * 4},
+                          {cu_seqlens, static_cast<size_t>(B) * 4 + 4}, {ancestors, static_cast<size_t>(N) * 8}};
+    for (const Buffer &in : ins)
+        if (overlaps(o, o_bytes, in.p, in.bytes) || overlaps(u, values * 4, in.p, in.bytes))
             return KDA_ERR_INVALID_ARG;
     if (overlaps(o, o_bytes, u, values * 4)) return KDA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
@@ -927,7 +943,10 @@ kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void 
                 overlaps(ys[i], bytes, ws[j], static_cast<size_t>(C) * 16) ||
                 (i < j && overlaps(ys[i], bytes, ys[j], bytes)))
                 return KDA_ERR_INVALID_ARG;
-        if (overlaps(ys[i], bytes, conv_state_pool, pool)) return KDA_ERR_INVALID_ARG;
+        const Buffer ins[] = {{conv_state_pool, pool}, {state_indices, static_cast<size_t>(B) * 4},
+                              {cu_seqlens, static_cast<size_t>(B) * 4 + 4}, {ancestors, static_cast<size_t>(N) * 8}};
+        for (const Buffer &in : ins)
+            if (overlaps(ys[i], bytes, in.p, in.bytes)) return KDA_ERR_INVALID_ARG;
     }
     if (!aligned16(conv_state_pool) || !aligned16(state_indices) || !aligned16(cu_seqlens) ||
         !aligned16(ancestors))
@@ -1035,6 +1054,22 @@ kda_status kda_paged_tree_decode(const void *q, int64_t q_row_stride, const kda_
     if (workspace_bytes < need || (need > 0 && workspace == nullptr))
         return KDA_ERR_WORKSPACE_TOO_SMALL;
     if (B == 0 || N == 0) return KDA_OK;
+    const size_t rows = static_cast<size_t>(N) * q_heads, requests = static_cast<size_t>(B) * 4;
+    const Buffer outs[] = {{o, rows * view.head_dim * 2}, {lse, rows * 4}, {workspace, need}};
+    const Buffer ins[] = {{view.k, view.bytes()}, {view.v, view.bytes()},
+                          {view.k_scale, static_cast<size_t>(view.heads) * 4},
+                          {view.v_scale, static_cast<size_t>(view.heads) * 4},
+                          {block_table, requests * max_pages}, {seq_lens, requests}, {cu_seqlens, requests + 4},
+                          {ancestors, static_cast<size_t>(N) * 8}};
+    for (int i = 0; i < 3; ++i) {
+        if (overlaps_rows(outs[i].p, outs[i].bytes, q, static_cast<size_t>(width) * 2,
+                          N > 1 ? static_cast<size_t>(q_row_stride) * 2 : 0, N))
+            return KDA_ERR_INVALID_ARG;
+        for (const Buffer &in : ins)
+            if (overlaps(outs[i].p, outs[i].bytes, in.p, in.bytes)) return KDA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return KDA_ERR_INVALID_ARG;
+    }
     DeviceInfo *dev = nullptr;
     st = current_device(&dev);
     if (st != KDA_OK) return st;
@@ -1085,7 +1120,8 @@ kda_status kda_paged_compact(const kda_paged_cache *cache, const int32_t *block_
     if (overlaps(kept_lens, rows, seq_lens, rows) || overlaps(kept_lens, rows, last, rows) ||
         overlaps(kept_lens, rows, cu_seqlens, rows + 4) ||
         overlaps(kept_lens, rows, ancestors, static_cast<size_t>(N) * 8) ||
-        overlaps(kept_lens, rows, block_table, rows * static_cast<size_t>(max_pages)))
+        overlaps(kept_lens, rows, block_table, rows * static_cast<size_t>(max_pages)) ||
+        overlaps(kept_lens, rows, view.k, view.bytes()) || overlaps(kept_lens, rows, view.v, view.bytes()))
         return KDA_ERR_INVALID_ARG;
     if (B == 0) return KDA_OK;
     DeviceInfo *dev = nullptr;

@@ -77,6 +77,12 @@ struct PagedView {
     int num_pages;
     int heads, head_dim;
     bool fp8;
+
+    // From a half's first byte to behind its last.
+    size_t bytes() const {
+        return static_cast<size_t>((num_pages - 1) * page_stride + (page.d - 1) * token_stride + (heads - 1) * head_stride) +
+               static_cast<size_t>(head_dim) * (fp8 ? 1 : 2);
+    }
 };
 
 cudaError_t launch_page_plan(const int32_t *cached_lens, const int32_t *new_lens,

@@ -804,6 +804,7 @@ size_t kda_paged_tree_decode_workspace_size(int B, int max_nodes, int q_heads, i
  *   lse         fp32 [N, q_heads] written, or NULL
  *   workspace   device scratch, >= kda_paged_tree_decode_workspace_size() bytes, 16-byte
  *               aligned; not shared with a concurrent call
+ * o, lse and the workspace must not overlap an input or one another.
  *
  * A node that sees no key gives o = 0 and lse = -inf; what it does not see has no part in its
  * output, whatever it holds.  A length below n or above max_pages * page_size counts as no keys
