@@ -1195,7 +1195,9 @@ kda_status kda_page_release(const int32_t *seq_lens, const int32_t *kept_lens,
                             int32_t *num_freed, void *stream) {
     if (max_pages < 0 || B < 0 || page_size < 1 || num_pages < 0 || max_freed < 0)
         return KDA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX ||
+        static_cast<int64_t>(B < kda::kReleaseRequests ? B : kda::kReleaseRequests) * max_pages > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
     if (num_freed == nullptr || (max_freed > 0 && freed == nullptr) ||
         (num_pages > 0 && shares == nullptr) ||
         (B > 0 && (seq_lens == nullptr || kept_lens == nullptr ||

@@ -9,7 +9,7 @@ namespace kda {
 namespace {
 
 constexpr int kForkThreads = 128;
-constexpr int kThreads = 1024;
+constexpr int kThreads = kReleaseRequests;
 constexpr int kRangePages = 1 << 20;  // pages whose bits fit shared memory (128 KB)
 constexpr int kRanks = 8;             // blocks of a release of many requests, a cluster
 // Up to these, one block: 16 requests' 60 pages each take it 6.9 us, a cluster 7.6; 64 requests' 12.4

@@ -13,6 +13,9 @@ namespace kda {
 
 constexpr int kTreeNodes = 64;
 
+// Requests whose pages a release takes as one list, with 32-bit places in it.
+constexpr int kReleaseRequests = 1024;
+
 struct TreeRows {
     int64_t first;  // row of node 0
     int n;          // nodes; 0 where there is nothing to do

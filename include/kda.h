@@ -901,7 +901,8 @@ kda_status kda_paged_copy(const int32_t *copies, int num_copies, const kda_paged
  * refused and keeps its pages.  A page that is given back more often than it is held is freed
  * once; a page outside 0 .. num_pages-1 is passed over; pages past max_freed are not listed
  * (their shares are 0: they are lost to the caller).  Each sets INVALID_ARG in the device error
- * word.  No array may overlap another.  B == 0 writes num_freed = 0.
+ * word.  No array may overlap another.  1024 rows of the table (or B, if fewer) must have fewer than
+ * 2^31 entries.  B == 0 writes num_freed = 0.
  */
 kda_status kda_page_release(const int32_t *seq_lens, const int32_t *kept_lens,
                             const int32_t *block_table, int max_pages, int B, int page_size,
