@@ -909,12 +909,7 @@ kda_status kda_recurrent_tree_commit(const void *k, const float *g, const float 
     a.N = N;
     a.u = const_cast<float *>(u);
     a.err = dev->error_word;
-    try {
-        return from_cuda(kda::launch_tree_commit(a, state_dtype == KDA_BF16,
-                                                 static_cast<cudaStream_t>(stream)));
-    } catch (...) {  // the list of kernels with raised shared-memory limits could not grow
-        return KDA_ERR_CUDA;
-    }
+    return from_cuda(kda::launch_tree_commit(a, state_dtype == KDA_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_short_conv_qkv_tree(const void *x_q, const void *x_k, const void *x_v,

@@ -20,8 +20,10 @@
 // three products hold less and took twice as long).  A block walks over units, each a
 // (request, head); up to 16 nodes three blocks share an SM, so that some compute while others wait.
 // The state comes by 16-byte copies (bulk copies of a row each took 5 us to issue), to rows 8 words
-// apart in the banks, in quarters of which two are there at a time: one meets the vectors while the
-// next arrives, and the next unit's first two come while this one's updates run.  A warp a node
+// apart in the banks.  An fp32 state of a call with up to 32 nodes comes in quarters of which two are there
+// at a time: one meets the vectors while the next arrives, and the next unit's first two come while
+// this one's updates run.  A bf16 state, and that of a call with more nodes, comes whole, while the updates
+// of the unit before run.  A warp a node
 // walks its path for E_i k_i, E_i q_i and the products (E_ij k_j) . k_i and . q_i.  Then a warp has
 // 16 columns of the product for all rows; then each thread solves its column of the updates, 8
 // nodes in registers, and the outputs follow.
