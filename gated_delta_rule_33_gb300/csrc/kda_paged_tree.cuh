@@ -32,9 +32,10 @@
 // grown by 2^7 (2^3 over an 8-bit cache): O is then rescaled, which waits for the last product (at
 // every growth, some row of a warp would grow in most tiles).
 //
-// Measured (floor): 1 request of 8 nodes, 301 keys 15 us; 32 requests of 16 nodes, 500-6000 keys, 8
-// heads to each of 8 key heads 82 us (48); 64 of 1-21 nodes over 8 bits 266 us (68); 12 of 64 nodes,
-// 12 heads to a key head 228 us (87).  The tensor cores are busy for 40 to 50 % of it: what bounds
+// Measured (floor): 1 request of 8 nodes, 301 keys 13.5 us; 32 requests of 16 nodes, 500-6000 keys, 8
+// heads to each of 8 key heads 81 us (48); 64 of 1-21 nodes over 8 bits 265 us (68); 12 of 64 nodes,
+// 12 heads to a key head 230-237 us (87).  The second case at 64 channels 64 us (24), at 256 151 us (97);
+// over 8 bits 69 (13), 99 (26) and 172 us (51).  The tensor cores are busy for 40 to 50 % of it: what bounds
 // it is the chain from scores over weights (2.4k cycles a tile) to outputs, as long as two products,
 // with the score buffers that tensor memory has room for.  Half of a step's keys for each warpgroup, or a
 // quarter for each of four, was slower (85 and 93 us in the second case).

@@ -32,7 +32,8 @@
 // with the product on the fp32 pipe, 280 as two tf32 words, 226 with 16-byte copies, 213 with
 // paths in packed pairs (219 as three bf16 words, which hold more), 211 walking over units, 207 with
 // a unit's place loaded ahead, 197 with the state in halves and a third block, 188 in quarters.
-// (512 threads a block: 244.)  What bounds it: some 2300 instructions a warp and unit, which fill
+// (512 threads a block: 244.)  Over a bf16 state 145 us (52).  64 requests of 24 nodes 427 us (105), of 64
+// nodes 1548 us (180), over a bf16 state 343 and 1385.  What bounds it: some 2300 instructions a warp and unit, which fill
 // half of the issue slots; a unit's phases (decays, paths, product, updates, outputs) are chains
 // with barriers between them, and three blocks do not fill all of their gaps.
 //
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, blocks_an_sm(kEights)) tree_decode_k
 // w owns rows w, w + 8, .., lane l the columns 4 l .. 4 l + 3, so a warp moves whole rows.  The
 // path's nodes act sixteen at a time: S <- Diag(E) S + sum_j (E_j k_j) u_j^T, E and E_j the decays
 // of the sixteen, and of those behind j.  Bound: the state is read and written once, 121 us for
-// 6144 heads of fp32 at a copy's rate.  With the two other memories' commits 132 us; 161 with the
+// 6144 heads of fp32 at a copy's rate.  With the two other memories' commits 137 us; 161 with the
 // path's rows loaded one after another, which waited behind the state each time (165 at two
 // blocks an SM).
 constexpr int kCommitNodes = 16;
